@@ -17,7 +17,7 @@
 #include <new>
 #include <vector>
 
-#include "internal.h"
+#include "operators.h"
 
 namespace vc {
 bool& pdl_enabled() {
@@ -531,6 +531,38 @@ std::vector<void*> copy_ptrs(void* const* p, int n) {
     } while (0)
 
 }  // namespace
+
+// The communicator as the operators' entry points (operators.cpp) see it.
+namespace vc {
+
+size_t dtype_size(int dt) { return elem_size(dt); }
+
+vResult_t comm_view(vcomm_t c, CommView* v) {
+    if (!comm_ok(c)) return vInvalidArgument;
+    const vResult_t s = sticky(c);
+    if (s != vSuccess) return s;
+    v->nRanks = c->nRanks;
+    v->device = c->device;
+    v->smCount = c->smCount;
+    v->debug = c->cfg.debug;
+    v->grouping = c->groupDepth > 0;
+    return vSuccess;
+}
+
+vResult_t comm_record(vcomm_t c, std::function<vResult_t()> call) {
+    GroupRec rec;
+    rec.launch = std::move(call);
+    c->group->push_back(std::move(rec));
+    return vSuccess;
+}
+
+vResult_t comm_launch(vcomm_t c, const char* what, const std::function<cudaError_t()>& launch) {
+    DeviceGuard g(c);
+    if (!g.ok) return vUnhandledCudaError;
+    return finish_launch(c, launch(), nullptr, what);
+}
+
+}  // namespace vc
 
 extern "C" {
 

@@ -63,6 +63,17 @@ class vPlanInfo_t(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class vRmsNormDesc_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_size_t), ("hidden", ctypes.c_size_t), ("sendStride", ctypes.c_size_t),
+                ("residualStride", ctypes.c_size_t), ("recvStride", ctypes.c_size_t), ("eps", ctypes.c_float),
+                ("datatype", ctypes.c_int), ("weightType", ctypes.c_int), ("quantGroup", ctypes.c_int)]
+
+
+class vTensorList_t(ctypes.Structure):
+    _fields_ = [("nTensors", ctypes.c_int), ("counts", ctypes.c_void_p), ("datatypes", ctypes.c_void_p),
+                ("replicated", ctypes.c_void_p), ("grads", ctypes.c_void_p), ("outs", ctypes.c_void_p)]
+
+
 _lib = None
 
 _SIGNATURES = {
@@ -108,6 +119,14 @@ _SIGNATURES = {
                  ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
     "vScatter": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int,
                   ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "vAllReduceRmsNorm": ([ctypes.c_void_p] * 9, ctypes.c_int),
+    "vAllReduceRmsNormQuant": ([ctypes.c_void_p] * 10, ctypes.c_int),
+    "vRmsNormBackwardWorkspace": ([ctypes.c_void_p] * 3, ctypes.c_int),
+    "vAllReduceRmsNormBackward": ([ctypes.c_void_p] * 9 + [ctypes.c_size_t] + [ctypes.c_void_p] * 2, ctypes.c_int),
+    "vGradNormWorkspace": ([ctypes.c_void_p] * 3, ctypes.c_int),
+    "vGradNorm": ([ctypes.c_void_p] * 3 + [ctypes.c_size_t] + [ctypes.c_void_p] * 2, ctypes.c_int),
+    "vClipGradNorm": ([ctypes.c_void_p, ctypes.c_float] + [ctypes.c_void_p] * 2 + [ctypes.c_size_t]
+                      + [ctypes.c_void_p] * 2, ctypes.c_int),
     "vAllReduceNoAlloc": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int,
                            ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p], ctypes.c_int),
 }
@@ -167,6 +186,8 @@ def _ptr_array(bufs, n_ranks: int):
     n = len(bufs)
     if n != n_ranks:
         raise VcommError(vInvalidArgument, f"expected {n_ranks} buffers (one per rank), got {n}")
+    if isinstance(bufs, ctypes.Array):              # from vBuffers
+        return bufs
     arr_t = _ARRAY_TYPES.get(n)
     if arr_t is None:
         arr_t = _ARRAY_TYPES[n] = ctypes.c_void_p * n
@@ -373,3 +394,128 @@ def vAllReduceNoAlloc(sendbuffs, recvbuffs, count: int, datatype, op, n_ranks: i
     _check(lib().vAllReduceNoAlloc(_ptr_array(sendbuffs, n_ranks), _ptr_array(recvbuffs, n_ranks), count, _dtype_code(datatype),
                                    _op_code(op), n_ranks, n_channels, proto, _stream(stream)),
            "vAllReduceNoAlloc")
+
+
+# ---- operators next to the collectives -------------------------------------------------------
+
+def vBuffers(bufs):
+    """The device addresses of a list of buffers (one per rank; None for NULL) as a C array,
+    which every call here takes in place of the list: a caller whose buffers stay where they
+    are marshals them once.  It holds addresses, not the tensors: the caller keeps those."""
+    bufs = list(bufs)
+    return _ptr_array(bufs, len(bufs))
+
+
+def vRmsNormDesc(rows: int, hidden: int, datatype, weight_type=None, eps: float = 1e-6, send_stride: int = 0,
+                 residual_stride: int = 0, recv_stride: int = 0, quant_group: int = 0) -> vRmsNormDesc_t:
+    """Sizes, strides (in elements, 0 for ``hidden``) and types of an RMS norm's calls; the
+    weight's type is the data's unless ``weight_type`` says float32."""
+    dt = _dtype_code(datatype)
+    return vRmsNormDesc_t(rows, hidden, send_stride, residual_stride, recv_stride, eps, dt,
+                          dt if weight_type is None else _dtype_code(weight_type), quant_group)
+
+
+def vAllReduceRmsNorm(desc, sendbuffs, residual, weight, residual_out, recvbuffs, rstd, comm, stream=None) -> None:
+    """All-reduce + residual + RMS norm; residual, residual_out, rstd and entries of recvbuffs
+    may be None."""
+    _check(lib().vAllReduceRmsNorm(ctypes.addressof(desc), *_norm_args(comm, sendbuffs, residual, weight, residual_out,
+                                                                       recvbuffs), _addr(rstd), comm, _stream(stream)),
+           "vAllReduceRmsNorm")
+
+
+def _norm_args(comm, sendbuffs, residual, weight, residual_out, recvbuffs):
+    n = _n_ranks(comm)
+    return (_ptr_array(sendbuffs, n), _addr(residual), _addr(weight), _addr(residual_out), _ptr_array(recvbuffs, n))
+
+
+def vAllReduceRmsNormQuant(desc, sendbuffs, residual, weight, residual_out, recvbuffs, scalebuffs, rstd, comm,
+                           stream=None) -> None:
+    """The same with e4m3 bytes in recvbuffs and their fp32 scales in scalebuffs."""
+    _check(lib().vAllReduceRmsNormQuant(ctypes.addressof(desc),
+                                        *_norm_args(comm, sendbuffs, residual, weight, residual_out, recvbuffs),
+                                        _ptr_array(scalebuffs, _n_ranks(comm)), _addr(rstd), comm, _stream(stream)),
+           "vAllReduceRmsNormQuant")
+
+
+def vRmsNormBackwardWorkspace(desc, comm) -> int:
+    """Bytes of workspace that vAllReduceRmsNormBackward needs for this descriptor."""
+    b = ctypes.c_size_t(0)
+    _check(lib().vRmsNormBackwardWorkspace(ctypes.addressof(desc), comm, ctypes.addressof(b)),
+           "vRmsNormBackwardWorkspace")
+    return b.value
+
+
+def _workspace(workspace) -> tuple[int | None, int]:
+    """Address and bytes of a workspace: a tensor, or (address, bytes)."""
+    if isinstance(workspace, tuple):
+        return workspace
+    return workspace.data_ptr(), workspace.nbytes
+
+
+def vAllReduceRmsNormBackward(desc, sendbuffs, hidden_states, rstd, weight, grad_residual, recvbuffs, grad_weight,
+                              workspace, comm, stream=None) -> None:
+    n = _n_ranks(comm)
+    _check(lib().vAllReduceRmsNormBackward(ctypes.addressof(desc), _ptr_array(sendbuffs, n), _addr(hidden_states),
+                                           _addr(rstd), _addr(weight), _addr(grad_residual), _ptr_array(recvbuffs, n),
+                                           _addr(grad_weight), *_workspace(workspace), comm, _stream(stream)),
+           "vAllReduceRmsNormBackward")
+
+
+class TensorList:
+    """A vTensorList_t with the arrays it points to.  It holds addresses, not the tensors."""
+
+    def __init__(self, n_ranks: int, counts, datatypes, replicated, grads, outs):
+        n = len(counts)
+        self.n_ranks = n_ranks
+        self._arrays = ((ctypes.c_size_t * n)(*counts), (ctypes.c_int * n)(*datatypes),
+                        None if replicated is None else (ctypes.c_ubyte * n)(*map(bool, replicated)),
+                        (ctypes.c_void_p * (n * n_ranks))(*grads),
+                        None if outs is None else (ctypes.c_void_p * (n * n_ranks))(*outs))
+        self.struct = vTensorList_t(n, *(None if a is None else ctypes.addressof(a) for a in self._arrays))
+        self.address = ctypes.addressof(self.struct)
+
+
+def vTensorList(grads, outs=None, replicated=None) -> TensorList:
+    """The gradients of a step: ``grads[r][t]`` is rank r's tensor t, ``outs`` (the clipped
+    gradients; None: in place) the same, ``replicated[t]`` whether every rank holds all of
+    tensor t (None: none).  A list whose tensors stay where they are serves every step."""
+    first = grads[0]
+    if replicated is not None and len(replicated) != len(first):
+        raise VcommError(vInvalidArgument, f"replicated names {len(replicated)} tensors of {len(first)}")
+    for side in (grads,) if outs is None else (grads, outs):
+        if len(side) != len(grads):
+            raise VcommError(vInvalidArgument, f"outputs of {len(side)} ranks for gradients of {len(grads)}")
+        for tensors in side:
+            if [(t.numel(), t.dtype) for t in tensors] != [(t.numel(), t.dtype) for t in first]:
+                raise VcommError(vInvalidArgument, "every rank's tensors have the same sizes and types")
+            if not all(t.is_contiguous() for t in tensors):
+                raise VcommError(vInvalidArgument, "tensors of a list are contiguous")
+    return TensorList(len(grads), [t.numel() for t in first], [_dtype_code(t.dtype) for t in first], replicated,
+                      [t.data_ptr() for tensors in grads for t in tensors],
+                      None if outs is None else [t.data_ptr() for tensors in outs for t in tensors])
+
+
+def _list(tensors: TensorList, comm) -> int:
+    n = _n_ranks(comm)
+    if tensors.n_ranks != n:
+        raise VcommError(vInvalidArgument, f"a tensor list of {tensors.n_ranks} ranks on a communicator of {n}")
+    return tensors.address
+
+
+def vGradNormWorkspace(tensors: TensorList, comm) -> int:
+    """Bytes of workspace that vGradNorm and vClipGradNorm need for this list."""
+    b = ctypes.c_size_t(0)
+    _check(lib().vGradNormWorkspace(_list(tensors, comm), comm, ctypes.addressof(b)), "vGradNormWorkspace")
+    return b.value
+
+
+def vGradNorm(tensors: TensorList, norm, workspace, comm, stream=None) -> None:
+    """norm[0] = the 2-norm of all the ranks' gradients together."""
+    _check(lib().vGradNorm(_list(tensors, comm), _addr(norm), *_workspace(workspace), comm, _stream(stream)),
+           "vGradNorm")
+
+
+def vClipGradNorm(tensors: TensorList, max_norm: float, norm, workspace, comm, stream=None) -> None:
+    """vGradNorm, then every gradient scaled by min(1, max_norm / (norm + 1e-6))."""
+    _check(lib().vClipGradNorm(_list(tensors, comm), max_norm, _addr(norm), *_workspace(workspace), comm,
+                               _stream(stream)), "vClipGradNorm")

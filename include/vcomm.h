@@ -300,6 +300,113 @@ vResult_t vGather(const void* const* sendbuffs, void* const* recvbuffs, size_t s
 vResult_t vScatter(const void* const* sendbuffs, void* const* recvbuffs, size_t recvcount,
                    vDataType_t datatype, int root, vcomm_t comm, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------------- */
+/* Operators next to the collectives: the all-reduce that ends a tensor-parallel     */
+/* product fused with the residual's addition and the RMS norm behind it, its 8-bit  */
+/* output and its backward pass, and the global gradient norm with clipping that     */
+/* follows the gradients' reduction.  They take the communicator, the stream and the */
+/* per-rank pointer arrays as the collectives do, return the same errors, may be     */
+/* grouped and captured, and hold every sum, statistic and norm in fp32 or more.     */
+/* They allocate no device memory: where one needs scratch, the caller passes it.    */
+/* ------------------------------------------------------------------------------- */
+
+/* Longest row of the norms, in elements. */
+#define VCOMM_MAX_HIDDEN 65536
+
+typedef struct {
+    size_t rows;               /* tokens, at most 2^31 - 1; 0 does nothing (the backward pass
+                                  writes a zero weight gradient) */
+    size_t hidden;             /* elements of a row, at most VCOMM_MAX_HIDDEN */
+    size_t sendStride;         /* elements between the rows of every send buffer; 0: hidden */
+    size_t residualStride;     /* the same of residual and residualOut, and of hiddenStates and
+                                  gradResidual in the backward pass; 0: hidden */
+    size_t recvStride;         /* the same of every receive buffer; 0: hidden */
+    float eps;                 /* >= 0, added to the mean square */
+    vDataType_t datatype;      /* vFloat32, vFloat16 or vBFloat16: of the sends, the residual, the
+                                  stream and the outputs */
+    vDataType_t weightType;    /* of the weight and its gradient: datatype or vFloat32 */
+    int quantGroup;            /* 8-bit output: 0 for one scale a row, 128 for one per 128
+                                  elements (the last group may be shorter) */
+} vRmsNormDesc_t;
+
+/* All-reduce, residual addition and RMS norm in one pass:
+ *   h = sum over ranks of sendbuffs[r] (in rank order) + residual      per element, in fp32
+ *   rstd = 1 / sqrt(mean over the row of h^2 + eps)
+ *   recvbuffs[r] = h * rstd * weight      for every rank r, rounded once to the data type
+ * residualOut gets h rounded to the data type, rstd (fp32, one per row) what the backward
+ * pass needs.  The residual stream is the same on every rank, so it is passed once.
+ * residual, residualOut and rstd may be NULL.  A rank whose recvbuffs entry is NULL gets no
+ * copy of the output; at least one has to want it.  Unlike vAllReduce's, the partial sums
+ * are not rounded to the data type from rank to rank.
+ * In place: recvbuffs[r] == sendbuffs[r] with equal strides, and residualOut == residual;
+ * no other overlap.  Any element-aligned pointer and stride is accepted: bytes between rows
+ * are not written, and read only within the 16-byte aligned blocks that hold a row's own
+ * elements.  An infinite or NaN element makes its own row NaN or zero as the formula has
+ * it, no other row. */
+vResult_t vAllReduceRmsNorm(const vRmsNormDesc_t* desc, const void* const* sendbuffs, const void* residual,
+                            const void* weight, void* residualOut, void* const* recvbuffs, float* rstd,
+                            vcomm_t comm, cudaStream_t stream);
+
+/* The same with the normed output in 8 bits (e4m3: 4 exponent bits, 3 mantissa bits, no
+ * infinity): recvbuffs[r] holds bytes, with recvStride bytes between rows, and scalebuffs[r]
+ * the fp32 scales, one per row or ceil(hidden / 128) per row, without gaps:
+ *   amax = max(2^-64, max |h * weight| * rstd) of the row or group, scale = amax / 448,
+ *   recvbuffs[r] = h * weight * rstd / scale rounded to the nearest e4m3 value.
+ * A NaN in a row or group makes its scale NaN.  A rank that wants the output wants its
+ * scales. */
+vResult_t vAllReduceRmsNormQuant(const vRmsNormDesc_t* desc, const void* const* sendbuffs, const void* residual,
+                                 const void* weight, void* residualOut, void* const* recvbuffs,
+                                 float* const* scalebuffs, float* rstd, vcomm_t comm, cudaStream_t stream);
+
+/* Backward pass of vAllReduceRmsNorm.  sendbuffs[r] is rank r's partial gradient of the
+ * normed output (its column-parallel product's input gradient), hiddenStates the stream that
+ * was normed (residualOut), rstd what the forward pass stored, gradResidual (may be NULL) the
+ * gradient that reaches the stream by another way:
+ *   dy = sum over ranks of sendbuffs[r],  xhat = hiddenStates * rstd,  g = dy * weight
+ *   recvbuffs[r] = rstd * (g - xhat * mean(g * xhat)) + gradResidual
+ *   gradWeight = sum over rows of dy * xhat
+ * The output is the gradient of the residual and, as the stream is a plain sum, of every
+ * rank's partial sum too.  recvbuffs entries may be NULL, but not all.  In place:
+ * recvbuffs[r] == sendbuffs[r] with equal strides, or one recvbuffs entry == gradResidual
+ * with equal strides.  The workspace is at least the number of bytes that
+ * vRmsNormBackwardWorkspace gives for the descriptor, 16-byte aligned, and used by nothing
+ * else until the call's work is done; a smaller one gives vInvalidArgument.  The same call
+ * gives the same bits. */
+vResult_t vRmsNormBackwardWorkspace(const vRmsNormDesc_t* desc, vcomm_t comm, size_t* bytes);
+vResult_t vAllReduceRmsNormBackward(const vRmsNormDesc_t* desc, const void* const* sendbuffs,
+                                    const void* hiddenStates, const float* rstd, const void* weight,
+                                    const void* gradResidual, void* const* recvbuffs, void* gradWeight,
+                                    void* workspace, size_t workspaceBytes, vcomm_t comm, cudaStream_t stream);
+
+/* Gradients of nTensors tensors on every rank.  A tensor is either split (each rank holds a
+ * piece of counts[t] elements: reduce-scattered or tensor-parallel) or replicated (each rank
+ * holds all of it: all-reduced).  Any number of tensors, of any sizes and types, up to 2^43
+ * elements in all.  The arrays are host memory and may be freed when the call returns. */
+typedef struct {
+    int nTensors;
+    const size_t* counts;               /* [nTensors] elements on each rank; 0: skipped */
+    const vDataType_t* datatypes;       /* [nTensors] vFloat32, vFloat16 or vBFloat16 */
+    const unsigned char* replicated;    /* [nTensors], or NULL: all split */
+    const void* const* grads;           /* [nRanks * nTensors], rank r's tensor t at r * nTensors + t */
+    void* const* outs;                  /* the clipped gradients, in the same order and types;
+                                           NULL: in place */
+} vTensorList_t;
+
+/* *norm (device memory, fp32) = the 2-norm of all ranks' gradients together, a replicated
+ * tensor counted once, by rank 0's copy.  Squares are taken and added in fp32 over at most
+ * 64 elements, their sums in fp64, in an order that the sizes fix.
+ * vClipGradNorm then scales every rank's gradients by min(1, maxNorm / (norm + 1e-6)),
+ * rounded once to their type (no element is rewritten in place where that factor is 1).  A
+ * norm that is not finite scales as the formula has it: infinity by 0, NaN by NaN.  maxNorm
+ * must be >= 0.  No tensor may overlap another, nor an output another tensor's gradient.
+ * The workspace is at least what vGradNormWorkspace gives for the list, 16-byte aligned,
+ * used by nothing else until the call's work is done. */
+vResult_t vGradNormWorkspace(const vTensorList_t* list, vcomm_t comm, size_t* bytes);
+vResult_t vGradNorm(const vTensorList_t* list, float* norm, void* workspace, size_t workspaceBytes,
+                    vcomm_t comm, cudaStream_t stream);
+vResult_t vClipGradNorm(const vTensorList_t* list, float maxNorm, float* norm, void* workspace,
+                        size_t workspaceBytes, vcomm_t comm, cudaStream_t stream);
+
 /* Ring all-reduce for callers that cannot allocate device memory.  The pages have no
  * counterpart to this call; it exists for code that must not call cudaMalloc (allocator
  * or memory-pool callbacks, which must not re-enter the allocator; runtimes that own all
