@@ -2,94 +2,100 @@
 //
 //   norm = sqrt(sum over all tensors of g^2),  g' = g min(1, maxNorm / (norm + 1e-6))
 //
-// The tensors are one flat space of 32 KiB chunks, so a launch covers large and small ones
-// alike.  A thread sums the squares of its part of a chunk in fp32 (at most 64 terms) and adds
-// chunks and threads in fp64; every sum's order follows from the sizes alone.
+// The tensors are cut into chunks of 32 KiB, listed once in device memory, so one launch
+// covers any number of large and small ones and a CTA finds its work with one load.  A thread
+// adds the squares of its part of a chunk in fp32 (at most 64 terms) and chunks and threads in
+// fp64; the order of every sum follows from the sizes alone, whichever CTA ends last.
 #include "norm.cuh"
 
 namespace vc {
 
 namespace {
 
-// The item that holds a chunk: the last whose first chunk is not beyond it.
-template <int CAP>
-__device__ __forceinline__ int find_item(const unsigned int* start, int n, unsigned int chunk) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (start[mid] <= chunk) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
+__device__ __forceinline__ GradChunk load_chunk(const GradChunk* p) {
+    GradChunk c;
+    const uint4 lo = *reinterpret_cast<const uint4*>(p);
+    const uint2 hi = *reinterpret_cast<const uint2*>(reinterpret_cast<const char*>(p) + 16);
+    c.in = (const char*)(((uint64_t)lo.y << 32) | lo.x);
+    c.out = (char*)(((uint64_t)lo.w << 32) | lo.z);
+    c.count = (int)hi.x;
+    c.dt = (int)hi.y;
+    return c;
 }
 
-template <int E>
-__device__ __forceinline__ Span span_long(long long e0, long long count) {
-    Span s;
-    s.lo = e0 < 0 ? (int)-e0 : 0;
-    s.hi = count - e0 < E ? (int)max(count - e0, 0ll) : E;
-    return s;
-}
-
-// Sum of squares of a thread's part of chunk `chunk` of a tensor.
+// Sum of squares of a thread's part of a chunk.
 template <int DT>
-__device__ __forceinline__ float chunk_squares(const GradItem& it, unsigned int chunk) {
+__device__ __forceinline__ float chunk_squares(const GradChunk& c) {
     constexpr int E = kVecElems<DT>;
     constexpr int ESZ = DTypeOf<DT>::size;
-    const int shift = (int)((uintptr_t)it.in & 15u) / ESZ;
-    const long long k0 = (long long)chunk * kGradChunkVecs + threadIdx.x;
-    const char* p = (const char*)it.in - shift * ESZ + k0 * 16;
-    const long long count = (long long)it.count;
+    const int shift = (int)((uintptr_t)c.in & 15u) / ESZ;
+    const char* p = c.in - shift * ESZ + (size_t)threadIdx.x * 16;
+    const int e0 = (int)threadIdx.x * E - shift;
     uint4 raw[kGradVecs];
 #pragma unroll
     for (int i = 0; i < kGradVecs; i++) {
-        const long long e0 = (k0 + i * kGradThreads) * E - shift;
         raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (e0 < count) raw[i] = ld_once(p + (size_t)i * kGradThreads * 16);
+        if (e0 + i * kGradThreads * E < c.count) raw[i] = ld_once(p + i * kGradThreads * 16);
     }
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float2 s[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
     for (int i = 0; i < kGradVecs; i++) {
-        const long long e0 = (k0 + i * kGradThreads) * E - shift;
+        const int e = e0 + i * kGradThreads * E;
         float f[E];
         widen_vec<DT>(raw[i], f);
-        if (e0 < 0 || e0 + E > count) {                // elements of other tensors
-            const Span sp = span_long<E>(e0, count);
+        if (e < 0 || e + E > c.count) {                // elements of other chunks
+            const Span sp = span_of<E>(e, c.count);
 #pragma unroll
             for (int j = 0; j < E; j++) f[j] = sp.has(j) ? f[j] : 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < E; j++) s[j & 3] = fmaf(f[j], f[j], s[j & 3]);
+        for (int j = 0; j < E; j += 2) {
+            const float2 x = make_float2(f[j], f[j + 1]);
+            s[j / 2 & 1] = fma2(x, x, s[j / 2 & 1]);
+        }
     }
-    return (s[0] + s[1]) + (s[2] + s[3]);
+    return (s[0].x + s[0].y) + (s[1].x + s[1].y);
 }
 
-template <int DT>
-__device__ __forceinline__ void chunk_scale(const GradItem& it, unsigned int chunk, float factor) {
+// Scale a thread's part of a chunk.  SAME: gradient and output start at the same offset from a
+// 16-byte boundary, so one load gives each vector of the output, and a thread's loads are all
+// under way before its first store; else two loads and a shift give it, two vectors at a time
+// (all eight at once took 254 registers).
+template <int DT, bool SAME>
+__device__ __forceinline__ void chunk_scale(const GradChunk& c, float factor) {
     constexpr int E = kVecElems<DT>;
     constexpr int ESZ = DTypeOf<DT>::size;
-    const int shift = (int)((uintptr_t)it.out & 15u) / ESZ;
-    const long long k0 = (long long)chunk * kGradChunkVecs + threadIdx.x;
-    const ptrdiff_t off = (ptrdiff_t)k0 * 16 - shift * ESZ;
-    const long long count = (long long)it.count;
-    uint4 raw[kGradVecs];
+    constexpr int K = SAME ? kGradVecs : 2;
+    const int shift = (int)((uintptr_t)c.out & 15u) / ESZ;
+#pragma unroll 1
+    for (int part = 0; part < kGradVecs; part += K) {
+        const int k = part * kGradThreads + (int)threadIdx.x;
+        const ptrdiff_t off = (ptrdiff_t)k * 16 - shift * ESZ;
+        const int e0 = k * E - shift;
+        uint4 raw[K];
 #pragma unroll
-    for (int i = 0; i < kGradVecs; i++) {
-        const long long e0 = (k0 + i * kGradThreads) * E - shift;
-        if (e0 < count)
-            raw[i] = load_vec<ESZ, true>((const char*)it.in + off + (ptrdiff_t)i * kGradThreads * 16,
-                                         span_long<E>(e0, count));
+        for (int i = 0; i < K; i++) {
+            const int e = e0 + i * kGradThreads * E;
+            const char* p = c.in + off + i * kGradThreads * 16;
+            if (e < c.count) raw[i] = SAME ? ld_once(p) : load_vec<ESZ, true>(p, span_of<E>(e, c.count));
+        }
+#pragma unroll
+        for (int i = 0; i < K; i++) {
+            const int e = e0 + i * kGradThreads * E;
+            if (e >= c.count) continue;
+            float f[E];
+            widen_vec<DT>(raw[i], f);
+            scale_by(f, factor);
+            char* p = c.out + off + i * kGradThreads * 16;
+            if (e >= 0 && e + E <= c.count) st_stream(p, narrow_vec<DT>(f));
+            else store_vec<DT, true>(p, span_of<E>(e, c.count), f);
+        }
     }
-#pragma unroll
-    for (int i = 0; i < kGradVecs; i++) {
-        const long long e0 = (k0 + i * kGradThreads) * E - shift;
-        if (e0 >= count) continue;
-        float f[E];
-        widen_vec<DT>(raw[i], f);
-#pragma unroll
-        for (int j = 0; j < E; j++) f[j] *= factor;
-        store_vec<DT, true>((char*)it.out + off + (ptrdiff_t)i * kGradThreads * 16, span_long<E>(e0, count), f);
-    }
+}
+template <int DT>
+__device__ __forceinline__ void chunk_scale(const GradChunk& c, float factor) {
+    if ((((uintptr_t)c.in ^ (uintptr_t)c.out) & 15u) == 0) chunk_scale<DT, true>(c, factor);
+    else chunk_scale<DT, false>(c, factor);
 }
 
 // Sum over the CTA in fp64, in an order that the CTA's size fixes; every thread gets it.
@@ -107,66 +113,57 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
 
 }  // namespace
 
-template <int CAP>
-__global__ void __launch_bounds__(kGradThreads) k_grad_squares(const __grid_constant__ GradArgs<CAP> a) {
+// The CTA that ends last adds all CTAs' sums, so that the norm takes one launch.
+__global__ void __launch_bounds__(kGradThreads) k_grad_norm(const __grid_constant__ GradNormArgs a) {
     pdl_begin();
-    __shared__ unsigned int start[CAP];
-    __shared__ double red[32];
-    for (int i = threadIdx.x; i < a.nItems; i += kGradThreads) start[i] = a.items[i].chunk0;
-    __syncthreads();
+    __shared__ double red[2][32];
+    __shared__ bool last;
     double sum = 0.0;
-    for (unsigned int c = blockIdx.x; c < a.nChunks; c += gridDim.x) {
-        const GradItem& it = a.items[find_item<CAP>(start, a.nItems, c)];
-        const unsigned int chunk = c - it.chunk0;
-        if (it.dt == kF32) sum += (double)chunk_squares<kF32>(it, chunk);
-        else if (it.dt == kF16) sum += (double)chunk_squares<kF16>(it, chunk);
-        else sum += (double)chunk_squares<kBF16>(it, chunk);
+    GradChunk c;
+    if (blockIdx.x < a.nChunks) c = load_chunk(a.chunks + blockIdx.x);
+    for (unsigned int i = blockIdx.x; i < a.nChunks; i += gridDim.x) {
+        GradChunk next = c;
+        if (a.nChunks - i > gridDim.x) next = load_chunk(a.chunks + i + gridDim.x);
+        if (c.dt == kF32) sum += (double)chunk_squares<kF32>(c);
+        else if (c.dt == kF16) sum += (double)chunk_squares<kF16>(c);
+        else sum += (double)chunk_squares<kBF16>(c);
+        c = next;
     }
-    sum = block_sum(sum, red);
-    if (threadIdx.x == 0) a.partials[blockIdx.x] = sum;
-}
-
-__global__ void __launch_bounds__(1024) k_grad_norm(const double* partials, int n, float* norm) {
-    pdl_begin();
-    __shared__ double red[32];
-    double s = 0.0;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) s += partials[i];
-    s = block_sum(s, red);
-    if (threadIdx.x == 0) *norm = (float)sqrt(s);
-}
-
-template <int CAP>
-__global__ void __launch_bounds__(kGradThreads) k_grad_clip(const __grid_constant__ GradArgs<CAP> a) {
-    pdl_begin();
-    __shared__ unsigned int start[CAP];
-    for (int i = threadIdx.x; i < a.nItems; i += kGradThreads) start[i] = a.items[i].chunk0;
+    sum = block_sum(sum, red[0]);
+    if (threadIdx.x == 0) {
+        __stcg(a.partials + blockIdx.x, sum);
+        __threadfence();
+        last = atomicAdd(a.done, 1u) == gridDim.x - 1;
+    }
     __syncthreads();
+    if (!last) return;
+    __threadfence();
+    double all = 0.0;
+    for (unsigned int i = threadIdx.x; i < gridDim.x; i += kGradThreads) all += __ldcg(a.partials + i);
+    all = block_sum(all, red[1]);
+    if (threadIdx.x == 0) {
+        *a.norm = (float)sqrt(all);
+        *a.done = 0u;
+    }
+}
+
+// One chunk a CTA, dispatched in order.
+__global__ void __launch_bounds__(kGradThreads) k_grad_clip(const __grid_constant__ GradClipArgs a) {
+    pdl_begin();
+    const GradChunk c = load_chunk(a.chunks + blockIdx.x);
     float factor = a.maxNorm / (*a.norm + 1e-6f);
     factor = factor > 1.0f ? 1.0f : factor;            // a NaN stays
-    for (unsigned int c = blockIdx.x; c < a.nChunks; c += gridDim.x) {
-        const GradItem& it = a.items[find_item<CAP>(start, a.nItems, c)];
-        if (factor == 1.0f && it.in == it.out) continue;
-        const unsigned int chunk = c - it.chunk0;
-        if (it.dt == kF32) chunk_scale<kF32>(it, chunk, factor);
-        else if (it.dt == kF16) chunk_scale<kF16>(it, chunk, factor);
-        else chunk_scale<kBF16>(it, chunk, factor);
-    }
+    if (factor == 1.0f && c.in == c.out) return;
+    if (c.dt == kF32) chunk_scale<kF32>(c, factor);
+    else if (c.dt == kF16) chunk_scale<kF16>(c, factor);
+    else chunk_scale<kBF16>(c, factor);
 }
 
-template <int CAP>
-cudaError_t launch_grad_squares(const GradArgs<CAP>& a, int grid, cudaStream_t s) {
-    return pdl_launch(k_grad_squares<CAP>, (unsigned)grid, kGradThreads, 0, s, a);
+cudaError_t launch_grad_norm(const GradNormArgs& a, int grid, cudaStream_t s) {
+    return pdl_launch(k_grad_norm, (unsigned)grid, kGradThreads, 0, s, a);
 }
-cudaError_t launch_grad_norm(const double* partials, int n, float* norm, cudaStream_t s) {
-    return pdl_launch(k_grad_norm, 1u, 1024u, 0, s, partials, n, norm);
+cudaError_t launch_grad_clip(const GradClipArgs& a, cudaStream_t s) {
+    return pdl_launch(k_grad_clip, a.nChunks, kGradThreads, 0, s, a);
 }
-template <int CAP>
-cudaError_t launch_grad_clip(const GradArgs<CAP>& a, cudaStream_t s) {
-    return pdl_launch(k_grad_clip<CAP>, a.nChunks, kGradThreads, 0, s, a);
-}
-template cudaError_t launch_grad_squares<kGradItemsSmall>(const GradArgs<kGradItemsSmall>&, int, cudaStream_t);
-template cudaError_t launch_grad_squares<kGradItemsLarge>(const GradArgs<kGradItemsLarge>&, int, cudaStream_t);
-template cudaError_t launch_grad_clip<kGradItemsSmall>(const GradArgs<kGradItemsSmall>&, cudaStream_t);
-template cudaError_t launch_grad_clip<kGradItemsLarge>(const GradArgs<kGradItemsLarge>&, cudaStream_t);
 
 }  // namespace vc

@@ -70,6 +70,91 @@ __device__ __forceinline__ Span span_of(int e0, int width) {
     return s;
 }
 
+// A thread's vectors of one row.
+template <int DT, int V>
+struct RowVecs {
+    static constexpr int E = kVecElems<DT>;
+    static constexpr int ESZ = DTypeOf<DT>::size;
+    int e0, step;                    // first element of vector 0, elements between vectors
+    Span sp[V];
+    bool on[V];                      // the vector holds elements of a row that exists
+    __device__ __forceinline__ void set(int e0_, int step_, int width, bool live) {
+        e0 = e0_;
+        step = step_;
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            sp[v] = span_of<E>(e0 + v * step, width);
+            on[v] = live && sp[v].any();
+        }
+    }
+    // Zero what lies outside the row (all of a vector that is not on).
+    __device__ __forceinline__ void mask(float (&f)[V][E]) const {
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            if (sp[v].full(E)) continue;
+#pragma unroll
+            for (int j = 0; j < E; j++) f[v][j] = sp[v].has(j) ? f[v][j] : 0.0f;
+        }
+    }
+};
+
+// Two fp32 additions, products or fused steps in one instruction (each rounded as the single
+// ones are).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+// max(a, |b|, |c|), where a NaN wins.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+    return r;
+}
+template <int E>
+__device__ __forceinline__ void add_to(float (&acc)[E], const float (&f)[E]) {
+#pragma unroll
+    for (int j = 0; j < E; j += 2) {
+        const float2 s = add2(make_float2(acc[j], acc[j + 1]), make_float2(f[j], f[j + 1]));
+        acc[j] = s.x;
+        acc[j + 1] = s.y;
+    }
+}
+template <int E>
+__device__ __forceinline__ void scale_by(float (&acc)[E], float k) {
+#pragma unroll
+    for (int j = 0; j < E; j += 2) {
+        const float2 s = mul2(make_float2(acc[j], acc[j + 1]), make_float2(k, k));
+        acc[j] = s.x;
+        acc[j + 1] = s.y;
+    }
+}
+template <int E>
+__device__ __forceinline__ void mul_by(float (&acc)[E], const float (&f)[E]) {
+#pragma unroll
+    for (int j = 0; j < E; j += 2) {
+        const float2 s = mul2(make_float2(acc[j], acc[j + 1]), make_float2(f[j], f[j + 1]));
+        acc[j] = s.x;
+        acc[j + 1] = s.y;
+    }
+}
+
 // Streamed once, so kept out of L1.  volatile: never moved above the wait for the previous
 // kernel, nor merged with another load of the address.
 __device__ __forceinline__ uint4 ld_once(const void* p) {
@@ -79,13 +164,9 @@ __device__ __forceinline__ uint4 ld_once(const void* p) {
     return v;
 }
 
-// Read by every row, so kept in L1.  Not the read-only path: the kernel may become resident
+// Read by every row, so through L1.  Not by the read-only path: the kernel may become resident
 // while the previous one still writes what it reads.
-__device__ __forceinline__ uint4 ld_shared_by_rows(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
+__device__ __forceinline__ uint4 ld_shared_by_rows(const void* p) { return *reinterpret_cast<const uint4*>(p); }
 
 // The 16 bytes at p (any element-aligned address).  GENERAL false: p is 16-byte aligned and
 // the whole vector lies in the row.  Elements outside the span come back undefined.
@@ -173,10 +254,11 @@ private:
 
 // Sum over the ranks, in rank order and in fp32, of one row's vectors of a thread.  UN ranks'
 // loads are in flight before the first is added.
-template <int DT, int V, bool GENERAL, typename Sends>
-__device__ __forceinline__ void sum_ranks(const Sends& send, int N, ptrdiff_t off, const Span (&sp)[V],
-                                          const bool (&on)[V], ptrdiff_t vecStep, float (&acc)[V][kVecElems<DT>]) {
+template <int DT, int V, bool GENERAL>
+__device__ __forceinline__ void sum_ranks(const void* const* send, int N, ptrdiff_t off, const RowVecs<DT, V>& rv,
+                                          float (&acc)[V][kVecElems<DT>]) {
     constexpr int E = kVecElems<DT>;
+    constexpr int ESZ = DTypeOf<DT>::size;
     constexpr int UN = GENERAL ? (V == 1 ? 4 : 2) : 8 / V;
 #pragma unroll
     for (int v = 0; v < V; v++)
@@ -190,7 +272,7 @@ __device__ __forceinline__ void sum_ranks(const Sends& send, int N, ptrdiff_t of
                 const char* p = (const char*)send[r + i] + off;
 #pragma unroll
                 for (int v = 0; v < V; v++)
-                    if (on[v]) raw[i][v] = load_vec<DTypeOf<DT>::size, GENERAL>(p + v * vecStep, sp[v]);
+                    if (rv.on[v]) raw[i][v] = load_vec<ESZ, GENERAL>(p + (ptrdiff_t)v * rv.step * ESZ, rv.sp[v]);
             }
         }
 #pragma unroll
@@ -198,14 +280,57 @@ __device__ __forceinline__ void sum_ranks(const Sends& send, int N, ptrdiff_t of
             if (r + i < N) {
 #pragma unroll
                 for (int v = 0; v < V; v++) {
-                    if (on[v]) {
+                    if (rv.on[v]) {
                         float f[E];
                         widen_vec<DT>(raw[i][v], f);
-#pragma unroll
-                        for (int j = 0; j < E; j++) acc[v][j] += f[j];
+                        add_to(acc[v], f);
                     }
                 }
             }
+        }
+    }
+}
+
+// ---- outputs that start at another offset from 16 bytes than the row's vectors -------------
+
+__device__ __forceinline__ uint4 ld_smem(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_smem(uint32_t p, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// `bytes` bytes at shared address `src` (any alignment) to dst, by a team of `threads`: whole
+// aligned 16-byte blocks, each cut from the two that hold it, and the ends in OSZ-byte elements.
+// Element stores alone would take 8 (16 for bytes) per vector; measured on 3 x 1537 x 2731 fp16
+// with every rank at its own offset, they made 41 us of a pass that takes FINAL_RAGGED.
+template <int OSZ>
+__device__ __forceinline__ void copy_out(char* dst, uint32_t src, int bytes, int t, int threads) {
+    const int head = min((int)((16u - (unsigned)((uintptr_t)dst & 15u)) & 15u), bytes);
+    const int blocks = (bytes - head) >> 4;
+    const unsigned sh = (src + head) & 15u;
+    const uint32_t from = src + head - sh;
+    for (int i = t; i < blocks; i += threads) {
+        const uint4 a = ld_smem(from + 16 * i);
+        st_stream(dst + head + (size_t)i * 16, sh == 0 ? a : shift_bytes(a, ld_smem(from + 16 * i + 16), sh));
+    }
+    const int tail = head + blocks * 16;
+    for (int k = t * OSZ; k < head + bytes - tail; k += threads * OSZ) {
+        const int at = k < head ? k : tail + k - head;
+        if (OSZ == 1) {
+            uint32_t v;
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(src + at) : "memory");
+            *(uint8_t*)(dst + at) = (uint8_t)v;
+        } else if (OSZ == 2) {
+            uint16_t v;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(src + at) : "memory");
+            *(uint16_t*)(dst + at) = v;
+        } else {
+            uint32_t v;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(src + at) : "memory");
+            *(uint32_t*)(dst + at) = v;
         }
     }
 }
@@ -230,23 +355,22 @@ __device__ __forceinline__ void st_cluster(const void* local, unsigned rank, uin
     asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(r), "r"(v) : "memory");
 }
 
-// Sum of `s` and, with MAX, the maximum of `m` (bits of non-negative floats, whose order is
-// that of the unsigned integers; a NaN is above everything) over the threads of a team.  The
+// Sum of `s` and, with MAX, the maximum of `m` (not negative; a NaN wins) over the threads of a team.  The
 // order of the additions depends on the shape alone.  All threads of the CTA call it; on a
 // cluster, cluster_arrive() has been called once before.  The words of `red` are not reused
 // by the same CTA before another barrier of it has passed.
 struct TeamScratch {
     float sum[32];
-    uint32_t max[32];
+    float max[32];
     float clusterSum[kNormMaxCluster];
-    uint32_t clusterMax[kNormMaxCluster];
+    float clusterMax[kNormMaxCluster];
 };
 template <bool MAX>
-__device__ __forceinline__ void team_reduce(TeamScratch& red, const NormShape& sh, float& s, uint32_t& m) {
+__device__ __forceinline__ void team_reduce(TeamScratch& red, const NormShape& sh, float& s, float& m) {
     const int lanes = sh.teamThreads < 32 ? sh.teamThreads : 32;
     for (int o = lanes >> 1; o > 0; o >>= 1) {
         s += __shfl_xor_sync(~0u, s, o);
-        if (MAX) m = max(m, __shfl_xor_sync(~0u, m, o));
+        if (MAX) m = max_abs(m, __shfl_xor_sync(~0u, m, o), 0.0f);
     }
     if (sh.teamThreads <= 32) return;
     const int warps = (int)blockDim.x >> 5, lane = threadIdx.x & 31;
@@ -256,29 +380,35 @@ __device__ __forceinline__ void team_reduce(TeamScratch& red, const NormShape& s
     }
     __syncthreads();
     s = lane < warps ? red.sum[lane] : 0.0f;
-    if (MAX) m = lane < warps ? red.max[lane] : 0u;
+    if (MAX) m = lane < warps ? red.max[lane] : 0.0f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         s += __shfl_xor_sync(~0u, s, o);
-        if (MAX) m = max(m, __shfl_xor_sync(~0u, m, o));
+        if (MAX) m = max_abs(m, __shfl_xor_sync(~0u, m, o), 0.0f);
     }
     if (sh.cluster == 1) return;
     cluster_wait();                  // every CTA of the cluster has started
     if (threadIdx.x < (unsigned)sh.cluster) {
         const unsigned me = cluster_rank();
         st_cluster(&red.clusterSum[me], threadIdx.x, __float_as_uint(s));
-        if (MAX) st_cluster(&red.clusterMax[me], threadIdx.x, m);
+        if (MAX) st_cluster(&red.clusterMax[me], threadIdx.x, __float_as_uint(m));
     }
     cluster_arrive();
     cluster_wait();
     s = 0.0f;
     for (int c = 0; c < sh.cluster; c++) {
         s += red.clusterSum[c];
-        if (MAX) m = max(m, red.clusterMax[c]);
+        if (MAX) m = max_abs(m, red.clusterMax[c], 0.0f);
     }
 }
 
-// Threads, vectors and rows of a launch.
+// Let a kernel use `bytes` of dynamic shared memory.
+template <typename K>
+inline cudaError_t allow_smem(K kernel, size_t bytes) {
+    if (bytes <= 32 * 1024) return cudaSuccess;        // with the static arrays, below the default 48 KiB
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
 template <typename K, typename... Args>
 inline cudaError_t norm_launch(K kernel, unsigned grid, const NormShape& sh, size_t smem, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};

@@ -16,39 +16,105 @@
 
 namespace vc {
 
+namespace {
+
+// Threads of a team that holds `vecs` vectors a thread of a row of nv vectors: part of a warp,
+// or whole warps.
+int team_threads(int nv, int vecs) {
+    const int need = (nv + vecs - 1) / vecs;
+    if (need > 32) return (need + 31) / 32 * 32;
+    int t = 1;
+    while (t < need) t *= 2;
+    return t;
+}
+void set_team(NormShape* s, int nv, int vecs) {
+    s->vecs = vecs;
+    s->teamThreads = team_threads(nv, vecs);
+    s->threads = std::max(s->teamThreads, kNormWarpCta);
+    if (s->teamThreads > 32) s->threads = s->teamThreads;
+    s->rowsPerCta = s->threads / s->teamThreads;
+}
+
+}  // namespace
+
 // Launch shape of the norm kernels.
-NormShape norm_shape(size_t rows, int hidden, int elemSize, int smCount, bool general) {
-    const int E = 16 / elemSize;
+NormShape norm_shape(const NormCall& c) {
+    const int E = 16 / c.elemSize;
     // a row that may start inside an aligned vector touches up to one vector more
-    const int nv = general ? (hidden + 2 * E - 2) / E : hidden / E;
-    NormShape s;
-    s.general = general ? 1 : 0;
+    const int nv = c.general ? (c.hidden + 2 * E - 2) / E : c.hidden / E;
+    NormShape s = {};
+    s.general = c.general ? 1 : 0;
     s.cluster = 1;
-    if (nv <= 128) {                 // a row fits 4 vectors of each lane of a warp
-        s.vecs = nv <= 32 ? 1 : nv <= 64 ? 2 : 4;
-        s.teamThreads = 1;
-        while (s.teamThreads * s.vecs < nv) s.teamThreads *= 2;
-        s.threads = kNormWarpCta;
-        s.rowsPerCta = s.threads / s.teamThreads;
-        return s;
+
+    // Staged: more vectors a thread means fewer instructions and barriers a row, as long as
+    // the last warp is not left half empty.
+    double best = 0;
+    for (const int vecs : {4, 2, 1}) {
+        const int team = team_threads(nv, vecs);
+        const double weight = vecs == 4 ? 1.0 : vecs == 2 ? 0.92 : 0.8;
+        const double use = weight * nv / ((double)team * vecs);
+        if (team <= kStageMaxThreads && use > best) {
+            best = use;
+            set_team(&s, nv, vecs);
+        }
     }
-    // rows longer than a CTA's registers hold
-    while ((nv + s.cluster - 1) / s.cluster > kNormMaxThreads * 4) s.cluster *= 2;
-    // few rows: split each over more CTAs while SMs are idle
-    while (s.cluster < kNormMaxCluster && rows * (size_t)s.cluster * 2 <= (size_t)smCount &&
-           nv / (s.cluster * 2) >= 64)
-        s.cluster *= 2;
-    const int per = (nv + s.cluster - 1) / s.cluster;
-    s.vecs = per <= 512 ? 1 : per <= 1024 ? 2 : 4;
-    s.teamThreads = ((per + s.vecs - 1) / s.vecs + 31) / 32 * 32;
-    s.threads = s.teamThreads;
-    s.rowsPerCta = 1;
+    // Bytes of dynamic shared memory for the shape as it stands.
+    const auto layout = [&]() {
+        const size_t vectors = (size_t)s.threads * s.vecs;
+        s.extraBytes = (int)(vectors * E * c.extraPerElem);
+        s.weightBytes = s.staged ? (int)(((size_t)s.teamThreads * s.vecs * E * c.weightSize + 30) / 16 * 16 + 80) : 0;
+        s.stageBytes = s.staged ? (int)std::min<size_t>(c.segments * vectors * 16 * (c.realign ? 2 : 1), 1 << 28) : 0;
+        // a row's vectors, and the block behind them that a realigned read may touch
+        s.rowBytes = c.general && (c.outRealign || s.cluster > 1) ? s.teamThreads * s.vecs * 16 + 16 : 0;
+        s.smemBytes = s.extraBytes + s.weightBytes + s.stageBytes + s.rowBytes * c.rowBuffers * s.rowsPerCta;
+    };
+    if (best > 0) {
+        // One staged row a CTA, and as many CTAs as have about 72 KiB under way per SM: less
+        // leaves the memory waiting, more makes it slower (8 x 4096 x 4096 bf16, 72 KiB a row:
+        // 93 us with one CTA, 105 us with two or with two stages; 1 x 16384 x 4096 to 8 bits,
+        // 16 KiB a row: 121, 102, 74 us with two, three, four).
+        s.staged = 1;
+        layout();
+        const int most = 224 * 1024, overhead = 4 * 1024;    // of the SM's, and of a CTA's static arrays
+        const int regs = s.vecs == 1 ? 64 : 128;
+        const int aim = std::max(1, (int)((72 * 1024 + s.stageBytes / 2) / std::max(1, s.stageBytes)));
+        if (s.smemBytes + overhead <= most) {
+            const int perSm = std::min({aim, most / (s.smemBytes + overhead), 65536 / (regs * s.threads), 16});
+            const size_t wave = (size_t)c.smCount * std::max(1, perSm);
+            s.staged = (c.rows + s.rowsPerCta - 1) / s.rowsPerCta > wave;
+            s.ctas = (int)wave;
+        } else {
+            s.staged = 0;
+        }
+    }
+    if (!s.staged) {
+        if (nv <= 32) {              // few rows: one vector a thread, as the latency counts
+            set_team(&s, nv, 1);
+        } else {
+            // rows longer than a CTA's registers hold
+            while ((nv + s.cluster - 1) / s.cluster > kNormMaxThreads * 4) s.cluster *= 2;
+            // few rows: split each over more CTAs while SMs are idle
+            while (s.cluster < kNormMaxCluster && c.rows * (size_t)s.cluster * 2 <= (size_t)c.smCount &&
+                   nv / (s.cluster * 2) >= 64)
+                s.cluster *= 2;
+            const int per = (nv + s.cluster - 1) / s.cluster;
+            s.vecs = per <= 512 ? 1 : per <= 1024 ? 2 : 4;
+            s.teamThreads = ((per + s.vecs - 1) / s.vecs + 31) / 32 * 32;
+            s.threads = s.teamThreads;
+            s.rowsPerCta = 1;
+        }
+        layout();
+    }
+    // a scale group of aligned rows is found in neighbouring lanes: teams with fewer lanes
+    // than a group has vectors take the general path
+    if (c.groups && s.teamThreads * E < kQuantGroup) s.general = 1;
     return s;
 }
 
 int norm_backward_parts(size_t rows, const NormShape& sh, int smCount) {
-    const int resident = sh.vecs == 1 ? 1024 : 512;    // threads of an SM, by their registers
-    const int perSm = std::max(1, resident / sh.threads);
+    if (sh.staged) return sh.ctas;
+    // direct loads, at up to 102 registers a thread
+    const int perSm = std::max(1, kNormMaxThreads / sh.threads);
     const size_t most = std::max<size_t>(1, (size_t)smCount * perSm / sh.cluster);
     return (int)std::min(most, (rows + sh.rowsPerCta - 1) / sh.rowsPerCta);
 }
@@ -112,21 +178,30 @@ vResult_t check_desc(const vRmsNormDesc_t* desc, Checked* k) {
 struct Buffers {
     int nOut = 0;
     bool aligned = true;
+    bool congruent = true;           // every input's rows start at the same offset from a vector's
+                                     // boundary as the first output's
+    bool outCongruent = true;        // and every other output's
+    uintptr_t offset = 0;            // the first output's offset, in elements
 };
 vResult_t check_buffers(const Checked& k, int nRanks, const void* const* send, void* const* recv, int osz,
                         const void** sendOut, void** out, int* index, Buffers* b) {
     const vRmsNormDesc_t& d = k.d;
     if (!send || !recv) return vInvalidArgument;
     const size_t e = 16 / (size_t)k.esz;
+    for (int r = nRanks - 1; r >= 0; r--)
+        if (recv[r]) b->offset = ((uintptr_t)recv[r] / osz) % e;
+    if (d.rows > 1) b->congruent = d.sendStride % e == d.recvStride % e && d.residualStride % e == d.recvStride % e;
     b->aligned = d.hidden % e == 0 &&
                  (d.rows == 1 || (d.sendStride % e == 0 && d.residualStride % e == 0 && d.recvStride % e == 0));
     for (int r = 0; r < nRanks; r++) {
         if (!send[r] || !at(send[r], k.esz)) return vInvalidArgument;
         sendOut[r] = send[r];
         b->aligned = b->aligned && at(send[r], 16);
+        b->congruent = b->congruent && ((uintptr_t)send[r] / k.esz) % e == b->offset;
         if (!recv[r]) continue;
         if (!at(recv[r], osz)) return vInvalidArgument;
         b->aligned = b->aligned && at(recv[r], e * osz);
+        b->outCongruent = b->outCongruent && ((uintptr_t)recv[r] / osz) % e == b->offset;
         if (index) index[b->nOut] = r;
         out[b->nOut++] = recv[r];
     }
@@ -142,7 +217,21 @@ vResult_t check_row_buffer(const Checked& k, const void* p, Buffers* b) {
     if (!p) return vSuccess;
     if (!at(p, k.esz)) return vInvalidArgument;
     b->aligned = b->aligned && at(p, 16);
+    b->congruent = b->congruent && ((uintptr_t)p / k.esz) % (16 / (size_t)k.esz) == b->offset;
     return vSuccess;
+}
+
+vc::NormCall norm_call(const Checked& k, const CommView& v, const Buffers& b) {
+    vc::NormCall c = {};
+    c.rows = k.d.rows;
+    c.hidden = (int)k.d.hidden;
+    c.elemSize = k.esz;
+    c.weightSize = (int)vc::dtype_size(k.d.weightType);
+    c.smCount = v.smCount;
+    c.general = !b.aligned;
+    c.realign = !b.congruent;
+    c.outRealign = !b.outCongruent;
+    return c;
 }
 
 vResult_t norm_forward(const vRmsNormDesc_t* desc, const void* const* send, const void* residual, const void* weight,
@@ -193,7 +282,15 @@ vResult_t norm_forward(const vRmsNormDesc_t* desc, const void* const* send, cons
     a.weightF32 = k.d.weightType == vFloat32;
     a.groups = k.d.quantGroup ? (int)((k.d.hidden + vc::kQuantGroup - 1) / vc::kQuantGroup) : 0;
     a.eps = k.d.eps;
-    a.shape = vc::norm_shape(a.rows, a.hidden, k.esz, v.smCount, !b.aligned);
+    vc::NormCall call = norm_call(k, v, b);
+    call.segments = v.nRanks + (residual ? 1 : 0);
+    call.groups = quant && a.groups > 0;
+    call.rowBuffers = 2;
+    const size_t e = 16 / (size_t)k.esz;
+    if (residualOut && (((uintptr_t)residualOut / k.esz) % e != b.offset ||
+                        (a.rows > 1 && a.residualStride % e != a.recvStride % e)))
+        call.outRealign = true;
+    a.shape = vc::norm_shape(call);
     return comm_launch(c, quant ? "allreduce rmsnorm quant" : "allreduce rmsnorm", [&]() {
         return quant ? vc::launch_allreduce_rmsnorm_quant(a, k.d.datatype, stream)
                      : vc::launch_allreduce_rmsnorm(a, k.d.datatype, stream);
@@ -246,7 +343,11 @@ vResult_t norm_backward(const vRmsNormDesc_t* desc, const void* const* send, con
     a.nRanks = v.nRanks;
     a.nOut = b.nOut;
     a.weightF32 = k.d.weightType == vFloat32;
-    a.shape = vc::norm_shape(a.rows, a.width, k.esz, v.smCount, !b.aligned);
+    vc::NormCall call = norm_call(k, v, b);
+    call.segments = v.nRanks + 1 + (gradResidual ? 1 : 0);
+    call.extraPerElem = sizeof(float);
+    call.rowBuffers = 1;
+    a.shape = vc::norm_shape(call);
     a.parts = vc::norm_backward_parts(a.rows, a.shape, v.smCount);
     if (!workspace || !at(workspace, 16) || workspaceBytes < (size_t)a.parts * k.d.hidden * sizeof(float))
         return vInvalidArgument;
@@ -255,161 +356,124 @@ vResult_t norm_backward(const vRmsNormDesc_t* desc, const void* const* send, con
 
 // ---- gradient norm and clipping ----------------------------------------------------------
 
-// Partial sums of one launch.
-constexpr int kSquaresCtasPerSm = 4;
+constexpr unsigned long long kListMagic = 0x766C697374763031ull;   // "vlistv01"
 
-vResult_t check_list(const vTensorList_t* l, int nRanks) {
-    if (!l || l->nTensors < 0) return vInvalidArgument;
-    if (l->nTensors == 0) return vSuccess;
-    if (!l->counts || !l->datatypes || !l->grads || (size_t)l->nTensors > (size_t)0x7FFFFFFF / nRanks)
-        return vInvalidArgument;
-    const size_t most = (size_t)1 << 43;     // of all pieces together: their chunks fit one grid
+size_t grad_partials(unsigned int chunks, int smCount) {
+    return std::max<size_t>(1, std::min<size_t>(chunks, (size_t)smCount * vc::kSquaresCtasPerSm));
+}
+
+// Cut one rank's tensor into chunks.
+void add_chunks(std::vector<vc::GradChunk>* v, const void* in, void* out, size_t count, vDataType_t dt) {
+    const size_t esz = vc::dtype_size(dt), e = 16 / esz;
+    // a chunk that starts off a 16-byte boundary touches one vector more than it fills
+    const bool aligned = at(in, 16) && at(out, 16);
+    const size_t most = (size_t)(aligned ? vc::kGradChunkVecs : vc::kGradChunkVecs - 1) * e;
+    for (size_t i = 0; i < count; i += most) {
+        vc::GradChunk c = {};
+        c.in = (const char*)in + i * esz;
+        c.out = (char*)out + i * esz;
+        c.count = (int)std::min(most, count - i);
+        c.dt = (int)dt;
+        v->push_back(c);
+    }
+}
+
+}  // namespace
+
+struct vgradlist {
+    unsigned long long magic;
+    int nRanks;
+    int device;
+    vc::GradChunk* chunks;           // device: the counted ones, then the rest
+    unsigned int* done;              // device: k_grad_norm's counter
+    unsigned int nCounted, nChunks;
+};
+
+namespace {
+
+vResult_t list_create(vGradList_t* list, int nRanks, int nTensors, const size_t* counts, const vDataType_t* datatypes,
+                      const unsigned char* replicated, const void* const* grads, void* const* outs) {
+    if (!list) return vInvalidArgument;
+    *list = nullptr;
+    if (nRanks < 1 || nRanks > VCOMM_MAX_RANKS || nTensors < 0 || nTensors > 0x7FFFFFFF / nRanks) return vInvalidArgument;
+    if (nTensors > 0 && (!counts || !datatypes || !grads)) return vInvalidArgument;
+    const size_t most = (size_t)1 << 40;     // of all pieces together: their chunks fit one grid
     size_t total = 0;
-    for (int t = 0; t < l->nTensors; t++) {
-        if (!is_float(l->datatypes[t]) || l->counts[t] > (most - total) / nRanks) return vInvalidArgument;
-        total += l->counts[t] * nRanks;
-        if (l->counts[t] == 0) continue;
-        const size_t esz = vc::dtype_size(l->datatypes[t]);
+    for (int t = 0; t < nTensors; t++) {
+        if (!is_float(datatypes[t]) || counts[t] > (most - total) / nRanks) return vInvalidArgument;
+        total += counts[t] * nRanks;
+        if (counts[t] == 0) continue;
+        const size_t esz = vc::dtype_size(datatypes[t]);
         for (int r = 0; r < nRanks; r++) {
-            const size_t i = (size_t)r * l->nTensors + t;
-            if (!l->grads[i] || !at(l->grads[i], esz)) return vInvalidArgument;
-            if (l->outs && (!l->outs[i] || !at(l->outs[i], esz))) return vInvalidArgument;
+            const size_t i = (size_t)r * nTensors + t;
+            if (!grads[i] || !at(grads[i], esz) || (outs && (!outs[i] || !at(outs[i], esz)))) return vInvalidArgument;
         }
     }
+    std::vector<vc::GradChunk> counted, rest;
+    for (int r = 0; r < nRanks; r++)
+        for (int t = 0; t < nTensors; t++) {
+            const size_t i = (size_t)r * nTensors + t;
+            if (counts[t] == 0) continue;
+            add_chunks(r > 0 && replicated && replicated[t] ? &rest : &counted, grads[i],
+                       outs ? outs[i] : const_cast<void*>(grads[i]), counts[t], datatypes[t]);
+        }
+    std::unique_ptr<vgradlist> l(new vgradlist());
+    l->nRanks = nRanks;
+    l->nCounted = (unsigned)counted.size();
+    counted.insert(counted.end(), rest.begin(), rest.end());
+    l->nChunks = (unsigned)counted.size();
+    cudaError_t e = cudaGetDevice(&l->device);
+    void* mem = nullptr;
+    const size_t bytes = counted.size() * sizeof(vc::GradChunk);
+    if (e == cudaSuccess) e = cudaMalloc(&mem, bytes + 32);
+    if (e == cudaSuccess && bytes) e = cudaMemcpy(mem, counted.data(), bytes, cudaMemcpyHostToDevice);
+    if (e == cudaSuccess) e = cudaMemset((char*)mem + bytes, 0, 32);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        if (mem) cudaFree(mem);
+        return vUnhandledCudaError;
+    }
+    l->chunks = (vc::GradChunk*)mem;
+    l->done = (unsigned int*)((char*)mem + bytes);
+    l->magic = kListMagic;
+    *list = l.release();
     return vSuccess;
 }
 
-// Call f(item) for every piece that the norm counts (`all` false) or that is scaled.
-template <typename F>
-void each_item(const vTensorList_t* l, int nRanks, bool all, F f) {
-    for (int r = 0; r < nRanks; r++)
-        for (int t = 0; t < l->nTensors; t++) {
-            if (l->counts[t] == 0 || (!all && r > 0 && l->replicated && l->replicated[t])) continue;
-            const size_t i = (size_t)r * l->nTensors + t;
-            vc::GradItem it;
-            it.in = l->grads[i];
-            it.out = l->outs ? l->outs[i] : const_cast<void*>(l->grads[i]);
-            it.count = l->counts[t];
-            it.chunk0 = 0;
-            it.dt = (unsigned)l->datatypes[t];
-            f(it);
-        }
+vResult_t check_list(vGradList_t l, const CommView& v) {
+    if (!l || l->magic != kListMagic || l->nRanks != v.nRanks || l->device != v.device) return vInvalidArgument;
+    return vSuccess;
 }
 
-size_t count_items(const vTensorList_t* l, int nRanks, bool all) {
-    size_t whole = 0, split = 0;
-    for (int t = 0; t < l->nTensors; t++) {
-        if (l->counts[t] == 0) continue;
-        if (!all && l->replicated && l->replicated[t]) whole++;
-        else split++;
-    }
-    return whole + split * (size_t)nRanks;
-}
-
-// Batches of the items in launches of at most CAP.
-template <int CAP, typename F>
-vResult_t batches(const vTensorList_t* l, int nRanks, bool all, F launch) {
-    std::unique_ptr<vc::GradArgs<CAP>> a(new vc::GradArgs<CAP>);
-    a->nItems = 0;
-    unsigned long long chunks = 0;
-    vResult_t res = vSuccess;
-    const auto flush = [&]() {
-        if (a->nItems == 0 || res != vSuccess) return;
-        a->nChunks = (unsigned)chunks;
-        res = launch(*a);
-        a->nItems = 0;
-        chunks = 0;
-    };
-    each_item(l, nRanks, all, [&](vc::GradItem it) {
-        const unsigned long long n = vc::grad_chunks(it.count, vc::dtype_size((int)it.dt));
-        if (a->nItems == CAP) flush();
-        it.chunk0 = (unsigned)chunks;
-        a->items[a->nItems++] = it;
-        chunks += n;
-    });
-    flush();
-    return res;
-}
-
-size_t squares_slots(const vTensorList_t* l, const CommView& v) {
-    const size_t n = count_items(l, v.nRanks, false);
-    return (n + vc::kGradItemsLarge - 1) / vc::kGradItemsLarge * (size_t)v.smCount * kSquaresCtasPerSm;
-}
-
-template <int CAP>
-vResult_t enqueue_norm(const vTensorList_t* l, const CommView& v, double* partials, float* norm, vcomm_t c,
-                       cudaStream_t stream) {
-    int used = 0;
-    const vResult_t r = batches<CAP>(l, v.nRanks, false, [&](vc::GradArgs<CAP>& a) {
-        const int grid = (int)std::min<unsigned>(a.nChunks, (unsigned)(v.smCount * kSquaresCtasPerSm));
-        a.partials = partials + used;
-        used += grid;
-        return comm_launch(c, "gradient squares", [&]() { return vc::launch_grad_squares<CAP>(a, grid, stream); });
-    });
-    if (r != vSuccess) return r;
-    return comm_launch(c, "gradient norm", [&]() { return vc::launch_grad_norm(partials, used, norm, stream); });
-}
-template <int CAP>
-vResult_t enqueue_clip(const vTensorList_t* l, const CommView& v, float maxNorm, const float* norm, vcomm_t c,
-                       cudaStream_t stream) {
-    return batches<CAP>(l, v.nRanks, true, [&](vc::GradArgs<CAP>& a) {
-        a.norm = norm;
-        a.maxNorm = maxNorm;
-        return comm_launch(c, "gradient clip", [&]() { return vc::launch_grad_clip<CAP>(a, stream); });
-    });
-}
-
-struct ListCopy {
-    std::vector<size_t> counts;
-    std::vector<vDataType_t> types;
-    std::vector<unsigned char> replicated;
-    std::vector<const void*> grads;
-    std::vector<void*> outs;
-    vTensorList_t list() const {
-        vTensorList_t l;
-        l.nTensors = (int)counts.size();
-        l.counts = counts.data();
-        l.datatypes = types.data();
-        l.replicated = replicated.empty() ? nullptr : replicated.data();
-        l.grads = grads.data();
-        l.outs = outs.empty() ? nullptr : outs.data();
-        return l;
-    }
-};
-
-vResult_t grad_norm(const vTensorList_t* l, bool clip, float maxNorm, float* norm, void* workspace,
-                    size_t workspaceBytes, vcomm_t c, cudaStream_t stream) {
+vResult_t grad_norm(vGradList_t l, bool clip, float maxNorm, float* norm, void* workspace, size_t workspaceBytes,
+                    vcomm_t c, cudaStream_t stream) {
     CommView v;
     vResult_t r = comm_view(c, &v);
     if (r != vSuccess) return r;
-    if ((r = check_list(l, v.nRanks)) != vSuccess) return r;
+    if ((r = check_list(l, v)) != vSuccess) return r;
     if (!norm || !at(norm, 4)) return vInvalidArgument;
     if (clip && !(maxNorm >= 0.0f)) return vInvalidArgument;
-    if (!workspace || !at(workspace, 16) || workspaceBytes < squares_slots(l, v) * sizeof(double))
-        return vInvalidArgument;
-    if (v.grouping) {
-        auto k = std::make_shared<ListCopy>();
-        const size_t n = (size_t)l->nTensors, all = n * v.nRanks;
-        k->counts.assign(l->counts, l->counts + n);
-        k->types.assign(l->datatypes, l->datatypes + n);
-        if (l->replicated) k->replicated.assign(l->replicated, l->replicated + n);
-        k->grads.assign(l->grads, l->grads + all);
-        if (l->outs) k->outs.assign(l->outs, l->outs + all);
+    const size_t parts = grad_partials(l->nCounted, v.smCount);
+    if (!workspace || !at(workspace, 16) || workspaceBytes < parts * sizeof(double)) return vInvalidArgument;
+    if (v.grouping)
         return vc::comm_record(c, [=]() {
-            return guarded([&]() {
-                const vTensorList_t copy = k->list();
-                return grad_norm(&copy, clip, maxNorm, norm, workspace, workspaceBytes, c, stream);
-            });
+            return guarded([&]() { return grad_norm(l, clip, maxNorm, norm, workspace, workspaceBytes, c, stream); });
         });
-    }
-    double* partials = (double*)workspace;
-    r = count_items(l, v.nRanks, false) <= (size_t)vc::kGradItemsSmall
-            ? enqueue_norm<vc::kGradItemsSmall>(l, v, partials, norm, c, stream)
-            : enqueue_norm<vc::kGradItemsLarge>(l, v, partials, norm, c, stream);
-    if (r != vSuccess || !clip) return r;
-    return count_items(l, v.nRanks, true) <= (size_t)vc::kGradItemsSmall
-               ? enqueue_clip<vc::kGradItemsSmall>(l, v, maxNorm, norm, c, stream)
-               : enqueue_clip<vc::kGradItemsLarge>(l, v, maxNorm, norm, c, stream);
+    vc::GradNormArgs a;
+    a.chunks = l->chunks;
+    a.nChunks = l->nCounted;
+    a.done = l->done;
+    a.partials = (double*)workspace;
+    a.norm = norm;
+    r = comm_launch(c, "gradient norm", [&]() { return vc::launch_grad_norm(a, (int)parts, stream); });
+    if (r != vSuccess || !clip || l->nChunks == 0) return r;
+    vc::GradClipArgs k;
+    k.chunks = l->chunks;
+    k.nChunks = l->nChunks;
+    k.norm = norm;
+    k.maxNorm = maxNorm;
+    return comm_launch(c, "gradient clip", [&]() { return vc::launch_grad_clip(k, stream); });
 }
 
 }  // namespace
@@ -443,11 +507,19 @@ vResult_t vRmsNormBackwardWorkspace(const vRmsNormDesc_t* desc, vcomm_t comm, si
     if (!bytes) return vInvalidArgument;
     *bytes = 16;
     if (k.d.rows == 0 || k.d.hidden == 0) return vSuccess;
-    // whatever the buffers' alignment turns out to be
-    for (const bool general : {false, true}) {
-        if (!general && k.d.hidden % (16 / k.esz) != 0) continue;
-        const vc::NormShape s = vc::norm_shape(k.d.rows, (int)k.d.hidden, k.esz, v.smCount, general);
-        *bytes = std::max(*bytes, (size_t)vc::norm_backward_parts(k.d.rows, s, v.smCount) * k.d.hidden * sizeof(float));
+    // whatever the buffers' alignment turns out to be, with or without a residual's gradient
+    for (int i = 0; i < 16; i++) {
+        Buffers b;
+        b.aligned = (i & 1) != 0;
+        b.congruent = (i & 2) != 0;
+        b.outCongruent = (i & 4) != 0;
+        if (b.aligned && (!b.congruent || !b.outCongruent || k.d.hidden % (16 / k.esz) != 0)) continue;
+        vc::NormCall call = norm_call(k, v, b);
+        call.segments = v.nRanks + 1 + (i >> 3);
+        call.extraPerElem = sizeof(float);
+        call.rowBuffers = 1;
+        const int parts = vc::norm_backward_parts(k.d.rows, vc::norm_shape(call), v.smCount);
+        *bytes = std::max(*bytes, (size_t)parts * k.d.hidden * sizeof(float));
     }
     return vSuccess;
 }
@@ -463,23 +535,42 @@ vResult_t vAllReduceRmsNormBackward(const vRmsNormDesc_t* desc, const void* cons
     });
 }
 
-vResult_t vGradNormWorkspace(const vTensorList_t* list, vcomm_t comm, size_t* bytes) {
+vResult_t vGradListCreate(vGradList_t* list, int nRanks, int nTensors, const size_t* counts,
+                          const vDataType_t* datatypes, const unsigned char* replicated, const void* const* grads,
+                          void* const* outs) {
+    return guarded([&]() { return list_create(list, nRanks, nTensors, counts, datatypes, replicated, grads, outs); });
+}
+
+vResult_t vGradListDestroy(vGradList_t l) {
+    if (!l || l->magic != kListMagic) return vInvalidArgument;
+    int prev = -1;
+    const bool other = cudaGetDevice(&prev) == cudaSuccess && prev != l->device;
+    if (other) cudaSetDevice(l->device);
+    const cudaError_t e = cudaFree(l->chunks);         // waits for the work that uses it
+    if (other) cudaSetDevice(prev);
+    l->magic = 0;
+    delete l;
+    if (e != cudaSuccess) cudaGetLastError();
+    return e == cudaSuccess ? vSuccess : vUnhandledCudaError;
+}
+
+vResult_t vGradNormWorkspace(vGradList_t list, vcomm_t comm, size_t* bytes) {
     CommView v;
     vResult_t r = comm_view(comm, &v);
     if (r != vSuccess) return r;
-    if ((r = check_list(list, v.nRanks)) != vSuccess) return r;
+    if ((r = check_list(list, v)) != vSuccess) return r;
     if (!bytes) return vInvalidArgument;
-    *bytes = std::max<size_t>(16, squares_slots(list, v) * sizeof(double));
+    *bytes = std::max<size_t>(16, grad_partials(list->nCounted, v.smCount) * sizeof(double));
     return vSuccess;
 }
 
-vResult_t vGradNorm(const vTensorList_t* list, float* norm, void* workspace, size_t workspaceBytes, vcomm_t comm,
+vResult_t vGradNorm(vGradList_t list, float* norm, void* workspace, size_t workspaceBytes, vcomm_t comm,
                     cudaStream_t stream) {
     Range range("vGradNorm");
     return guarded([&]() { return grad_norm(list, false, 0.0f, norm, workspace, workspaceBytes, comm, stream); });
 }
 
-vResult_t vClipGradNorm(const vTensorList_t* list, float maxNorm, float* norm, void* workspace, size_t workspaceBytes,
+vResult_t vClipGradNorm(vGradList_t list, float maxNorm, float* norm, void* workspace, size_t workspaceBytes,
                         vcomm_t comm, cudaStream_t stream) {
     Range range("vClipGradNorm");
     return guarded([&]() { return grad_norm(list, true, maxNorm, norm, workspace, workspaceBytes, comm, stream); });

@@ -39,7 +39,15 @@ struct NormShape {
     int cluster;                     // CTAs that share a row
     int threads;                     // threads per CTA
     int general;                     // some buffer or row may start off a 16-byte boundary
+    int staged;                      // many rows: ctas CTAs stride over them and stage the next one
+    int ctas;
+    int weightBytes;                 // dynamic shared memory: of the staged weight,
+    int stageBytes;                  // of the staged row of every team,
+    int rowBytes;                    // of a row buffer (0: the outputs need none),
+    int extraBytes;                  // of the caller's, in front,
+    int smemBytes;                   // and altogether
 };
+constexpr int kStageMaxThreads = 512;
 // Elements that one 128-element scale group covers.
 constexpr int kQuantGroup = 128;
 constexpr int kNormMaxThreads = 640;     // of a CTA that holds 4 vectors a thread
@@ -47,7 +55,20 @@ constexpr int kNormWarpCta = 128;        // threads of a CTA whose teams are par
 constexpr int kNormMaxCluster = 8;
 constexpr int kNormGroupSlots = 168;     // scale groups of one CTA: at most 640 * 4 * 8 / 128 + 1,
                                          // or 128 / team * (team * 4 * 8 / 128 + 1) of small teams
-NormShape norm_shape(size_t rows, int hidden, int elemSize, int smCount, bool general);
+// What a launch has to be shaped for.
+struct NormCall {
+    size_t rows;
+    int hidden, elemSize, weightSize;
+    int segments;                    // inputs that every row is read from
+    int smCount;
+    bool general;                    // as in NormShape
+    bool realign;                    // inputs may start at other offsets from 16 bytes than the first output
+    bool outRealign;                 // other outputs may
+    bool groups;                     // 8-bit output with a scale per 128 elements
+    int rowBuffers;                  // row buffers that a team needs for such outputs
+    int extraPerElem;                // shared memory per element of a row for the caller
+};
+NormShape norm_shape(const NormCall& c);
 
 struct NormArgs {
     const void* send[VCOMM_MAX_RANKS];
@@ -94,41 +115,33 @@ cudaError_t launch_rmsnorm_backward(const NormBackwardArgs& a, vDataType_t dt, c
 
 // ---- gradient norm and clipping ----------------------------------------------------------
 
-// One tensor of one rank.  The table travels in the kernels' parameter block.
-struct GradItem {
-    const void* in;
-    void* out;
-    unsigned long long count;
-    unsigned int chunk0;             // first chunk of this tensor in the launch
-    unsigned int dt;                 // vDataType_t
+// A piece of one tensor of one rank, at most kGradChunkVecs vectors wherever it starts.
+struct alignas(32) GradChunk {
+    const char* in;
+    char* out;
+    int count;                       // elements
+    int dt;                          // vDataType_t
+    int pad[2];
 };
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 8;         // vectors of a chunk that each thread holds
 constexpr int kGradChunkVecs = kGradThreads * kGradVecs;   // 32 KiB
-template <int CAP>
-struct GradArgs {
-    int nItems;
-    unsigned int nChunks;
-    double* partials;                // this launch's sums of squares
-    const float* norm;               // clipping: the norm
-    float maxNorm;
-    int pad;
-    GradItem items[CAP];
-};
-// Tables of two sizes: launching with a 4 KiB parameter block costs less host time.
-constexpr int kGradItemsSmall = 120;
-constexpr int kGradItemsLarge = 1000;
-static_assert(sizeof(GradArgs<kGradItemsLarge>) <= 32764, "kernel parameters are limited to 32,764 bytes");
-// Chunks that cover `count` elements wherever they start.
-inline unsigned long long grad_chunks(unsigned long long count, size_t elemSize) {
-    const unsigned long long e = 16 / elemSize;
-    return (count + 2 * e - 2) / e / kGradChunkVecs + 1;
-}
+constexpr int kSquaresCtasPerSm = 4;
 
-template <int CAP>
-cudaError_t launch_grad_squares(const GradArgs<CAP>& a, int grid, cudaStream_t s);
-cudaError_t launch_grad_norm(const double* partials, int n, float* norm, cudaStream_t s);
-template <int CAP>
-cudaError_t launch_grad_clip(const GradArgs<CAP>& a, cudaStream_t s);
+struct GradNormArgs {
+    const GradChunk* chunks;         // those that count towards the norm
+    unsigned int nChunks;
+    unsigned int* done;              // CTAs that have written their sum: zero between calls
+    double* partials;                // one sum of squares per CTA
+    float* norm;
+};
+struct GradClipArgs {
+    const GradChunk* chunks;
+    unsigned int nChunks;
+    const float* norm;
+    float maxNorm;
+};
+cudaError_t launch_grad_norm(const GradNormArgs& a, int grid, cudaStream_t s);
+cudaError_t launch_grad_clip(const GradClipArgs& a, cudaStream_t s);
 
 }  // namespace vc

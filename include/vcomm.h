@@ -307,7 +307,7 @@ vResult_t vScatter(const void* const* sendbuffs, void* const* recvbuffs, size_t 
 /* follows the gradients' reduction.  They take the communicator, the stream and the */
 /* per-rank pointer arrays as the collectives do, return the same errors, may be     */
 /* grouped and captured, and hold every sum, statistic and norm in fp32 or more.     */
-/* They allocate no device memory: where one needs scratch, the caller passes it.    */
+/* Where one needs scratch memory, the caller passes it.                             */
 /* ------------------------------------------------------------------------------- */
 
 /* Longest row of the norms, in elements. */
@@ -378,33 +378,43 @@ vResult_t vAllReduceRmsNormBackward(const vRmsNormDesc_t* desc, const void* cons
                                     const void* gradResidual, void* const* recvbuffs, void* gradWeight,
                                     void* workspace, size_t workspaceBytes, vcomm_t comm, cudaStream_t stream);
 
-/* Gradients of nTensors tensors on every rank.  A tensor is either split (each rank holds a
- * piece of counts[t] elements: reduce-scattered or tensor-parallel) or replicated (each rank
- * holds all of it: all-reduced).  Any number of tensors, of any sizes and types, up to 2^43
- * elements in all.  The arrays are host memory and may be freed when the call returns. */
-typedef struct {
-    int nTensors;
-    const size_t* counts;               /* [nTensors] elements on each rank; 0: skipped */
-    const vDataType_t* datatypes;       /* [nTensors] vFloat32, vFloat16 or vBFloat16 */
-    const unsigned char* replicated;    /* [nTensors], or NULL: all split */
-    const void* const* grads;           /* [nRanks * nTensors], rank r's tensor t at r * nTensors + t */
-    void* const* outs;                  /* the clipped gradients, in the same order and types;
-                                           NULL: in place */
-} vTensorList_t;
+/* The gradients that a norm is taken over: nTensors tensors on each of nRanks ranks.  A tensor
+ * is either split (each rank holds a piece of counts[t] elements: reduce-scattered or
+ * tensor-parallel) or replicated (each rank holds all of it: all-reduced).  Any number of
+ * tensors, of any sizes, up to 2^40 elements in all.
+ *   counts      [nTensors] elements on each rank; 0: skipped
+ *   datatypes   [nTensors] vFloat32, vFloat16 or vBFloat16
+ *   replicated  [nTensors], or NULL: all split
+ *   grads       [nRanks * nTensors], rank r's tensor t at r * nTensors + t
+ *   outs        the clipped gradients, in the same order and types; NULL: in place
+ * The arrays are host memory and may be freed when the call returns.  The list lives on the
+ * current device; it holds the tensors' addresses, so it serves every step for as long as they
+ * stay where they are, and the only device memory that these operators allocate: a table of 32
+ * bytes per 32 KiB of gradients.  Creating and destroying a list waits for the device, so
+ * neither goes into a graph's capture.  vGradListCreate leaves *list NULL on an error; a NULL
+ * or destroyed list gives vInvalidArgument. */
+typedef struct vgradlist* vGradList_t;
+vResult_t vGradListCreate(vGradList_t* list, int nRanks, int nTensors, const size_t* counts,
+                          const vDataType_t* datatypes, const unsigned char* replicated,
+                          const void* const* grads, void* const* outs);
+vResult_t vGradListDestroy(vGradList_t list);
 
 /* *norm (device memory, fp32) = the 2-norm of all ranks' gradients together, a replicated
  * tensor counted once, by rank 0's copy.  Squares are taken and added in fp32 over at most
- * 64 elements, their sums in fp64, in an order that the sizes fix.
+ * 64 elements, their sums in fp64, in an order that the sizes fix.  A square above fp32's
+ * range makes the norm infinite.
  * vClipGradNorm then scales every rank's gradients by min(1, maxNorm / (norm + 1e-6)),
  * rounded once to their type (no element is rewritten in place where that factor is 1).  A
  * norm that is not finite scales as the formula has it: infinity by 0, NaN by NaN.  maxNorm
  * must be >= 0.  No tensor may overlap another, nor an output another tensor's gradient.
- * The workspace is at least what vGradNormWorkspace gives for the list, 16-byte aligned,
- * used by nothing else until the call's work is done. */
-vResult_t vGradNormWorkspace(const vTensorList_t* list, vcomm_t comm, size_t* bytes);
-vResult_t vGradNorm(const vTensorList_t* list, float* norm, void* workspace, size_t workspaceBytes,
+ * The list has as many ranks as the communicator and lives on its device; calls on one list
+ * must not overlap on the GPU (they share its counter).  The workspace is at least what
+ * vGradNormWorkspace gives for the list, 16-byte aligned, used by nothing else until the
+ * call's work is done. */
+vResult_t vGradNormWorkspace(vGradList_t list, vcomm_t comm, size_t* bytes);
+vResult_t vGradNorm(vGradList_t list, float* norm, void* workspace, size_t workspaceBytes,
                     vcomm_t comm, cudaStream_t stream);
-vResult_t vClipGradNorm(const vTensorList_t* list, float maxNorm, float* norm, void* workspace,
+vResult_t vClipGradNorm(vGradList_t list, float maxNorm, float* norm, void* workspace,
                         size_t workspaceBytes, vcomm_t comm, cudaStream_t stream);
 
 /* Ring all-reduce for callers that cannot allocate device memory.  The pages have no

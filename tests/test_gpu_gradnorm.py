@@ -234,16 +234,15 @@ def test_refusals(comms):
 
     ptrs = [t.data_ptr() for r in g for t in r]
     counts, types = [64, 8], [V.vFloat32, V.vBFloat16]
-    for bad in (V.TensorList(n, counts, [V.vFloat32, V.vInt32], None, ptrs, None),
-                V.TensorList(n, counts, types, None, [None] + ptrs[1:], None),
-                V.TensorList(n, counts, types, None, [ptrs[0] + 2] + ptrs[1:], None),
-                V.TensorList(n, counts, types, None, ptrs, [None] + ptrs[1:]),
-                V.TensorList(n, counts, types, None, ptrs, ptrs[:3] + [ptrs[3] + 1]),
-                V.TensorList(n, [64, 1 << 43], types, None, ptrs, None),
-                V.TensorList(n, [64, (1 << 64) - 1], types, None, ptrs, None)):
-        refused(lambda: V.vGradNorm(bad, norm, ws, comm))
-        refused(lambda: V.vClipGradNorm(bad, 1.0, norm, ws, comm))
-        refused(lambda: V.vGradNormWorkspace(bad, comm))
+    for bad in ((n, counts, [V.vFloat32, V.vInt32], None, ptrs, None), (n, counts, types, None, [None] + ptrs[1:], None),
+                (n, counts, types, None, [ptrs[0] + 2] + ptrs[1:], None), (n, counts, types, None, ptrs, [None] + ptrs[1:]),
+                (n, counts, types, None, ptrs, ptrs[:3] + [ptrs[3] + 1]), (n, [64, 1 << 41], types, None, ptrs, None),
+                (n, [64, (1 << 64) - 1], types, None, ptrs, None), (0, counts, types, None, [], None)):
+        refused(lambda: V.TensorList(*bad))
+    gone = V.vTensorList(g)
+    gone.close()
+    refused(lambda: V.vGradNorm(gone, norm, ws, comm))
+    refused(lambda: V.vGradNormWorkspace(gone, comm))
     refused(lambda: V.vGradNorm(good, None, ws, comm))
     refused(lambda: V.vGradNorm(good, norm.data_ptr() + 2, ws, comm))
     refused(lambda: V.vGradNorm(good, norm, (None, need), comm))

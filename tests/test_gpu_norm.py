@@ -23,6 +23,9 @@ SIZES = [(1, 1, 1), (2, 5, 1), (1, 3, 7), (3, 17, 8), (1, 200, 31), (2, 33, 64),
          (1, 9, 129), (2, 40, 255), (1, 65, 512), (5, 11, 1000), (1, 3, 1023), (2, 301, 1024), (1, 2, 1025),
          (8, 1, 4096), (3, 160, 4096), (2, 170, 4097), (1, 1, 5120), (64, 2, 640), (2, 155, 8200), (1, 160, 16384),
          (2, 3, 20480), (1, 160, 20481), (1, 2, 40961), (1, 2, 65535), (2, 3, 65536)]
+# enough rows for CTAs to stride over: parts of a warp, whole warps, long rows
+MANY = [(1, 45000, 64), (2, 9001, 200), (1, 5003, 520), (3, 3001, 1000), (8, 1301, 1024), (1, 2601, 1031), (2, 1400, 4097),
+        (1, 700, 16384)]
 TYPES = [(BF16, BF16), (BF16, F32), (F16, F16), (F32, F32)]
 
 
@@ -108,7 +111,7 @@ def run_forward(comm, n, rows, hidden, dtype, wtype, seed, residual=True, send_p
 
 
 @pytest.mark.parametrize("dtype,wtype", TYPES)
-@pytest.mark.parametrize("n,rows,hidden", SIZES)
+@pytest.mark.parametrize("n,rows,hidden", SIZES + MANY)
 def test_forward(comms, n, rows, hidden, dtype, wtype):
     run_forward(comms(n), n, rows, hidden, dtype, wtype, seed=hidden + n)
 
@@ -117,7 +120,8 @@ def test_forward(comms, n, rows, hidden, dtype, wtype):
 @pytest.mark.parametrize("kw", [dict(send_pad=3), dict(res_pad=5), dict(recv_pad=1), dict(offset=1), dict(recv_offset=3),
                                 dict(weight_offset=1), dict(send_pad=8, res_pad=16, recv_pad=24),
                                 dict(send_pad=1, res_pad=2, recv_pad=3, offset=5, recv_offset=2, weight_offset=7)])
-@pytest.mark.parametrize("n,rows,hidden", [(3, 21, 96), (2, 5, 1000), (1, 300, 1030), (2, 3, 4099), (1, 2, 33000)])
+@pytest.mark.parametrize("n,rows,hidden", [(3, 21, 96), (2, 5, 1000), (1, 300, 1030), (2, 3, 4099), (1, 2, 33000),
+                                           (2, 9000, 136), (1, 2700, 1030), (3, 900, 4099)])
 def test_forward_strides_and_offsets(comms, n, rows, hidden, dtype, wtype, kw):
     run_forward(comms(n), n, rows, hidden, dtype, wtype, seed=7, **kw)
 
@@ -134,9 +138,9 @@ def test_forward_optional_arguments(comms, hidden):
         R.assert_close(o, ref["y"], ref["dy"], BF16, "no stream, no rstd")
 
 
-@pytest.mark.parametrize("hidden", [256, 1001, 2048, 30000])
-def test_forward_in_place(comms, hidden):
-    n, rows = 3, 37
+@pytest.mark.parametrize("rows,hidden", [(37, 256), (37, 1001), (37, 2048), (37, 30000), (3000, 256), (3000, 1001)])
+def test_forward_in_place(comms, rows, hidden):
+    n = 3
     xs, res, w, sends = make(n, rows, hidden, BF16, F32, 11)
     stream = place(res)
     V.vAllReduceRmsNorm(V.vRmsNormDesc(rows, hidden, BF16, F32, EPS), sends, stream, place(w), stream, sends, None, comms(n))
@@ -146,9 +150,9 @@ def test_forward_in_place(comms, hidden):
         R.assert_close(s, ref["y"], ref["dy"], BF16, "in place")
 
 
-@pytest.mark.parametrize("hidden", [96, 1000, 1003, 24000])
-def test_rows_with_infinities_and_nans_stay_alone(comms, hidden):
-    n, rows = 2, 9
+@pytest.mark.parametrize("rows,hidden", [(9, 96), (9, 1000), (9, 1003), (9, 24000), (2700, 1000), (2700, 1003)])
+def test_rows_with_infinities_and_nans_stay_alone(comms, rows, hidden):
+    n = 2
     xs, res, w, _ = make(n, rows, hidden, BF16, BF16, 13)
     xs[1, 2, hidden // 2] = float("nan")
     xs[0, 5, hidden - 1] = float("inf")
@@ -222,7 +226,7 @@ def run_quant(comm, n, rows, hidden, dtype, wtype, group, seed, send_pad=0, recv
 
 @pytest.mark.parametrize("dtype,wtype", TYPES)
 @pytest.mark.parametrize("group", [0, 128])
-@pytest.mark.parametrize("n,rows,hidden", SIZES)
+@pytest.mark.parametrize("n,rows,hidden", SIZES + MANY)
 def test_quantised(comms, n, rows, hidden, dtype, wtype, group):
     run_quant(comms(n), n, rows, hidden, dtype, wtype, group, seed=hidden)
 
@@ -231,7 +235,8 @@ def test_quantised(comms, n, rows, hidden, dtype, wtype, group):
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("kw", [dict(send_pad=3), dict(recv_pad=5), dict(recv_offset=1), dict(offset=1),
                                 dict(recv_offset=3, recv_pad=2, send_pad=1, offset=2)])
-@pytest.mark.parametrize("n,rows,hidden", [(2, 21, 96), (1, 6, 300), (3, 4, 1029), (1, 2, 33000)])
+@pytest.mark.parametrize("n,rows,hidden", [(2, 21, 96), (1, 6, 300), (3, 4, 1029), (1, 2, 33000), (2, 9000, 136),
+                                           (3, 2000, 1029)])
 def test_quantised_strides_and_offsets(comms, n, rows, hidden, dtype, group, kw):
     run_quant(comms(n), n, rows, hidden, dtype, dtype, group, 5, **kw)
 
@@ -292,7 +297,7 @@ def run_backward(comm, n, rows, hidden, dtype, wtype, seed, residual=True, send_
 
 
 @pytest.mark.parametrize("dtype,wtype", TYPES)
-@pytest.mark.parametrize("n,rows,hidden", SIZES + [(1, 5000, 64), (2, 3001, 257), (1, 2000, 2048)])
+@pytest.mark.parametrize("n,rows,hidden", SIZES + MANY + [(1, 5000, 64), (2, 3001, 257), (1, 2000, 2048)])
 def test_backward(comms, n, rows, hidden, dtype, wtype):
     run_backward(comms(n), n, rows, hidden, dtype, wtype, seed=hidden + n)
 
@@ -301,7 +306,8 @@ def test_backward(comms, n, rows, hidden, dtype, wtype):
 @pytest.mark.parametrize("kw", [dict(send_pad=3), dict(res_pad=5), dict(recv_pad=1), dict(offset=1), dict(recv_offset=3),
                                 dict(weight_offset=1), dict(residual=False),
                                 dict(send_pad=1, res_pad=2, recv_pad=3, offset=5, recv_offset=2, weight_offset=7)])
-@pytest.mark.parametrize("n,rows,hidden", [(3, 21, 96), (2, 5, 1000), (1, 900, 1030), (2, 3, 4099), (1, 200, 21003)])
+@pytest.mark.parametrize("n,rows,hidden", [(3, 21, 96), (2, 5, 1000), (1, 900, 1030), (2, 3, 4099), (1, 200, 21003),
+                                           (2, 9000, 136), (3, 2000, 1030)])
 def test_backward_strides_and_offsets(comms, n, rows, hidden, dtype, wtype, kw):
     run_backward(comms(n), n, rows, hidden, dtype, wtype, seed=9, **kw)
 
@@ -326,7 +332,7 @@ def test_backward_optional_arguments_and_in_place(comms):
     R.assert_close(dw, ref["dw"], ref["ddw"], BF16, "weight gradient")
 
 
-@pytest.mark.parametrize("n,rows,hidden", [(1, 700, 64), (2, 333, 1001), (4, 1000, 2048)])
+@pytest.mark.parametrize("n,rows,hidden", [(1, 700, 64), (2, 333, 1001), (4, 1000, 2048), (2, 3000, 1001), (1, 45000, 72)])
 def test_backward_gives_the_same_bits_again(comms, n, rows, hidden):
     dys, dres, w, sends = make(n, rows, hidden, BF16, F32, 23)
     hid = place(torch.randn(rows, hidden).to(BF16))
