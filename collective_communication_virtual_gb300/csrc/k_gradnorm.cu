@@ -44,9 +44,8 @@ __device__ __forceinline__ float chunk_squares(const GradChunk& c) {
         float f[E];
         widen_vec<DT>(raw[i], f);
         if (e < 0 || e + E > c.count) {                // elements of other chunks
-            const Span sp = span_of<E>(e, c.count);
 #pragma unroll
-            for (int j = 0; j < E; j++) f[j] = sp.has(j) ? f[j] : 0.0f;
+            for (int j = 0; j < E; j++) f[j] = e + j >= 0 && e + j < c.count ? f[j] : 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < E; j += 2) {
@@ -57,45 +56,41 @@ __device__ __forceinline__ float chunk_squares(const GradChunk& c) {
     return (s[0].x + s[0].y) + (s[1].x + s[1].y);
 }
 
-// Scale a thread's part of a chunk.  SAME: gradient and output start at the same offset from a
-// 16-byte boundary, so one load gives each vector of the output, and a thread's loads are all
-// under way before its first store; else two loads and a shift give it, two vectors at a time
-// (all eight at once took 254 registers).
-template <int DT, bool SAME>
+template <int DT>
+__device__ __forceinline__ void scale_elem(const char* in, char* out, int e, float factor) {
+    constexpr int ESZ = DTypeOf<DT>::size;
+    st_elem<ESZ>(out, e, f32_to_elem<DT>(elem_to_f32<DT>(ld_elem<ESZ>(in, e)) * factor));
+}
+// Scale a thread's part of a chunk.  A thread's loads are all under way before its first store.
+// Gradients and outputs at different offsets from 16 bytes go element by element.
+template <int DT>
 __device__ __forceinline__ void chunk_scale(const GradChunk& c, float factor) {
     constexpr int E = kVecElems<DT>;
     constexpr int ESZ = DTypeOf<DT>::size;
-    constexpr int K = SAME ? kGradVecs : 2;
+    if ((((uintptr_t)c.in ^ (uintptr_t)c.out) & 15u) != 0) {
+#pragma unroll 8
+        for (int e = threadIdx.x; e < c.count; e += kGradThreads) scale_elem<DT>(c.in, c.out, e, factor);
+        return;
+    }
     const int shift = (int)((uintptr_t)c.out & 15u) / ESZ;
-#pragma unroll 1
-    for (int part = 0; part < kGradVecs; part += K) {
-        const int k = part * kGradThreads + (int)threadIdx.x;
-        const ptrdiff_t off = (ptrdiff_t)k * 16 - shift * ESZ;
-        const int e0 = k * E - shift;
-        uint4 raw[K];
+    const ptrdiff_t off = (ptrdiff_t)threadIdx.x * 16 - shift * ESZ;
+    const int e0 = (int)threadIdx.x * E - shift;
+    uint4 raw[kGradVecs];
 #pragma unroll
-        for (int i = 0; i < K; i++) {
-            const int e = e0 + i * kGradThreads * E;
-            const char* p = c.in + off + i * kGradThreads * 16;
-            if (e < c.count) raw[i] = SAME ? ld_once(p) : load_vec<ESZ, true>(p, span_of<E>(e, c.count));
-        }
+    for (int i = 0; i < kGradVecs; i++)
+        if (e0 + i * kGradThreads * E < c.count) raw[i] = ld_once(c.in + off + i * kGradThreads * 16);
 #pragma unroll
-        for (int i = 0; i < K; i++) {
-            const int e = e0 + i * kGradThreads * E;
-            if (e >= c.count) continue;
+    for (int i = 0; i < kGradVecs; i++) {
+        const int e = e0 + i * kGradThreads * E;
+        if (e >= 0 && e + E <= c.count) {
             float f[E];
             widen_vec<DT>(raw[i], f);
             scale_by(f, factor);
-            char* p = c.out + off + i * kGradThreads * 16;
-            if (e >= 0 && e + E <= c.count) st_stream(p, narrow_vec<DT>(f));
-            else store_vec<DT, true>(p, span_of<E>(e, c.count), f);
+            st_stream(c.out + off + i * kGradThreads * 16, narrow_vec<DT>(f));
+        } else {                                       // the vector that begins or ends the chunk
+            for (int j = max(e, 0); j < min(e + E, c.count); j++) scale_elem<DT>(c.in, c.out, j, factor);
         }
     }
-}
-template <int DT>
-__device__ __forceinline__ void chunk_scale(const GradChunk& c, float factor) {
-    if ((((uintptr_t)c.in ^ (uintptr_t)c.out) & 15u) == 0) chunk_scale<DT, true>(c, factor);
-    else chunk_scale<DT, false>(c, factor);
 }
 
 // Sum over the CTA in fp64, in an order that the CTA's size fixes; every thread gets it.

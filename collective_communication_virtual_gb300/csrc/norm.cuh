@@ -1,12 +1,11 @@
 // norm.cuh -- what the RMS norm kernels share: 16-byte vectors of a row wherever the row
 // starts, their fp32 values, and the reductions over the threads that share a row.
 //
-// A row is cut into vectors of E = 16 / elemSize elements.  Vector k covers the elements
-// [k E - shift, k E - shift + E), where shift is the row's offset (in elements) from a
-// 16-byte boundary in the first output, so that the stores of that output are whole
-// aligned vectors but for the first and the last.  Inputs with another offset are cut from
-// the two aligned vectors that hold the bytes.  No load leaves the aligned 16-byte blocks
-// that hold elements of the row.
+// A row is cut into vectors of E = 16 / elemSize elements from its first element on, so a
+// thread holds the same columns of every row.  GENERAL kernels serve rows that start off a
+// 16-byte boundary or end inside a vector: inputs are cut from the two aligned blocks that
+// hold a vector's bytes, outputs leave through a row buffer in shared memory as whole aligned
+// blocks.  No load leaves the aligned 16-byte blocks that hold elements of the row.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -55,45 +54,27 @@ __device__ __forceinline__ uint4 narrow_vec(const float (&f)[kVecElems<DT>]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Elements of a vector that lie inside its row: [lo, hi).
-struct Span {
-    int lo, hi;
-    __device__ __forceinline__ bool full(int e) const { return lo == 0 && hi == e; }
-    __device__ __forceinline__ bool any() const { return lo < hi; }
-    __device__ __forceinline__ bool has(int j) const { return j >= lo && j < hi; }
-};
-template <int E>
-__device__ __forceinline__ Span span_of(int e0, int width) {
-    Span s;
-    s.lo = e0 < 0 ? -e0 : 0;
-    s.hi = width - e0 < E ? width - e0 : E;
-    return s;
-}
-
-// A thread's vectors of one row.
+// A thread's vectors of a row: columns [e0 + v step, e0 + v step + E).
 template <int DT, int V>
 struct RowVecs {
     static constexpr int E = kVecElems<DT>;
-    static constexpr int ESZ = DTypeOf<DT>::size;
-    int e0, step;                    // first element of vector 0, elements between vectors
-    Span sp[V];
-    bool on[V];                      // the vector holds elements of a row that exists
-    __device__ __forceinline__ void set(int e0_, int step_, int width, bool live) {
-        e0 = e0_;
-        step = step_;
+    int e0, step;
+    int left[V];                     // elements of vector v inside the row: E for a whole one
+    bool last[V];                    // the row has no vector behind it
+    __device__ __forceinline__ RowVecs(int first, int stride, int width) : e0(first), step(stride) {
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            sp[v] = span_of<E>(e0 + v * step, width);
-            on[v] = live && sp[v].any();
+            left[v] = max(0, min(E, width - (e0 + v * step)));
+            last[v] = e0 + v * step + E >= width;
         }
     }
-    // Zero what lies outside the row (all of a vector that is not on).
+    // Zero what lies behind the row's end.
     __device__ __forceinline__ void mask(float (&f)[V][E]) const {
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            if (sp[v].full(E)) continue;
+            if (left[v] == E) continue;
 #pragma unroll
-            for (int j = 0; j < E; j++) f[v][j] = sp[v].has(j) ? f[v][j] : 0.0f;
+            for (int j = 0; j < E; j++) f[v][j] = j < left[v] ? f[v][j] : 0.0f;
         }
     }
 };
@@ -168,98 +149,52 @@ __device__ __forceinline__ uint4 ld_once(const void* p) {
 // while the previous one still writes what it reads.
 __device__ __forceinline__ uint4 ld_shared_by_rows(const void* p) { return *reinterpret_cast<const uint4*>(p); }
 
-// The 16 bytes at p (any element-aligned address).  GENERAL false: p is 16-byte aligned and
-// the whole vector lies in the row.  Elements outside the span come back undefined.
-template <int ESZ, bool GENERAL>
-__device__ __forceinline__ uint4 load_vec(const char* p, Span sp) {
-    if (!GENERAL) return ld_once(p);
+// The 16 bytes at p, of which the first `left` elements are wanted (at least one).  GENERAL
+// false: p is 16-byte aligned.  The other elements come back undefined.
+template <int ESZ, bool GENERAL, bool ONCE = true>
+__device__ __forceinline__ uint4 load_vec(const char* p, int left) {
+    const auto ld = [](const char* q) { return ONCE ? ld_once(q) : ld_shared_by_rows(q); };
+    if (!GENERAL) return ld(p);
     const unsigned sh = (unsigned)((uintptr_t)p & 15u);
-    const char* q = p - sh;
-    if (sh == 0) return ld_once(q);
-    const int inFirst = (int)(16u - sh) / ESZ;         // elements that the first block holds
-    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-    if (sp.lo < inFirst) a = *reinterpret_cast<const uint4*>(q);
-    if (sp.hi > inFirst) b = *reinterpret_cast<const uint4*>(q + 16);
+    if (sh == 0) return ld(p);
+    const uint4 a = ld(p - sh);
+    uint4 b = make_uint4(0u, 0u, 0u, 0u);
+    if (left > (int)(16u - sh) / ESZ) b = ld(p - sh + 16);
     return shift_bytes(a, b, sh);
 }
 
-// Store the span of a vector at p: whole and aligned in one access, else by element.
+// The weight's E values from element e on (`left` of them inside the row).
 template <int DT, bool GENERAL>
-__device__ __forceinline__ void store_vec(char* p, Span sp, const float (&f)[kVecElems<DT>]) {
+__device__ __forceinline__ void load_weight(const void* w, bool f32, int e, int left, float (&f)[kVecElems<DT>]) {
     constexpr int E = kVecElems<DT>;
-    const uint4 v = narrow_vec<DT>(f);
-    if (!GENERAL || (sp.full(E) && ((uintptr_t)p & 15u) == 0)) {
-        st_stream(p, v);
-        return;
-    }
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    constexpr int ESZ = DTypeOf<DT>::size;
+    if constexpr (DT != kF32) {
+        if (f32) {
 #pragma unroll
-    for (int j = 0; j < E; j++) {
-        if (!sp.has(j)) continue;
-        if (DT == kF32) *(uint32_t*)(p + 4 * j) = w[j & 3];
-        else *(uint16_t*)(p + 2 * j) = (uint16_t)(w[(j >> 1) & 3] >> (16 * (j & 1)));
+            for (int i = 0; i < E; i += 4) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (left > i) v = load_vec<4, GENERAL, false>((const char*)w + (size_t)(e + i) * 4, left - i);
+                f[i] = __uint_as_float(v.x);
+                f[i + 1] = __uint_as_float(v.y);
+                f[i + 2] = __uint_as_float(v.z);
+                f[i + 3] = __uint_as_float(v.w);
+            }
+            return;
+        }
     }
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (left > 0) v = load_vec<ESZ, GENERAL, false>((const char*)w + (size_t)e * ESZ, left);
+    widen_vec<DT>(v, f);
 }
-
-// The weight's E values for the elements [e0, e0 + E) of a row, in its own type.
-template <int DT>
-struct WeightVec {
-    static constexpr int E = kVecElems<DT>;
-    uint4 raw[E / 4];                // E fp32 values, or one vector of the data's type
-    template <bool GENERAL>
-    __device__ __forceinline__ void load(const void* w, bool f32, int e0, Span sp) {
-        if (DT == kF32 || !f32) {
-            raw[0] = load_weight<DTypeOf<DT>::size, GENERAL>((const char*)w + (ptrdiff_t)e0 * DTypeOf<DT>::size, sp);
-        } else {
-#pragma unroll
-            for (int i = 0; i < E / 4; i++) {
-                Span part;
-                part.lo = sp.lo - 4 * i < 0 ? 0 : sp.lo - 4 * i;
-                part.hi = sp.hi - 4 * i > 4 ? 4 : sp.hi - 4 * i;
-                raw[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (!GENERAL || part.any())
-                    raw[i] = load_weight<4, GENERAL>((const char*)w + ((ptrdiff_t)e0 + 4 * i) * 4, part);
-            }
-        }
-    }
-    __device__ __forceinline__ void get(bool f32, float (&f)[E]) const {
-        if (DT == kF32 || !f32) {
-            widen_vec<DT>(raw[0], f);
-        } else {
-#pragma unroll
-            for (int i = 0; i < E / 4; i++) {
-                f[4 * i] = __uint_as_float(raw[i].x);
-                f[4 * i + 1] = __uint_as_float(raw[i].y);
-                f[4 * i + 2] = __uint_as_float(raw[i].z);
-                f[4 * i + 3] = __uint_as_float(raw[i].w);
-            }
-        }
-    }
-
-private:
-    // Every row reads the weight, so it goes through L1, unlike the streamed buffers.
-    template <int ESZ, bool GENERAL>
-    static __device__ __forceinline__ uint4 load_weight(const char* p, Span sp) {
-        if (!GENERAL) return ld_shared_by_rows(p);
-        const unsigned sh = (unsigned)((uintptr_t)p & 15u);
-        const char* q = p - sh;
-        if (sh == 0) return ld_shared_by_rows(q);
-        const int inFirst = (int)(16u - sh) / ESZ;
-        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-        if (sp.lo < inFirst) a = ld_shared_by_rows(q);
-        if (sp.hi > inFirst) b = ld_shared_by_rows(q + 16);
-        return shift_bytes(a, b, sh);
-    }
-};
 
 // Sum over the ranks, in rank order and in fp32, of one row's vectors of a thread.  UN ranks'
 // loads are in flight before the first is added.
 template <int DT, int V, bool GENERAL>
-__device__ __forceinline__ void sum_ranks(const void* const* send, int N, ptrdiff_t off, const RowVecs<DT, V>& rv,
+__device__ __forceinline__ void sum_ranks(const void* const* send, int N, size_t off, bool live, const RowVecs<DT, V>& rv,
                                           float (&acc)[V][kVecElems<DT>]) {
     constexpr int E = kVecElems<DT>;
     constexpr int ESZ = DTypeOf<DT>::size;
-    constexpr int UN = GENERAL ? (V == 1 ? 4 : 2) : 8 / V;
+    constexpr int UN = GENERAL ? (V == 1 ? 4 : V == 2 ? 2 : 1) : 8 / V;
 #pragma unroll
     for (int v = 0; v < V; v++)
 #pragma unroll
@@ -271,8 +206,11 @@ __device__ __forceinline__ void sum_ranks(const void* const* send, int N, ptrdif
             if (r + i < N) {
                 const char* p = (const char*)send[r + i] + off;
 #pragma unroll
-                for (int v = 0; v < V; v++)
-                    if (rv.on[v]) raw[i][v] = load_vec<ESZ, GENERAL>(p + (ptrdiff_t)v * rv.step * ESZ, rv.sp[v]);
+                for (int v = 0; v < V; v++) {
+                    raw[i][v] = make_uint4(0u, 0u, 0u, 0u);
+                    if (live && rv.left[v] > 0)
+                        raw[i][v] = load_vec<ESZ, GENERAL>(p + (size_t)v * rv.step * ESZ, rv.left[v]);
+                }
             }
         }
 #pragma unroll
@@ -280,18 +218,16 @@ __device__ __forceinline__ void sum_ranks(const void* const* send, int N, ptrdif
             if (r + i < N) {
 #pragma unroll
                 for (int v = 0; v < V; v++) {
-                    if (rv.on[v]) {
-                        float f[E];
-                        widen_vec<DT>(raw[i][v], f);
-                        add_to(acc[v], f);
-                    }
+                    float f[E];
+                    widen_vec<DT>(raw[i][v], f);
+                    add_to(acc[v], f);
                 }
             }
         }
     }
 }
 
-// ---- outputs that start at another offset from 16 bytes than the row's vectors -------------
+// ---- outputs ---------------------------------------------------------------------------------
 
 __device__ __forceinline__ uint4 ld_smem(uint32_t p) {
     uint4 v;
@@ -302,33 +238,30 @@ __device__ __forceinline__ void st_smem(uint32_t p, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// `bytes` bytes at shared address `src` (any alignment) to dst, by a team of `threads`: whole
-// aligned 16-byte blocks, each cut from the two that hold it, and the ends in OSZ-byte elements.
-// Element stores alone would take 8 (16 for bytes) per vector; measured on 3 x 1537 x 2731 fp16
-// with every rank at its own offset, they made 41 us of a pass that takes FINAL_RAGGED.
+// `bytes` bytes at the 16-byte aligned shared address `src` to dst (any alignment), by a team of
+// `threads`: whole aligned blocks of dst, each cut from the two of src that hold it, and the
+// ends in OSZ-byte elements.
 template <int OSZ>
 __device__ __forceinline__ void copy_out(char* dst, uint32_t src, int bytes, int t, int threads) {
-    const int head = min((int)((16u - (unsigned)((uintptr_t)dst & 15u)) & 15u), bytes);
-    const int blocks = (bytes - head) >> 4;
-    const unsigned sh = (src + head) & 15u;
-    const uint32_t from = src + head - sh;
-    for (int i = t; i < blocks; i += threads) {
-        const uint4 a = ld_smem(from + 16 * i);
-        st_stream(dst + head + (size_t)i * 16, sh == 0 ? a : shift_bytes(a, ld_smem(from + 16 * i + 16), sh));
+    const unsigned sh = (16u - (unsigned)((uintptr_t)dst & 15u)) & 15u;    // bytes before the first block
+    const int blocks = (bytes - (int)sh) >> 4;
+    if (sh == 0) {
+        for (int i = t; i < blocks; i += threads) st_stream(dst + (size_t)i * 16, ld_smem(src + 16 * i));
+    } else {
+        for (int i = t; i < blocks; i += threads)
+            st_stream(dst + sh + (size_t)i * 16, shift_bytes(ld_smem(src + 16 * i), ld_smem(src + 16 * i + 16), sh));
     }
-    const int tail = head + blocks * 16;
+    const int head = min((int)sh, bytes), tail = head + max(blocks, 0) * 16;
     for (int k = t * OSZ; k < head + bytes - tail; k += threads * OSZ) {
         const int at = k < head ? k : tail + k - head;
+        uint32_t v;
         if (OSZ == 1) {
-            uint32_t v;
             asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(src + at) : "memory");
             *(uint8_t*)(dst + at) = (uint8_t)v;
         } else if (OSZ == 2) {
-            uint16_t v;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(src + at) : "memory");
-            *(uint16_t*)(dst + at) = v;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(src + at) : "memory");
+            *(uint16_t*)(dst + at) = (uint16_t)v;
         } else {
-            uint32_t v;
             asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(src + at) : "memory");
             *(uint32_t*)(dst + at) = v;
         }

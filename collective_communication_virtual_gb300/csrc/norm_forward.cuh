@@ -29,46 +29,33 @@ __device__ __forceinline__ uint2 pack_e4m3(const float (&f)[E]) {
     return make_uint2(h[0] | (h[1] << 16), h[E / 2 - 2] | (h[E / 2 - 1] << 16));
 }
 template <int E>
-__device__ __forceinline__ void store_e4m3(char* p, Span sp, bool whole, const float (&f)[E]) {
-    const uint2 q = pack_e4m3<E>(f);
-    if (whole && ((uintptr_t)p & (E - 1)) == 0) {
-        if (E == 8) *reinterpret_cast<uint2*>(p) = q;
-        else *reinterpret_cast<uint32_t*>(p) = q.x;
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < E; j++)
-        if (sp.has(j)) *reinterpret_cast<uint8_t*>(p + j) = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
-}
-template <int E>
 __device__ __forceinline__ void st_smem_e4m3(uint32_t p, const float (&f)[E]) {
     const uint2 q = pack_e4m3<E>(f);
     if (E == 8) asm volatile("st.shared.v2.u32 [%0], {%1,%2};" :: "r"(p), "r"(q.x), "r"(q.y) : "memory");
     else asm volatile("st.shared.u32 [%0], %1;" :: "r"(p), "r"(q.x) : "memory");
 }
 
+// A row's address, its team and the thread's place in it.
+struct RowPlace {
+    size_t row;
+    bool live;                       // the row exists
+    int t, part, col0;               // thread of the team, CTA of the cluster, its first column
+    uint32_t buf;                    // GENERAL: the team's row buffers in shared memory
+};
+
 // What a row's team does once a thread has its part of h: the stream, the reduction, the scaled
-// output.  weight(v, f) gives the weight's values for vector v.  groupMax: this row's maxima of
-// the CTA's scale groups, zero on entry (GENERAL; aligned rows keep theirs in registers).
-// rowBuf: the team's two row buffers in shared memory (its stream, then its output), 0 where
-// every output's rows start at the frame's offset from 16 bytes.
+// output.  weight(v, f) gives the weight's values for vector v, zeros behind the row's end.
 // Q: 0 output in the data's type, 1 8 bits with one scale a row, 2 with one per 128 elements.
 template <int DT, int V, bool GENERAL, int Q, typename Weight>
-__device__ __forceinline__ void finish_row(const NormArgs& a, TeamScratch& red, uint32_t* groupMax, uint32_t rowBuf,
-                                           size_t row, bool live, int t, int team, int part, const RowVecs<DT, V>& rv,
+__device__ __forceinline__ void finish_row(const NormArgs& a, TeamScratch& red, const RowPlace& at, const RowVecs<DT, V>& rv,
                                            float (&h)[V][kVecElems<DT>], Weight weight) {
     constexpr int E = kVecElems<DT>;
     constexpr int ESZ = DTypeOf<DT>::size;
     const NormShape& sh = a.shape;
-    const bool clustered = sh.cluster > 1;
-    const int e0 = rv.e0, step = rv.step;
-    // columns of this CTA, and where its first one lies in a row buffer (elements)
-    const int col0 = part * sh.teamThreads * V * E;
-    const int columns = min(a.hidden - col0, clustered ? sh.teamThreads * V * E : a.hidden);
-    const int bufShift = col0 + t * E - e0;
-    const ptrdiff_t resOff = ((ptrdiff_t)(row * a.residualStride) + e0) * ESZ;
-    const bool streamBuf = GENERAL && rowBuf && a.residualOut && ((uintptr_t)a.residualOut + resOff) & 15u;
-    // Vectors outside the row hold zeros from here on, and only the stores ask for them.
+    const int columns = min(a.hidden - at.col0, sh.teamThreads * V * E);   // of this CTA
+    const size_t resOff = (at.row * a.residualStride + at.col0) * ESZ;
+    const int mine = rv.e0 - at.col0;                  // the thread's first column of them
+    // From here on a thread holds zeros behind the row's end, and only the stores ask for it.
     if (GENERAL) rv.mask(h);
     float2 two = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -78,156 +65,95 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, TeamScratch& red, 
             const float2 x = make_float2(h[v][j], h[v][j + 1]);
             two = fma2(x, x, two);
         }
-        if (streamBuf) st_smem(rowBuf + (uint32_t)(v * sh.teamThreads + t) * 16u, narrow_vec<DT>(h[v]));
-        else if (a.residualOut && rv.on[v])
-            store_vec<DT, GENERAL>((char*)a.residualOut + resOff + (ptrdiff_t)v * step * ESZ, rv.sp[v], h[v]);
+        if (!a.residualOut) continue;
+        if (GENERAL) st_smem(at.buf + (uint32_t)((mine + v * rv.step) * ESZ), narrow_vec<DT>(h[v]));
+        else if (at.live && rv.left[v] > 0)
+            st_stream((char*)a.residualOut + resOff + (size_t)(mine + v * rv.step) * ESZ, narrow_vec<DT>(h[v]));
     }
     float sum = two.x + two.y;
 
     // From here on h holds h w.
     float top = 0.0f, lead[V];
-    const int groupsHere = Q == 2 ? (a.hidden + kQuantGroup - 1) / kQuantGroup : 0;
-    const int groupBase = !clustered ? team * groupsHere : -(part * sh.teamThreads * V * E / kQuantGroup);
 #pragma unroll
     for (int v = 0; v < V; v++) {
         float f[E];
         weight(v, f);
         mul_by(h[v], f);
-    }
-    if (GENERAL && Q) rv.mask(h);                      // the weight outside the row is undefined
+        if (!Q) continue;
+        float m = Q == 1 ? top : 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; v++) {
-        const int e = e0 + v * step;
+        for (int j = 0; j < E; j += 2) m = max_abs(m, h[v][j], h[v][j + 1]);
         if (Q == 1) {
-#pragma unroll
-            for (int j = 0; j < E; j += 2) top = max_abs(top, h[v][j], h[v][j + 1]);
-        }
-        if (Q == 2 && !GENERAL) {
-            // a group lies in 128 / E neighbouring lanes (smaller teams take the general path)
-            float m = 0.0f;
-#pragma unroll
-            for (int j = 0; j < E; j += 2) m = max_abs(m, h[v][j], h[v][j + 1]);
-#pragma unroll
-            for (int o = kQuantGroup / E / 2; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(~0u, m, o), 0.0f);
+            top = m;
+        } else {
+            // a group lies in 128 / E neighbouring lanes, or a row in fewer: one vector a thread then
+            const int lanes = min(kQuantGroup / E, sh.teamThreads);
+            for (int o = lanes >> 1; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(~0u, m, o), 0.0f);
             lead[v] = m;
-        }
-        if (Q == 2 && GENERAL && rv.on[v]) {
-            // m0 is of the group of element e + E - 1, m1 of the one before it
-            float m0 = 0.0f, m1 = 0.0f;
-#pragma unroll
-            for (int j = 0; j < E; j++) {
-                if (((e + j) >> 7) != ((e + E - 1) >> 7)) m1 = max_abs(m1, h[v][j], 0.0f);
-                else m0 = max_abs(m0, h[v][j], 0.0f);
-            }
-            const int last = (e + rv.sp[v].hi - 1) >> 7, first = (e + rv.sp[v].lo) >> 7;
-            const int g0 = (e + E - 1) >> 7;
-            // bits of non-negative floats order as the floats do, a NaN above all
-            if (g0 <= last && g0 >= first) atomicMax(&groupMax[groupBase + g0], __float_as_uint(m0));
-            if (g0 - 1 >= first && g0 - 1 <= last) atomicMax(&groupMax[groupBase + g0 - 1], __float_as_uint(m1));
         }
     }
     if (GENERAL) __syncwarp();                         // a larger team's barrier is in its reduction
     team_reduce<Q == 1>(red, sh, sum, top);
     const float rstd = __frsqrt_rn(sum / (float)a.hidden + a.eps);
-    if (a.rstd && live && t == 0 && part == 0) a.rstd[row] = rstd;
-    if (streamBuf && live)
-        copy_out<ESZ>((char*)a.residualOut + ((ptrdiff_t)(row * a.residualStride) + col0) * ESZ,
-                      rowBuf + (uint32_t)(bufShift * ESZ), columns * ESZ, t, sh.teamThreads);
-    const uint32_t outBuf = rowBuf + (uint32_t)sh.rowBytes;
-    const auto team_sync = [&]() {
-        if (sh.teamThreads > 32) __syncthreads();
-        else __syncwarp();
-    };
-
-    if (Q == 0) {
-#pragma unroll
-        for (int v = 0; v < V; v++) scale_by(h[v], rstd);
-        const ptrdiff_t off = ((ptrdiff_t)(row * a.recvStride) + e0) * ESZ;
-        if (GENERAL && rowBuf) {
-#pragma unroll
-            for (int v = 0; v < V; v++)
-                st_smem(outBuf + (uint32_t)(v * sh.teamThreads + t) * 16u, narrow_vec<DT>(h[v]));
-            team_sync();
-        }
-        for (int o = 0; o < a.nOut; o++) {
-            char* p = (char*)a.recv[o] + off;
-            if (GENERAL && rowBuf && ((uintptr_t)p & 15u)) {
-                if (live)
-                    copy_out<ESZ>((char*)a.recv[o] + ((ptrdiff_t)(row * a.recvStride) + col0) * ESZ,
-                                  outBuf + (uint32_t)(bufShift * ESZ), columns * ESZ, t, sh.teamThreads);
-                continue;
-            }
-#pragma unroll
-            for (int v = 0; v < V; v++)
-                if (rv.on[v]) store_vec<DT, GENERAL>(p + (ptrdiff_t)v * step * ESZ, rv.sp[v], h[v]);
-        }
-        return;
-    }
+    if (a.rstd && at.live && at.t == 0 && at.part == 0) a.rstd[at.row] = rstd;
+    if (GENERAL && a.residualOut && at.live)
+        copy_out<ESZ>((char*)a.residualOut + resOff, at.buf, columns * ESZ, at.t, sh.teamThreads);
 
     // A row (group) with a NaN has NaN as its scale.
     const auto amax_of = [&](float m) {
         const float f = m * rstd;
         return f < kLeastAmax ? kLeastAmax : f;
     };
-    const ptrdiff_t off = (ptrdiff_t)(row * a.recvStride) + e0;
     float amax[V];
 #pragma unroll
     for (int v = 0; v < V; v++) {
-        const int e = e0 + v * step;
-        if (Q == 1 || !GENERAL) {
-            amax[v] = amax_of(Q == 1 ? top : lead[v]);
-            scale_by(h[v], rstd * (kE4m3Max / amax[v]));
-        } else if (rv.on[v]) {
-            const int g0 = (e + E - 1) >> 7;
-            const float k0 = rstd * (kE4m3Max / amax_of(__uint_as_float(groupMax[groupBase + min(g0, groupsHere - 1)])));
-            const float k1 = g0 > 0 && (e >> 7) != g0 ? rstd * (kE4m3Max / amax_of(__uint_as_float(groupMax[groupBase + g0 - 1]))) : k0;
-#pragma unroll
-            for (int j = 0; j < E; j++) h[v][j] *= ((e + j) >> 7) != g0 ? k1 : k0;
-        }
+        if (Q) amax[v] = amax_of(Q == 1 ? top : lead[v]);
+        scale_by(h[v], Q ? rstd * (kE4m3Max / amax[v]) : rstd);
     }
-    if (GENERAL && rowBuf) {
-#pragma unroll
-        for (int v = 0; v < V; v++) st_smem_e4m3<E>(outBuf + (uint32_t)((v * sh.teamThreads + t) * E), h[v]);
-        team_sync();
-    }
-    for (int o = 0; o < a.nOut; o++) {
-        if (GENERAL && rowBuf && (((uintptr_t)a.recv[o] + off) & (E - 1))) {
-            if (live)
-                copy_out<1>((char*)a.recv[o] + (ptrdiff_t)(row * a.recvStride) + col0, outBuf + (uint32_t)bufShift, columns,
-                            t, sh.teamThreads);
-            continue;
-        }
-#pragma unroll
-        for (int v = 0; v < V; v++)
-            if (rv.on[v])
-                store_e4m3<E>((char*)a.recv[o] + off + (ptrdiff_t)v * step, rv.sp[v], !GENERAL || rv.sp[v].full(E), h[v]);
-    }
-    if (!live) return;
-    if (Q == 1) {
-        if (t == 0 && part == 0)
-            for (int o = 0; o < a.nOut; o++) a.scales[o][row] = amax[0] / kE4m3Max;
-    } else if (!GENERAL) {
+    constexpr int OSZ = Q ? 1 : ESZ;
+    const size_t off = (at.row * a.recvStride + at.col0) * OSZ;
+    if (GENERAL) {
+        const uint32_t buf = at.buf + (uint32_t)sh.rowBytes;
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            if (!rv.on[v] || (t & (kQuantGroup / E - 1)) != 0) continue;
-            const size_t at = row * (size_t)a.groups + ((e0 + v * step) >> 7);
-            for (int o = 0; o < a.nOut; o++) a.scales[o][at] = amax[v] / kE4m3Max;
+            const uint32_t p = buf + (uint32_t)((mine + v * rv.step) * OSZ);
+            if (Q) st_smem_e4m3<E>(p, h[v]);
+            else st_smem(p, narrow_vec<DT>(h[v]));
         }
-    } else {
-        const int gFirst = clustered ? part * sh.teamThreads * V * E / kQuantGroup : 0;
-        const int gEnd = clustered ? min(groupsHere, (part + 1) * sh.teamThreads * V * E / kQuantGroup) : groupsHere;
-        for (int g = gFirst + t; g < gEnd; g += sh.teamThreads) {
-            const float scale = amax_of(__uint_as_float(groupMax[groupBase + g])) / kE4m3Max;
-            for (int o = 0; o < a.nOut; o++) a.scales[o][row * (size_t)a.groups + g] = scale;
+        if (sh.teamThreads > 32) __syncthreads();
+        else __syncwarp();
+        if (at.live)
+            for (int o = 0; o < a.nOut; o++)
+                copy_out<OSZ>((char*)a.recv[o] + off, buf, columns * OSZ, at.t, sh.teamThreads);
+    } else if (at.live) {
+        for (int o = 0; o < a.nOut; o++) {
+            char* p = (char*)a.recv[o] + off + (size_t)mine * OSZ;
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                if (rv.left[v] == 0) continue;
+                char* q = p + (size_t)v * rv.step * OSZ;
+                if (Q == 0) {
+                    st_stream(q, narrow_vec<DT>(h[v]));
+                } else {
+                    const uint2 b = pack_e4m3<E>(h[v]);
+                    if (E == 8) *reinterpret_cast<uint2*>(q) = b;
+                    else *reinterpret_cast<uint32_t*>(q) = b.x;
+                }
+            }
         }
     }
-}
-
-// Offset of a row from a vector's boundary in the first output, in elements.
-template <int DT, int OSZ>
-__device__ __forceinline__ int frame_shift(const NormArgs& a, size_t row) {
-    constexpr int E = kVecElems<DT>;
-    return (int)(((uintptr_t)a.recv[0] + row * a.recvStride * OSZ) & (E * OSZ - 1)) / OSZ;
+    if constexpr (Q == 1) {
+        if (at.live && at.t == 0 && at.part == 0)
+            for (int o = 0; o < a.nOut; o++) a.scales[o][at.row] = amax[0] / kE4m3Max;
+    }
+    if constexpr (Q == 2) {
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            const int e = rv.e0 + v * rv.step;
+            if (!at.live || rv.left[v] == 0 || (e & (kQuantGroup - 1)) != 0) continue;     // a group's first vector
+            for (int o = 0; o < a.nOut; o++) a.scales[o][at.row * (size_t)a.groups + e / kQuantGroup] = amax[v] / kE4m3Max;
+        }
+    }
 }
 
 // Few rows, or rows too long to stage: every team takes one row and loads it directly.
@@ -238,140 +164,103 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) k_allreduce_rmsnorm(const 
     constexpr int ESZ = DTypeOf<DT>::size;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ TeamScratch red;
-    __shared__ uint32_t groupMax[Q == 2 && GENERAL ? kNormGroupSlots : 1];
     const NormShape& sh = a.shape;
-    const bool clustered = sh.cluster > 1;
-    const int t = sh.rowsPerCta > 1 ? (int)threadIdx.x & (sh.teamThreads - 1) : (int)threadIdx.x;
     const int team = sh.rowsPerCta > 1 ? (int)threadIdx.x / sh.teamThreads : 0;
-    const int part = clustered ? (int)cluster_rank() : 0;
-    const size_t row = (size_t)(blockIdx.x / (unsigned)sh.cluster) * sh.rowsPerCta + team;
-    const bool live = row < a.rows;
-    if (clustered) cluster_arrive();
-    if (Q == 2 && GENERAL) {
-        for (int i = threadIdx.x; i < kNormGroupSlots; i += blockDim.x) groupMax[i] = 0u;
-        __syncthreads();
-    }
-    // CTAs of a cluster cut the row at multiples of a vector from its start, so that a scale
-    // group never spans two CTAs.
-    const int shift = GENERAL && live && !clustered ? frame_shift<DT, Q ? 1 : ESZ>(a, row) : 0;
-    RowVecs<DT, V> rv;
-    rv.set((part * sh.teamThreads * V + t) * E - shift, sh.teamThreads * E, a.hidden, live);
+    RowPlace at;
+    at.t = sh.rowsPerCta > 1 ? (int)threadIdx.x & (sh.teamThreads - 1) : (int)threadIdx.x;
+    at.part = sh.cluster > 1 ? (int)cluster_rank() : 0;
+    at.col0 = at.part * sh.teamThreads * V * E;
+    at.row = (size_t)(blockIdx.x / (unsigned)sh.cluster) * sh.rowsPerCta + team;
+    at.live = at.row < a.rows;
+    at.buf = (uint32_t)__cvta_generic_to_shared(smem) + (uint32_t)(2 * team * sh.rowBytes);
+    if (sh.cluster > 1) cluster_arrive();
+    const RowVecs<DT, V> rv(at.col0 + at.t * E, sh.teamThreads * E, a.hidden);
 
     // The weight's and the residual's loads are under way while the ranks' are awaited.
-    WeightVec<DT> w[V];
+    float w[V][E];
     uint4 res[V];
 #pragma unroll
     for (int v = 0; v < V; v++) {
         const int e = rv.e0 + v * rv.step;
-        if (rv.on[v]) w[v].template load<GENERAL>(a.weight, a.weightF32, e, rv.sp[v]);
-        if (a.residual && rv.on[v])
-            res[v] = load_vec<ESZ, GENERAL>((const char*)a.residual + ((ptrdiff_t)(row * a.residualStride) + e) * ESZ,
-                                            rv.sp[v]);
+        load_weight<DT, GENERAL>(a.weight, a.weightF32, e, rv.left[v], w[v]);
+        res[v] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.residual && at.live && rv.left[v] > 0)
+            res[v] = load_vec<ESZ, GENERAL>((const char*)a.residual + (at.row * a.residualStride + e) * ESZ, rv.left[v]);
     }
+    if (GENERAL) rv.mask(w);
     float h[V][E];
-    sum_ranks<DT, V, GENERAL>(a.send, a.nRanks, ((ptrdiff_t)(row * a.sendStride) + rv.e0) * ESZ, rv, h);
-    if (a.residual) {
+    sum_ranks<DT, V, GENERAL>(a.send, a.nRanks, (at.row * a.sendStride + rv.e0) * ESZ, at.live, rv, h);
 #pragma unroll
-        for (int v = 0; v < V; v++) {
-            if (!rv.on[v]) continue;
-            float f[E];
-            widen_vec<DT>(res[v], f);
-            add_to(h[v], f);
-        }
+    for (int v = 0; v < V; v++) {
+        float f[E];
+        widen_vec<DT>(res[v], f);
+        add_to(h[v], f);
     }
-    const uint32_t rowBuf = GENERAL && sh.rowBytes ? (uint32_t)__cvta_generic_to_shared(smem) +
-                                                         (uint32_t)(2 * team * sh.rowBytes) : 0u;
-    finish_row<DT, V, GENERAL, Q>(a, red, groupMax, rowBuf, row, live, t, team, part, rv, h, [&](int v, float (&f)[E]) {
-        if (rv.on[v]) {
-            w[v].get(a.weightF32, f);
-        } else {
+    finish_row<DT, V, GENERAL, Q>(a, red, at, rv, h, [&](int v, float (&f)[E]) {
 #pragma unroll
-            for (int j = 0; j < E; j++) f[j] = 0.0f;
-        }
+        for (int j = 0; j < E; j++) f[j] = w[v][j];
     });
 }
 
-// Many rows: CTAs stride over them, the next row's loads under way while one is finished.
-template <int V> constexpr int staged_min_ctas() { return V == 4 ? 1 : V == 2 ? 1 : 2; }
+// Many rows: a CTA takes sh.rounds rows (of each of its teams) one behind the other, the next
+// row's loads under way while one is finished.  CTAs start in order and stay near one another,
+// which the memory rewards: CTAs that stride over all rows drift apart (1 x 16384 x 4096 bf16:
+// 83 us against 97).
 template <int DT, int V, bool GENERAL, int Q>
-__global__ void __launch_bounds__(kStageMaxThreads, staged_min_ctas<V>())
+__global__ void __launch_bounds__(kStageMaxThreads, V == 1 ? 2 : 1)
 k_allreduce_rmsnorm_staged(const __grid_constant__ NormArgs a) {
     pdl_begin();
     constexpr int E = kVecElems<DT>;
     constexpr int ESZ = DTypeOf<DT>::size;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ TeamScratch red[2];
-    __shared__ uint32_t groupMax[Q == 2 && GENERAL ? 3 * kNormGroupSlots : 1];
     const NormShape& sh = a.shape;
-    const int t = sh.rowsPerCta > 1 ? (int)threadIdx.x & (sh.teamThreads - 1) : (int)threadIdx.x;
     const int team = sh.rowsPerCta > 1 ? (int)threadIdx.x / sh.teamThreads : 0;
-    const int N = a.nRanks;
-    const int segments = N + (a.residual ? 1 : 0);
-    const uint32_t base0 = (uint32_t)__cvta_generic_to_shared(smem);
-    StageAddr stage;
-    stage.pitch = blockDim.x * 16u;
-    stage.base = base0 + (uint32_t)sh.weightBytes + threadIdx.x * 16u;
-    stage.second = (uint32_t)segments * V * stage.pitch;
-    const WeightSmem ws = stage_weight(a.weight, a.weightF32, a.weightF32 ? 4 : ESZ, a.hidden, base0,
-                                       sh.weightBytes);
-    const uint32_t rowBuf = GENERAL && sh.rowBytes
-                                ? base0 + (uint32_t)(sh.weightBytes + sh.stageBytes + 2 * team * sh.rowBytes) : 0u;
-    if (Q == 2 && GENERAL)
-        for (int i = threadIdx.x; i < 3 * kNormGroupSlots; i += blockDim.x) groupMax[i] = 0u;
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+    RowPlace at;
+    at.t = sh.rowsPerCta > 1 ? (int)threadIdx.x & (sh.teamThreads - 1) : (int)threadIdx.x;
+    at.part = at.col0 = 0;
+    at.buf = base + (uint32_t)(sh.weightBytes + sh.stageBytes + 2 * team * sh.rowBytes);
+    const RowVecs<DT, V> rv(at.t * E, sh.teamThreads * E, a.hidden);
+    const StageAddr stage = stage_addr<GENERAL>(base + (uint32_t)sh.weightBytes, sh);
+    const int N = a.nRanks, segments = N + (a.residual ? 1 : 0);
 
-    const auto frame = [&](size_t row, RowVecs<DT, V>& rv) {
-        const bool live = row < a.rows;
-        const int shift = GENERAL && live ? frame_shift<DT, Q ? 1 : ESZ>(a, row) : 0;
-        rv.set(t * E - shift, sh.teamThreads * E, a.hidden, live);
+    const size_t first = (size_t)blockIdx.x * sh.rounds * sh.rowsPerCta;
+    const size_t end = min(a.rows, first + (size_t)sh.rounds * sh.rowsPerCta);
+    // address of a segment's element rv.e0: the ranks', then the residual's
+    const auto segment = [&](int s, size_t row) {
+        return s < N ? (const char*)a.send[s] + (row * a.sendStride + rv.e0) * ESZ
+                     : (const char*)a.residual + (row * a.residualStride + rv.e0) * ESZ;
     };
-    // address of a segment's element e0: the ranks', then the residual's
-    const auto segment = [&](int s, size_t row, int e0) {
-        return s < N ? (const char*)a.send[s] + ((ptrdiff_t)(row * a.sendStride) + e0) * ESZ
-                     : (const char*)a.residual + ((ptrdiff_t)(row * a.residualStride) + e0) * ESZ;
-    };
-    // start a row's copies; none for a row past the end, whose vectors are all off
     const auto fetch = [&](size_t row) {
-        RowVecs<DT, V> rv;
-        frame(row, rv);
-        for (int s = 0; s < segments; s++) stage_segment<DT, V, GENERAL>(stage, s, segment(s, row, rv.e0), rv);
+        if (row < end)
+            for (int s = 0; s < segments; s++) stage_segment<DT, V, GENERAL>(stage, s, segment(s, row), rv);
         copies_commit();
     };
-    const size_t first = (size_t)blockIdx.x * sh.rowsPerCta, stride = (size_t)gridDim.x * sh.rowsPerCta;
-    if (!GENERAL) {
-        RowVecs<DT, V> rv;
-        frame(first + team, rv);
-        stage_zeros<DT, V>(stage, segments, rv);
-    }
+    if (!GENERAL) stage_zeros<DT, V>(stage, segments, rv);
     fetch(first + team);
-    copies_wait();
-    __syncthreads();                                   // the weight has been copied, by all threads
-    int flip = 0, turn = 0;
+    stage_weight<DT, GENERAL>(a.weight, a.weightF32, a.hidden, base, sh.weightBytes);
+    __syncthreads();
+    int flip = 0;
     // every team of a CTA runs the same number of rounds
-    for (size_t base = first; base < a.rows; base += stride) {
-        const size_t row = base + team;
-        RowVecs<DT, V> rv;
-        frame(row, rv);
+    for (size_t row0 = first; row0 < end; row0 += sh.rowsPerCta) {
+        at.row = row0 + team;
+        at.live = at.row < end;
         float h[V][E];
 #pragma unroll
         for (int v = 0; v < V; v++)
 #pragma unroll
             for (int j = 0; j < E; j++) h[v][j] = 0.0f;
         copies_wait();
+        if (GENERAL) __syncwarp();
 #pragma unroll 2
         for (int s = 0; s < segments; s++)
-            add_segment<DT, V, GENERAL>(stage, s, GENERAL ? (unsigned)(uintptr_t)segment(s, row, rv.e0) & 15u : 0u, rv, h);
-        fetch(row + stride);
-        uint32_t* groups = groupMax;
-        if (Q == 2 && GENERAL) {
-            // Three sets of maxima: this row's, the one the last row may still be read from, and
-            // the next row's, which is cleared now.
-            const int mine = (a.hidden + kQuantGroup - 1) / kQuantGroup, after = turn == 2 ? 0 : turn + 1;
-            groups = groupMax + turn * kNormGroupSlots;
-            for (int g = t; g < mine; g += sh.teamThreads) groupMax[after * kNormGroupSlots + team * mine + g] = 0u;
-            turn = after;
-        }
-        finish_row<DT, V, GENERAL, Q>(a, red[flip], groups, rowBuf, row, row < a.rows, t, team, 0, rv, h,
-                                      [&](int v, float (&f)[E]) { weight_vec<DT, GENERAL>(ws, rv.e0 + v * rv.step, f); });
+            add_segment<DT, V, GENERAL>(stage, s, GENERAL ? (unsigned)(uintptr_t)segment(s, at.row) & 15u : 0u, h);
+        if (GENERAL) __syncwarp();
+        fetch(at.row + sh.rowsPerCta);
+        finish_row<DT, V, GENERAL, Q>(a, red[flip], at, rv, h, [&](int v, float (&f)[E]) {
+            staged_weight<DT>(base, a.weightF32, rv.e0 + v * rv.step, f);
+        });
         flip ^= 1;
     }
     copies_wait();
@@ -384,7 +273,8 @@ static cudaError_t norm_launch_g(const NormArgs& a, cudaStream_t s) {
                                     : allow_smem(k_allreduce_rmsnorm<DT, V, GENERAL, Q>, sh.smemBytes);
     if (e != cudaSuccess) return e;
     if (sh.staged)
-        return norm_launch(k_allreduce_rmsnorm_staged<DT, V, GENERAL, Q>, (unsigned)sh.ctas, sh, sh.smemBytes, s, a);
+        return norm_launch(k_allreduce_rmsnorm_staged<DT, V, GENERAL, Q>, (unsigned)((a.rows + (size_t)sh.rounds * sh.rowsPerCta - 1) / ((size_t)sh.rounds * sh.rowsPerCta)), sh,
+                           sh.smemBytes, s, a);
     const size_t ctas = (a.rows + sh.rowsPerCta - 1) / sh.rowsPerCta * (size_t)sh.cluster;
     return norm_launch(k_allreduce_rmsnorm<DT, V, GENERAL, Q>, (unsigned)ctas, sh, sh.smemBytes, s, a);
 }

@@ -40,17 +40,27 @@ void set_team(NormShape* s, int nv, int vecs) {
 // Launch shape of the norm kernels.
 NormShape norm_shape(const NormCall& c) {
     const int E = 16 / c.elemSize;
-    // a row that may start inside an aligned vector touches up to one vector more
-    const int nv = c.general ? (c.hidden + 2 * E - 2) / E : c.hidden / E;
+    const int nv = (c.hidden + E - 1) / E;
     NormShape s = {};
     s.general = c.general ? 1 : 0;
     s.cluster = 1;
+    // Bytes of dynamic shared memory for the shape as it stands.
+    const auto layout = [&]() {
+        s.extraBytes = c.backward ? s.threads * s.vecs * E * (int)sizeof(float) : 0;
+        s.weightBytes = s.staged ? s.teamThreads * s.vecs * E * c.weightSize : 0;
+        s.stageBytes = s.staged ? (c.segments * s.vecs * stage_blocks(s.threads, s.teamThreads, c.general) + 1) * 16 : 0;
+        // a row's vectors, and the block behind them that a realigned read may touch
+        s.rowBytes = c.general ? s.teamThreads * s.vecs * 16 + 16 : 0;
+        s.smemBytes = s.extraBytes + s.weightBytes + s.stageBytes + s.rowBytes * (c.backward ? 1 : 2) * s.rowsPerCta;
+    };
 
     // Staged: more vectors a thread means fewer instructions and barriers a row, as long as
     // the last warp is not left half empty.
     double best = 0;
     for (const int vecs : {4, 2, 1}) {
         const int team = team_threads(nv, vecs);
+        // a scale group is found in neighbouring lanes: no team of fewer lanes than it spans
+        if (c.groups && vecs > 1 && team * E < kQuantGroup) continue;
         const double weight = vecs == 4 ? 1.0 : vecs == 2 ? 0.92 : 0.8;
         const double use = weight * nv / ((double)team * vecs);
         if (team <= kStageMaxThreads && use > best) {
@@ -58,31 +68,21 @@ NormShape norm_shape(const NormCall& c) {
             set_team(&s, nv, vecs);
         }
     }
-    // Bytes of dynamic shared memory for the shape as it stands.
-    const auto layout = [&]() {
-        const size_t vectors = (size_t)s.threads * s.vecs;
-        s.extraBytes = (int)(vectors * E * c.extraPerElem);
-        s.weightBytes = s.staged ? (int)(((size_t)s.teamThreads * s.vecs * E * c.weightSize + 30) / 16 * 16 + 80) : 0;
-        s.stageBytes = s.staged ? (int)std::min<size_t>(c.segments * vectors * 16 * (c.realign ? 2 : 1), 1 << 28) : 0;
-        // a row's vectors, and the block behind them that a realigned read may touch
-        s.rowBytes = c.general && (c.outRealign || s.cluster > 1) ? s.teamThreads * s.vecs * 16 + 16 : 0;
-        s.smemBytes = s.extraBytes + s.weightBytes + s.stageBytes + s.rowBytes * c.rowBuffers * s.rowsPerCta;
-    };
     if (best > 0) {
-        // One staged row a CTA, and as many CTAs as have about 72 KiB under way per SM: less
-        // leaves the memory waiting, more makes it slower (8 x 4096 x 4096 bf16, 72 KiB a row:
-        // 93 us with one CTA, 105 us with two or with two stages; 1 x 16384 x 4096 to 8 bits,
-        // 16 KiB a row: 121, 102, 74 us with two, three, four).
         s.staged = 1;
         layout();
-        const int most = 224 * 1024, overhead = 4 * 1024;    // of the SM's, and of a CTA's static arrays
+        const int most = 224 * 1024, overhead = 2 * 1024;    // of the SM's, and of a CTA's static arrays
         const int regs = s.vecs == 1 ? 64 : 128;
-        const int aim = std::max(1, (int)((72 * 1024 + s.stageBytes / 2) / std::max(1, s.stageBytes)));
+        const size_t groups = (c.rows + s.rowsPerCta - 1) / s.rowsPerCta;
         if (s.smemBytes + overhead <= most) {
-            const int perSm = std::min({aim, most / (s.smemBytes + overhead), 65536 / (regs * s.threads), 16});
-            const size_t wave = (size_t)c.smCount * std::max(1, perSm);
-            s.staged = (c.rows + s.rowsPerCta - 1) / s.rowsPerCta > wave;
+            // About 72 KiB under way per SM: less leaves the memory waiting, more makes it slower.
+            const int aim = std::max(1, (72 * 1024 + s.stageBytes / 2) / s.stageBytes);
+            const int perSm = std::max(1, std::min({c.backward ? aim : 16, most / (s.smemBytes + overhead),
+                                                    65536 / (regs * s.threads), 16}));
+            const size_t wave = (size_t)c.smCount * perSm;
+            s.staged = groups > wave;
             s.ctas = (int)wave;
+            s.rounds = (int)std::max<size_t>(1, std::min<size_t>(4, groups / wave));
         } else {
             s.staged = 0;
         }
@@ -105,9 +105,6 @@ NormShape norm_shape(const NormCall& c) {
         }
         layout();
     }
-    // a scale group of aligned rows is found in neighbouring lanes: teams with fewer lanes
-    // than a group has vectors take the general path
-    if (c.groups && s.teamThreads * E < kQuantGroup) s.general = 1;
     return s;
 }
 
@@ -178,30 +175,21 @@ vResult_t check_desc(const vRmsNormDesc_t* desc, Checked* k) {
 struct Buffers {
     int nOut = 0;
     bool aligned = true;
-    bool congruent = true;           // every input's rows start at the same offset from a vector's
-                                     // boundary as the first output's
-    bool outCongruent = true;        // and every other output's
-    uintptr_t offset = 0;            // the first output's offset, in elements
 };
 vResult_t check_buffers(const Checked& k, int nRanks, const void* const* send, void* const* recv, int osz,
                         const void** sendOut, void** out, int* index, Buffers* b) {
     const vRmsNormDesc_t& d = k.d;
     if (!send || !recv) return vInvalidArgument;
     const size_t e = 16 / (size_t)k.esz;
-    for (int r = nRanks - 1; r >= 0; r--)
-        if (recv[r]) b->offset = ((uintptr_t)recv[r] / osz) % e;
-    if (d.rows > 1) b->congruent = d.sendStride % e == d.recvStride % e && d.residualStride % e == d.recvStride % e;
     b->aligned = d.hidden % e == 0 &&
                  (d.rows == 1 || (d.sendStride % e == 0 && d.residualStride % e == 0 && d.recvStride % e == 0));
     for (int r = 0; r < nRanks; r++) {
         if (!send[r] || !at(send[r], k.esz)) return vInvalidArgument;
         sendOut[r] = send[r];
         b->aligned = b->aligned && at(send[r], 16);
-        b->congruent = b->congruent && ((uintptr_t)send[r] / k.esz) % e == b->offset;
         if (!recv[r]) continue;
         if (!at(recv[r], osz)) return vInvalidArgument;
         b->aligned = b->aligned && at(recv[r], e * osz);
-        b->outCongruent = b->outCongruent && ((uintptr_t)recv[r] / osz) % e == b->offset;
         if (index) index[b->nOut] = r;
         out[b->nOut++] = recv[r];
     }
@@ -217,7 +205,6 @@ vResult_t check_row_buffer(const Checked& k, const void* p, Buffers* b) {
     if (!p) return vSuccess;
     if (!at(p, k.esz)) return vInvalidArgument;
     b->aligned = b->aligned && at(p, 16);
-    b->congruent = b->congruent && ((uintptr_t)p / k.esz) % (16 / (size_t)k.esz) == b->offset;
     return vSuccess;
 }
 
@@ -229,8 +216,6 @@ vc::NormCall norm_call(const Checked& k, const CommView& v, const Buffers& b) {
     c.weightSize = (int)vc::dtype_size(k.d.weightType);
     c.smCount = v.smCount;
     c.general = !b.aligned;
-    c.realign = !b.congruent;
-    c.outRealign = !b.outCongruent;
     return c;
 }
 
@@ -284,12 +269,7 @@ vResult_t norm_forward(const vRmsNormDesc_t* desc, const void* const* send, cons
     a.eps = k.d.eps;
     vc::NormCall call = norm_call(k, v, b);
     call.segments = v.nRanks + (residual ? 1 : 0);
-    call.groups = quant && a.groups > 0;
-    call.rowBuffers = 2;
-    const size_t e = 16 / (size_t)k.esz;
-    if (residualOut && (((uintptr_t)residualOut / k.esz) % e != b.offset ||
-                        (a.rows > 1 && a.residualStride % e != a.recvStride % e)))
-        call.outRealign = true;
+    call.groups = a.groups > 0;
     a.shape = vc::norm_shape(call);
     return comm_launch(c, quant ? "allreduce rmsnorm quant" : "allreduce rmsnorm", [&]() {
         return quant ? vc::launch_allreduce_rmsnorm_quant(a, k.d.datatype, stream)
@@ -345,8 +325,7 @@ vResult_t norm_backward(const vRmsNormDesc_t* desc, const void* const* send, con
     a.weightF32 = k.d.weightType == vFloat32;
     vc::NormCall call = norm_call(k, v, b);
     call.segments = v.nRanks + 1 + (gradResidual ? 1 : 0);
-    call.extraPerElem = sizeof(float);
-    call.rowBuffers = 1;
+    call.backward = true;
     a.shape = vc::norm_shape(call);
     a.parts = vc::norm_backward_parts(a.rows, a.shape, v.smCount);
     if (!workspace || !at(workspace, 16) || workspaceBytes < (size_t)a.parts * k.d.hidden * sizeof(float))
@@ -508,16 +487,13 @@ vResult_t vRmsNormBackwardWorkspace(const vRmsNormDesc_t* desc, vcomm_t comm, si
     *bytes = 16;
     if (k.d.rows == 0 || k.d.hidden == 0) return vSuccess;
     // whatever the buffers' alignment turns out to be, with or without a residual's gradient
-    for (int i = 0; i < 16; i++) {
+    for (int i = 0; i < 4; i++) {
         Buffers b;
         b.aligned = (i & 1) != 0;
-        b.congruent = (i & 2) != 0;
-        b.outCongruent = (i & 4) != 0;
-        if (b.aligned && (!b.congruent || !b.outCongruent || k.d.hidden % (16 / k.esz) != 0)) continue;
+        if (b.aligned && k.d.hidden % (16 / k.esz) != 0) continue;
         vc::NormCall call = norm_call(k, v, b);
-        call.segments = v.nRanks + 1 + (i >> 3);
-        call.extraPerElem = sizeof(float);
-        call.rowBuffers = 1;
+        call.segments = v.nRanks + 1 + (i >> 1);
+        call.backward = true;
         const int parts = vc::norm_backward_parts(k.d.rows, vc::norm_shape(call), v.smCount);
         *bytes = std::max(*bytes, (size_t)parts * k.d.hidden * sizeof(float));
     }

@@ -38,23 +38,29 @@ struct NormShape {
     int rowsPerCta;                  // teams in a CTA
     int cluster;                     // CTAs that share a row
     int threads;                     // threads per CTA
-    int general;                     // some buffer or row may start off a 16-byte boundary
-    int staged;                      // many rows: ctas CTAs stride over them and stage the next one
-    int ctas;
+    int general;                     // some row may start off a 16-byte boundary or end inside a vector
+    int staged;                      // many rows: a CTA stages the next row while it finishes one
+    int rounds;                      // staged, forward: rows that each team of a CTA takes
+    int ctas;                        // staged: CTAs of one full wave (the backward pass's grid)
     int weightBytes;                 // dynamic shared memory: of the staged weight,
     int stageBytes;                  // of the staged row of every team,
-    int rowBytes;                    // of a row buffer (0: the outputs need none),
-    int extraBytes;                  // of the caller's, in front,
+    int rowBytes;                    // of a row buffer (GENERAL: two a team, the backward pass one),
+    int extraBytes;                  // of the weight gradient's sums, in front,
     int smemBytes;                   // and altogether
 };
 constexpr int kStageMaxThreads = 512;
-// Elements that one 128-element scale group covers.
+// 16-byte blocks of shared memory for one vector a thread of one input.  General: the blocks of
+// a team's lanes of a warp lie side by side, with room for one more behind the last lane's.
+#if defined(__CUDACC__)
+__host__ __device__
+#endif
+constexpr int stage_blocks(int threads, int teamThreads, bool general) {
+    return !general ? threads : teamThreads >= 32 ? threads / 32 * 33 : threads / teamThreads * (teamThreads + 1);
+}
 constexpr int kQuantGroup = 128;
 constexpr int kNormMaxThreads = 640;     // of a CTA that holds 4 vectors a thread
 constexpr int kNormWarpCta = 128;        // threads of a CTA whose teams are parts of a warp
 constexpr int kNormMaxCluster = 8;
-constexpr int kNormGroupSlots = 168;     // scale groups of one CTA: at most 640 * 4 * 8 / 128 + 1,
-                                         // or 128 / team * (team * 4 * 8 / 128 + 1) of small teams
 // What a launch has to be shaped for.
 struct NormCall {
     size_t rows;
@@ -62,11 +68,8 @@ struct NormCall {
     int segments;                    // inputs that every row is read from
     int smCount;
     bool general;                    // as in NormShape
-    bool realign;                    // inputs may start at other offsets from 16 bytes than the first output
-    bool outRealign;                 // other outputs may
+    bool backward;
     bool groups;                     // 8-bit output with a scale per 128 elements
-    int rowBuffers;                  // row buffers that a team needs for such outputs
-    int extraPerElem;                // shared memory per element of a row for the caller
 };
 NormShape norm_shape(const NormCall& c);
 
