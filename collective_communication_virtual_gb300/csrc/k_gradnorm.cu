@@ -37,7 +37,7 @@ __device__ __forceinline__ float chunk_squares(const GradChunk& c) {
         raw[i] = make_uint4(0u, 0u, 0u, 0u);
         if (e0 + i * kGradThreads * E < c.count) raw[i] = ld_once(p + i * kGradThreads * 16);
     }
-    float2 s[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < kGradVecs; i++) {
         const int e = e0 + i * kGradThreads * E;
@@ -48,12 +48,9 @@ __device__ __forceinline__ float chunk_squares(const GradChunk& c) {
             for (int j = 0; j < E; j++) f[j] = e + j >= 0 && e + j < c.count ? f[j] : 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < E; j += 2) {
-            const float2 x = make_float2(f[j], f[j + 1]);
-            s[j / 2 & 1] = fma2(x, x, s[j / 2 & 1]);
-        }
+        for (int j = 0; j < E; j++) s[j & 3] = fmaf(f[j], f[j], s[j & 3]);
     }
-    return (s[0].x + s[0].y) + (s[1].x + s[1].y);
+    return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 template <int DT>
@@ -142,10 +139,11 @@ __global__ void __launch_bounds__(kGradThreads) k_grad_norm(const __grid_constan
     }
 }
 
-// One chunk a CTA, dispatched in order.
+// One chunk a CTA, in order from the last one: the norm has just read those, so up to the size
+// of L2 they need not be read from memory again.
 __global__ void __launch_bounds__(kGradThreads) k_grad_clip(const __grid_constant__ GradClipArgs a) {
     pdl_begin();
-    const GradChunk c = load_chunk(a.chunks + blockIdx.x);
+    const GradChunk c = load_chunk(a.chunks + (gridDim.x - 1 - blockIdx.x));
     float factor = a.maxNorm / (*a.norm + 1e-6f);
     factor = factor > 1.0f ? 1.0f : factor;            // a NaN stays
     if (factor == 1.0f && c.in == c.out) return;

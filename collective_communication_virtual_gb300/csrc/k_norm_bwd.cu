@@ -100,7 +100,7 @@ __device__ __forceinline__ void finish_row_backward(const NormBackwardArgs& a, T
         rv.mask(xhat);
         rv.mask(g);
     }
-    float2 two = make_float2(0.0f, 0.0f);
+    float2 two[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
     for (int v = 0; v < V; v++) {
         if (live) dw.add(v, g[v], xhat[v]);
@@ -109,9 +109,9 @@ __device__ __forceinline__ void finish_row_backward(const NormBackwardArgs& a, T
         mul_by(g[v], f);
 #pragma unroll
         for (int j = 0; j < E; j += 2)
-            two = fma2(make_float2(g[v][j], g[v][j + 1]), make_float2(xhat[v][j], xhat[v][j + 1]), two);
+            two[j / 2 & 1] = fma2(make_float2(g[v][j], g[v][j + 1]), make_float2(xhat[v][j], xhat[v][j + 1]), two[j / 2 & 1]);
     }
-    float sum = two.x + two.y, none = 0.0f;
+    float sum = (two[0].x + two[0].y) + (two[1].x + two[1].y), none = 0.0f;
     team_reduce<false>(red, sh, sum, none);
     const float c = -(sum / (float)a.width);
     const int mine = rv.e0 - col0;
@@ -254,12 +254,10 @@ k_rmsnorm_backward_staged(const __grid_constant__ NormBackwardArgs a) {
 #pragma unroll 2
         for (int s = 0; s < N; s++) add_segment<DT, V, GENERAL>(stage, s, shift_of(s), g);
         const unsigned shHid = shift_of(N), shRes = a.gradResidual ? shift_of(N + 1) : 0u;
+        staged<V, GENERAL>(stage, N, shHid, hid);
 #pragma unroll
-        for (int v = 0; v < V; v++) {
-            hid[v] = staged<DT, V, GENERAL>(stage, N, v, shHid);
-            res[v] = make_uint4(0u, 0u, 0u, 0u);
-            if (a.gradResidual) res[v] = staged<DT, V, GENERAL>(stage, N + 1, v, shRes);
-        }
+        for (int v = 0; v < V; v++) res[v] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.gradResidual) staged<V, GENERAL>(stage, N + 1, shRes, res);
         if (GENERAL) __syncwarp();
         fetch(row + stride);
         finish_row_backward<DT, V, GENERAL>(a, red[flip], row, row < a.rows, rstd, t, 0, buf, rv, dw, g, hid, res,
@@ -283,8 +281,10 @@ __global__ void __launch_bounds__(kSumThreads) k_sum_columns(const float* partia
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + x;
     float s = 0.0f;
-    if (c < width)
+    if (c < width) {
+#pragma unroll 8
         for (int r = y; r < rows; r += 32) s += partials[(size_t)r * width + c];
+    }
     part[y][x] = s;
     __syncthreads();
     s = part[x][y];                                    // warp y: column y's 32 sums

@@ -136,6 +136,25 @@ __device__ __forceinline__ void mul_by(float (&acc)[E], const float (&f)[E]) {
     }
 }
 
+// Bytes [4 W + r / 8, + 16) of the 32 bytes a, b, for r in 0..24 bits.
+template <int W>
+__device__ __forceinline__ uint4 shift_words(const uint4& a, const uint4& b, unsigned r) {
+    const uint32_t w[9] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, 0u};
+    return make_uint4(__funnelshift_r(w[W], w[W + 1], r), __funnelshift_r(w[W + 1], w[W + 2], r),
+                      __funnelshift_r(w[W + 2], w[W + 3], r), __funnelshift_r(w[W + 3], w[W + 4], r));
+}
+// f(shift) with shift(a, b) = bytes [sh, sh + 16) of a, b: one branch for any number of vectors.
+template <typename F>
+__device__ __forceinline__ void with_shift(unsigned sh, F f) {
+    const unsigned r = (sh & 3u) * 8u;
+    switch (sh >> 2) {
+    case 0: f([r](const uint4& a, const uint4& b) { return shift_words<0>(a, b, r); }); break;
+    case 1: f([r](const uint4& a, const uint4& b) { return shift_words<1>(a, b, r); }); break;
+    case 2: f([r](const uint4& a, const uint4& b) { return shift_words<2>(a, b, r); }); break;
+    default: f([r](const uint4& a, const uint4& b) { return shift_words<3>(a, b, r); }); break;
+    }
+}
+
 // Streamed once, so kept out of L1.  volatile: never moved above the wait for the previous
 // kernel, nor merged with another load of the address.
 __device__ __forceinline__ uint4 ld_once(const void* p) {
@@ -248,8 +267,11 @@ __device__ __forceinline__ void copy_out(char* dst, uint32_t src, int bytes, int
     if (sh == 0) {
         for (int i = t; i < blocks; i += threads) st_stream(dst + (size_t)i * 16, ld_smem(src + 16 * i));
     } else {
-        for (int i = t; i < blocks; i += threads)
-            st_stream(dst + sh + (size_t)i * 16, shift_bytes(ld_smem(src + 16 * i), ld_smem(src + 16 * i + 16), sh));
+        with_shift(sh, [&](auto shift) {
+#pragma unroll 2
+            for (int i = t; i < blocks; i += threads)
+                st_stream(dst + sh + (size_t)i * 16, shift(ld_smem(src + 16 * i), ld_smem(src + 16 * i + 16)));
+        });
     }
     const int head = min((int)sh, bytes), tail = head + max(blocks, 0) * 16;
     for (int k = t * OSZ; k < head + bytes - tail; k += threads * OSZ) {

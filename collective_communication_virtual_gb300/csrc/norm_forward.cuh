@@ -57,20 +57,20 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, TeamScratch& red, 
     const int mine = rv.e0 - at.col0;                  // the thread's first column of them
     // From here on a thread holds zeros behind the row's end, and only the stores ask for it.
     if (GENERAL) rv.mask(h);
-    float2 two = make_float2(0.0f, 0.0f);
+    float2 two[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
     for (int v = 0; v < V; v++) {
 #pragma unroll
         for (int j = 0; j < E; j += 2) {
             const float2 x = make_float2(h[v][j], h[v][j + 1]);
-            two = fma2(x, x, two);
+            two[j / 2 & 1] = fma2(x, x, two[j / 2 & 1]);
         }
         if (!a.residualOut) continue;
         if (GENERAL) st_smem(at.buf + (uint32_t)((mine + v * rv.step) * ESZ), narrow_vec<DT>(h[v]));
         else if (at.live && rv.left[v] > 0)
             st_stream((char*)a.residualOut + resOff + (size_t)(mine + v * rv.step) * ESZ, narrow_vec<DT>(h[v]));
     }
-    float sum = two.x + two.y;
+    float sum = (two[0].x + two[0].y) + (two[1].x + two[1].y);
 
     // From here on h holds h w.
     float top = 0.0f, lead[V];
@@ -80,11 +80,11 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, TeamScratch& red, 
         weight(v, f);
         mul_by(h[v], f);
         if (!Q) continue;
-        float m = Q == 1 ? top : 0.0f;
+        float m = 0.0f;
 #pragma unroll
         for (int j = 0; j < E; j += 2) m = max_abs(m, h[v][j], h[v][j + 1]);
         if (Q == 1) {
-            top = m;
+            top = max_abs(top, m, 0.0f);
         } else {
             // a group lies in 128 / E neighbouring lanes, or a row in fewer: one vector a thread then
             const int lanes = min(kQuantGroup / E, sh.teamThreads);
@@ -202,10 +202,12 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) k_allreduce_rmsnorm(const 
     });
 }
 
-// Many rows: a CTA takes sh.rounds rows (of each of its teams) one behind the other, the next
-// row's loads under way while one is finished.  CTAs start in order and stay near one another,
-// which the memory rewards: CTAs that stride over all rows drift apart (1 x 16384 x 4096 bf16:
-// 83 us against 97).
+// Many rows: the next row's loads under way while one is finished.  A CTA takes sh.rounds rows
+// (of each of its teams) one behind the other: CTAs start in order and stay near one another,
+// which the memory rewards (1 x 16384 x 4096 bf16: 83 us; 97 us where as many CTAs stride over
+// all rows and drift apart).  Rows so long that one CTA fills an SM's share of the memory are
+// strided over (sh.rounds 0): a new CTA's first row would find nothing else under way
+// (8 x 4096 x 4096: 93 us against 98).
 template <int DT, int V, bool GENERAL, int Q>
 __global__ void __launch_bounds__(kStageMaxThreads, V == 1 ? 2 : 1)
 k_allreduce_rmsnorm_staged(const __grid_constant__ NormArgs a) {
@@ -225,8 +227,9 @@ k_allreduce_rmsnorm_staged(const __grid_constant__ NormArgs a) {
     const StageAddr stage = stage_addr<GENERAL>(base + (uint32_t)sh.weightBytes, sh);
     const int N = a.nRanks, segments = N + (a.residual ? 1 : 0);
 
-    const size_t first = (size_t)blockIdx.x * sh.rounds * sh.rowsPerCta;
-    const size_t end = min(a.rows, first + (size_t)sh.rounds * sh.rowsPerCta);
+    const size_t first = (size_t)blockIdx.x * max(1, sh.rounds) * sh.rowsPerCta;
+    const size_t step = sh.rounds ? sh.rowsPerCta : (size_t)gridDim.x * sh.rowsPerCta;
+    const size_t end = sh.rounds ? min(a.rows, first + (size_t)sh.rounds * sh.rowsPerCta) : a.rows;
     // address of a segment's element rv.e0: the ranks', then the residual's
     const auto segment = [&](int s, size_t row) {
         return s < N ? (const char*)a.send[s] + (row * a.sendStride + rv.e0) * ESZ
@@ -243,7 +246,7 @@ k_allreduce_rmsnorm_staged(const __grid_constant__ NormArgs a) {
     __syncthreads();
     int flip = 0;
     // every team of a CTA runs the same number of rounds
-    for (size_t row0 = first; row0 < end; row0 += sh.rowsPerCta) {
+    for (size_t row0 = first; row0 < end; row0 += step) {
         at.row = row0 + team;
         at.live = at.row < end;
         float h[V][E];
@@ -257,7 +260,7 @@ k_allreduce_rmsnorm_staged(const __grid_constant__ NormArgs a) {
         for (int s = 0; s < segments; s++)
             add_segment<DT, V, GENERAL>(stage, s, GENERAL ? (unsigned)(uintptr_t)segment(s, at.row) & 15u : 0u, h);
         if (GENERAL) __syncwarp();
-        fetch(at.row + sh.rowsPerCta);
+        fetch(at.row + step);
         finish_row<DT, V, GENERAL, Q>(a, red[flip], at, rv, h, [&](int v, float (&f)[E]) {
             staged_weight<DT>(base, a.weightF32, rv.e0 + v * rv.step, f);
         });
@@ -272,9 +275,7 @@ static cudaError_t norm_launch_g(const NormArgs& a, cudaStream_t s) {
     const cudaError_t e = sh.staged ? allow_smem(k_allreduce_rmsnorm_staged<DT, V, GENERAL, Q>, sh.smemBytes)
                                     : allow_smem(k_allreduce_rmsnorm<DT, V, GENERAL, Q>, sh.smemBytes);
     if (e != cudaSuccess) return e;
-    if (sh.staged)
-        return norm_launch(k_allreduce_rmsnorm_staged<DT, V, GENERAL, Q>, (unsigned)((a.rows + (size_t)sh.rounds * sh.rowsPerCta - 1) / ((size_t)sh.rounds * sh.rowsPerCta)), sh,
-                           sh.smemBytes, s, a);
+    if (sh.staged) return norm_launch(k_allreduce_rmsnorm_staged<DT, V, GENERAL, Q>, (unsigned)sh.ctas, sh, sh.smemBytes, s, a);
     const size_t ctas = (a.rows + sh.rowsPerCta - 1) / sh.rowsPerCta * (size_t)sh.cluster;
     return norm_launch(k_allreduce_rmsnorm<DT, V, GENERAL, Q>, (unsigned)ctas, sh, sh.smemBytes, s, a);
 }

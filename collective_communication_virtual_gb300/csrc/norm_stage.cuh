@@ -54,13 +54,20 @@ __device__ __forceinline__ void stage_segment(const StageAddr& s, int seg, const
             copy_block_async(at + v * s.pitch + 16, q - sh + 16);
     }
 }
-// The vector back from shared memory.  GENERAL: elements outside the row are undefined; else a
-// vector outside the row is zero.
-template <int DT, int V, bool GENERAL>
-__device__ __forceinline__ uint4 staged(const StageAddr& s, int seg, int v, unsigned sh) {
-    const uint32_t at = s.base + (uint32_t)(seg * V + v) * s.pitch;
-    if (!GENERAL || sh == 0) return ld_smem(at);
-    return shift_bytes(ld_smem(at), ld_smem(at + 16), sh);
+// One input's vectors back from shared memory.  GENERAL: elements outside the row are undefined;
+// else a vector outside the row is zero.
+template <int V, bool GENERAL>
+__device__ __forceinline__ void staged(const StageAddr& s, int seg, unsigned sh, uint4 (&out)[V]) {
+    const uint32_t at = s.base + (uint32_t)(seg * V) * s.pitch;
+    if (!GENERAL || sh == 0) {
+#pragma unroll
+        for (int v = 0; v < V; v++) out[v] = ld_smem(at + v * s.pitch);
+        return;
+    }
+    with_shift(sh, [&](auto shift) {
+#pragma unroll
+        for (int v = 0; v < V; v++) out[v] = shift(ld_smem(at + v * s.pitch), ld_smem(at + v * s.pitch + 16));
+    });
 }
 // Aligned rows: the vectors of a thread that lie outside every row are never copied, and are
 // zero from here on, so that nothing but the stores need ask for them.
@@ -78,8 +85,7 @@ __device__ __forceinline__ void stage_zeros(const StageAddr& s, int segments, co
 template <int DT, int V, bool GENERAL>
 __device__ __forceinline__ void add_segment(const StageAddr& s, int seg, unsigned sh, float (&acc)[V][kVecElems<DT>]) {
     uint4 raw[V];
-#pragma unroll
-    for (int v = 0; v < V; v++) raw[v] = staged<DT, V, GENERAL>(s, seg, v, sh);
+    staged<V, GENERAL>(s, seg, sh, raw);
 #pragma unroll
     for (int v = 0; v < V; v++) {
         float f[kVecElems<DT>];

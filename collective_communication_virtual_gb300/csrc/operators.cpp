@@ -30,8 +30,7 @@ int team_threads(int nv, int vecs) {
 void set_team(NormShape* s, int nv, int vecs) {
     s->vecs = vecs;
     s->teamThreads = team_threads(nv, vecs);
-    s->threads = std::max(s->teamThreads, kNormWarpCta);
-    if (s->teamThreads > 32) s->threads = s->teamThreads;
+    s->threads = s->teamThreads > 32 ? s->teamThreads : kNormWarpCta;
     s->rowsPerCta = s->threads / s->teamThreads;
 }
 
@@ -54,14 +53,16 @@ NormShape norm_shape(const NormCall& c) {
         s.smemBytes = s.extraBytes + s.weightBytes + s.stageBytes + s.rowBytes * (c.backward ? 1 : 2) * s.rowsPerCta;
     };
 
-    // Staged: more vectors a thread means fewer instructions and barriers a row, as long as
-    // the last warp is not left half empty.
+    // Staged: more vectors a thread means fewer instructions and barriers a row, as long as the
+    // last warp is not left half empty.  With few rows per SM their latency counts for more
+    // (3 x 1537 x 2731: 22 us with two vectors, 26 with four; 1 x 16000 x 2047: 68 and 64).
+    const bool few = c.rows <= (size_t)c.smCount * 16;
     double best = 0;
     for (const int vecs : {4, 2, 1}) {
         const int team = team_threads(nv, vecs);
         // a scale group is found in neighbouring lanes: no team of fewer lanes than it spans
         if (c.groups && vecs > 1 && team * E < kQuantGroup) continue;
-        const double weight = vecs == 4 ? 1.0 : vecs == 2 ? 0.92 : 0.8;
+        const double weight = vecs == 4 ? (few ? 0.8 : 1.0) : vecs == 2 ? 0.92 : 0.8;
         const double use = weight * nv / ((double)team * vecs);
         if (team <= kStageMaxThreads && use > best) {
             best = use;
@@ -71,20 +72,26 @@ NormShape norm_shape(const NormCall& c) {
     if (best > 0) {
         s.staged = 1;
         layout();
+        // CTAs of small teams: several rows each, but no more than keep the SM's CTAs several too
+        while (s.teamThreads <= 32 && s.threads > 32 && s.threads > s.teamThreads && s.stageBytes > 40 * 1024) {
+            s.threads /= 2;
+            s.rowsPerCta = s.threads / s.teamThreads;
+            layout();
+        }
         const int most = 224 * 1024, overhead = 2 * 1024;    // of the SM's, and of a CTA's static arrays
         const int regs = s.vecs == 1 ? 64 : 128;
         const size_t groups = (c.rows + s.rowsPerCta - 1) / s.rowsPerCta;
-        if (s.smemBytes + overhead <= most) {
-            // About 72 KiB under way per SM: less leaves the memory waiting, more makes it slower.
-            const int aim = std::max(1, (72 * 1024 + s.stageBytes / 2) / s.stageBytes);
-            const int perSm = std::max(1, std::min({c.backward ? aim : 16, most / (s.smemBytes + overhead),
-                                                    65536 / (regs * s.threads), 16}));
-            const size_t wave = (size_t)c.smCount * perSm;
-            s.staged = groups > wave;
+        // About 72 KiB under way per SM: less leaves the memory waiting, more makes it slower
+        // where the CTAs do not keep step.
+        const int aim = (72 * 1024 + s.stageBytes - 1) / s.stageBytes;
+        const int fit = std::max(1, std::min({most / (s.smemBytes + overhead), 65536 / (regs * s.threads), 16}));
+        const size_t wave = (size_t)c.smCount * std::min(aim, fit);
+        s.staged = s.smemBytes + overhead <= most && groups > wave;
+        if (c.backward || aim == 1) {
             s.ctas = (int)wave;
-            s.rounds = (int)std::max<size_t>(1, std::min<size_t>(4, groups / wave));
         } else {
-            s.staged = 0;
+            s.rounds = (int)std::max<size_t>(1, std::min<size_t>(4, groups * 2 / ((size_t)c.smCount * 5)));
+            s.ctas = (int)((groups + s.rounds - 1) / s.rounds);
         }
     }
     if (!s.staged) {

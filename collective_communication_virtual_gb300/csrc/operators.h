@@ -40,8 +40,9 @@ struct NormShape {
     int threads;                     // threads per CTA
     int general;                     // some row may start off a 16-byte boundary or end inside a vector
     int staged;                      // many rows: a CTA stages the next row while it finishes one
-    int rounds;                      // staged, forward: rows that each team of a CTA takes
-    int ctas;                        // staged: CTAs of one full wave (the backward pass's grid)
+    int rounds;                      // staged, forward: rows that each team of a CTA takes; 0: the CTAs
+                                     // stride over all rows, as in the backward pass
+    int ctas;                        // staged: the grid
     int weightBytes;                 // dynamic shared memory: of the staged weight,
     int stageBytes;                  // of the staged row of every team,
     int rowBytes;                    // of a row buffer (GENERAL: two a team, the backward pass one),
