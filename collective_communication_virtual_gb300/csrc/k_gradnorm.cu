@@ -53,11 +53,6 @@ __device__ __forceinline__ float chunk_squares(const GradChunk& c) {
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-template <int DT>
-__device__ __forceinline__ void scale_elem(const char* in, char* out, int e, float factor) {
-    constexpr int ESZ = DTypeOf<DT>::size;
-    st_elem<ESZ>(out, e, f32_to_elem<DT>(elem_to_f32<DT>(ld_elem<ESZ>(in, e)) * factor));
-}
 // Scale a thread's part of a chunk.  A thread's loads are all under way before its first store.
 // Gradients and outputs at different offsets from 16 bytes go element by element.
 template <int DT>
@@ -66,7 +61,8 @@ __device__ __forceinline__ void chunk_scale(const GradChunk& c, float factor) {
     constexpr int ESZ = DTypeOf<DT>::size;
     if ((((uintptr_t)c.in ^ (uintptr_t)c.out) & 15u) != 0) {
 #pragma unroll 8
-        for (int e = threadIdx.x; e < c.count; e += kGradThreads) scale_elem<DT>(c.in, c.out, e, factor);
+        for (int e = threadIdx.x; e < c.count; e += kGradThreads)
+            st_elem<ESZ>(c.out, e, f32_to_elem<DT>(elem_to_f32<DT>(ld_elem<ESZ>(c.in, e)) * factor));
         return;
     }
     const int shift = (int)((uintptr_t)c.out & 15u) / ESZ;
@@ -79,13 +75,16 @@ __device__ __forceinline__ void chunk_scale(const GradChunk& c, float factor) {
 #pragma unroll
     for (int i = 0; i < kGradVecs; i++) {
         const int e = e0 + i * kGradThreads * E;
+        if (e >= c.count) continue;
+        float f[E];
+        widen_vec<DT>(raw[i], f);
+        scale_by(f, factor);
         if (e >= 0 && e + E <= c.count) {
-            float f[E];
-            widen_vec<DT>(raw[i], f);
-            scale_by(f, factor);
             st_stream(c.out + off + i * kGradThreads * 16, narrow_vec<DT>(f));
         } else {                                       // the vector that begins or ends the chunk
-            for (int j = max(e, 0); j < min(e + E, c.count); j++) scale_elem<DT>(c.in, c.out, j, factor);
+#pragma unroll
+            for (int j = 0; j < E; j++)
+                if (e + j >= 0 && e + j < c.count) st_elem<ESZ>(c.out, e + j, f32_to_elem<DT>(f[j]));
         }
     }
 }
