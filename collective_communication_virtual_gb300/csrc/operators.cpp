@@ -240,8 +240,10 @@ vResult_t norm_forward(const vRmsNormDesc_t* desc, const void* const* send, cons
         const std::vector<const void*> s(send, send + v.nRanks);
         const std::vector<void*> o(recv, recv + v.nRanks);
         const std::vector<float*> q = quant ? std::vector<float*>(scales, scales + v.nRanks) : std::vector<float*>();
-        return vc::comm_record(c, [=]() {   // allocates nothing when it runs
-            return norm_forward(&d, s.data(), residual, weight, residualOut, o.data(), q.data(), quant, rstd, c, stream);
+        return vc::comm_record(c, [=]() {
+            return guarded([&]() {
+                return norm_forward(&d, s.data(), residual, weight, residualOut, o.data(), q.data(), quant, rstd, c, stream);
+            });
         });
     }
     if (k.d.rows == 0 || k.d.hidden == 0) return vSuccess;
@@ -298,8 +300,10 @@ vResult_t norm_backward(const vRmsNormDesc_t* desc, const void* const* send, con
         const std::vector<const void*> s(send, send + v.nRanks);
         const std::vector<void*> o(recv, recv + v.nRanks);
         return vc::comm_record(c, [=]() {
-            return norm_backward(&d, s.data(), hidden, rstd, weight, gradResidual, o.data(), gradWeight, workspace,
-                                 workspaceBytes, c, stream);
+            return guarded([&]() {
+                return norm_backward(&d, s.data(), hidden, rstd, weight, gradResidual, o.data(), gradWeight, workspace,
+                                     workspaceBytes, c, stream);
+            });
         });
     }
     if (k.d.hidden == 0) return vSuccess;

@@ -177,14 +177,23 @@ def _addr(x) -> int | None:
     return x.data_ptr()
 
 
+class Buffers:
+    """What vBuffers makes: the C array of the addresses and where it lies."""
+    __slots__ = ("array", "address", "count")
+
+    def __init__(self, array):
+        self.array, self.address, self.count = array, ctypes.addressof(array), len(array)
+
+
 def _ptr_array(bufs, n_ranks: int):
     """A C array of the buffers' device addresses (None for NULL).  The library reads
     exactly n_ranks entries, so a list of another length is refused here."""
-    n = len(bufs)
+    made = type(bufs) is Buffers                    # by vBuffers
+    n = bufs.count if made else len(bufs)
     if n != n_ranks:
         raise VcommError(vInvalidArgument, f"expected {n_ranks} buffers (one per rank), got {n}")
-    if isinstance(bufs, ctypes.Array):              # from vBuffers
-        return bufs
+    if made:
+        return bufs.address
     arr_t = _ARRAY_TYPES.get(n)
     if arr_t is None:
         arr_t = _ARRAY_TYPES[n] = ctypes.c_void_p * n
@@ -411,12 +420,12 @@ def vAllReduceNoAlloc(sendbuffs, recvbuffs, count: int, datatype, op, n_ranks: i
 
 # ---- operators next to the collectives -------------------------------------------------------
 
-def vBuffers(bufs):
+def vBuffers(bufs) -> Buffers:
     """The device addresses of a list of buffers (one per rank; None for NULL) as a C array,
     which every call here takes in place of the list: a caller whose buffers stay where they
     are marshals them once.  It holds addresses, not the tensors: the caller keeps those."""
     bufs = list(bufs)
-    return _ptr_array(bufs, len(bufs))
+    return Buffers(_ptr_array(bufs, len(bufs)))
 
 
 def vRmsNormDesc(rows: int, hidden: int, datatype, weight_type=None, eps: float = 1e-6, send_stride: int = 0,
@@ -431,22 +440,19 @@ def vRmsNormDesc(rows: int, hidden: int, datatype, weight_type=None, eps: float 
 def vAllReduceRmsNorm(desc, sendbuffs, residual, weight, residual_out, recvbuffs, rstd, comm, stream=None) -> None:
     """All-reduce + residual + RMS norm; residual, residual_out, rstd and entries of recvbuffs
     may be None."""
-    _check(lib().vAllReduceRmsNorm(ctypes.addressof(desc), *_norm_args(comm, sendbuffs, residual, weight, residual_out,
-                                                                       recvbuffs), _addr(rstd), comm, _stream(stream)),
-           "vAllReduceRmsNorm")
-
-
-def _norm_args(comm, sendbuffs, residual, weight, residual_out, recvbuffs):
     n = _n_ranks(comm)
-    return (_ptr_array(sendbuffs, n), _addr(residual), _addr(weight), _addr(residual_out), _ptr_array(recvbuffs, n))
+    _check(lib().vAllReduceRmsNorm(ctypes.addressof(desc), _ptr_array(sendbuffs, n), _addr(residual), _addr(weight),
+                                   _addr(residual_out), _ptr_array(recvbuffs, n), _addr(rstd), comm, _stream(stream)),
+           "vAllReduceRmsNorm")
 
 
 def vAllReduceRmsNormQuant(desc, sendbuffs, residual, weight, residual_out, recvbuffs, scalebuffs, rstd, comm,
                            stream=None) -> None:
     """The same with e4m3 bytes in recvbuffs and their fp32 scales in scalebuffs."""
-    _check(lib().vAllReduceRmsNormQuant(ctypes.addressof(desc),
-                                        *_norm_args(comm, sendbuffs, residual, weight, residual_out, recvbuffs),
-                                        _ptr_array(scalebuffs, _n_ranks(comm)), _addr(rstd), comm, _stream(stream)),
+    n = _n_ranks(comm)
+    _check(lib().vAllReduceRmsNormQuant(ctypes.addressof(desc), _ptr_array(sendbuffs, n), _addr(residual),
+                                        _addr(weight), _addr(residual_out), _ptr_array(recvbuffs, n),
+                                        _ptr_array(scalebuffs, n), _addr(rstd), comm, _stream(stream)),
            "vAllReduceRmsNormQuant")
 
 
@@ -507,6 +513,8 @@ def vTensorList(grads, outs=None, replicated=None) -> TensorList:
     """The gradients of a step: ``grads[r][t]`` is rank r's tensor t, ``outs`` (the clipped
     gradients; None: in place) the same, ``replicated[t]`` whether every rank holds all of
     tensor t (None: none).  A list whose tensors stay where they are serves every step."""
+    if not grads:
+        raise VcommError(vInvalidArgument, "a tensor list of no ranks")
     first = grads[0]
     if replicated is not None and len(replicated) != len(first):
         raise VcommError(vInvalidArgument, f"replicated names {len(replicated)} tensors of {len(first)}")
