@@ -237,7 +237,8 @@ k_rmsnorm_backward_staged(const __grid_constant__ NormBackwardArgs a) {
     fetch(first + team);
     float rstd = first + team < a.rows ? a.rstd[first + team] : 0.0f;
     stage_weight<DT, GENERAL>(a.weight, a.weightF32, a.width, weight, sh.weightBytes);
-    __syncthreads();
+    copies_wait();
+    __syncthreads();                                   // the weight, copied by all threads
     int flip = 0;
     for (size_t base = first; base < a.rows; base += stride) {
         const size_t row = base + team;
@@ -271,28 +272,33 @@ k_rmsnorm_backward_staged(const __grid_constant__ NormBackwardArgs a) {
     dw.write(smem, sh, a.partials + (size_t)blockIdx.x * a.width, a.width);
 }
 
-// gradWeight[c] = sum of the partial rows' column c: 32 columns a CTA, the rows dealt to its
-// 32 warps and their sums added in warp order.
-constexpr int kSumThreads = 1024;
+// gradWeight[c] = sum of the partial rows' column c: 16 columns a CTA, the rows dealt to 32
+// groups of its threads, whose sums are added in a fixed order.  CTAs of 512 threads: they become
+// resident while the pass above still runs, and larger ones take the place of its next launch's.
+constexpr int kSumColumns = 16;
+constexpr int kSumGroups = 32;
+constexpr int kSumThreads = kSumColumns * kSumGroups;
 template <int DT>
 __global__ void __launch_bounds__(kSumThreads) k_sum_columns(const float* partials, int rows, int width, void* out) {
     pdl_begin();
-    __shared__ float part[32][33];
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + x;
+    __shared__ float part[kSumGroups][kSumColumns + 1];
+    const int x = threadIdx.x % kSumColumns, y = threadIdx.x / kSumColumns;
+    const int c = blockIdx.x * kSumColumns + x;
     float s = 0.0f;
     if (c < width) {
 #pragma unroll 8
-        for (int r = y; r < rows; r += 32) s += partials[(size_t)r * width + c];
+        for (int r = y; r < rows; r += kSumGroups) s += partials[(size_t)r * width + c];
     }
     part[y][x] = s;
     __syncthreads();
-    s = part[x][y];                                    // warp y: column y's 32 sums
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    s = part[lane][w];                                 // warp w: column w's 32 sums
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-    const int cy = blockIdx.x * 32 + y;
-    if (x == 0 && cy < width) st_elem<DTypeOf<DT>::size>(out, cy, f32_to_elem<DT>(s));
+    const int cw = blockIdx.x * kSumColumns + w;
+    if (lane == 0 && cw < width) st_elem<DTypeOf<DT>::size>(out, cw, f32_to_elem<DT>(s));
 }
+static_assert(kSumThreads / 32 == kSumColumns, "one warp per column");
 
 template <int DT, int V, bool GENERAL>
 static cudaError_t bwd_launch(const NormBackwardArgs& a, cudaStream_t s) {
@@ -313,7 +319,7 @@ static cudaError_t bwd_launch_dt(const NormBackwardArgs& a, cudaStream_t s) {
     default: e = g ? bwd_launch<DT, 4, true>(a, s) : bwd_launch<DT, 4, false>(a, s); break;
     }
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((a.width + 31) / 32);
+    const unsigned grid = (unsigned)((a.width + kSumColumns - 1) / kSumColumns);
     if (a.weightF32)
         return pdl_launch(k_sum_columns<kF32>, grid, kSumThreads, 0, s, (const float*)a.partials, a.parts, a.width,
                           a.gradWeight);

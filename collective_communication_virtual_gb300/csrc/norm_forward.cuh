@@ -243,7 +243,8 @@ k_allreduce_rmsnorm_staged(const __grid_constant__ NormArgs a) {
     if (!GENERAL) stage_zeros<DT, V>(stage, segments, rv);
     fetch(first + team);
     stage_weight<DT, GENERAL>(a.weight, a.weightF32, a.hidden, base, sh.weightBytes);
-    __syncthreads();
+    copies_wait();
+    __syncthreads();                                   // the weight, copied by all threads
     int flip = 0;
     // every team of a CTA runs the same number of rounds
     for (size_t row0 = first; row0 < end; row0 += step) {

@@ -95,11 +95,14 @@ __device__ __forceinline__ void add_segment(const StageAddr& s, int seg, unsigne
 }
 
 // The weight in shared memory, in its own type, element j at base + j * size, with zeros behind
-// it up to the end of the team's last vector.
+// it up to the end of the team's last vector.  Starts copies that the caller waits for.
 template <int DT, bool GENERAL>
 __device__ __forceinline__ void stage_weight(const void* w, bool f32, int width, uint32_t smem, int bytes) {
     const int size = f32 ? 4 : DTypeOf<DT>::size, per = 16 / size;
-    for (int i = threadIdx.x; i < bytes / 16; i += blockDim.x) {
+    const bool aligned = !GENERAL || ((uintptr_t)w & 15u) == 0;
+    const int whole = aligned ? width / per : 0;       // blocks that hold nothing else
+    for (int i = threadIdx.x; i < whole; i += blockDim.x) copy_block_async(smem + 16 * i, (const char*)w + (size_t)i * 16);
+    for (int i = whole + (int)threadIdx.x; i < bytes / 16; i += blockDim.x) {
         const int left = width - i * per;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (left > 0) {
@@ -117,6 +120,7 @@ __device__ __forceinline__ void stage_weight(const void* w, bool f32, int width,
         }
         st_smem(smem + 16 * i, v);
     }
+    copies_commit();
 }
 template <int DT>
 __device__ __forceinline__ void staged_weight(uint32_t smem, bool f32, int e, float (&f)[kVecElems<DT>]) {

@@ -55,14 +55,17 @@ NormShape norm_shape(const NormCall& c) {
 
     // Staged: more vectors a thread means fewer instructions and barriers a row, as long as the
     // last warp is not left half empty.  With few rows per SM their latency counts for more
-    // (3 x 1537 x 2731: 22 us with two vectors, 26 with four; 1 x 16000 x 2047: 68 and 64).
+    // (3 x 1537 x 2731: 21 us with two vectors, 24 with four; 1 x 16000 x 2047: 66 and 59).  The
+    // backward pass keeps its sums in registers with two (1 x 16384 x 4096: 95 us, 104 with four),
+    // but rows that fill a warp save more with four (1 x 16000 x 1024: 33 and 29).
     const bool few = c.rows <= (size_t)c.smCount * 16;
     double best = 0;
     for (const int vecs : {4, 2, 1}) {
         const int team = team_threads(nv, vecs);
         // a scale group is found in neighbouring lanes: no team of fewer lanes than it spans
         if (c.groups && vecs > 1 && team * E < kQuantGroup) continue;
-        const double weight = vecs == 4 ? (few ? 0.8 : 1.0) : vecs == 2 ? 0.92 : 0.8;
+        const bool four = !few && (!c.backward || team == 32);
+        const double weight = vecs == 4 ? (four ? 1.0 : 0.8) : vecs == 2 ? 0.92 : 0.8;
         const double use = weight * nv / ((double)team * vecs);
         if (team <= kStageMaxThreads && use > best) {
             best = use;
@@ -78,19 +81,30 @@ NormShape norm_shape(const NormCall& c) {
             s.rowsPerCta = s.threads / s.teamThreads;
             layout();
         }
-        const int most = 224 * 1024, overhead = 2 * 1024;    // of the SM's, and of a CTA's static arrays
-        const int regs = s.vecs == 1 ? 64 : 128;
+        const int most = 228 * 1024, overhead = 1792;        // the SM's; a CTA's own and its static arrays
+        const int regs = s.vecs == 1 ? 64 : s.vecs == 2 && !c.backward ? 104 : 128;    // of a thread, at most
         const size_t groups = (c.rows + s.rowsPerCta - 1) / s.rowsPerCta;
         // About 72 KiB under way per SM: less leaves the memory waiting, more makes it slower
-        // where the CTAs do not keep step.
-        const int aim = (72 * 1024 + s.stageBytes - 1) / s.stageBytes;
+        // where the CTAs do not keep step.  (48 KiB in the backward pass with two vectors a thread.)
+        const int goal = c.backward && s.vecs == 2 ? 48 * 1024 : 72 * 1024;
+        const int aim = (goal + s.stageBytes - 1) / s.stageBytes;
         const int fit = std::max(1, std::min({most / (s.smemBytes + overhead), 65536 / (regs * s.threads), 16}));
-        const size_t wave = (size_t)c.smCount * std::min(aim, fit);
+        // unaligned rows take more instructions than one CTA issues while it waits (8 x 2000 x 4097:
+        // 92 us with one, 67 with two)
+        const int perSm = std::min(c.general ? std::max(2, aim) : aim, fit);
+        const size_t wave = (size_t)c.smCount * perSm;
         s.staged = s.smemBytes + overhead <= most && groups > wave;
         if (c.backward || aim == 1) {
+            // Every SM its share of the one wave: enough shared memory that no more fit, or CTAs
+            // that arrive while another kernel still holds some SMs crowd on the others (two of
+            // 152 CTAs on some SMs: 8 x 4096 x 4096 backward 102 -> 126 us).
             s.ctas = (int)wave;
+            if (s.staged && perSm <= 6) s.smemBytes = std::max(s.smemBytes, 228 * 1024 / (perSm + 1));
         } else {
-            s.rounds = (int)std::max<size_t>(1, std::min<size_t>(4, groups * 2 / ((size_t)c.smCount * 5)));
+            // rounds save prologues; short of CTAs, and with two long rows an SM, two are enough
+            // (4 x 4096 x 5120: 65 us with two, 68 with four; 1 x 16384 x 4096 to 8 bits: 79 and 74)
+            const size_t mostRounds = aim <= 2 && fit >= 2 && !c.general ? 2 : 4;
+            s.rounds = (int)std::max<size_t>(1, std::min(mostRounds, groups * 2 / ((size_t)c.smCount * 5)));
             s.ctas = (int)((groups + s.rounds - 1) / s.rounds);
         }
     }
