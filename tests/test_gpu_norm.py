@@ -23,8 +23,9 @@ SIZES = [(1, 1, 1), (2, 5, 1), (1, 3, 7), (3, 17, 8), (1, 200, 31), (2, 33, 64),
          (1, 9, 129), (2, 40, 255), (1, 65, 512), (5, 11, 1000), (1, 3, 1023), (2, 301, 1024), (1, 2, 1025),
          (8, 1, 4096), (3, 160, 4096), (2, 170, 4097), (1, 1, 5120), (64, 2, 640), (2, 155, 8200), (1, 160, 16384),
          (2, 3, 20480), (1, 160, 20481), (1, 2, 40961), (1, 2, 65535), (2, 3, 65536)]
-# enough rows for CTAs to stride over: parts of a warp, whole warps, long rows
-MANY = [(1, 45000, 64), (2, 9001, 200), (1, 5003, 520), (3, 3001, 1000), (8, 1301, 1024), (1, 2601, 1031), (2, 1400, 4097),
+# enough rows for CTAs to take several: parts of a warp, whole warps, long rows, rows of which
+# one fills an SM's share (aligned and not), rows that are too much to stage
+MANY = [(8, 400, 4096), (8, 401, 4099), (16, 330, 8192), (24, 310, 9001), (1, 45000, 64), (2, 9001, 200), (1, 5003, 520), (3, 3001, 1000), (8, 1301, 1024), (1, 2601, 1031), (2, 1400, 4097),
         (1, 700, 16384)]
 TYPES = [(BF16, BF16), (BF16, F32), (F16, F16), (F32, F32)]
 
@@ -443,6 +444,38 @@ def test_on_another_stream_in_a_group_and_in_a_graph(comms):
     back = R.backward(torch.stack([o.cpu() for o in outs]), stream.cpu(), rstd.cpu(), w, None)
     R.assert_close(dh[0], back["dh"], back["ddh"], BF16, "replayed backward")
     R.assert_close(gw, back["dw"], back["ddw"], BF16, "replayed weight gradient")
+
+
+def test_two_streams_and_plain_launches(monkeypatch):
+    # the same calls on two streams at once, on a communicator without early launches
+    monkeypatch.setenv("VCOMM_PDL", "0")
+    n, rows, hidden = 2, 3000, 1024
+    comm = V.vcommInit(n)
+    try:
+        desc = V.vRmsNormDesc(rows, hidden, BF16, eps=EPS)
+        runs = []
+        for seed in (51, 52):
+            xs, res, w, sends = make(n, rows, hidden, BF16, BF16, seed)
+            outs = [torch.zeros(rows, hidden, dtype=BF16, device=DEV) for _ in range(n)]
+            dh = [torch.zeros(rows, hidden, dtype=BF16, device=DEV) for _ in range(n)]
+            ws = torch.empty(V.vRmsNormBackwardWorkspace(desc, comm), dtype=torch.uint8, device=DEV)
+            runs.append((xs, res, w, sends, place(res), place(w), torch.zeros(rows, hidden, dtype=BF16, device=DEV), outs,
+                         torch.zeros(rows, device=DEV), dh, torch.zeros(hidden, dtype=BF16, device=DEV), ws,
+                         torch.cuda.Stream()))
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for xs, res, w, sends, dres, dw, stream, outs, rstd, dh, gw, ws, side in runs:
+                V.vAllReduceRmsNorm(desc, sends, dres, dw, stream, outs, rstd, comm, stream=side)
+                V.vAllReduceRmsNormBackward(desc, outs, stream, rstd, dw, None, dh, gw, ws, comm, stream=side)
+        torch.cuda.synchronize()
+        for xs, res, w, sends, dres, dw, stream, outs, rstd, dh, gw, ws, side in runs:
+            ref = R.forward(xs, res, w, EPS)
+            R.assert_close(outs[1], ref["y"], ref["dy"], BF16, "output")
+            back = R.backward(torch.stack([o.cpu() for o in outs]), stream.cpu(), rstd.cpu(), w, None)
+            R.assert_close(dh[0], back["dh"], back["ddh"], BF16, "gradient")
+            R.assert_close(gw, back["dw"], back["ddw"], BF16, "weight gradient")
+    finally:
+        V.vcommDestroy(comm)
 
 
 def test_a_chain_without_waits_keeps_stream_order(comms):
