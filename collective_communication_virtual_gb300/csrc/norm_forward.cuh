@@ -8,8 +8,14 @@
 //   2^-64; scale = amax / 448; q_j = e4m3(h_j w_j (rstd 448 / amax))
 //
 // Every input byte is read once and every output byte written once: a thread keeps its part
-// of h and of the weight in registers across the row's reduction.  The maxima are taken of
-// |h w| before rstd is known, so a row needs one reduction, not two.
+// of h in registers across the row's reduction.  The maxima are taken of |h w| before rstd is
+// known, so a row needs one reduction, not two.
+//
+// Bound by memory where rows are many: 8 ranks x 4096 x 4096 bf16 (604 MB) take 96 us, 0.93 of
+// the measured copy rate; 1 x 16384 x 4096 to 8 bits (470 MB) 74 us, 0.93.  Rows off 16 bytes
+// take about twice the instructions and are bound by those (3 x 1537 x 2731 fp16, every rank at
+// its own offset: 21 us, 0.47; 1 x 16000 x 2047 bf16: 59 us, 0.65).  One row over 8 ranks takes
+// 3.7 us, a launch and two trips to memory.
 #pragma once
 
 #include "norm_stage.cuh"
@@ -156,7 +162,8 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, TeamScratch& red, 
     }
 }
 
-// Few rows, or rows too long to stage: every team takes one row and loads it directly.
+// Few rows, or rows too long to stage: every team takes one row and loads it directly, one
+// vector a thread where that reaches, split over a cluster of up to 8 CTAs while SMs are idle.
 template <int DT, int V, bool GENERAL, int Q>
 __global__ void __launch_bounds__(kNormMaxThreads, 1) k_allreduce_rmsnorm(const __grid_constant__ NormArgs a) {
     pdl_begin();
@@ -204,10 +211,10 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) k_allreduce_rmsnorm(const 
 
 // Many rows: the next row's loads under way while one is finished.  A CTA takes sh.rounds rows
 // (of each of its teams) one behind the other: CTAs start in order and stay near one another,
-// which the memory rewards (1 x 16384 x 4096 bf16: 83 us; 97 us where as many CTAs stride over
+// which the memory rewards (1 x 16384 x 4096 bf16: 82 us; 97 us where as many CTAs stride over
 // all rows and drift apart).  Rows so long that one CTA fills an SM's share of the memory are
 // strided over (sh.rounds 0): a new CTA's first row would find nothing else under way
-// (8 x 4096 x 4096: 93 us against 98).
+// (8 x 4096 x 4096: 96 us against 98).
 template <int DT, int V, bool GENERAL, int Q>
 __global__ void __launch_bounds__(kStageMaxThreads, V == 1 ? 2 : 1)
 k_allreduce_rmsnorm_staged(const __grid_constant__ NormArgs a) {

@@ -7,7 +7,7 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstring>
+#include <cstdio>
 #include <memory>
 #include <new>
 #include <vector>
@@ -240,6 +240,15 @@ vc::NormCall norm_call(const Checked& k, const CommView& v, const Buffers& b) {
     return c;
 }
 
+void debug_norm(const CommView& v, const char* what, const Checked& k, const vc::NormShape& s) {
+    if (!v.debug) return;
+    std::fprintf(stderr,
+                 "vcomm INFO %s rows=%zu hidden=%zu dt=%d N=%d vecs=%d team=%d rows/cta=%d cluster=%d general=%d staged=%d "
+                 "rounds=%d smem=%d\n",
+                 what, k.d.rows, k.d.hidden, (int)k.d.datatype, v.nRanks, s.vecs, s.teamThreads, s.rowsPerCta, s.cluster,
+                 s.general, s.staged, s.rounds, s.smemBytes);
+}
+
 vResult_t norm_forward(const vRmsNormDesc_t* desc, const void* const* send, const void* residual, const void* weight,
                        void* residualOut, void* const* recv, float* const* scales, bool quant, float* rstd, vcomm_t c,
                        cudaStream_t stream) {
@@ -294,6 +303,7 @@ vResult_t norm_forward(const vRmsNormDesc_t* desc, const void* const* send, cons
     call.segments = v.nRanks + (residual ? 1 : 0);
     call.groups = a.groups > 0;
     a.shape = vc::norm_shape(call);
+    debug_norm(v, quant ? "AllReduceRmsNormQuant" : "AllReduceRmsNorm", k, a.shape);
     return comm_launch(c, quant ? "allreduce rmsnorm quant" : "allreduce rmsnorm", [&]() {
         return quant ? vc::launch_allreduce_rmsnorm_quant(a, k.d.datatype, stream)
                      : vc::launch_allreduce_rmsnorm(a, k.d.datatype, stream);
@@ -355,6 +365,7 @@ vResult_t norm_backward(const vRmsNormDesc_t* desc, const void* const* send, con
     a.parts = vc::norm_backward_parts(a.rows, a.shape, v.smCount);
     if (!workspace || !at(workspace, 16) || workspaceBytes < (size_t)a.parts * k.d.hidden * sizeof(float))
         return vInvalidArgument;
+    debug_norm(v, "AllReduceRmsNormBackward", k, a.shape);
     return comm_launch(c, "rmsnorm backward", [&]() { return vc::launch_rmsnorm_backward(a, k.d.datatype, stream); });
 }
 
@@ -464,9 +475,14 @@ vResult_t grad_norm(vGradList_t l, bool clip, float maxNorm, float* norm, void* 
         return vc::comm_record(c, [=]() {
             return guarded([&]() { return grad_norm(l, clip, maxNorm, norm, workspace, workspaceBytes, c, stream); });
         });
+    if (v.debug)
+        std::fprintf(stderr, "vcomm INFO %s chunks=%u counted=%u N=%d\n", clip ? "ClipGradNorm" : "GradNorm", l->nChunks,
+                     l->nCounted, v.nRanks);
     vc::GradNormArgs a;
     a.chunks = l->chunks;
     a.nChunks = l->nCounted;
+    const size_t keep = clip ? v.l2Bytes / 2 / (16 * vc::kGradChunkVecs) : 0;
+    a.keepFrom = l->nCounted - (unsigned)std::min<size_t>(keep, l->nCounted);
     a.done = l->done;
     a.partials = (double*)workspace;
     a.norm = norm;
