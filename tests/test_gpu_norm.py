@@ -350,6 +350,43 @@ def test_backward_gives_the_same_bits_again(comms, n, rows, hidden):
         assert torch.equal(dw, got[0][0]) and torch.equal(o, got[0][1])
 
 
+@pytest.mark.parametrize("n,rows,hidden", [(2, 5, 512), (1, 64, 96), (3, 17, 1001)])
+def test_backward_of_few_rows_many_times_and_replayed(comms, n, rows, hidden):
+    # the pass whose last CTA adds up the weight's gradient: more calls than counters, with other
+    # calls between, and replays of a capture between eager calls
+    comm = comms(n)
+    dys, dres, w, sends = make(n, rows, hidden, BF16, F32, 25)
+    hid = torch.randn(rows, hidden, generator=torch.Generator().manual_seed(3)).to(BF16)
+    rstd = (hid.float().square().mean(1) + EPS).rsqrt()
+    desc = V.vRmsNormDesc(rows, hidden, BF16, F32, EPS)
+    ws = torch.empty(V.vRmsNormBackwardWorkspace(desc, comm), dtype=torch.uint8, device=DEV)
+    args = (sends, place(hid), rstd.to(DEV), place(w), place(dres))
+    ref = R.backward(dys, hid, rstd, w, dres)
+    outs = [torch.empty(rows, hidden, dtype=BF16, device=DEV) for _ in range(n)]
+
+    def run(dw):
+        V.vAllReduceRmsNormBackward(desc, *args, outs, dw, ws, comm)
+
+    captured = torch.empty(hidden, device=DEV)
+    run(captured)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(captured)
+    got = []
+    for i in range(150):
+        got.append(torch.full((hidden,), CANARY, device=DEV))
+        run(got[-1])
+        if i % 50 == 0:
+            captured.zero_()
+            graph.replay()
+            got.append(captured.clone())
+    torch.cuda.synchronize()
+    R.assert_close(got[0], ref["dw"], ref["ddw"], F32, "weight gradient")
+    R.assert_close(outs[0], ref["dh"], ref["ddh"], BF16, "gradient")
+    assert all(torch.equal(g, got[0]) for g in got)
+
+
 @pytest.mark.parametrize("n,rows,hidden", [(2, 4, 40), (1, 4, 301), (3, 3, 1024)])
 def test_backward_against_differences_of_the_forward_pass(comms, n, rows, hidden):
     """dL of L = sum(y a) + sum(h b) along a random direction of each input, against the
