@@ -176,8 +176,7 @@ __device__ __forceinline__ void finish_row_backward(const NormBackwardArgs& a, T
         if (sh.teamThreads > 32) __syncthreads();
         else __syncwarp();
         const int columns = min(a.width - col0, sh.teamThreads * V * E);
-        if (live)
-            for (int o = 0; o < a.nOut; o++) copy_out<ESZ>((char*)a.recv[o] + off, buf, columns * ESZ, t, sh.teamThreads);
+        if (live) copy_out_all<ESZ>(a.recv, a.nOut, a.outSame, off, buf, columns * ESZ, t, sh.teamThreads);
         __syncwarp();                                  // a small team's buffer is free again
     } else if (live) {
         for (int o = 0; o < a.nOut; o++) {

@@ -290,6 +290,42 @@ __device__ __forceinline__ void copy_out(char* dst, uint32_t src, int bytes, int
     }
 }
 
+// The same to n >= 2 outputs that all lie at one offset from 16 bytes: each block is cut once
+// (8 x 2000 x 4097: 60 us, 66 one output at a time).
+template <int OSZ>
+__device__ __forceinline__ void copy_out_same(void* const* dst, int n, size_t off, uint32_t src, int bytes, int t, int threads) {
+    const unsigned sh = (16u - (unsigned)(((uintptr_t)dst[0] + off) & 15u)) & 15u;
+    const int blocks = (bytes - (int)sh) >> 4;
+    for (int i = t; i < blocks; i += threads) {
+        uint4 v = ld_smem(src + 16 * i);
+        if (sh != 0) v = shift_bytes(v, ld_smem(src + 16 * i + 16), sh);
+        for (int o = 0; o < n; o++) st_stream((char*)dst[o] + off + sh + (size_t)i * 16, v);
+    }
+    const int head = min((int)sh, bytes), tail = head + max(blocks, 0) * 16;
+    for (int k = t * OSZ; k < head + bytes - tail; k += threads * OSZ) {
+        const int at = k < head ? k : tail + k - head;
+        uint32_t v;
+        if (OSZ == 1) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(src + at) : "memory");
+        else if (OSZ == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(src + at) : "memory");
+        else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(src + at) : "memory");
+        for (int o = 0; o < n; o++) {
+            char* p = (char*)dst[o] + off + at;
+            if (OSZ == 1) *(uint8_t*)p = (uint8_t)v;
+            else if (OSZ == 2) *(uint16_t*)p = (uint16_t)v;
+            else *(uint32_t*)p = v;
+        }
+    }
+}
+template <int OSZ>
+__device__ __forceinline__ void copy_out_all(void* const* dst, int n, bool same, size_t off, uint32_t src, int bytes, int t,
+                                             int threads) {
+    if (same && n > 1) {
+        copy_out_same<OSZ>(dst, n, off, src, bytes, t, threads);
+        return;
+    }
+    for (int o = 0; o < n; o++) copy_out<OSZ>((char*)dst[o] + off, src, bytes, t, threads);
+}
+
 // ---- reductions over a team ---------------------------------------------------------------
 
 __device__ __forceinline__ unsigned cluster_rank() {

@@ -128,9 +128,7 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, TeamScratch& red, 
         }
         if (sh.teamThreads > 32) __syncthreads();
         else __syncwarp();
-        if (at.live)
-            for (int o = 0; o < a.nOut; o++)
-                copy_out<OSZ>((char*)a.recv[o] + off, buf, columns * OSZ, at.t, sh.teamThreads);
+        if (at.live) copy_out_all<OSZ>(a.recv, a.nOut, a.outSame, off, buf, columns * OSZ, at.t, sh.teamThreads);
     } else if (at.live) {
         for (int o = 0; o < a.nOut; o++) {
             char* p = (char*)a.recv[o] + off + (size_t)mine * OSZ;

@@ -196,6 +196,7 @@ vResult_t check_desc(const vRmsNormDesc_t* desc, Checked* k) {
 struct Buffers {
     int nOut = 0;
     bool aligned = true;
+    bool outSame = true;             // the outputs all start at one offset from 16 bytes
 };
 vResult_t check_buffers(const Checked& k, int nRanks, const void* const* send, void* const* recv, int osz,
                         const void** sendOut, void** out, int* index, Buffers* b) {
@@ -213,6 +214,7 @@ vResult_t check_buffers(const Checked& k, int nRanks, const void* const* send, v
         b->aligned = b->aligned && at(recv[r], e * osz);
         if (index) index[b->nOut] = r;
         out[b->nOut++] = recv[r];
+        b->outSame = b->outSame && at((const void*)((uintptr_t)recv[r] ^ (uintptr_t)out[0]), 16);
     }
     return b->nOut ? vSuccess : vInvalidArgument;
 }
@@ -296,6 +298,7 @@ vResult_t norm_forward(const vRmsNormDesc_t* desc, const void* const* send, cons
     a.hidden = (int)k.d.hidden;
     a.nRanks = v.nRanks;
     a.nOut = b.nOut;
+    a.outSame = b.outSame;
     a.weightF32 = k.d.weightType == vFloat32;
     a.groups = k.d.quantGroup ? (int)((k.d.hidden + vc::kQuantGroup - 1) / vc::kQuantGroup) : 0;
     a.eps = k.d.eps;
@@ -357,6 +360,7 @@ vResult_t norm_backward(const vRmsNormDesc_t* desc, const void* const* send, con
     a.width = (int)k.d.hidden;
     a.nRanks = v.nRanks;
     a.nOut = b.nOut;
+    a.outSame = b.outSame;
     a.weightF32 = k.d.weightType == vFloat32;
     vc::NormCall call = norm_call(k, v, b);
     call.segments = v.nRanks + 1 + (gradResidual ? 1 : 0);

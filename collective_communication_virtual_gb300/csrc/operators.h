@@ -91,6 +91,7 @@ struct NormArgs {
     int hidden;
     int nRanks;
     int nOut;
+    int outSame;                     // the outputs all start at one offset from 16 bytes
     int weightF32;                   // the weight is fp32 (else the data's type)
     int groups;                      // 8-bit output: groups of 128 per row, 0: one scale a row
     float eps;
@@ -113,6 +114,7 @@ struct NormBackwardArgs {
     int width;
     int nRanks;
     int nOut;
+    int outSame;
     int weightF32;
     int parts;                           // CTAs (clusters) that stride over the rows
     unsigned int* done;                  // few parts: counter of the CTAs that are done, the last of
