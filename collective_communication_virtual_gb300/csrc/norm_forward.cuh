@@ -11,7 +11,7 @@
 // of h in registers across the row's reduction.  The maxima are taken of |h w| before rstd is
 // known, so a row needs one reduction, not two.
 //
-// Bound by memory where rows are many: 8 ranks x 4096 x 4096 bf16 (604 MB) take 96 us, 0.93 of
+// Bound by memory where rows are many: 8 ranks x 4096 x 4096 bf16 (604 MB) take 93 us, 0.96 of
 // the measured copy rate; 1 x 16384 x 4096 to 8 bits (470 MB) 74 us, 0.93.  Rows off 16 bytes
 // take about twice the instructions and are bound by those (3 x 1537 x 2731 fp16, every rank at
 // its own offset: 21 us, 0.47; 1 x 16000 x 2047 bf16: 59 us, 0.65).  One row over 8 ranks takes
@@ -210,9 +210,10 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) k_allreduce_rmsnorm(const 
 // Many rows: the next row's loads under way while one is finished.  A CTA takes sh.rounds rows
 // (of each of its teams) one behind the other: CTAs start in order and stay near one another,
 // which the memory rewards (1 x 16384 x 4096 bf16: 82 us; 97 us where as many CTAs stride over
-// all rows and drift apart).  Rows so long that one CTA fills an SM's share of the memory are
-// strided over (sh.rounds 0): a new CTA's first row would find nothing else under way
-// (8 x 4096 x 4096: 96 us against 98).
+// all rows and drift apart; 4 x 4096 x 8192: 102 and 114, 8 x 4096 x 4096: 93 and 95).  Only
+// unaligned rows so long that one CTA fills an SM's share of the memory are strided over
+// (sh.rounds 0), as what a CTA does before its first row costs most there (8 x 2000 x 4097: 60 us,
+// 66 in rounds).
 template <int DT, int V, bool GENERAL, int Q>
 __global__ void __launch_bounds__(kStageMaxThreads, V == 1 ? 2 : 1)
 k_allreduce_rmsnorm_staged(const __grid_constant__ NormArgs a) {

@@ -54,11 +54,11 @@ NormShape norm_shape(const NormCall& c) {
     };
 
     // Staged: more vectors a thread means fewer instructions and barriers a row, as long as the
-    // last warp is not left half empty.  With few rows per SM their latency counts for more
-    // (3 x 1537 x 2731: 21 us with two vectors, 24 with four; 1 x 16000 x 2047: 66 and 59).  The
-    // backward pass keeps its sums in registers with two (1 x 16384 x 4096: 95 us, 104 with four),
-    // but rows that fill a warp save more with four (1 x 16000 x 1024: 33 and 29).
-    const bool few = c.rows <= (size_t)c.smCount * 16;
+    // last warp is not left half empty.  With few rows per SM and several inputs a row's latency
+    // counts for more (3 x 1537 x 2731: 21 us with two vectors, 24 with four; but 1 x 1500 x 4096:
+    // 13 and 11).  The backward pass keeps its sums in registers with two (1 x 16384 x 4096: 95 us,
+    // 104 with four), but rows that fill a warp save more with four (1 x 16000 x 1024: 33 and 29).
+    const bool few = c.rows <= (size_t)c.smCount * 16 && c.segments >= 4;
     double best = 0;
     for (const int vecs : {4, 2, 1}) {
         const int team = team_threads(nv, vecs);
@@ -94,17 +94,29 @@ NormShape norm_shape(const NormCall& c) {
         const int perSm = std::min(c.general ? std::max(2, aim) : aim, fit);
         const size_t wave = (size_t)c.smCount * perSm;
         s.staged = s.smemBytes + overhead <= most && groups > wave;
-        if (c.backward || aim == 1) {
+        if (c.backward || (c.general && aim == 1)) {
             // Every SM its share of the one wave: enough shared memory that no more fit, or CTAs
             // that arrive while another kernel still holds some SMs crowd on the others (two of
             // 152 CTAs on some SMs: 8 x 4096 x 4096 backward 102 -> 126 us).
             s.ctas = (int)wave;
             if (s.staged && perSm <= 6) s.smemBytes = std::max(s.smemBytes, 228 * 1024 / (perSm + 1));
         } else {
-            // rounds save prologues; short of CTAs, and with two long rows an SM, two are enough
-            // (4 x 4096 x 5120: 65 us with two, 68 with four; 1 x 16384 x 4096 to 8 bits: 79 and 74)
-            const size_t mostRounds = aim <= 2 && fit >= 2 && !c.general ? 2 : 4;
-            s.rounds = (int)std::max<size_t>(1, std::min(mostRounds, groups * 2 / ((size_t)c.smCount * 5)));
+            // Up to four rows a CTA, or as many as make one wave of few: a wave costs its rows and
+            // a prologue of about 0.6 of one, and a wave that is nearly empty costs as much as a
+            // full one (2 x 1500 x 8192, a wave of 304: 26 us with 3 or 5 rows a CTA, 31 with 4).
+            // With two long rows an SM and many waves, two are enough (4 x 4096 x 5120: 65 us with
+            // two, 68 with four; 1 x 16384 x 4096 to 8 bits, with more an SM: 79 and 74).
+            const size_t resident = (size_t)c.smCount * fit, one = (groups + resident - 1) / resident;
+            const size_t cap = aim <= 2 && fit >= 2 && !c.general ? 2 : 4;
+            double least = 0;
+            for (size_t r = 1; r <= 6; r++) {
+                if (r > cap && r != one) continue;
+                const double cost = (double)(((groups + r - 1) / r + resident - 1) / resident) * ((double)r + 0.6);
+                if (s.rounds == 0 || cost < least) {
+                    least = cost;
+                    s.rounds = (int)r;
+                }
+            }
             s.ctas = (int)((groups + s.rounds - 1) / s.rounds);
         }
     }
