@@ -156,8 +156,7 @@ __device__ __forceinline__ void finish_row_backward(const NormBackwardArgs& a, T
     float sum = (two[0].x + two[0].y) + (two[1].x + two[1].y), none = 0.0f;
     team_reduce<false>(red, sh, sum, none);
     const float c = -(sum / (float)a.width);
-    const int mine = rv.e0 - col0;
-    const size_t off = (row * a.recvStride + col0) * ESZ;
+    const int mine = t * E;                            // the thread's first column of this CTA's
 #pragma unroll
     for (int v = 0; v < V; v++) {
         float f[E];
@@ -176,11 +175,12 @@ __device__ __forceinline__ void finish_row_backward(const NormBackwardArgs& a, T
         if (sh.teamThreads > 32) __syncthreads();
         else __syncwarp();
         const int columns = min(a.width - col0, sh.teamThreads * V * E);
+        const size_t off = (row * a.recvStride + col0) * ESZ;
         if (live) copy_out_all<ESZ>(a.recv, a.nOut, a.outSame, off, buf, columns * ESZ, t, sh.teamThreads);
         __syncwarp();                                  // a small team's buffer is free again
     } else if (live) {
         for (int o = 0; o < a.nOut; o++) {
-            char* p = (char*)a.recv[o] + off + (size_t)mine * ESZ;
+            char* p = (char*)a.recv[o] + (row * a.recvStride + rv.e0) * ESZ;
 #pragma unroll
             for (int v = 0; v < V; v++)
                 if (rv.left[v] > 0) st_stream(p + (size_t)v * rv.step * ESZ, narrow_vec<DT>(g[v]));
@@ -244,7 +244,9 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) k_rmsnorm_backward(const _
     sum_if_last<DT>(a);
 }
 
-// Many rows: CTAs stride over them, the next row's loads under way while one is finished.
+// Many rows: CTAs stride over them, the next row's loads under way while one is finished.  A row
+// that one CTA cannot hold is shared by the two of a cluster (8 x 2000 x 16384 bf16: 232 us, 0.75 of
+// the measured copy rate, 277 with direct loads; 1 x 2000 x 16384 fp32: 121 us, 0.64, and 192).
 template <int DT, int V, bool GENERAL>
 __global__ void __launch_bounds__(kStageMaxThreads, V == 1 ? 2 : 1)
 k_rmsnorm_backward_staged(const __grid_constant__ NormBackwardArgs a) {
@@ -261,7 +263,10 @@ k_rmsnorm_backward_staged(const __grid_constant__ NormBackwardArgs a) {
     dw.init(smem);
     const uint32_t weight = (uint32_t)__cvta_generic_to_shared(smem) + (uint32_t)sh.extraBytes;
     const uint32_t buf = weight + (uint32_t)(sh.weightBytes + sh.stageBytes + team * sh.rowBytes);
-    const RowVecs<DT, V> rv(t * E, sh.teamThreads * E, a.width);
+    const bool clustered = sh.cluster > 1;
+    const int col0 = clustered ? (int)cluster_rank() * sh.teamThreads * V * E : 0;
+    if (clustered) cluster_arrive();
+    const RowVecs<DT, V> rv(col0 + t * E, sh.teamThreads * E, a.width);
     const StageAddr stage = stage_addr<GENERAL>(weight + (uint32_t)sh.weightBytes, sh);
 
     // address of a segment's element rv.e0: the ranks', the stream's, the residual's gradient
@@ -274,11 +279,12 @@ k_rmsnorm_backward_staged(const __grid_constant__ NormBackwardArgs a) {
             for (int s = 0; s < segments; s++) stage_segment<DT, V, GENERAL>(stage, s, segment(s, row), rv);
         copies_commit();
     };
-    const size_t first = (size_t)blockIdx.x * sh.rowsPerCta, stride = (size_t)gridDim.x * sh.rowsPerCta;
+    const unsigned index = clustered ? blockIdx.x / (unsigned)sh.cluster : blockIdx.x;
+    const size_t first = (size_t)index * sh.rowsPerCta, stride = (size_t)sh.ctas * sh.rowsPerCta;
     if (!GENERAL) stage_zeros<DT, V>(stage, segments, rv);
     fetch(first + team);
     float rstd = first + team < a.rows ? a.rstd[first + team] : 0.0f;
-    stage_weight<DT, GENERAL>(a.weight, a.weightF32, a.width, weight, sh.weightBytes);
+    stage_weight<DT, GENERAL>(a.weight, a.weightF32, col0, a.width, weight, sh.weightBytes);
     copies_wait();
     __syncthreads();                                   // the weight, copied by all threads
     int flip = 0;
@@ -303,15 +309,17 @@ k_rmsnorm_backward_staged(const __grid_constant__ NormBackwardArgs a) {
         if (a.gradResidual) staged<V, GENERAL>(stage, N + 1, shRes, res);
         if (GENERAL) __syncwarp();
         fetch(row + stride);
-        finish_row_backward<DT, V, GENERAL>(a, red[flip], row, row < a.rows, rstd, t, 0, buf, rv, dw, g, hid, res,
+        finish_row_backward<DT, V, GENERAL>(a, red[flip], row, row < a.rows, rstd, t, col0, buf, rv, dw, g, hid, res,
                                             [&](int v, float (&f)[E]) {
-                                                staged_weight<DT>(weight, a.weightF32, rv.e0 + v * rv.step, f);
+                                                staged_weight<DT>(weight, a.weightF32, t * E + v * rv.step, f);
                                             });
+        if (clustered) cluster_arrive();
         rstd = rstdNext;
         flip ^= 1;
     }
+    if (clustered) cluster_wait();
     copies_wait();
-    dw.write(smem, sh, a.partials + (size_t)blockIdx.x * a.width, a.width);
+    dw.write(smem, sh, a.partials + (size_t)index * a.width + col0, min(a.width - col0, sh.teamThreads * V * E));
 }
 
 // gradWeight[c] = sum of the partial rows' column c: 16 columns a CTA, the rows dealt to 32
@@ -348,8 +356,9 @@ static cudaError_t bwd_launch(const NormBackwardArgs& a, cudaStream_t s) {
     const cudaError_t e = sh.staged ? allow_smem(k_rmsnorm_backward_staged<DT, V, GENERAL>, sh.smemBytes)
                                     : allow_smem(k_rmsnorm_backward<DT, V, GENERAL>, sh.smemBytes);
     if (e != cudaSuccess) return e;
-    if (sh.staged) return norm_launch(k_rmsnorm_backward_staged<DT, V, GENERAL>, (unsigned)a.parts, sh, sh.smemBytes, s, a);
-    return norm_launch(k_rmsnorm_backward<DT, V, GENERAL>, (unsigned)(a.parts * sh.cluster), sh, sh.smemBytes, s, a);
+    const unsigned grid = (unsigned)(a.parts * sh.cluster);
+    if (sh.staged) return norm_launch(k_rmsnorm_backward_staged<DT, V, GENERAL>, grid, sh, sh.smemBytes, s, a);
+    return norm_launch(k_rmsnorm_backward<DT, V, GENERAL>, grid, sh, sh.smemBytes, s, a);
 }
 template <int DT>
 static cudaError_t bwd_launch_dt(const NormBackwardArgs& a, cudaStream_t s) {

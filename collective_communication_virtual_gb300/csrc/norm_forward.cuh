@@ -12,7 +12,7 @@
 // known, so a row needs one reduction, not two.
 //
 // Bound by memory where rows are many: 8 ranks x 4096 x 4096 bf16 (604 MB) take 93 us, 0.96 of
-// the measured copy rate; 1 x 16384 x 4096 to 8 bits (470 MB) 74 us, 0.93.  Rows off 16 bytes
+// the measured copy rate; 1 x 16384 x 4096 to 8 bits (470 MB) 75 us, 0.93.  Rows off 16 bytes
 // take about twice the instructions and are bound by those (3 x 1537 x 2731 fp16, every rank at
 // its own offset: 21 us, 0.47; 1 x 16000 x 2047 bf16: 59 us, 0.65).  One row over 8 ranks takes
 // 3.7 us, a launch and two trips to memory.
@@ -59,8 +59,7 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, TeamScratch& red, 
     constexpr int ESZ = DTypeOf<DT>::size;
     const NormShape& sh = a.shape;
     const int columns = min(a.hidden - at.col0, sh.teamThreads * V * E);   // of this CTA
-    const size_t resOff = (at.row * a.residualStride + at.col0) * ESZ;
-    const int mine = rv.e0 - at.col0;                  // the thread's first column of them
+    const int mine = at.t * E;                         // the thread's first column of them
     // From here on a thread holds zeros behind the row's end, and only the stores ask for it.
     if (GENERAL) rv.mask(h);
     float2 two[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
@@ -74,7 +73,7 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, TeamScratch& red, 
         if (!a.residualOut) continue;
         if (GENERAL) st_smem(at.buf + (uint32_t)((mine + v * rv.step) * ESZ), narrow_vec<DT>(h[v]));
         else if (at.live && rv.left[v] > 0)
-            st_stream((char*)a.residualOut + resOff + (size_t)(mine + v * rv.step) * ESZ, narrow_vec<DT>(h[v]));
+            st_stream((char*)a.residualOut + (at.row * a.residualStride + rv.e0 + v * rv.step) * ESZ, narrow_vec<DT>(h[v]));
     }
     float sum = (two[0].x + two[0].y) + (two[1].x + two[1].y);
 
@@ -103,7 +102,7 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, TeamScratch& red, 
     const float rstd = __frsqrt_rn(sum / (float)a.hidden + a.eps);
     if (a.rstd && at.live && at.t == 0 && at.part == 0) a.rstd[at.row] = rstd;
     if (GENERAL && a.residualOut && at.live)
-        copy_out<ESZ>((char*)a.residualOut + resOff, at.buf, columns * ESZ, at.t, sh.teamThreads);
+        copy_out<ESZ>((char*)a.residualOut + (at.row * a.residualStride + at.col0) * ESZ, at.buf, columns * ESZ, at.t, sh.teamThreads);
 
     // A row (group) with a NaN has NaN as its scale.
     const auto amax_of = [&](float m) {
@@ -117,8 +116,8 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, TeamScratch& red, 
         scale_by(h[v], Q ? rstd * (kE4m3Max / amax[v]) : rstd);
     }
     constexpr int OSZ = Q ? 1 : ESZ;
-    const size_t off = (at.row * a.recvStride + at.col0) * OSZ;
     if (GENERAL) {
+        const size_t off = (at.row * a.recvStride + at.col0) * OSZ;
         const uint32_t buf = at.buf + (uint32_t)sh.rowBytes;
 #pragma unroll
         for (int v = 0; v < V; v++) {
@@ -131,7 +130,7 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, TeamScratch& red, 
         if (at.live) copy_out_all<OSZ>(a.recv, a.nOut, a.outSame, off, buf, columns * OSZ, at.t, sh.teamThreads);
     } else if (at.live) {
         for (int o = 0; o < a.nOut; o++) {
-            char* p = (char*)a.recv[o] + off + (size_t)mine * OSZ;
+            char* p = (char*)a.recv[o] + (at.row * a.recvStride + rv.e0) * OSZ;
 #pragma unroll
             for (int v = 0; v < V; v++) {
                 if (rv.left[v] == 0) continue;
@@ -214,7 +213,12 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) k_allreduce_rmsnorm(const 
 // unaligned rows so long that one CTA fills an SM's share of the memory are strided over
 // (sh.rounds 0), as what a CTA does before its first row costs most there (8 x 2000 x 4097: 60 us,
 // 66 in rounds).
-template <int DT, int V, bool GENERAL, int Q>
+//
+// SHARED: the CTAs of a cluster share a row that one cannot hold, and finish it together.  An
+// instance of its own, as what it adds costs the others up to 2 % (3 x 1537 x 2731: 21.2 us, 20.9
+// without).  1 x 4096 x 32768 bf16 takes 231 us (0.68 of the measured copy rate; 387 with direct
+// loads), 8 x 1500 x 16384 148 us (0.88; 160): each row waits for two barriers of its cluster.
+template <int DT, int V, bool GENERAL, int Q, bool SHARED>
 __global__ void __launch_bounds__(kStageMaxThreads, V == 1 ? 2 : 1)
 k_allreduce_rmsnorm_staged(const __grid_constant__ NormArgs a) {
     pdl_begin();
@@ -227,14 +231,17 @@ k_allreduce_rmsnorm_staged(const __grid_constant__ NormArgs a) {
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     RowPlace at;
     at.t = sh.rowsPerCta > 1 ? (int)threadIdx.x & (sh.teamThreads - 1) : (int)threadIdx.x;
-    at.part = at.col0 = 0;
+    at.part = SHARED ? (int)cluster_rank() : 0;
+    at.col0 = at.part * sh.teamThreads * V * E;
+    if (SHARED) cluster_arrive();
     at.buf = base + (uint32_t)(sh.weightBytes + sh.stageBytes + 2 * team * sh.rowBytes);
-    const RowVecs<DT, V> rv(at.t * E, sh.teamThreads * E, a.hidden);
+    const RowVecs<DT, V> rv(at.col0 + at.t * E, sh.teamThreads * E, a.hidden);
     const StageAddr stage = stage_addr<GENERAL>(base + (uint32_t)sh.weightBytes, sh);
     const int N = a.nRanks, segments = N + (a.residual ? 1 : 0);
 
-    const size_t first = (size_t)blockIdx.x * max(1, sh.rounds) * sh.rowsPerCta;
-    const size_t step = sh.rounds ? sh.rowsPerCta : (size_t)gridDim.x * sh.rowsPerCta;
+    const unsigned index = SHARED ? blockIdx.x / (unsigned)sh.cluster : blockIdx.x;
+    const size_t first = (size_t)index * max(1, sh.rounds) * sh.rowsPerCta;
+    const size_t step = (size_t)(sh.rounds ? 1 : sh.ctas) * sh.rowsPerCta;
     const size_t end = sh.rounds ? min(a.rows, first + (size_t)sh.rounds * sh.rowsPerCta) : a.rows;
     // address of a segment's element rv.e0: the ranks', then the residual's
     const auto segment = [&](int s, size_t row) {
@@ -248,11 +255,11 @@ k_allreduce_rmsnorm_staged(const __grid_constant__ NormArgs a) {
     };
     if (!GENERAL) stage_zeros<DT, V>(stage, segments, rv);
     fetch(first + team);
-    stage_weight<DT, GENERAL>(a.weight, a.weightF32, a.hidden, base, sh.weightBytes);
+    stage_weight<DT, GENERAL>(a.weight, a.weightF32, at.col0, a.hidden, base, sh.weightBytes);
     copies_wait();
     __syncthreads();                                   // the weight, copied by all threads
     int flip = 0;
-    // every team of a CTA runs the same number of rounds
+    // every team of a CTA, and every CTA of a cluster, runs the same number of rounds
     for (size_t row0 = first; row0 < end; row0 += step) {
         at.row = row0 + team;
         at.live = at.row < end;
@@ -269,22 +276,25 @@ k_allreduce_rmsnorm_staged(const __grid_constant__ NormArgs a) {
         if (GENERAL) __syncwarp();
         fetch(at.row + step);
         finish_row<DT, V, GENERAL, Q>(a, red[flip], at, rv, h, [&](int v, float (&f)[E]) {
-            staged_weight<DT>(base, a.weightF32, rv.e0 + v * rv.step, f);
+            staged_weight<DT>(base, a.weightF32, at.t * E + v * rv.step, f);
         });
+        if (SHARED) cluster_arrive();
         flip ^= 1;
     }
+    if (SHARED) cluster_wait();
     copies_wait();
 }
 
 template <int DT, int V, bool GENERAL, int Q>
 static cudaError_t norm_launch_g(const NormArgs& a, cudaStream_t s) {
     const NormShape& sh = a.shape;
-    const cudaError_t e = sh.staged ? allow_smem(k_allreduce_rmsnorm_staged<DT, V, GENERAL, Q>, sh.smemBytes)
-                                    : allow_smem(k_allreduce_rmsnorm<DT, V, GENERAL, Q>, sh.smemBytes);
+    const auto kernel = !sh.staged       ? k_allreduce_rmsnorm<DT, V, GENERAL, Q>
+                        : sh.cluster > 1 ? k_allreduce_rmsnorm_staged<DT, V, GENERAL, Q, true>
+                                         : k_allreduce_rmsnorm_staged<DT, V, GENERAL, Q, false>;
+    const cudaError_t e = allow_smem(kernel, sh.smemBytes);
     if (e != cudaSuccess) return e;
-    if (sh.staged) return norm_launch(k_allreduce_rmsnorm_staged<DT, V, GENERAL, Q>, (unsigned)sh.ctas, sh, sh.smemBytes, s, a);
-    const size_t ctas = (a.rows + sh.rowsPerCta - 1) / sh.rowsPerCta * (size_t)sh.cluster;
-    return norm_launch(k_allreduce_rmsnorm<DT, V, GENERAL, Q>, (unsigned)ctas, sh, sh.smemBytes, s, a);
+    const size_t teams = sh.staged ? (size_t)sh.ctas : (a.rows + sh.rowsPerCta - 1) / sh.rowsPerCta;
+    return norm_launch(kernel, (unsigned)(teams * (size_t)sh.cluster), sh, sh.smemBytes, s, a);
 }
 template <int DT, int V, int Q>
 static cudaError_t norm_launch_v(const NormArgs& a, cudaStream_t s) {

@@ -94,19 +94,22 @@ __device__ __forceinline__ void add_segment(const StageAddr& s, int seg, unsigne
     }
 }
 
-// The weight in shared memory, in its own type, element j at base + j * size, with zeros behind
-// it up to the end of the team's last vector.  Starts copies that the caller waits for.
+// The CTA's part of the weight, from column col0 on, in shared memory, in its own type, with
+// zeros behind the row's end up to that of the team's last vector.  Starts copies that the caller
+// waits for.
 template <int DT, bool GENERAL>
-__device__ __forceinline__ void stage_weight(const void* w, bool f32, int width, uint32_t smem, int bytes) {
+__device__ __forceinline__ void stage_weight(const void* all, bool f32, int col0, int columns, uint32_t smem, int bytes) {
     const int size = f32 ? 4 : DTypeOf<DT>::size, per = 16 / size;
+    const char* w = (const char*)all + (size_t)col0 * size;
+    const int width = max(0, min(columns - col0, bytes / size));
     const bool aligned = !GENERAL || ((uintptr_t)w & 15u) == 0;
     const int whole = aligned ? width / per : 0;       // blocks that hold nothing else
-    for (int i = threadIdx.x; i < whole; i += blockDim.x) copy_block_async(smem + 16 * i, (const char*)w + (size_t)i * 16);
+    for (int i = threadIdx.x; i < whole; i += blockDim.x) copy_block_async(smem + 16 * i, w + (size_t)i * 16);
     for (int i = whole + (int)threadIdx.x; i < bytes / 16; i += blockDim.x) {
         const int left = width - i * per;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (left > 0) {
-            const char* p = (const char*)w + (size_t)i * 16;
+            const char* p = w + (size_t)i * 16;
             v = f32 ? load_vec<4, GENERAL, false>(p, left) : load_vec<DTypeOf<DT>::size, GENERAL, false>(p, left);
         }
         if (GENERAL && left > 0 && left < per) {       // zeros, not what follows the weight in memory

@@ -59,21 +59,25 @@ NormShape norm_shape(const NormCall& c) {
     // 13 and 11).  The backward pass keeps its sums in registers with two (1 x 16384 x 4096: 95 us,
     // 104 with four), but rows that fill a warp save more with four (1 x 16000 x 1024: 33 and 29).
     const bool few = c.rows <= (size_t)c.smCount * 16 && c.segments >= 4;
-    double best = 0;
-    for (const int vecs : {4, 2, 1}) {
-        const int team = team_threads(nv, vecs);
-        // a scale group is found in neighbouring lanes: no team of fewer lanes than it spans
-        if (c.groups && vecs > 1 && team * E < kQuantGroup) continue;
-        const bool four = !few && (!c.backward || team == 32);
-        const double weight = vecs == 4 ? (four ? 1.0 : 0.8) : vecs == 2 ? 0.92 : 0.8;
-        const double use = weight * nv / ((double)team * vecs);
-        if (team <= kStageMaxThreads && use > best) {
-            best = use;
-            set_team(&s, nv, vecs);
+    const int most = 228 * 1024, overhead = 1792;            // the SM's; a CTA's own and its static arrays
+    const auto stage = [&]() {
+        const int part = (nv + s.cluster - 1) / s.cluster;
+        double best = 0;
+        for (const int vecs : {4, 2, 1}) {
+            const int team = team_threads(part, vecs);
+            // a scale group is found in neighbouring lanes: no team of fewer lanes than it spans
+            if (c.groups && vecs > 1 && team * E < kQuantGroup) continue;
+            // a cluster's CTAs are whole teams of several warps
+            if (team > kStageMaxThreads || (s.cluster > 1 && team <= 32)) continue;
+            const bool four = !few && (!c.backward || team == 32);
+            const double weight = vecs == 4 ? (four ? 1.0 : 0.8) : vecs == 2 ? 0.92 : 0.8;
+            const double use = weight * part / ((double)team * vecs);
+            if (use > best) {
+                best = use;
+                set_team(&s, part, vecs);
+            }
         }
-    }
-    if (best > 0) {
-        s.staged = 1;
+        if (best == 0) return false;
         layout();
         // CTAs of small teams: several rows each, but no more than keep the SM's CTAs several too
         while (s.teamThreads <= 32 && s.threads > 32 && s.threads > s.teamThreads && s.stageBytes > 40 * 1024) {
@@ -81,7 +85,22 @@ NormShape norm_shape(const NormCall& c) {
             s.rowsPerCta = s.threads / s.teamThreads;
             layout();
         }
-        const int most = 228 * 1024, overhead = 1792;        // the SM's; a CTA's own and its static arrays
+        return s.smemBytes + overhead <= most;
+    };
+    // A row too long for one CTA's threads or shared memory is shared by the CTAs of a cluster: of
+    // eight in the forward pass, which leaves an SM several (8 x 1500 x 16384: 147 us, 162 of four,
+    // 170 of two, 189 with direct loads); of two where the rows are strided over, as larger
+    // clusters do not fill all SMs at once (backward, 1 x 2000 x 16384 fp32: 120 us, 300 of four,
+    // 192 with direct loads).  Rows that direct loads hold with two vectors a thread are no faster
+    // that way (32 x 2000 x 4096: 171 us, 195 of eight; backward, 16 x 2000 x 8192: 214, 226 of
+    // two), unless they are unaligned (backward, 16 x 2000 x 9001: 299 us, 464 with direct loads).
+    s.staged = 1;
+    bool fits = stage();
+    if (!fits && (c.general || nv > kNormMaxThreads * 2)) {
+        s.cluster = c.backward || c.general ? 2 : kNormMaxCluster;
+        fits = stage();
+    }
+    if (fits) {
         const int regs = s.vecs == 1 ? 64 : s.vecs == 2 && !c.backward ? 104 : 128;    // of a thread, at most
         const size_t groups = (c.rows + s.rowsPerCta - 1) / s.rowsPerCta;
         // About 72 KiB under way per SM: less leaves the memory waiting, more makes it slower
@@ -92,8 +111,9 @@ NormShape norm_shape(const NormCall& c) {
         // unaligned rows take more instructions than one CTA issues while it waits (8 x 2000 x 4097:
         // 92 us with one, 67 with two)
         const int perSm = std::min(c.general ? std::max(2, aim) : aim, fit);
-        const size_t wave = (size_t)c.smCount * perSm;
-        s.staged = s.smemBytes + overhead <= most && groups > wave;
+        const size_t wave = std::max<size_t>(1, (size_t)c.smCount * perSm / s.cluster);
+        // few rows shared by eight CTAs: direct loads (8 x 150 x 16384: 17.5 us, staged 20)
+        s.staged = groups > wave && (s.cluster <= 2 || c.rows > (size_t)c.smCount);
         if (c.backward || (c.general && aim == 1)) {
             // Every SM its share of the one wave: enough shared memory that no more fit, or CTAs
             // that arrive while another kernel still holds some SMs crowd on the others (two of
@@ -101,16 +121,17 @@ NormShape norm_shape(const NormCall& c) {
             s.ctas = (int)wave;
             if (s.staged && perSm <= 6) s.smemBytes = std::max(s.smemBytes, 228 * 1024 / (perSm + 1));
         } else {
-            // Up to four rows a CTA, or as many as make one wave of few: a wave costs its rows and
-            // a prologue of about 0.6 of one, and a wave that is nearly empty costs as much as a
-            // full one (2 x 1500 x 8192, a wave of 304: 26 us with 3 or 5 rows a CTA, 31 with 4).
+            // Up to four rows a CTA (cluster), or as many as make one wave of CTAs: a wave costs its
+            // rows and a prologue of about 0.6 of one, and a wave that is nearly empty costs as much
+            // as a full one (2 x 1500 x 8192, a wave of 304: 26 us with 3 or 5 rows a CTA, 31 with 4).
             // With two long rows an SM and many waves, two are enough (4 x 4096 x 5120: 65 us with
             // two, 68 with four; 1 x 16384 x 4096 to 8 bits, with more an SM: 79 and 74).
-            const size_t resident = (size_t)c.smCount * fit, one = (groups + resident - 1) / resident;
+            const size_t resident = std::max<size_t>(1, (size_t)c.smCount * fit / s.cluster);
+            const size_t one = (groups + resident - 1) / resident;
             const size_t cap = aim <= 2 && fit >= 2 && !c.general ? 2 : 4;
             double least = 0;
             for (size_t r = 1; r <= 6; r++) {
-                if (r > cap && r != one) continue;
+                if (r > cap && (r != one || s.cluster > 1)) continue;
                 const double cost = (double)(((groups + r - 1) / r + resident - 1) / resident) * ((double)r + 0.6);
                 if (s.rounds == 0 || cost < least) {
                     least = cost;
@@ -120,8 +141,10 @@ NormShape norm_shape(const NormCall& c) {
             s.ctas = (int)((groups + s.rounds - 1) / s.rounds);
         }
     }
-    if (!s.staged) {
-        if (nv <= 32) {              // few rows: one vector a thread, as the latency counts
+    if (!fits || !s.staged) {        // few rows, or a row that not even a cluster can stage
+        s.staged = 0;
+        s.cluster = 1;
+        if (nv <= 32) {              // one vector a thread, as the latency counts
             set_team(&s, nv, 1);
         } else {
             // rows longer than a CTA's registers hold
@@ -131,7 +154,13 @@ NormShape norm_shape(const NormCall& c) {
                    nv / (s.cluster * 2) >= 64)
                 s.cluster *= 2;
             const int per = (nv + s.cluster - 1) / s.cluster;
-            s.vecs = per <= 512 ? 1 : per <= 1024 ? 2 : 4;
+            // One vector a thread where that makes one wave of CTAs at 72 registers a thread
+            // (1 x 150 x 4096: 2.6 us, 3.1 with two), else two (1 x 300 x 4096: 3.1 us, 4.5 with one;
+            // 32 x 2000 x 4096: 171 and 185).
+            const int warps = (per + 31) / 32;
+            const size_t wave = (size_t)c.smCount * std::max(1, 65536 / (72 * 32 * warps));
+            const bool one = per <= kNormMaxThreads && (c.backward || c.rows * (size_t)s.cluster <= wave);
+            s.vecs = one ? 1 : per <= kNormMaxThreads * 2 ? 2 : 4;
             s.teamThreads = ((per + s.vecs - 1) / s.vecs + 31) / 32 * 32;
             s.threads = s.teamThreads;
             s.rowsPerCta = 1;

@@ -46,7 +46,7 @@ struct NormShape {
     int staged;                      // many rows: a CTA stages the next row while it finishes one
     int rounds;                      // staged, forward: rows that each team of a CTA takes; 0: the CTAs
                                      // stride over all rows, as in the backward pass
-    int ctas;                        // staged: the grid
+    int ctas;                        // staged: CTAs (clusters) of the grid
     int weightBytes;                 // dynamic shared memory: of the staged weight,
     int stageBytes;                  // of the staged row of every team,
     int rowBytes;                    // of a row buffer (GENERAL: two a team, the backward pass one),

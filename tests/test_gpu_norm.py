@@ -592,3 +592,29 @@ def test_refusals(comms):
     V.vcommGroupStart(comm)
     V.vAllReduceRmsNorm(d, sends, None, None, None, recvs, None, comm)
     refused(lambda: V.vcommGroupEnd(comm))
+
+
+# rows too long for one CTA to stage, and enough of them that each cluster takes several
+LONG = [(1, 400, 32776), (8, 330, 16384), (3, 290, 24001), (2, 230, 65536), (16, 170, 12296), (64, 90, 4096), (40, 161, 2100)]
+
+
+@pytest.mark.parametrize("dtype,wtype", TYPES)
+@pytest.mark.parametrize("kw", [dict(), dict(send_pad=1, recv_offset=3, offset=5, weight_offset=1)])
+@pytest.mark.parametrize("n,rows,hidden", LONG)
+def test_long_rows_forward(comms, n, rows, hidden, dtype, wtype, kw):
+    run_forward(comms(n), n, rows, hidden, dtype, wtype, seed=hidden + n, **kw)
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("dtype,wtype", TYPES)
+@pytest.mark.parametrize("kw", [dict(), dict(send_pad=1, recv_offset=3, offset=5)])
+@pytest.mark.parametrize("n,rows,hidden", LONG)
+def test_long_rows_quantised(comms, n, rows, hidden, dtype, wtype, group, kw):
+    run_quant(comms(n), n, rows, hidden, dtype, wtype, group, seed=hidden, **kw)
+
+
+@pytest.mark.parametrize("dtype,wtype", TYPES)
+@pytest.mark.parametrize("kw", [dict(), dict(send_pad=1, recv_offset=3, offset=5, weight_offset=1)])
+@pytest.mark.parametrize("n,rows,hidden", LONG)
+def test_long_rows_backward(comms, n, rows, hidden, dtype, wtype, kw):
+    run_backward(comms(n), n, rows, hidden, dtype, wtype, seed=hidden + n, **kw)
