@@ -518,17 +518,20 @@ def vTensorList(grads, outs=None, replicated=None) -> TensorList:
     first = grads[0]
     if replicated is not None and len(replicated) != len(first):
         raise VcommError(vInvalidArgument, f"replicated names {len(replicated)} tensors of {len(first)}")
+    counts, dtypes = [t.numel() for t in first], [t.dtype for t in first]
+    addresses = []
     for side in (grads,) if outs is None else (grads, outs):
         if len(side) != len(grads):
             raise VcommError(vInvalidArgument, f"outputs of {len(side)} ranks for gradients of {len(grads)}")
         for tensors in side:
-            if [(t.numel(), t.dtype) for t in tensors] != [(t.numel(), t.dtype) for t in first]:
+            if [t.numel() for t in tensors] != counts or [t.dtype for t in tensors] != dtypes:
                 raise VcommError(vInvalidArgument, "every rank's tensors have the same sizes and types")
-            if not all(t.is_contiguous() for t in tensors):
+            if not all([t.is_contiguous() for t in tensors]):
                 raise VcommError(vInvalidArgument, "tensors of a list are contiguous")
-    return TensorList(len(grads), [t.numel() for t in first], [_dtype_code(t.dtype) for t in first], replicated,
-                      [t.data_ptr() for tensors in grads for t in tensors],
-                      None if outs is None else [t.data_ptr() for tensors in outs for t in tensors])
+        addresses.append([t.data_ptr() for tensors in side for t in tensors])
+    codes = {d: _dtype_code(d) for d in set(dtypes)}
+    return TensorList(len(grads), counts, [codes[d] for d in dtypes], replicated, addresses[0],
+                      None if outs is None else addresses[1])
 
 
 def _list(tensors: TensorList, comm) -> int | None:
