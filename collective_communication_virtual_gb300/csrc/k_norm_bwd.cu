@@ -9,8 +9,7 @@
 //
 // dh needs one sum along the row, dw one down the columns.  A CTA (or cluster) strides over
 // the rows and keeps its dw, in fp32; each writes its sums as one row of the workspace, and a
-// second launch, or the last CTA where those rows are few, adds them up.  The order of the
-// additions follows from the shapes alone.
+// second launch adds them up.  The order of the additions follows from the shapes alone.
 //
 // Bound by memory: 8 ranks x 4096 x 4096 bf16 (604 MB) take 102 us, 0.87 of the measured copy
 // rate (100 us without the second launch); 1 x 8192 x 2048 fp32 (268 MB) 49 us, 0.81 (45 us).
@@ -81,45 +80,6 @@ struct WeightSums {
         }
     }
 };
-
-// The CTA that ends last adds the parts up, in their order, if there are few of them.
-template <int DT>
-__device__ __forceinline__ void sum_if_last(const NormBackwardArgs& a) {
-    if (!a.done) return;
-    __shared__ bool last;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(a.done, 1u) == gridDim.x - 1;
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    const auto store = [&](int c, float s) {
-        if (a.weightF32) ((float*)a.gradWeight)[c] = s;
-        else st_elem<DTypeOf<DT>::size>(a.gradWeight, c, f32_to_elem<DT>(s));
-    };
-    if (a.width % 4 == 0) {
-        for (int c = threadIdx.x * 4; c < a.width; c += blockDim.x * 4) {
-            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-            for (int p = 0; p < a.parts; p++) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(a.partials + (size_t)p * a.width + c));
-                s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
-            }
-            store(c, s.x);
-            store(c + 1, s.y);
-            store(c + 2, s.z);
-            store(c + 3, s.w);
-        }
-    } else {
-        for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
-            float s = 0.0f;
-#pragma unroll 16
-            for (int p = 0; p < a.parts; p++) s += __ldcg(a.partials + (size_t)p * a.width + c);
-            store(c, s);
-        }
-    }
-    if (threadIdx.x == 0) *a.done = 0u;
-}
 
 // A row once a thread has its part: g holds dy on entry, hid the row that was normed, res the
 // residual's gradient (zeros where there is none).  weight(v, f): zeros behind the row's end.
@@ -241,7 +201,6 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) k_rmsnorm_backward(const _
     }
     if (clustered) cluster_wait();
     dw.write(smem, sh, a.partials + index * a.width + col0, min(a.width - col0, sh.teamThreads * V * E));
-    sum_if_last<DT>(a);
 }
 
 // Many rows: CTAs stride over them, the next row's loads under way while one is finished.  A row
@@ -369,7 +328,7 @@ static cudaError_t bwd_launch_dt(const NormBackwardArgs& a, cudaStream_t s) {
     case 2: e = g ? bwd_launch<DT, 2, true>(a, s) : bwd_launch<DT, 2, false>(a, s); break;
     default: e = g ? bwd_launch<DT, 4, true>(a, s) : bwd_launch<DT, 4, false>(a, s); break;
     }
-    if (e != cudaSuccess || a.done) return e;
+    if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((a.width + kSumColumns - 1) / kSumColumns);
     if (a.weightF32)
         return pdl_launch(k_sum_columns<kF32>, grid, kSumThreads, 0, s, (const float*)a.partials, a.parts, a.width,

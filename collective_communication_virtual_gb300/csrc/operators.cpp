@@ -410,8 +410,6 @@ vResult_t norm_backward(const vRmsNormDesc_t* desc, const void* const* send, con
     a.parts = vc::norm_backward_parts(a.rows, a.shape, v.smCount);
     if (!workspace || !at(workspace, 16) || workspaceBytes < (size_t)a.parts * k.d.hidden * sizeof(float))
         return vInvalidArgument;
-    a.done = !a.shape.staged && vc::norm_backward_fused(a.parts, a.width, a.shape.threads) ? vc::comm_counter(c, stream)
-                                                                                           : nullptr;
     debug_norm(v, "AllReduceRmsNormBackward", k, a.shape);
     return comm_launch(c, "rmsnorm backward", [&]() { return vc::launch_rmsnorm_backward(a, k.d.datatype, stream); });
 }

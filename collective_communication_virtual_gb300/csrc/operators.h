@@ -23,9 +23,6 @@ struct CommView {
 vResult_t comm_view(vcomm_t c, CommView* v);
 // Record a call of an open group; vcommGroupEnd runs it.
 vResult_t comm_record(vcomm_t c, std::function<vResult_t()> call);
-// A counter of the communicator's, zero; the kernel that takes it leaves it zero (see
-// kTileCounterSlots for which calls may share one).
-unsigned int* comm_counter(vcomm_t c, cudaStream_t stream);
 // Run `launch` with the communicator's device and launch mode, and take note of its error.
 vResult_t comm_launch(vcomm_t c, const char* what, const std::function<cudaError_t()>& launch);
 
@@ -117,17 +114,10 @@ struct NormBackwardArgs {
     int outSame;
     int weightF32;
     int parts;                           // CTAs (clusters) that stride over the rows
-    unsigned int* done;                  // few parts: counter of the CTAs that are done, the last of
-                                         // which adds the parts up; NULL: a second launch does
     NormShape shape;
 };
 // CTAs (clusters) of the backward pass: its workspace holds one row of fp32 sums for each.
 int norm_backward_parts(size_t rows, const NormShape& sh, int smCount);
-// Whether the last CTA of the pass may add the parts up: at most 48 loads a thread, which take
-// it less than a second launch (2 us on the device, 2.5 us of host time).
-constexpr bool norm_backward_fused(int parts, int width, int threads) {
-    return (long long)parts * ((width + (width % 4 == 0 ? 4 : 1) * threads - 1) / ((width % 4 == 0 ? 4 : 1) * threads)) <= 48;
-}
 cudaError_t launch_rmsnorm_backward(const NormBackwardArgs& a, vDataType_t dt, cudaStream_t s);
 
 // ---- gradient norm and clipping ----------------------------------------------------------

@@ -99,7 +99,6 @@ struct vcomm {
     unsigned int* tileCounters;      // variable all-to-all tile counters (device)
     unsigned int tileCounterSeq;     // eager calls: next pair of the rotating set
     unsigned int capturedCounterSeq; // captured calls: next pair of the captured set
-    bool untracked;                  // launches that use a counter without an event of their own
     unsigned long long endMagic;
 };
 
@@ -257,15 +256,6 @@ bool stream_capturing(cudaStream_t stream) {
         return false;
     }
     return cs != cudaStreamCaptureStatusNone;
-}
-
-// The next pair of zeroed counters.  A captured launch replays with the pair it was captured
-// with: it takes one of the captured set, which eager launches never rotate into.
-unsigned int* next_counter_pair(vcomm* c, cudaStream_t stream) {
-    const size_t pair = stream_capturing(stream)
-                            ? vc::kTileCounterSlots + (size_t)(c->capturedCounterSeq++ % vc::kCapturedCounterSlots)
-                            : (size_t)(c->tileCounterSeq++ % vc::kTileCounterSlots);
-    return c->tileCounters + 2 * pair;
 }
 
 // Record, on `stream`, the point after the launch just enqueued (one event per stream).
@@ -567,11 +557,6 @@ vResult_t comm_record(vcomm_t c, std::function<vResult_t()> call) {
     return vSuccess;
 }
 
-unsigned int* comm_counter(vcomm_t c, cudaStream_t stream) {
-    c->untracked = true;             // an event per launch would cost what the counter saves
-    return next_counter_pair(c, stream);
-}
-
 vResult_t comm_launch(vcomm_t c, const char* what, const std::function<cudaError_t()>& launch) {
     DeviceGuard g(c);
     if (!g.ok) return vUnhandledCudaError;
@@ -660,7 +645,6 @@ vResult_t vcommDestroy(vcomm_t c) {
     if (!comm_ok(c)) return vInvalidArgument;
     DeviceGuard g(c);
     wait_tracked(c);
-    if (c->untracked && cudaDeviceSynchronize() != cudaSuccess) cudaGetLastError();
     free_comm(c);
     return vSuccess;
 }
@@ -1114,7 +1098,12 @@ vResult_t vAllToAllv(const void* const* send, void* const* recv, const int32_t* 
     a.nRanks = c->nRanks;
     a.elemSize = (int)esz;
     a.tileBytes = 64 * 1024;
-    a.tileCounter = next_counter_pair(c, stream);
+    // A captured launch replays with the pair it was captured with: it takes one of the
+    // captured set, which eager launches never rotate into.
+    const size_t pair = stream_capturing(stream)
+                            ? vc::kTileCounterSlots + (size_t)(c->capturedCounterSeq++ % vc::kCapturedCounterSlots)
+                            : (size_t)(c->tileCounterSeq++ % vc::kTileCounterSlots);
+    a.tileCounter = c->tileCounters + 2 * pair;
     a.status = c->statusDev;
     a.statusHost = c->statusHostDev;
     return finish_launch(c, vc::launch_alltoallv(a, p.gridCtas, p.threadsPerCta, stream), stream, "alltoallv",

@@ -141,8 +141,7 @@ typedef enum {
 vResult_t vcommInit(vcomm_t* comm, int nRanks, int nChannels, vProto_t protocol);
 
 /* Wait for the last enqueued work that uses the communicator's device memory (staged
- * ring transfers, variable all-to-all, bulk-copy fan-out; once vAllReduceRmsNormBackward has
- * run on it, for the whole device), then free everything it owns.
+ * ring transfers, variable all-to-all, bulk-copy fan-out), then free everything it owns.
  * The other collectives touch only the caller's buffers and need not have finished.
  * A NULL or already destroyed communicator gives vInvalidArgument. */
 vResult_t vcommDestroy(vcomm_t comm);
@@ -372,8 +371,7 @@ vResult_t vAllReduceRmsNormQuant(const vRmsNormDesc_t* desc, const void* const* 
  * with equal strides.  The workspace is at least the number of bytes that
  * vRmsNormBackwardWorkspace gives for the descriptor, 16-byte aligned, and used by nothing
  * else until the call's work is done; a smaller one gives vInvalidArgument.  The same call
- * gives the same bits.  Calls of few rows take a counter of the communicator's: how many may
- * be in flight together is as for vAllToAllv. */
+ * gives the same bits. */
 vResult_t vRmsNormBackwardWorkspace(const vRmsNormDesc_t* desc, vcomm_t comm, size_t* bytes);
 vResult_t vAllReduceRmsNormBackward(const vRmsNormDesc_t* desc, const void* const* sendbuffs,
                                     const void* hiddenStates, const float* rstd, const void* weight,
