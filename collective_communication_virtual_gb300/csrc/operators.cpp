@@ -8,8 +8,9 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
-#include <memory>
+#include <mutex>
 #include <new>
+#include <unordered_map>
 #include <vector>
 
 #include "operators.h"
@@ -416,8 +417,6 @@ vResult_t norm_backward(const vRmsNormDesc_t* desc, const void* const* send, con
 
 // ---- gradient norm and clipping ----------------------------------------------------------
 
-constexpr unsigned long long kListMagic = 0x766C697374763031ull;   // "vlistv01"
-
 size_t grad_partials(unsigned int chunks, int smCount) {
     return std::max<size_t>(1, std::min<size_t>(chunks, (size_t)smCount * vc::kSquaresCtasPerSm));
 }
@@ -438,10 +437,7 @@ void add_chunks(std::vector<vc::GradChunk>* v, const void* in, void* out, size_t
     }
 }
 
-}  // namespace
-
-struct vgradlist {
-    unsigned long long magic;
+struct GradList {
     int nRanks;
     int device;
     vc::GradChunk* chunks;           // device: the counted ones, then the rest
@@ -449,7 +445,17 @@ struct vgradlist {
     unsigned int nCounted, nChunks;
 };
 
-namespace {
+// The lists that exist.  A handle is a list's number, given once and never an address, so that
+// the handle of a destroyed list is known for one without looking at freed memory.
+struct GradLists {
+    std::mutex lock;
+    std::unordered_map<uintptr_t, GradList> live;
+    uintptr_t last = 0;
+};
+GradLists& grad_lists() {
+    static GradLists* lists = new GradLists;           // outlives the caller's own statics
+    return *lists;
+}
 
 vResult_t list_create(vGradList_t* list, int nRanks, int nTensors, const size_t* counts, const vDataType_t* datatypes,
                       const unsigned char* replicated, const void* const* grads, void* const* outs) {
@@ -477,13 +483,17 @@ vResult_t list_create(vGradList_t* list, int nRanks, int nTensors, const size_t*
             add_chunks(r > 0 && replicated && replicated[t] ? &rest : &counted, grads[i],
                        outs ? outs[i] : const_cast<void*>(grads[i]), counts[t], datatypes[t]);
         }
-    std::unique_ptr<vgradlist> l(new vgradlist());
-    l->nRanks = nRanks;
-    l->nCounted = (unsigned)counted.size();
+    GradList l = {};
+    l.nRanks = nRanks;
+    l.nCounted = (unsigned)counted.size();
     counted.insert(counted.end(), rest.begin(), rest.end());
-    l->nChunks = (unsigned)counted.size();
-    cudaError_t e = cudaGetDevice(&l->device);
-    void* mem = nullptr;
+    l.nChunks = (unsigned)counted.size();
+    cudaError_t e = cudaGetDevice(&l.device);
+    struct Memory {
+        void* p = nullptr;
+        ~Memory() { if (p) cudaFree(p); }
+    } own;
+    void*& mem = own.p;
     const size_t bytes = counted.size() * sizeof(vc::GradChunk);
     if (e == cudaSuccess) e = cudaMalloc(&mem, bytes + 32);
     if (e == cudaSuccess && bytes) e = cudaMemcpy(mem, counted.data(), bytes, cudaMemcpyHostToDevice);
@@ -491,51 +501,77 @@ vResult_t list_create(vGradList_t* list, int nRanks, int nTensors, const size_t*
     if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
     if (e != cudaSuccess) {
         cudaGetLastError();
-        if (mem) cudaFree(mem);
         return vUnhandledCudaError;
     }
-    l->chunks = (vc::GradChunk*)mem;
-    l->done = (unsigned int*)((char*)mem + bytes);
-    l->magic = kListMagic;
-    *list = l.release();
+    l.chunks = (vc::GradChunk*)mem;
+    l.done = (unsigned int*)((char*)mem + bytes);
+    GradLists& all = grad_lists();
+    std::lock_guard<std::mutex> hold(all.lock);
+    all.live.emplace(all.last + 1, l);
+    mem = nullptr;
+    *list = (vGradList_t)++all.last;
     return vSuccess;
 }
 
-vResult_t check_list(vGradList_t l, const CommView& v) {
-    if (!l || l->magic != kListMagic || l->nRanks != v.nRanks || l->device != v.device) return vInvalidArgument;
+vResult_t find_list(vGradList_t handle, const CommView& v, GradList* l) {
+    GradLists& all = grad_lists();
+    std::lock_guard<std::mutex> hold(all.lock);
+    const auto i = all.live.find((uintptr_t)handle);
+    if (i == all.live.end() || i->second.nRanks != v.nRanks || i->second.device != v.device) return vInvalidArgument;
+    *l = i->second;
     return vSuccess;
 }
 
-vResult_t grad_norm(vGradList_t l, bool clip, float maxNorm, float* norm, void* workspace, size_t workspaceBytes,
+vResult_t list_destroy(vGradList_t handle) {
+    GradList l;
+    {
+        GradLists& all = grad_lists();
+        std::lock_guard<std::mutex> hold(all.lock);
+        const auto i = all.live.find((uintptr_t)handle);
+        if (i == all.live.end()) return vInvalidArgument;
+        l = i->second;
+        all.live.erase(i);
+    }
+    int prev = -1;
+    const bool other = cudaGetDevice(&prev) == cudaSuccess && prev != l.device;
+    if (other) cudaSetDevice(l.device);
+    const cudaError_t e = cudaFree(l.chunks);          // waits for the work that uses it
+    if (other) cudaSetDevice(prev);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e == cudaSuccess ? vSuccess : vUnhandledCudaError;
+}
+
+vResult_t grad_norm(vGradList_t handle, bool clip, float maxNorm, float* norm, void* workspace, size_t workspaceBytes,
                     vcomm_t c, cudaStream_t stream) {
     CommView v;
     vResult_t r = comm_view(c, &v);
     if (r != vSuccess) return r;
-    if ((r = check_list(l, v)) != vSuccess) return r;
+    GradList l;
+    if ((r = find_list(handle, v, &l)) != vSuccess) return r;
     if (!norm || !at(norm, 4)) return vInvalidArgument;
     if (clip && !(maxNorm >= 0.0f)) return vInvalidArgument;
-    const size_t parts = grad_partials(l->nCounted, v.smCount);
+    const size_t parts = grad_partials(l.nCounted, v.smCount);
     if (!workspace || !at(workspace, 16) || workspaceBytes < parts * sizeof(double)) return vInvalidArgument;
     if (v.grouping)
         return vc::comm_record(c, [=]() {
-            return guarded([&]() { return grad_norm(l, clip, maxNorm, norm, workspace, workspaceBytes, c, stream); });
+            return guarded([&]() { return grad_norm(handle, clip, maxNorm, norm, workspace, workspaceBytes, c, stream); });
         });
     if (v.debug)
-        std::fprintf(stderr, "vcomm INFO %s chunks=%u counted=%u N=%d\n", clip ? "ClipGradNorm" : "GradNorm", l->nChunks,
-                     l->nCounted, v.nRanks);
+        std::fprintf(stderr, "vcomm INFO %s chunks=%u counted=%u N=%d\n", clip ? "ClipGradNorm" : "GradNorm", l.nChunks,
+                     l.nCounted, v.nRanks);
     vc::GradNormArgs a;
-    a.chunks = l->chunks;
-    a.nChunks = l->nCounted;
+    a.chunks = l.chunks;
+    a.nChunks = l.nCounted;
     const size_t keep = clip ? v.l2Bytes / 2 / (16 * vc::kGradChunkVecs) : 0;
-    a.keepFrom = l->nCounted - (unsigned)std::min<size_t>(keep, l->nCounted);
-    a.done = l->done;
+    a.keepFrom = l.nCounted - (unsigned)std::min<size_t>(keep, l.nCounted);
+    a.done = l.done;
     a.partials = (double*)workspace;
     a.norm = norm;
     r = comm_launch(c, "gradient norm", [&]() { return vc::launch_grad_norm(a, (int)parts, stream); });
-    if (r != vSuccess || !clip || l->nChunks == 0) return r;
+    if (r != vSuccess || !clip || l.nChunks == 0) return r;
     vc::GradClipArgs k;
-    k.chunks = l->chunks;
-    k.nChunks = l->nChunks;
+    k.chunks = l.chunks;
+    k.nChunks = l.nChunks;
     k.norm = norm;
     k.maxNorm = maxNorm;
     return comm_launch(c, "gradient clip", [&]() { return vc::launch_grad_clip(k, stream); });
@@ -603,27 +639,22 @@ vResult_t vGradListCreate(vGradList_t* list, int nRanks, int nTensors, const siz
     return guarded([&]() { return list_create(list, nRanks, nTensors, counts, datatypes, replicated, grads, outs); });
 }
 
-vResult_t vGradListDestroy(vGradList_t l) {
-    if (!l || l->magic != kListMagic) return vInvalidArgument;
-    int prev = -1;
-    const bool other = cudaGetDevice(&prev) == cudaSuccess && prev != l->device;
-    if (other) cudaSetDevice(l->device);
-    const cudaError_t e = cudaFree(l->chunks);         // waits for the work that uses it
-    if (other) cudaSetDevice(prev);
-    l->magic = 0;
-    delete l;
-    if (e != cudaSuccess) cudaGetLastError();
-    return e == cudaSuccess ? vSuccess : vUnhandledCudaError;
+vResult_t vGradListDestroy(vGradList_t list) {
+    return guarded([&]() { return list_destroy(list); });
 }
 
 vResult_t vGradNormWorkspace(vGradList_t list, vcomm_t comm, size_t* bytes) {
     CommView v;
     vResult_t r = comm_view(comm, &v);
     if (r != vSuccess) return r;
-    if ((r = check_list(list, v)) != vSuccess) return r;
-    if (!bytes) return vInvalidArgument;
-    *bytes = std::max<size_t>(16, grad_partials(list->nCounted, v.smCount) * sizeof(double));
-    return vSuccess;
+    return guarded([&]() {
+        GradList l;
+        const vResult_t f = find_list(list, v, &l);
+        if (f != vSuccess) return f;
+        if (!bytes) return vInvalidArgument;
+        *bytes = std::max<size_t>(16, grad_partials(l.nCounted, v.smCount) * sizeof(double));
+        return vSuccess;
+    });
 }
 
 vResult_t vGradNorm(vGradList_t list, float* norm, void* workspace, size_t workspaceBytes, vcomm_t comm,

@@ -391,8 +391,10 @@ vResult_t vAllReduceRmsNormBackward(const vRmsNormDesc_t* desc, const void* cons
  * current device; it holds the tensors' addresses, so it serves every step for as long as they
  * stay where they are, and the only device memory that these operators allocate: a table of 32
  * bytes per 32 KiB of gradients.  Creating and destroying a list waits for the device, so
- * neither goes into a graph's capture.  vGradListCreate leaves *list NULL on an error; a NULL
- * or destroyed list gives vInvalidArgument. */
+ * neither goes into a graph's capture.  vGradListCreate leaves *list NULL on an error.  A NULL
+ * or destroyed list gives vInvalidArgument, from every call and from the end of a group that
+ * recorded it while it lived; its handle is not given to another list.  A graph that captured a
+ * call holds the list's table: the list has to outlive its last replay. */
 typedef struct vgradlist* vGradList_t;
 vResult_t vGradListCreate(vGradList_t* list, int nRanks, int nTensors, const size_t* counts,
                           const vDataType_t* datatypes, const unsigned char* replicated,

@@ -1,6 +1,7 @@
 // operators_host.cpp -- the operators' entry points (csrc/operators.cpp) without a GPU: device
 // memory is host memory, a launch is counted, and the communicator is the four functions below.
 // That is all the operators may use of it: anything else leaves the link with an undefined name.
+#include <atomic>
 #include <cstdlib>
 #include <cstring>
 #include <functional>
@@ -11,7 +12,8 @@
 
 namespace {
 
-int g_ranks = 1, g_grouping = 0, g_launches = 0, g_allocated = 0;
+int g_ranks = 1, g_grouping = 0;
+std::atomic<int> g_launches{0}, g_allocated{0};
 std::vector<std::function<vResult_t()>> g_recorded;
 
 }  // namespace
@@ -77,7 +79,8 @@ cudaError_t cudaGetLastError() { return cudaSuccess; }
 
 void host_start(int ranks) {
     g_ranks = ranks;
-    g_grouping = g_launches = 0;
+    g_grouping = 0;
+    g_launches = 0;
     g_recorded.clear();
 }
 int host_launches() { return g_launches; }

@@ -6,6 +6,7 @@ import ctypes
 import os
 import shutil
 import subprocess
+import threading
 
 import pytest
 import torch
@@ -51,3 +52,71 @@ def test_the_backward_pass_needs_nothing_of_the_communicator_but_its_launches(ho
     assert host.vAllReduceRmsNormBackward(d, a, 0x30000, 0x40000, 0x50000, None, a, 0x60000, 0x70000, need.value, COMM,
                                           None) == V.vSuccess
     assert host.host_launches() == 1
+
+
+class Lists:
+    """Gradient lists of one fp32 tensor of 64 elements on each of two ranks."""
+
+    def __init__(self, host):
+        self.host = host
+        host.host_start(2)
+        self.counts, self.types, self.grads = (ctypes.c_size_t * 1)(64), (ctypes.c_int * 1)(V.vFloat32), ints(0x10000, 0x20000)
+
+    def make(self):
+        handle = ctypes.c_void_p()
+        at = ctypes.addressof
+        assert self.host.vGradListCreate(at(handle), 2, 1, at(self.counts), at(self.types), None, at(self.grads), None) == V.vSuccess
+        return handle.value
+
+    def uses(self, handle):
+        """What each call answers: the workspace's, the norm's and the clipping's."""
+        need = ctypes.c_size_t()
+        return [self.host.vGradNormWorkspace(handle, COMM, ctypes.addressof(need)),
+                self.host.vGradNorm(handle, 0x30000, 0x40000, 1 << 20, COMM, None),
+                self.host.vClipGradNorm(handle, 1.0, 0x30000, 0x40000, 1 << 20, COMM, None)]
+
+
+def test_a_destroyed_list_is_refused_everywhere(host):
+    lists = Lists(host)
+    before = host.host_allocated()
+    first = lists.make()
+    assert lists.uses(first) == [V.vSuccess] * 3
+    assert host.vGradListDestroy(first) == V.vSuccess
+    for _ in range(2):
+        launches = host.host_launches()
+        assert lists.uses(first) == [V.vInvalidArgument] * 3
+        assert host.vGradListDestroy(first) == V.vInvalidArgument
+        assert host.host_launches() == launches
+        lists.make()                 # a later list does not answer to the old handle
+    assert host.host_allocated() == before + 2
+
+
+def test_a_list_destroyed_before_its_group_ends_is_refused_there(host):
+    lists = Lists(host)
+    handle = lists.make()
+    host.host_group(1)
+    assert host.vClipGradNorm(handle, 1.0, 0x30000, 0x40000, 1 << 20, COMM, None) == V.vSuccess
+    assert host.vGradListDestroy(handle) == V.vSuccess
+    assert host.host_group_end() == V.vInvalidArgument
+    assert host.host_launches() == 0
+
+
+def test_lists_of_several_threads(host):
+    # created, used and destroyed on four threads at once, the last use after the destruction
+    lists = Lists(host)
+    wrong = []
+
+    def work():
+        for _ in range(500):
+            handle = lists.make()
+            if lists.uses(handle) != [V.vSuccess] * 3 or host.vGradListDestroy(handle) != V.vSuccess:
+                wrong.append(handle)
+            if lists.uses(handle) != [V.vInvalidArgument] * 3:
+                wrong.append(handle)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
