@@ -393,11 +393,14 @@ __device__ __forceinline__ void team_reduce(TeamScratch& red, const NormShape& s
     }
 }
 
-// Let a kernel use `bytes` of dynamic shared memory.
+// Let a kernel use `bytes` of dynamic shared memory.  The limit belongs to the kernel, not to the
+// launch, and host threads share it: it is set to one value, the most that any shape takes, so that
+// no thread lowers it between another's setting and launch.
+static_assert(2 * sizeof(TeamScratch) <= kNormStaticSmem, "the kernels' static arrays");
 template <typename K>
 inline cudaError_t allow_smem(K kernel, size_t bytes) {
     if (bytes <= 32 * 1024) return cudaSuccess;        // with the static arrays, below the default 48 KiB
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxSmem);
 }
 
 template <typename K, typename... Args>

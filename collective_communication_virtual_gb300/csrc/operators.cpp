@@ -60,7 +60,7 @@ NormShape norm_shape(const NormCall& c) {
     // 13 and 11).  The backward pass keeps its sums in registers with two (1 x 16384 x 4096: 95 us,
     // 104 with four), but rows that fill a warp save more with four (1 x 16000 x 1024: 33 and 29).
     const bool few = c.rows <= (size_t)c.smCount * 16 && c.segments >= 4;
-    const int most = 228 * 1024, overhead = 1792;            // the SM's; a CTA's own and its static arrays
+    const int most = 228 * 1024, overhead = 1024 + kNormStaticSmem;    // the SM's; a CTA's own and its static arrays
     const auto stage = [&]() {
         const int part = (nv + s.cluster - 1) / s.cluster;
         double best = 0;

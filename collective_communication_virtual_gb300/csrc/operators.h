@@ -63,6 +63,8 @@ constexpr int kQuantGroup = 128;
 constexpr int kNormMaxThreads = 640;     // of a CTA that holds 4 vectors a thread
 constexpr int kNormWarpCta = 128;        // threads of a CTA whose teams are parts of a warp
 constexpr int kNormMaxCluster = 8;
+constexpr int kNormStaticSmem = 768;                         // of a CTA, at most
+constexpr int kNormMaxSmem = 227 * 1024 - kNormStaticSmem;   // dynamic, of a CTA
 // What a launch has to be shaped for.
 struct NormCall {
     size_t rows;

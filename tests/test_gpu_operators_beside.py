@@ -2,6 +2,8 @@
 and buffers that are input and output at once."""
 from __future__ import annotations
 
+import threading
+
 import pytest
 import torch
 
@@ -74,3 +76,65 @@ def test_few_rows_backward_beside_a_long_all_to_all(captured):
     finally:
         torch.cuda.synchronize()
         V.vcommDestroy(comm)
+
+
+@pytest.mark.parametrize("op", ["norm", "quant", "backward"])
+def test_two_host_threads_with_shapes_of_different_shared_memory(op):
+    # one instance of the kernel, launched with 40 KiB a CTA by one thread and with twice that by
+    # the other, each on its own communicator
+    rows, hidden = 3000, 4096
+    got = {}
+
+    def work(n):
+        torch.cuda.set_device(0)
+        comm = V.vcommInit(n)
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                gen = torch.Generator().manual_seed(n)
+                xs = torch.randn(n, rows, hidden, generator=gen).to(BF16)
+                hid = torch.randn(rows, hidden, generator=gen).to(BF16)
+                desc = V.vRmsNormDesc(rows, hidden, BF16, eps=EPS)
+                send, recv = xs.to(DEV), torch.empty(n, rows, hidden, dtype=BF16, device=DEV)
+                if op == "quant":
+                    recv = torch.empty(n, rows, hidden, dtype=torch.uint8, device=DEV)
+                sends, recvs = V.vBuffers(send.unbind()), V.vBuffers(recv.unbind())
+                scale = torch.empty(n, rows, device=DEV)
+                scales = V.vBuffers(scale.unbind())
+                w = torch.ones(hidden, dtype=BF16, device=DEV)
+                other = hid.to(DEV)
+                rstd = (other.float().square().mean(1) + EPS).rsqrt()
+                dw = torch.empty(hidden, dtype=BF16, device=DEV)
+                space = torch.empty(V.vRmsNormBackwardWorkspace(desc, comm), dtype=torch.uint8, device=DEV)
+            stream.synchronize()
+            for i in range(3000):
+                if op == "norm":
+                    V.vAllReduceRmsNorm(desc, sends, other, w, None, recvs, None, comm, stream=stream)
+                elif op == "quant":
+                    V.vAllReduceRmsNormQuant(desc, sends, other, w, None, recvs, scales, None, comm, stream=stream)
+                else:
+                    V.vAllReduceRmsNormBackward(desc, sends, other, rstd, w, None, recvs, dw, space, comm, stream=stream)
+            stream.synchronize()
+            first = recv[0].cpu()
+            if op == "norm":
+                ref = R.forward(xs, hid, w.cpu(), EPS)
+                R.assert_close(first, ref["y"], ref["dy"], BF16, "output")
+            elif op == "quant":
+                R.assert_quantised(first.view(torch.float8_e4m3fn).double(), scale[0].double().cpu()[:, None],
+                                   R.forward(xs, hid, w.cpu(), EPS), 0, "output")
+            else:
+                ref = R.backward(xs, hid, rstd.cpu(), w.cpu(), None)
+                R.assert_close(first, ref["dh"], ref["ddh"], BF16, "gradient")
+            got[n] = V.vcommGetAsyncError(comm)
+        except Exception as e:       # reported below, by the thread that counts
+            got[n] = e
+        finally:
+            torch.cuda.synchronize()
+            V.vcommDestroy(comm)
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in (3, 8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert got == {3: V.vSuccess, 8: V.vSuccess}
