@@ -481,8 +481,10 @@ def vAllReduceRmsNormBackward(desc, sendbuffs, hidden_states, rstd, weight, grad
 
 
 class TensorList:
-    """A vGradList_t: the gradients of a step by their addresses (it does not keep the tensors).
-    ``close`` destroys it, as losing its last reference does."""
+    """A vGradList_t: the gradients of a step by their addresses.  ``close`` destroys it, as losing
+    its last reference does.  Made by vTensorList it holds the tensors until then, so that their
+    memory is no other's while a call may still scale it; made from addresses it holds nothing."""
+    tensors = None
 
     def __init__(self, n_ranks: int, counts, datatypes, replicated, grads, outs):
         n = len(counts)
@@ -499,7 +501,7 @@ class TensorList:
 
     def close(self) -> None:
         if self.handle is not None:
-            handle, self.handle = self.handle, None
+            handle, self.handle, self.tensors = self.handle, None, None
             _check(lib().vGradListDestroy(handle), "vGradListDestroy")
 
     def __del__(self):
@@ -512,7 +514,10 @@ class TensorList:
 def vTensorList(grads, outs=None, replicated=None) -> TensorList:
     """The gradients of a step: ``grads[r][t]`` is rank r's tensor t, ``outs`` (the clipped
     gradients; None: in place) the same, ``replicated[t]`` whether every rank holds all of
-    tensor t (None: none).  A list whose tensors stay where they are serves every step."""
+    tensor t (None: none).  The list is of these tensors, which it holds: it serves every step that
+    fills them anew (``zero_grad(set_to_none=False)``, gradients in buffers of the caller's).  Where
+    a step brings new tensors (``set_to_none=True``), it still is of the old ones, and a new list
+    has to be made."""
     if not grads:
         raise VcommError(vInvalidArgument, "a tensor list of no ranks")
     first = grads[0]
@@ -530,8 +535,10 @@ def vTensorList(grads, outs=None, replicated=None) -> TensorList:
                 raise VcommError(vInvalidArgument, "tensors of a list are contiguous")
         addresses.append([t.data_ptr() for tensors in side for t in tensors])
     codes = {d: _dtype_code(d) for d in set(dtypes)}
-    return TensorList(len(grads), counts, [codes[d] for d in dtypes], replicated, addresses[0],
+    made = TensorList(len(grads), counts, [codes[d] for d in dtypes], replicated, addresses[0],
                       None if outs is None else addresses[1])
+    made.tensors = [list(tensors) for side in (grads, outs or []) for tensors in side]
+    return made
 
 
 def _list(tensors: TensorList, comm) -> int | None:

@@ -3,10 +3,12 @@
 from __future__ import annotations
 
 import ctypes
+import gc
 import os
 import shutil
 import subprocess
 import threading
+import weakref
 
 import pytest
 import torch
@@ -120,3 +122,49 @@ def test_lists_of_several_threads(host):
     for t in threads:
         t.join()
     assert not wrong
+
+
+# ---- the binding's tensor lists ----------------------------------------------------------------
+
+class FakeLists:
+    """The list calls of the library, on handles of its own."""
+
+    def __init__(self):
+        self.live, self.made, self.calls = set(), 0, []
+
+    def vGradListCreate(self, out, *args):
+        self.made += 1
+        self.live.add(self.made)
+        ctypes.c_void_p.from_address(out).value = self.made
+        return V.vSuccess
+
+    def vGradListDestroy(self, handle):
+        self.live.remove(handle)
+        return V.vSuccess
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            return V.vSuccess
+        return call
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    made = FakeLists()
+    monkeypatch.setattr(V, "lib", lambda: made)
+    monkeypatch.setitem(V._N_RANKS, COMM.value, 1)
+    return made
+
+
+def test_a_tensor_list_holds_its_tensors(fake):
+    # memory that the list's calls scale must not become another tensor's while the list lives
+    grad, out = torch.ones(5), torch.ones(5)
+    seen = [weakref.ref(grad), weakref.ref(out)]
+    tensors = V.vTensorList([[grad]], [[out]])
+    del grad, out
+    gc.collect()
+    assert all(r() is not None for r in seen)
+    tensors.close()
+    gc.collect()
+    assert all(r() is None for r in seen)
