@@ -480,20 +480,28 @@ def vAllReduceRmsNormBackward(desc, sendbuffs, hidden_states, rstd, weight, grad
            "vAllReduceRmsNormBackward")
 
 
+_dropped_lists: list[int] = []       # handles of lists that lost their last reference
+
+
 class TensorList:
-    """A vGradList_t: the gradients of a step by their addresses.  ``close`` destroys it, as losing
-    its last reference does.  Made by vTensorList it holds the tensors until then, so that their
-    memory is no other's while a call may still scale it; made from addresses it holds nothing."""
-    tensors = None
+    """A vGradList_t: the gradients of a step by their addresses.  Made by vTensorList it holds
+    the tensors, so that their memory is no other's while a call may still scale it; made from
+    addresses it holds nothing.
+
+    ``close`` destroys it.  One that loses its last reference is destroyed when the next list is
+    made: destruction frees device memory and waits for the device, which is not allowed while a
+    graph is being captured, and references are lost at any time."""
+    handle = tensors = None
 
     def __init__(self, n_ranks: int, counts, datatypes, replicated, grads, outs):
+        while _dropped_lists:
+            _check(lib().vGradListDestroy(_dropped_lists.pop()), "vGradListDestroy")
         n = len(counts)
         arrays = ((ctypes.c_size_t * n)(*counts), (ctypes.c_int * n)(*datatypes),
                   None if replicated is None else (ctypes.c_ubyte * n)(*map(bool, replicated)),
                   (ctypes.c_void_p * (n * n_ranks))(*grads),
                   None if outs is None else (ctypes.c_void_p * (n * n_ranks))(*outs))
         handle = ctypes.c_void_p()
-        self.handle = None
         self.n_ranks = n_ranks
         _check(lib().vGradListCreate(ctypes.addressof(handle), n_ranks, n,
                                      *(None if a is None else ctypes.addressof(a) for a in arrays)), "vGradListCreate")
@@ -504,11 +512,9 @@ class TensorList:
             handle, self.handle, self.tensors = self.handle, None, None
             _check(lib().vGradListDestroy(handle), "vGradListDestroy")
 
-    def __del__(self):
-        try:
-            self.close()
-        except Exception:            # the interpreter or the device is on its way out
-            pass
+    def __del__(self, dropped=_dropped_lists):
+        if self.handle is not None:
+            dropped.append(self.handle)
 
 
 def vTensorList(grads, outs=None, replicated=None) -> TensorList:

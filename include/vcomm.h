@@ -394,7 +394,7 @@ vResult_t vAllReduceRmsNormBackward(const vRmsNormDesc_t* desc, const void* cons
  * neither goes into a graph's capture.  vGradListCreate leaves *list NULL on an error.  A NULL
  * or destroyed list gives vInvalidArgument, from every call and from the end of a group that
  * recorded it while it lived; its handle is not given to another list.  A graph that captured a
- * call holds the list's table: the list has to outlive its last replay. */
+ * call reads the list's table: the list has to outlive its last replay. */
 typedef struct vgradlist* vGradList_t;
 vResult_t vGradListCreate(vGradList_t* list, int nRanks, int nTensors, const size_t* counts,
                           const vDataType_t* datatypes, const unsigned char* replicated,

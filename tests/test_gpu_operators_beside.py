@@ -138,3 +138,28 @@ def test_two_host_threads_with_shapes_of_different_shared_memory(op):
     for t in threads:
         t.join()
     assert got == {3: V.vSuccess, 8: V.vSuccess}
+
+
+def test_a_list_that_is_lost_while_a_graph_is_captured():
+    comm = V.vcommInit(1)
+    try:
+        grad = torch.full((1000,), 2.0, device=DEV)
+        kept = V.vTensorList([[grad]])
+        lost = [V.vTensorList([[torch.ones(10, device=DEV)]])]
+        space = torch.empty(V.vGradNormWorkspace(kept, comm), dtype=torch.uint8, device=DEV)
+        norm = torch.zeros(1, device=DEV)
+        V.vGradNorm(kept, norm, space, comm)
+        torch.cuda.synchronize()
+        norm.zero_()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            lost.clear()
+            V.vGradNorm(kept, norm, space, comm)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert abs(norm.item() - 4000 ** 0.5) <= R.NORM_REL * 1.01 * 4000 ** 0.5
+        V.vTensorList([[grad]]).close()
+        assert V.vcommGetAsyncError(comm) == V.vSuccess
+    finally:
+        torch.cuda.synchronize()
+        V.vcommDestroy(comm)

@@ -168,3 +168,20 @@ def test_a_tensor_list_holds_its_tensors(fake):
     tensors.close()
     gc.collect()
     assert all(r() is None for r in seen)
+
+
+def test_a_list_without_references_is_destroyed_by_the_next_one(fake):
+    # not where the reference is lost, which may be within a graph's capture
+    tensors = V.vTensorList([[torch.ones(5)]])
+    first = tensors.handle
+    del tensors
+    gc.collect()
+    assert fake.live == {first}
+    kept = V.vTensorList([[torch.ones(5)]])
+    assert fake.live == {kept.handle} and kept.handle != first
+    kept.close()
+    assert not fake.live
+    del kept
+    gc.collect()
+    V.vTensorList([[torch.ones(5)]]).close()
+    assert not fake.live
