@@ -492,6 +492,7 @@ class TensorList:
     made: destruction frees device memory and waits for the device, which is not allowed while a
     graph is being captured, and references are lost at any time."""
     handle = tensors = None
+    on_host = False                  # tensors of host memory: no call takes the list
 
     def __init__(self, n_ranks: int, counts, datatypes, replicated, grads, outs):
         while _dropped_lists:
@@ -529,21 +530,35 @@ def vTensorList(grads, outs=None, replicated=None) -> TensorList:
     first = grads[0]
     if replicated is not None and len(replicated) != len(first):
         raise VcommError(vInvalidArgument, f"replicated names {len(replicated)} tensors of {len(first)}")
-    counts, dtypes = [t.numel() for t in first], [t.dtype for t in first]
     addresses = []
-    for side in (grads,) if outs is None else (grads, outs):
-        if len(side) != len(grads):
-            raise VcommError(vInvalidArgument, f"outputs of {len(side)} ranks for gradients of {len(grads)}")
-        for tensors in side:
-            if [t.numel() for t in tensors] != counts or [t.dtype for t in tensors] != dtypes:
-                raise VcommError(vInvalidArgument, "every rank's tensors have the same sizes and types")
-            if not all([t.is_contiguous() for t in tensors]):
-                raise VcommError(vInvalidArgument, "tensors of a list are contiguous")
-        addresses.append([t.data_ptr() for tensors in side for t in tensors])
+    try:
+        counts, dtypes = [t.numel() for t in first], [t.dtype for t in first]
+        devices = [t.get_device() for t in first]
+        for side in (grads,) if outs is None else (grads, outs):
+            if len(side) != len(grads):
+                raise VcommError(vInvalidArgument, f"outputs of {len(side)} ranks for gradients of {len(grads)}")
+            for tensors in side:
+                if [t.numel() for t in tensors] != counts or [t.dtype for t in tensors] != dtypes:
+                    raise VcommError(vInvalidArgument, "every rank's tensors have the same sizes and types")
+                if [t.get_device() for t in tensors] != devices:
+                    raise VcommError(vInvalidArgument, "a list's tensors lie on one device")
+                if not all([t.is_contiguous() for t in tensors]):
+                    raise VcommError(vInvalidArgument, "tensors of a list are contiguous")
+            addresses.append([t.data_ptr() for tensors in side for t in tensors])
+    except (AttributeError, TypeError):
+        raise VcommError(vInvalidArgument, "a list's entries are tensors: leave out parameters without a gradient") from None
+    if len(set(devices)) > 1:
+        raise VcommError(vInvalidArgument, "a list's tensors lie on one device")
+    device = devices[0] if devices else None
+    if device is not None and device >= 0:
+        import torch
+        if device != torch.cuda.current_device():
+            raise VcommError(vInvalidArgument, f"tensors on device {device}; a list lives on the current device")
     codes = {d: _dtype_code(d) for d in set(dtypes)}
     made = TensorList(len(grads), counts, [codes[d] for d in dtypes], replicated, addresses[0],
                       None if outs is None else addresses[1])
     made.tensors = [list(tensors) for side in (grads, outs or []) for tensors in side]
+    made.on_host = device == -1
     return made
 
 
@@ -551,6 +566,8 @@ def _list(tensors: TensorList, comm) -> int | None:
     n = _n_ranks(comm)
     if tensors.n_ranks != n:
         raise VcommError(vInvalidArgument, f"a tensor list of {tensors.n_ranks} ranks on a communicator of {n}")
+    if tensors.on_host:
+        raise VcommError(vInvalidArgument, "the list's tensors are in host memory")
     return tensors.handle
 
 

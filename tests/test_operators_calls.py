@@ -154,7 +154,10 @@ def fake(monkeypatch):
     made = FakeLists()
     monkeypatch.setattr(V, "lib", lambda: made)
     monkeypatch.setitem(V._N_RANKS, COMM.value, 1)
-    return made
+    before = V._dropped_lists[:]     # handles of the library's own
+    V._dropped_lists.clear()
+    yield made
+    V._dropped_lists[:] = before
 
 
 def test_a_tensor_list_holds_its_tensors(fake):
@@ -185,3 +188,46 @@ def test_a_list_without_references_is_destroyed_by_the_next_one(fake):
     gc.collect()
     V.vTensorList([[torch.ones(5)]]).close()
     assert not fake.live
+
+
+def refused(call, *args, **kw):
+    with pytest.raises(V.VcommError) as e:
+        call(*args, **kw)
+    assert e.value.code == V.vInvalidArgument
+
+
+def test_a_list_of_host_tensors_is_taken_by_no_call(fake):
+    tensors = V.vTensorList([[torch.ones(5)]])
+    space = (0x10000, 1 << 20)
+    refused(V.vGradNormWorkspace, tensors, COMM)
+    refused(V.vGradNorm, tensors, 0x20000, space, COMM, stream=0)
+    refused(V.vClipGradNorm, tensors, 1.0, 0x20000, space, COMM, stream=0)
+    assert not fake.calls
+
+
+class OnDevice(torch.Tensor):
+    """A host tensor that says it lies on a device."""
+    device_index = 0
+
+    def get_device(self):
+        return self.device_index
+
+
+def on_device(index):
+    t = torch.ones(5).as_subclass(OnDevice)
+    t.device_index = index
+    return t
+
+
+def test_entries_that_are_no_tensors_or_lie_elsewhere_are_refused(fake, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    here, there, host = on_device(0), on_device(1), torch.ones(5)
+    V.vGradNormWorkspace(V.vTensorList([[here]], [[here]]), COMM)
+    for grads in ([[None]], [[here, None]], [[here], [None]], [None], [[3]]):        # a frozen parameter's gradient
+        refused(V.vTensorList, grads)
+    refused(V.vTensorList, [[here]], [[None]])
+    for grads in ([[here, there]], [[here], [there]], [[here, host]], [[there]]):
+        refused(V.vTensorList, grads)
+    for outs in ([[there]], [[host]]):
+        refused(V.vTensorList, [[here]], outs)
+    assert fake.made == 1
