@@ -30,32 +30,9 @@ __device__ __forceinline__ GradChunk load_chunk(const GradChunk* p) {
     return c;
 }
 
-// L2 hints: half of L2's size of what the clipping reads again stays, what is read or written for
-// the last time goes first (clipping 67 MB: 38.5 -> 32.9 us, 134 MB: 66.7 -> 61.5 us).
-__device__ __forceinline__ uint64_t keep_policy() {
-    uint64_t p;
-    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-__device__ __forceinline__ uint64_t pass_policy() {
-    uint64_t p;
-    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-__device__ __forceinline__ uint4 ld_hint(const void* p, uint64_t policy) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p), "l"(policy));
-    return v;
-}
-__device__ __forceinline__ void st_hint(void* p, uint4 v, uint64_t policy) {
-    asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1,%2,%3,%4}, %5;"
-                 :: "l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "l"(policy) : "memory");
-}
-
 // Sum of squares of a thread's part of a chunk.
 template <int DT>
-__device__ __forceinline__ float chunk_squares(const GradChunk& c, uint64_t policy) {
+__device__ __forceinline__ float chunk_squares(const GradChunk& c) {
     constexpr int E = kVecElems<DT>;
     constexpr int ESZ = DTypeOf<DT>::size;
     const int shift = (int)((uintptr_t)c.in & 15u) / ESZ;
@@ -65,7 +42,7 @@ __device__ __forceinline__ float chunk_squares(const GradChunk& c, uint64_t poli
 #pragma unroll
     for (int i = 0; i < kGradVecs; i++) {
         raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (e0 + i * kGradThreads * E < c.count) raw[i] = ld_hint(p + i * kGradThreads * 16, policy);
+        if (e0 + i * kGradThreads * E < c.count) raw[i] = ld_once(p + i * kGradThreads * 16);
     }
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -99,10 +76,9 @@ __device__ __forceinline__ void chunk_scale(const GradChunk& c, float factor) {
     const ptrdiff_t off = (ptrdiff_t)threadIdx.x * 16 - shift * ESZ;
     const int e0 = (int)threadIdx.x * E - shift;
     uint4 raw[kGradVecs];
-    const uint64_t policy = pass_policy();
 #pragma unroll
     for (int i = 0; i < kGradVecs; i++)
-        if (e0 + i * kGradThreads * E < c.count) raw[i] = ld_hint(c.in + off + i * kGradThreads * 16, policy);
+        if (e0 + i * kGradThreads * E < c.count) raw[i] = ld_once(c.in + off + i * kGradThreads * 16);
 #pragma unroll
     for (int i = 0; i < kGradVecs; i++) {
         const int e = e0 + i * kGradThreads * E;
@@ -111,7 +87,7 @@ __device__ __forceinline__ void chunk_scale(const GradChunk& c, float factor) {
         widen_vec<DT>(raw[i], f);
         scale_by(f, factor);
         if (e >= 0 && e + E <= c.count) {
-            st_hint(c.out + off + i * kGradThreads * 16, narrow_vec<DT>(f), policy);
+            st_stream(c.out + off + i * kGradThreads * 16, narrow_vec<DT>(f));
         } else {                                       // the vector that begins or ends the chunk
 #pragma unroll
             for (int j = 0; j < E; j++)
@@ -140,16 +116,14 @@ __global__ void __launch_bounds__(kGradThreads) k_grad_norm(const __grid_constan
     __shared__ double red[2][32];
     __shared__ bool last;
     double sum = 0.0;
-    const uint64_t keep = keep_policy(), pass = pass_policy();
     GradChunk c;
     if (blockIdx.x < a.nChunks) c = load_chunk(a.chunks + blockIdx.x);
     for (unsigned int i = blockIdx.x; i < a.nChunks; i += gridDim.x) {
         GradChunk next = c;
         if (a.nChunks - i > gridDim.x) next = load_chunk(a.chunks + i + gridDim.x);
-        const uint64_t policy = i >= a.keepFrom ? keep : pass;
-        if (c.dt == kF32) sum += (double)chunk_squares<kF32>(c, policy);
-        else if (c.dt == kF16) sum += (double)chunk_squares<kF16>(c, policy);
-        else sum += (double)chunk_squares<kBF16>(c, policy);
+        if (c.dt == kF32) sum += (double)chunk_squares<kF32>(c);
+        else if (c.dt == kF16) sum += (double)chunk_squares<kF16>(c);
+        else sum += (double)chunk_squares<kBF16>(c);
         c = next;
     }
     sum = block_sum(sum, red[0]);
@@ -171,7 +145,9 @@ __global__ void __launch_bounds__(kGradThreads) k_grad_norm(const __grid_constan
 }
 
 // One chunk a CTA, in order from the last one: the norm has just read those, so up to the size
-// of L2 they need not be read from memory again.
+// of L2 they need not be read from memory again.  No hint keeps them there or lets the outputs go
+// first: in place, 34 MB, such hints saved the call 3 us and cost the next kernels 7, whose data
+// the kept lines displaced.
 __global__ void __launch_bounds__(kGradThreads) k_grad_clip(const __grid_constant__ GradClipArgs a) {
     pdl_begin();
     const GradChunk c = load_chunk(a.chunks + (gridDim.x - 1 - blockIdx.x));

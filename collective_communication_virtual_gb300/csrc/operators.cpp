@@ -562,8 +562,6 @@ vResult_t grad_norm(vGradList_t handle, bool clip, float maxNorm, float* norm, v
     vc::GradNormArgs a;
     a.chunks = l.chunks;
     a.nChunks = l.nCounted;
-    const size_t keep = clip ? v.l2Bytes / 2 / (16 * vc::kGradChunkVecs) : 0;
-    a.keepFrom = l.nCounted - (unsigned)std::min<size_t>(keep, l.nCounted);
     a.done = l.done;
     a.partials = (double*)workspace;
     a.norm = norm;

@@ -15,7 +15,6 @@ struct CommView {
     int nRanks;
     int device;
     int smCount;
-    size_t l2Bytes;
     bool debug;
     bool grouping;                   // between vcommGroupStart and vcommGroupEnd
 };
@@ -140,7 +139,6 @@ constexpr int kSquaresCtasPerSm = 4;
 struct GradNormArgs {
     const GradChunk* chunks;         // those that count towards the norm
     unsigned int nChunks;
-    unsigned int keepFrom;           // chunks from here on stay in L2 for the clipping
     unsigned int* done;              // CTAs that have written their sum: zero between calls
     double* partials;                // one sum of squares per CTA
     float* norm;

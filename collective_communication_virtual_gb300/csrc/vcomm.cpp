@@ -544,7 +544,6 @@ vResult_t comm_view(vcomm_t c, CommView* v) {
     v->nRanks = c->nRanks;
     v->device = c->device;
     v->smCount = c->smCount;
-    v->l2Bytes = c->l2Bytes;
     v->debug = c->cfg.debug;
     v->grouping = c->groupDepth > 0;
     return vSuccess;

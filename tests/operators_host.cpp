@@ -36,7 +36,6 @@ vResult_t comm_view(vcomm_t c, CommView* v) {
     v->nRanks = g_ranks;
     v->device = 0;
     v->smCount = 152;
-    v->l2Bytes = (size_t)129 << 20;
     v->debug = false;
     v->grouping = g_grouping != 0;
     return vSuccess;
