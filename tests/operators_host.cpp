@@ -83,6 +83,24 @@ void host_start(int ranks) {
     g_recorded.clear();
 }
 int host_launches() { return g_launches; }
+// The launch shape of a norm, as the fields that the tests read, in their order.
+void host_norm_shape(size_t rows, int hidden, int elemSize, int weightSize, int segments, int general, int backward, int groups,
+                     int* out) {
+    vc::NormCall c = {};
+    c.rows = rows;
+    c.hidden = hidden;
+    c.elemSize = elemSize;
+    c.weightSize = weightSize;
+    c.segments = segments;
+    c.smCount = 152;
+    c.general = general != 0;
+    c.backward = backward != 0;
+    c.groups = groups != 0;
+    const vc::NormShape s = vc::norm_shape(c);
+    const int fields[] = {s.vecs, s.teamThreads, s.rowsPerCta, s.cluster, s.threads, s.staged, s.rounds, s.ctas, s.smemBytes,
+                          backward ? vc::norm_backward_parts(rows, s, 152) : 0};
+    std::memcpy(out, fields, sizeof(fields));
+}
 int host_allocated() { return g_allocated; }
 void host_group(int on) { g_grouping = on; }
 // As vcommGroupEnd: runs what was recorded and returns the first error.

@@ -231,3 +231,66 @@ def test_entries_that_are_no_tensors_or_lie_elsewhere_are_refused(fake, monkeypa
     for outs in ([[there]], [[host]]):
         refused(V.vTensorList, [[here]], outs)
     assert fake.made == 1
+
+
+# ---- launch shapes of the norms ------------------------------------------------------------------
+
+SHAPE = ("vecs", "team", "per_cta", "cluster", "threads", "staged", "rounds", "ctas", "smem", "parts")
+MOST_SMEM = 227 * 1024 - 2 * 320         # of a CTA, less the kernels' static arrays
+ROWS = [1, 2, 3, 31, 76, 77, 153, 300, 1500, 2433, 4096, 9001, 45000, 1 << 20, (1 << 31) - 1]
+WIDTHS = [1, 2, 7, 8, 31, 64, 100, 128, 129, 255, 512, 1000, 1031, 2047, 2048, 2731, 4096, 4099, 5120, 8192, 9001, 10241, 12296,
+          16384, 20480, 20481, 24001, 32768, 40961, 65535, 65536]
+
+
+@pytest.mark.parametrize("elem,weight", [(2, 2), (2, 4), (4, 4)])
+@pytest.mark.parametrize("mode", ["plain", "groups", "backward"])
+def test_launch_shapes_hold_every_row_within_the_hardware(host, elem, weight, mode):
+    out = (ctypes.c_int * len(SHAPE))()
+    per = 16 // elem
+    for hidden in WIDTHS:
+        for segments in (1, 2, 3, 4, 5, 9, 17, 33, 64, 65, 66):
+            for general in (0, 1) if hidden % per == 0 else (1,):
+                for rows in ROWS:
+                    host.host_norm_shape(ctypes.c_size_t(rows), hidden, elem, weight, segments, general, mode == "backward",
+                                         mode == "groups", out)
+                    s = dict(zip(SHAPE, out))
+                    at = (hidden, segments, general, rows, s)
+                    # a row's columns, by the team's threads
+                    assert s["vecs"] in (1, 2, 4) and s["cluster"] in (1, 2, 4, 8), at
+                    assert s["cluster"] * s["team"] * s["vecs"] * per >= hidden, at
+                    assert s["threads"] == s["team"] * s["per_cta"] and s["threads"] % 32 == 0, at
+                    assert s["threads"] <= (512 if s["staged"] else 640) and s["smem"] <= MOST_SMEM, at
+                    assert s["team"] % 32 == 0 or s["team"] in (1, 2, 4, 8, 16), at
+                    # the CTAs of a cluster meet at barriers that only teams of several warps reach
+                    assert s["cluster"] == 1 or (s["per_cta"] == 1 and s["team"] > 32), at
+                    # a group's maximum is found in neighbouring lanes of one warp
+                    if mode == "groups":
+                        assert s["vecs"] == 1 or s["team"] * per >= 128, at
+                        assert s["cluster"] == 1 or s["team"] * s["vecs"] * per % 128 == 0, at
+                    # every row, once
+                    if mode == "backward":
+                        assert 1 <= s["parts"] <= 16 * 152, at
+                    elif s["staged"] and s["rounds"]:
+                        assert 1 <= s["rounds"] <= 6, at
+                        assert (s["ctas"] - 1) * s["rounds"] * s["per_cta"] < rows <= s["ctas"] * s["rounds"] * s["per_cta"], at
+                    elif s["staged"]:
+                        assert 1 <= s["ctas"] <= 16 * 152, at
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_backward_workspace_is_enough_whatever_the_buffers_alignment(host, dtype):
+    esz = dtype.itemsize
+    need = ctypes.c_size_t()
+    for ranks in (1, 2, 8, 31):
+        host.host_start(ranks)
+        for hidden in (8, 100, 1001, 1024, 2048, 4096, 9001, 16384, 65536):
+            for rows in (1, 40, 200, 1500, 20000):
+                desc = V.vRmsNormDesc(rows, hidden, dtype)
+                d = ctypes.addressof(desc)
+                assert host.vRmsNormBackwardWorkspace(d, COMM, ctypes.addressof(need)) == V.vSuccess
+                for offset in (0, esz):
+                    for residual in (None, 0x50000):
+                        bufs = ints(*[0x100000 + offset] * ranks)
+                        a = ctypes.addressof(bufs)
+                        assert host.vAllReduceRmsNormBackward(d, a, 0x30000, 0x40000, 0x60000, residual, a, 0x70000, 0x80000,
+                                                              need.value, COMM, None) == V.vSuccess, (ranks, hidden, rows)
