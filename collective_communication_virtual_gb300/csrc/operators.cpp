@@ -102,7 +102,9 @@ NormShape norm_shape(const NormCall& c) {
         fits = stage();
     }
     if (fits) {
-        const int regs = s.vecs == 1 ? 64 : s.vecs == 2 && !c.backward ? 104 : 128;    // of a thread, at most
+        // Registers of a thread, at most: the launch bounds give 64 and 128, and the forward instances
+        // with two vectors take 80 to 107 (in eights).
+        const int regs = s.vecs == 1 ? 64 : s.vecs == 2 && !c.backward ? 112 : 128;
         const size_t groups = (c.rows + s.rowsPerCta - 1) / s.rowsPerCta;
         // About 72 KiB under way per SM: less leaves the memory waiting, more makes it slower
         // where the CTAs do not keep step.  (48 KiB in the backward pass with two vectors a thread.)
@@ -173,7 +175,7 @@ NormShape norm_shape(const NormCall& c) {
 
 int norm_backward_parts(size_t rows, const NormShape& sh, int smCount) {
     if (sh.staged) return sh.ctas;
-    // direct loads, at up to 102 registers a thread
+    // direct loads: the launch bounds leave an SM room for kNormMaxThreads, at 96 registers a thread
     const int perSm = std::max(1, kNormMaxThreads / sh.threads);
     const size_t most = std::max<size_t>(1, (size_t)smCount * perSm / sh.cluster);
     return (int)std::min(most, (rows + sh.rowsPerCta - 1) / sh.rowsPerCta);
