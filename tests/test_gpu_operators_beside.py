@@ -163,3 +163,127 @@ def test_a_list_that_is_lost_while_a_graph_is_captured():
     finally:
         torch.cuda.synchronize()
         V.vcommDestroy(comm)
+
+
+# ---- sums that are exact --------------------------------------------------------------------
+
+# rows of teams of part of a warp, a warp and a CTA, dealt out unevenly; few rows; rows shared by a
+# cluster; (ranks, rows, hidden)
+EXACT = [(1, 45000, 64), (1, 44999, 64), (1, 45001, 71), (2, 9001, 200), (2, 3001, 257), (1, 16001, 1024), (3, 2003, 2048),
+         (1, 9001, 2047), (8, 1301, 4096), (1, 40, 512), (2, 331, 1001), (1, 401, 32776), (8, 331, 16384), (3, 291, 24001),
+         (2, 231, 65536)]
+
+
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,rows,hidden", EXACT)
+def test_the_weight_gradient_of_small_integers_is_exact(n, rows, hidden, dtype, offset):
+    # with rstd = 1 every term and every partial sum is a whole number below 2^24, so no row may be
+    # missing or counted twice, whatever the order
+    gen = torch.Generator().manual_seed(rows + hidden)
+    dys = torch.randint(-2, 3, (n, rows, hidden), generator=gen, dtype=torch.int8)
+    hid = torch.randint(-3, 4, (rows, hidden), generator=gen, dtype=torch.int8)
+
+    def place(t):
+        flat = torch.empty(t.numel() + offset, dtype=dtype, device=DEV)
+        flat[offset:].copy_(t.flatten())
+        return flat[offset:].view(t.shape)
+
+    comm = V.vcommInit(n)
+    try:
+        desc = V.vRmsNormDesc(rows, hidden, dtype, F32, EPS)
+        space = torch.full((V.vRmsNormBackwardWorkspace(desc, comm),), 0xFF, dtype=torch.uint8, device=DEV)
+        dw = torch.full((hidden,), 77.0, device=DEV)
+        outs = [None] * (n - 1) + [torch.empty(rows, hidden, dtype=dtype, device=DEV)]
+        V.vAllReduceRmsNormBackward(desc, [place(d) for d in dys], place(hid), torch.ones(rows, device=DEV),
+                                    torch.ones(hidden, device=DEV), None, outs, dw, space, comm)
+        torch.cuda.synchronize()
+    finally:
+        V.vcommDestroy(comm)
+    want = (dys.to(torch.int32).sum(0) * hid.to(torch.int32)).sum(0)
+    assert want.abs().max() < 1 << 24
+    assert torch.equal(dw.cpu().to(torch.int32), want.to(torch.int32)) and (dw == dw.round()).all()
+
+
+# ---- in place, and values that are not finite ---------------------------------------------------
+
+# rows that one CTA stages, and rows shared by a cluster, aligned and not
+SHARED = [(3, 37, 2048), (2, 3000, 1001), (1, 400, 32776), (8, 330, 16384), (3, 290, 24001), (2, 230, 65536), (64, 90, 4096),
+          (40, 161, 2100)]
+
+
+def make(n, rows, hidden, seed):
+    gen = torch.Generator().manual_seed(seed)
+    xs = (torch.randn(n, rows, hidden, generator=gen) / n ** 0.5).to(BF16)
+    other, more = (torch.randn(rows, hidden, generator=gen).to(BF16) for _ in range(2))
+    w = 1 + 0.2 * torch.randn(hidden, generator=gen)
+    return xs, other, more, w
+
+
+@pytest.mark.parametrize("n,rows,hidden", SHARED)
+def test_forward_in_place(n, rows, hidden):
+    xs, res, _, w = make(n, rows, hidden, 71)
+    comm = V.vcommInit(n)
+    try:
+        send, stream = [x.to(DEV) for x in xs], res.to(DEV)
+        V.vAllReduceRmsNorm(V.vRmsNormDesc(rows, hidden, BF16, F32, EPS), send, stream, w.to(DEV), stream, send, None, comm)
+        torch.cuda.synchronize()
+    finally:
+        V.vcommDestroy(comm)
+    ref = R.forward(xs, res, w, EPS)
+    R.assert_close(stream, ref["h"], ref["dh"], BF16, "stream")
+    for r in range(n):
+        R.assert_close(send[r], ref["y"], ref["dy"], BF16, f"rank {r}")
+
+
+@pytest.mark.parametrize("over", ["send", "residual"])
+@pytest.mark.parametrize("n,rows,hidden", SHARED)
+def test_backward_in_place(n, rows, hidden, over):
+    dys, hid, dres, w = make(n, rows, hidden, 72)
+    rstd = (hid.float().square().mean(1) + EPS).rsqrt()
+    comm = V.vcommInit(n)
+    try:
+        desc = V.vRmsNormDesc(rows, hidden, BF16, F32, EPS)
+        space = torch.empty(V.vRmsNormBackwardWorkspace(desc, comm), dtype=torch.uint8, device=DEV)
+        send, grad, dw = [d.to(DEV) for d in dys], dres.to(DEV), torch.empty(hidden, device=DEV)
+        outs = send if over == "send" else [None] * (n - 1) + [grad]
+        V.vAllReduceRmsNormBackward(desc, send, hid.to(DEV), rstd.to(DEV), w.to(DEV), grad, outs, dw, space, comm)
+        torch.cuda.synchronize()
+    finally:
+        V.vcommDestroy(comm)
+    ref = R.backward(dys, hid, rstd, w, dres)
+    R.assert_close(dw, ref["dw"], ref["ddw"], F32, "weight gradient")
+    for o in outs:
+        if o is not None:
+            R.assert_close(o, ref["dh"], ref["ddh"], BF16, "gradient")
+
+
+@pytest.mark.parametrize("n,rows,hidden", [(2, 9, 96), (1, 40, 1003), (2, 2700, 1000), (1, 9001, 200), (2, 230, 65536),
+                                           (3, 290, 24001)])
+def test_backward_rows_with_infinities_and_nans(n, rows, hidden):
+    # a bad element spoils its own row of the gradient and its own column of the weight's, no other
+    dys, hid, dres, w = make(n, rows, hidden, 73)
+    dys[0, 2, hidden // 2] = float("nan")
+    dys[n - 1, 4, hidden - 1] = float("inf")
+    hid[6, 1] = float("-inf")
+    dres[8, 3] = float("nan")
+    rstd = (hid.float().square().mean(1) + EPS).rsqrt()      # 0 where the row holds an infinity
+    comm = V.vcommInit(n)
+    try:
+        desc = V.vRmsNormDesc(rows, hidden, BF16, F32, EPS)
+        space = torch.empty(V.vRmsNormBackwardWorkspace(desc, comm), dtype=torch.uint8, device=DEV)
+        outs, dw = [torch.empty(rows, hidden, dtype=BF16, device=DEV) for _ in range(n)], torch.empty(hidden, device=DEV)
+        V.vAllReduceRmsNormBackward(desc, [d.to(DEV) for d in dys], hid.to(DEV), rstd.to(DEV), w.to(DEV), dres.to(DEV), outs,
+                                    dw, space, comm)
+        torch.cuda.synchronize()
+    finally:
+        V.vcommDestroy(comm)
+    ref = R.backward(dys, hid, rstd, w, dres)
+    for got, want, slack, dtype, what in ((outs[n - 1], ref["dh"], ref["ddh"], BF16, "gradient"),
+                                          (dw, ref["dw"], ref["ddw"], F32, "weight gradient")):
+        got = got.double().cpu()
+        fine = want.isfinite()
+        R.assert_close(got[fine], want[fine], slack[fine], dtype, what)
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf()), what
+    spoilt = ~ref["dh"].isfinite()
+    assert spoilt[[2, 4, 6]].all() and spoilt[8].sum() == 1 and not spoilt[[0, 1, 3, 5, 7]].any()
