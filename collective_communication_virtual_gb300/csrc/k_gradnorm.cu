@@ -5,7 +5,8 @@
 // The tensors are cut into chunks of 32 KiB, listed once in device memory, so one launch
 // covers any number of large and small ones and a CTA finds its work with one load.  A thread
 // adds the squares of its part of a chunk in fp32 (at most 64 terms) and chunks and threads in
-// fp64; the order of every sum follows from the sizes alone, whichever CTA ends last.
+// fp64; the order of every sum follows from the sizes and the tensors' offsets from 16 bytes,
+// whichever CTA ends last.
 //
 // Bound by memory: the norm reads every gradient once (8 x 33.5 M bf16 elements, 537 MB: 79 us,
 // 1.00 of the measured copy rate), the clipping reads it again, as the factor depends on all of

@@ -371,7 +371,7 @@ vResult_t vAllReduceRmsNormQuant(const vRmsNormDesc_t* desc, const void* const* 
  * with equal strides.  The workspace is at least the number of bytes that
  * vRmsNormBackwardWorkspace gives for the descriptor, 16-byte aligned, and used by nothing
  * else until the call's work is done; a smaller one gives vInvalidArgument.  The same call
- * gives the same bits. */
+ * (on buffers of the same offsets from 16 bytes) gives the same bits. */
 vResult_t vRmsNormBackwardWorkspace(const vRmsNormDesc_t* desc, vcomm_t comm, size_t* bytes);
 vResult_t vAllReduceRmsNormBackward(const vRmsNormDesc_t* desc, const void* const* sendbuffs,
                                     const void* hiddenStates, const float* rstd, const void* weight,
@@ -403,8 +403,8 @@ vResult_t vGradListDestroy(vGradList_t list);
 
 /* *norm (device memory, fp32) = the 2-norm of all ranks' gradients together, a replicated
  * tensor counted once, by rank 0's copy.  Squares are taken and added in fp32 over at most
- * 64 elements, their sums in fp64, in an order that the sizes fix.  A square above fp32's
- * range makes the norm infinite.
+ * 64 elements, their sums in fp64, in an order that the sizes and the tensors' offsets from 16
+ * bytes fix.  A square above fp32's range makes the norm infinite, one below it adds nothing.
  * vClipGradNorm then scales every rank's gradients by min(1, maxNorm / (norm + 1e-6)),
  * rounded once to their type (no element is rewritten in place where that factor is 1).  A
  * norm that is not finite scales as the formula has it: infinity by 0, NaN by NaN.  maxNorm
