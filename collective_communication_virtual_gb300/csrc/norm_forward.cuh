@@ -12,7 +12,8 @@
 // known, so a row needs one reduction, not two.
 //
 // Bound by memory where rows are many: 8 ranks x 4096 x 4096 bf16 (604 MB) take 93 us, 0.96 of
-// the measured copy rate; 1 x 16384 x 4096 to 8 bits (470 MB) 75 us, 0.93.  Rows off 16 bytes
+// the measured copy rate; 1 x 16384 x 4096 to 8 bits (470 MB) 75 us, 0.93, and with a scale per 128
+// elements, four shuffles a vector more, 91 us, 0.76.  Rows off 16 bytes
 // take about twice the instructions and are bound by those (3 x 1537 x 2731 fp16, every rank at
 // its own offset: 21 us, 0.47; 1 x 16000 x 2047 bf16: 59 us, 0.65).  One row over 8 ranks takes
 // 3.7 us, a launch and two trips to memory.
