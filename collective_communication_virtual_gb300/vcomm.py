@@ -495,8 +495,12 @@ class TensorList:
     on_host = False                  # tensors of host memory: no call takes the list
 
     def __init__(self, n_ranks: int, counts, datatypes, replicated, grads, outs):
-        while _dropped_lists:
-            _check(lib().vGradListDestroy(_dropped_lists.pop()), "vGradListDestroy")
+        while True:
+            try:
+                dropped = _dropped_lists.pop()
+            except IndexError:       # none, or another thread has just taken the last
+                break
+            _check(lib().vGradListDestroy(dropped), "vGradListDestroy")
         n = len(counts)
         arrays = ((ctypes.c_size_t * n)(*counts), (ctypes.c_int * n)(*datatypes),
                   None if replicated is None else (ctypes.c_ubyte * n)(*map(bool, replicated)),
