@@ -3,17 +3,14 @@
 // a bad argument returns vInvalidArgument and launches nothing, the communicator's sticky
 // error is returned by every call, and nothing is thrown through the C interface.
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
-#include <cmath>
 #include <cstdio>
 #include <mutex>
-#include <new>
 #include <unordered_map>
 #include <vector>
 
-#include "operators.h"
+#include "entry.h"
 
 namespace vc {
 
@@ -46,12 +43,12 @@ NormShape norm_shape(const NormCall& c) {
     s.cluster = 1;
     // Bytes of dynamic shared memory for the shape as it stands.
     const auto layout = [&]() {
-        s.extraBytes = c.backward ? s.threads * s.vecs * E * (int)sizeof(float) : 0;
+        s.extraBytes = c.backward ? s.threads * s.vecs * E * (int)sizeof(float) * (1 + c.extraSums) : 0;
         s.weightBytes = s.staged ? s.teamThreads * s.vecs * E * c.weightSize : 0;
         s.stageBytes = s.staged ? (c.segments * s.vecs * stage_blocks(s.threads, s.teamThreads, c.general) + 1) * 16 : 0;
         // a row's vectors, and the block behind them that a realigned read may touch
         s.rowBytes = c.general ? s.teamThreads * s.vecs * 16 + 16 : 0;
-        s.smemBytes = s.extraBytes + s.weightBytes + s.stageBytes + s.rowBytes * (c.backward ? 1 : 2) * s.rowsPerCta;
+        s.smemBytes = s.extraBytes + s.weightBytes + s.stageBytes + s.rowBytes * ((c.backward ? 1 : 2) + c.extraRowBuffers) * s.rowsPerCta;
     };
 
     // Staged: more vectors a thread means fewer instructions and barriers a row, as long as the
@@ -104,7 +101,7 @@ NormShape norm_shape(const NormCall& c) {
     if (fits) {
         // Registers of a thread, at most: the launch bounds give 64 and 128, and the forward instances
         // with two vectors take 80 to 107 (in eights).
-        const int regs = s.vecs == 1 ? 64 : s.vecs == 2 && !c.backward ? 112 : 128;
+        const int regs = c.regs ? c.regs : s.vecs == 1 ? 64 : s.vecs == 2 && !c.backward ? 112 : 128;
         const size_t groups = (c.rows + s.rowsPerCta - 1) / s.rowsPerCta;
         // About 72 KiB under way per SM: less leaves the memory waiting, more makes it slower
         // where the CTAs do not keep step.  (48 KiB in the backward pass with two vectors a thread.)
@@ -156,17 +153,22 @@ NormShape norm_shape(const NormCall& c) {
             while (s.cluster < kNormMaxCluster && c.rows * (size_t)s.cluster * 2 <= (size_t)c.smCount &&
                    nv / (s.cluster * 2) >= 64)
                 s.cluster *= 2;
-            const int per = (nv + s.cluster - 1) / s.cluster;
-            // One vector a thread where that makes one wave of CTAs at 72 registers a thread
-            // (1 x 150 x 4096: 2.6 us, 3.1 with two), else two (1 x 300 x 4096: 3.1 us, 4.5 with one;
-            // 32 x 2000 x 4096: 171 and 185).
-            const int warps = (per + 31) / 32;
-            const size_t wave = (size_t)c.smCount * std::max(1, 65536 / (72 * 32 * warps));
-            const bool one = per <= kNormMaxThreads && (c.backward || c.rows * (size_t)s.cluster <= wave);
-            s.vecs = one ? 1 : per <= kNormMaxThreads * 2 ? 2 : 4;
-            s.teamThreads = ((per + s.vecs - 1) / s.vecs + 31) / 32 * 32;
-            s.threads = s.teamThreads;
-            s.rowsPerCta = 1;
+            for (;; s.cluster *= 2) {
+                const int per = (nv + s.cluster - 1) / s.cluster;
+                // One vector a thread where that makes one wave of CTAs at 72 registers a thread
+                // (1 x 150 x 4096: 2.6 us, 3.1 with two), else two (1 x 300 x 4096: 3.1 us, 4.5 with one;
+                // 32 x 2000 x 4096: 171 and 185).
+                const int warps = (per + 31) / 32;
+                const size_t wave = (size_t)c.smCount * std::max(1, 65536 / (72 * 32 * warps));
+                const bool one = per <= kNormMaxThreads && (c.backward || c.rows * (size_t)s.cluster <= wave);
+                s.vecs = one ? 1 : per <= kNormMaxThreads * 2 ? 2 : 4;
+                s.teamThreads = ((per + s.vecs - 1) / s.vecs + 31) / 32 * 32;
+                s.threads = s.teamThreads;
+                s.rowsPerCta = 1;
+                layout();
+                // sums down the columns and row buffers that one CTA has no room for
+                if (s.smemBytes <= kNormMaxSmem || s.cluster == kNormMaxCluster) break;
+            }
         }
         layout();
     }
@@ -184,107 +186,6 @@ int norm_backward_parts(size_t rows, const NormShape& sh, int smCount) {
 }  // namespace vc
 
 namespace {
-
-using vc::comm_launch;
-using vc::comm_view;
-using vc::CommView;
-
-struct Range {
-    explicit Range(const char* name) { nvtxRangePushA(name); }
-    ~Range() { nvtxRangePop(); }
-    Range(const Range&) = delete;
-    Range& operator=(const Range&) = delete;
-};
-
-bool is_float(int dt) { return dt == vFloat32 || dt == vFloat16 || dt == vBFloat16; }
-
-bool at(const void* p, size_t align) { return ((uintptr_t)p & (align - 1)) == 0; }
-
-// Run `f`, giving vSystemError for a failed allocation.
-template <typename F>
-vResult_t guarded(F f) {
-    try {
-        return f();
-    } catch (const std::bad_alloc&) {
-        return vSystemError;
-    } catch (...) {
-        return vInternalError;
-    }
-}
-
-struct Checked {
-    vRmsNormDesc_t d;                // strides filled in
-    int esz;
-};
-
-vResult_t check_desc(const vRmsNormDesc_t* desc, Checked* k) {
-    if (!desc) return vInvalidArgument;
-    vRmsNormDesc_t& d = k->d;
-    d = *desc;
-    if (!is_float(d.datatype)) return vInvalidArgument;
-    if (d.weightType != vFloat32 && d.weightType != d.datatype) return vInvalidArgument;
-    if (d.hidden > VCOMM_MAX_HIDDEN || d.rows > 0x7FFFFFFFull) return vInvalidArgument;
-    if (!(d.eps >= 0.0f) || std::isinf(d.eps)) return vInvalidArgument;
-    if (d.quantGroup != 0 && d.quantGroup != vc::kQuantGroup) return vInvalidArgument;
-    for (size_t* s : {&d.sendStride, &d.residualStride, &d.recvStride}) {
-        if (*s == 0) *s = d.hidden;
-        if (*s < d.hidden || *s > ((size_t)1 << 62) / (4 * std::max<size_t>(1, d.rows))) return vInvalidArgument;
-    }
-    k->esz = (int)vc::dtype_size(d.datatype);
-    return vSuccess;
-}
-
-// The sends, the wanted outputs (compacted into `out`, their indices into `index`) and
-// whether every vector of every row starts on a 16-byte boundary (an output of osz-byte
-// elements: on one of its own vectors' size).
-struct Buffers {
-    int nOut = 0;
-    bool aligned = true;
-    bool outSame = true;             // the outputs all start at one offset from 16 bytes
-};
-vResult_t check_buffers(const Checked& k, int nRanks, const void* const* send, void* const* recv, int osz,
-                        const void** sendOut, void** out, int* index, Buffers* b) {
-    const vRmsNormDesc_t& d = k.d;
-    if (!send || !recv) return vInvalidArgument;
-    const size_t e = 16 / (size_t)k.esz;
-    b->aligned = d.hidden % e == 0 &&
-                 (d.rows == 1 || (d.sendStride % e == 0 && d.residualStride % e == 0 && d.recvStride % e == 0));
-    for (int r = 0; r < nRanks; r++) {
-        if (!send[r] || !at(send[r], k.esz)) return vInvalidArgument;
-        sendOut[r] = send[r];
-        b->aligned = b->aligned && at(send[r], 16);
-        if (!recv[r]) continue;
-        if (!at(recv[r], osz)) return vInvalidArgument;
-        b->aligned = b->aligned && at(recv[r], e * osz);
-        if (index) index[b->nOut] = r;
-        out[b->nOut++] = recv[r];
-        b->outSame = b->outSame && at((const void*)((uintptr_t)recv[r] ^ (uintptr_t)out[0]), 16);
-    }
-    return b->nOut ? vSuccess : vInvalidArgument;
-}
-
-vResult_t check_weight(const Checked& k, const void* weight, Buffers* b) {
-    if (!weight || !at(weight, vc::dtype_size(k.d.weightType))) return vInvalidArgument;
-    b->aligned = b->aligned && at(weight, 16);
-    return vSuccess;
-}
-vResult_t check_row_buffer(const Checked& k, const void* p, Buffers* b) {
-    if (!p) return vSuccess;
-    if (!at(p, k.esz)) return vInvalidArgument;
-    b->aligned = b->aligned && at(p, 16);
-    return vSuccess;
-}
-
-vc::NormCall norm_call(const Checked& k, const CommView& v, const Buffers& b) {
-    vc::NormCall c = {};
-    c.rows = k.d.rows;
-    c.hidden = (int)k.d.hidden;
-    c.elemSize = k.esz;
-    c.weightSize = (int)vc::dtype_size(k.d.weightType);
-    c.smCount = v.smCount;
-    c.general = !b.aligned;
-    return c;
-}
 
 void debug_norm(const CommView& v, const char* what, const Checked& k, const vc::NormShape& s) {
     if (!v.debug) return;

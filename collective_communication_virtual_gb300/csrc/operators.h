@@ -73,6 +73,9 @@ struct NormCall {
     bool general;                    // as in NormShape
     bool backward;
     bool groups;                     // 8-bit output with a scale per 128 elements
+    int extraSums;                   // backward: sums down the columns besides the weight's gradient
+    int extraRowBuffers;             // GENERAL: row buffers of a team besides those above
+    int regs;                        // registers of a thread where they are not the RMS norm's; 0: they are
 };
 NormShape norm_shape(const NormCall& c);
 
@@ -120,6 +123,59 @@ struct NormBackwardArgs {
 // CTAs (clusters) of the backward pass: its workspace holds one row of fp32 sums for each.
 int norm_backward_parts(size_t rows, const NormShape& sh, int smCount);
 cudaError_t launch_rmsnorm_backward(const NormBackwardArgs& a, vDataType_t dt, cudaStream_t s);
+
+// ---- block norm: the norms after and before a block ---------------------------------------
+
+struct BlockNormArgs {
+    const void* send[VCOMM_MAX_RANKS];
+    void* recv[VCOMM_MAX_RANKS];     // the nOut outputs that are wanted, in rank order
+    const void* residual;            // may be NULL
+    const void* post;                // the weight of the norm after the block
+    const void* gate;                // may be NULL
+    const void* pre;                 // the weight of the norm before the next one
+    void* blockOut;                  // may be NULL, as the next two
+    void* residualOut;
+    float* rstd;                     // the block's, then the stream's
+    size_t rows;
+    size_t sendStride, residualStride, recvStride;     // elements between rows
+    int hidden;
+    int nRanks;
+    int nOut;
+    int outSame;
+    int weightF32;
+    float eps;
+    float scale;                     // of the residual
+    NormShape shape;
+};
+cudaError_t launch_block_norm(const BlockNormArgs& a, vDataType_t dt, cudaStream_t s);
+
+struct BlockNormBackwardArgs {
+    const void* send[VCOMM_MAX_RANKS];   // every rank's partial gradient of the normed output
+    void* recv[VCOMM_MAX_RANKS];         // the nOut outputs that are wanted
+    const void* hidden;                  // the stream that was normed
+    const void* block;                   // the block's output that was normed
+    const void* gradStream;              // may be NULL
+    const void* post;
+    const void* gate;                    // may be NULL
+    const void* pre;
+    const float* rstd;                   // the block's, then the stream's
+    void* gradResidual;                  // may be NULL
+    float* partials;                     // [parts][2][width]
+    void* gradPost;
+    void* gradGate;                      // may be NULL
+    void* gradPre;
+    size_t rows;
+    size_t sendStride, residualStride, recvStride;
+    int width;
+    int nRanks;
+    int nOut;
+    int outSame;
+    int weightF32;
+    int parts;                           // CTAs (clusters) that stride over the rows
+    float scale;
+    NormShape shape;
+};
+cudaError_t launch_block_norm_backward(const BlockNormBackwardArgs& a, vDataType_t dt, cudaStream_t s);
 
 // ---- gradient norm and clipping ----------------------------------------------------------
 

@@ -69,6 +69,12 @@ class vRmsNormDesc_t(ctypes.Structure):
                 ("datatype", ctypes.c_int), ("weightType", ctypes.c_int), ("quantGroup", ctypes.c_int)]
 
 
+class vBlockNormDesc_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_size_t), ("hidden", ctypes.c_size_t), ("sendStride", ctypes.c_size_t),
+                ("residualStride", ctypes.c_size_t), ("recvStride", ctypes.c_size_t), ("eps", ctypes.c_float),
+                ("residualScale", ctypes.c_float), ("datatype", ctypes.c_int), ("weightType", ctypes.c_int)]
+
+
 _lib = None
 
 _SIGNATURES = {
@@ -118,6 +124,9 @@ _SIGNATURES = {
     "vAllReduceRmsNormQuant": ([ctypes.c_void_p] * 10, ctypes.c_int),
     "vRmsNormBackwardWorkspace": ([ctypes.c_void_p] * 3, ctypes.c_int),
     "vAllReduceRmsNormBackward": ([ctypes.c_void_p] * 9 + [ctypes.c_size_t] + [ctypes.c_void_p] * 2, ctypes.c_int),
+    "vAllReduceBlockNorm": ([ctypes.c_void_p] * 12, ctypes.c_int),
+    "vBlockNormBackwardWorkspace": ([ctypes.c_void_p] * 3, ctypes.c_int),
+    "vAllReduceBlockNormBackward": ([ctypes.c_void_p] * 15 + [ctypes.c_size_t] + [ctypes.c_void_p] * 2, ctypes.c_int),
     "vGradListCreate": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_int] + [ctypes.c_void_p] * 5, ctypes.c_int),
     "vGradListDestroy": ([ctypes.c_void_p], ctypes.c_int),
     "vGradNormWorkspace": ([ctypes.c_void_p] * 3, ctypes.c_int),
@@ -478,6 +487,46 @@ def vAllReduceRmsNormBackward(desc, sendbuffs, hidden_states, rstd, weight, grad
                                            _addr(rstd), _addr(weight), _addr(grad_residual), _ptr_array(recvbuffs, n),
                                            _addr(grad_weight), *_workspace(workspace), comm, _stream(stream)),
            "vAllReduceRmsNormBackward")
+
+
+def vBlockNormDesc(rows: int, hidden: int, datatype, weight_type=None, eps: float = 1e-6, residual_scale: float = 1.0,
+                   send_stride: int = 0, residual_stride: int = 0, recv_stride: int = 0) -> vBlockNormDesc_t:
+    """Sizes, strides (in elements, 0 for ``hidden``) and types of a block norm's calls; the weights'
+    type is the data's unless ``weight_type`` says float32."""
+    dt = _dtype_code(datatype)
+    return vBlockNormDesc_t(rows, hidden, send_stride, residual_stride, recv_stride, eps, residual_scale, dt,
+                            dt if weight_type is None else _dtype_code(weight_type))
+
+
+def vAllReduceBlockNorm(desc, sendbuffs, residual, post_weight, gate, pre_weight, block_out, residual_out, recvbuffs, rstd,
+                        comm, stream=None) -> None:
+    """All-reduce, the norm after a block, its gate, the scaled residual and the norm before the next
+    block; residual, gate, block_out, residual_out, rstd and entries of recvbuffs may be None."""
+    n = _n_ranks(comm)
+    _check(lib().vAllReduceBlockNorm(ctypes.addressof(desc), _ptr_array(sendbuffs, n), _addr(residual), _addr(post_weight),
+                                     _addr(gate), _addr(pre_weight), _addr(block_out), _addr(residual_out),
+                                     _ptr_array(recvbuffs, n), _addr(rstd), comm, _stream(stream)), "vAllReduceBlockNorm")
+
+
+def vBlockNormBackwardWorkspace(desc, comm) -> int:
+    """Bytes of workspace that vAllReduceBlockNormBackward needs for this descriptor."""
+    b = ctypes.c_size_t(0)
+    _check(lib().vBlockNormBackwardWorkspace(ctypes.addressof(desc), comm, ctypes.addressof(b)),
+           "vBlockNormBackwardWorkspace")
+    return b.value
+
+
+def vAllReduceBlockNormBackward(desc, sendbuffs, hidden_states, block, rstd, post_weight, gate, pre_weight, grad_stream,
+                                grad_residual, recvbuffs, grad_post_weight, grad_gate, grad_pre_weight, workspace, comm,
+                                stream=None) -> None:
+    """Backward pass of vAllReduceBlockNorm; grad_stream, grad_residual and entries of recvbuffs may be
+    None, grad_gate exactly where gate is."""
+    n = _n_ranks(comm)
+    _check(lib().vAllReduceBlockNormBackward(ctypes.addressof(desc), _ptr_array(sendbuffs, n), _addr(hidden_states),
+                                             _addr(block), _addr(rstd), _addr(post_weight), _addr(gate), _addr(pre_weight),
+                                             _addr(grad_stream), _addr(grad_residual), _ptr_array(recvbuffs, n),
+                                             _addr(grad_post_weight), _addr(grad_gate), _addr(grad_pre_weight),
+                                             *_workspace(workspace), comm, _stream(stream)), "vAllReduceBlockNormBackward")
 
 
 _dropped_lists: list[int] = []       # handles of lists that lost their last reference

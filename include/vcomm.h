@@ -378,6 +378,58 @@ vResult_t vAllReduceRmsNormBackward(const vRmsNormDesc_t* desc, const void* cons
                                     const void* gradResidual, void* const* recvbuffs, void* gradWeight,
                                     void* workspace, size_t workspaceBytes, vcomm_t comm, cudaStream_t stream);
 
+/* The norms after and before a block, with its gate and the residual's scale, behind the
+ * all-reduce of the block's partial sums:
+ *   b = sum over ranks of sendbuffs[r] (in rank order)               per element, in fp32
+ *   n = b * rstd[0] * postWeight,  rstd[0] = 1 / sqrt(mean over the row of b^2 + eps)
+ *   h = residualScale * residual + gate * n
+ *   recvbuffs[r] = h * rstd[1] * preWeight,  rstd[1] = 1 / sqrt(mean over the row of h^2 + eps)
+ * gate is one value per channel, shared by all rows.  blockOut gets b, residualOut h, each
+ * rounded once to the data type; rstd (fp32, [2][rows]) first the block's values, then the
+ * stream's: these are what the backward pass needs.  residual, gate (then 1), blockOut,
+ * residualOut and rstd may be NULL, and so may recvbuffs entries, but not all.
+ * In place: recvbuffs[r] == sendbuffs[r] with equal strides, and residualOut == residual; no
+ * other overlap.  Pointers, strides and values as for vAllReduceRmsNorm. */
+typedef struct {
+    size_t rows;               /* as in vRmsNormDesc_t */
+    size_t hidden;
+    size_t sendStride;         /* elements between the rows of every send buffer; 0: hidden */
+    size_t residualStride;     /* the same of residual, residualOut and blockOut, and of
+                                  hiddenStates, block, gradStream and gradResidual */
+    size_t recvStride;         /* the same of every receive buffer; 0: hidden */
+    float eps;                 /* >= 0, added to both mean squares */
+    float residualScale;       /* finite */
+    vDataType_t datatype;      /* vFloat32, vFloat16 or vBFloat16 */
+    vDataType_t weightType;    /* of both weights, the gate and their gradients: datatype or vFloat32 */
+} vBlockNormDesc_t;
+vResult_t vAllReduceBlockNorm(const vBlockNormDesc_t* desc, const void* const* sendbuffs, const void* residual,
+                              const void* postWeight, const void* gate, const void* preWeight, void* blockOut,
+                              void* residualOut, void* const* recvbuffs, float* rstd, vcomm_t comm, cudaStream_t stream);
+
+/* Backward pass of vAllReduceBlockNorm.  sendbuffs[r] is rank r's partial gradient of the normed
+ * output, hiddenStates and block what the forward pass stored (residualOut, blockOut), gradStream
+ * (may be NULL) the gradient that reaches the stream h by another way:
+ *   dy = sum over ranks of sendbuffs[r],  x2 = hiddenStates * rstd[1],  g2 = dy * preWeight
+ *   dh = rstd[1] * (g2 - x2 * mean(g2 * x2)) + gradStream
+ *   gradResidual = residualScale * dh
+ *   x1 = block * rstd[0],  g1 = dh * gate * postWeight
+ *   recvbuffs[r] = rstd[0] * (g1 - x1 * mean(g1 * x1))
+ *   gradPreWeight = sum over rows of dy * x2,  gradPostWeight = gate * sum over rows of dh * x1,
+ *   gradGate = postWeight * the same sum
+ * The output is the gradient of every rank's partial sum.  gradResidual may be NULL, and so may
+ * recvbuffs entries, but not all; gradGate is NULL exactly where gate is.  In place:
+ * recvbuffs[r] == sendbuffs[r] with equal strides, gradResidual == gradStream; no other overlap.
+ * rows == 0 writes zero weight gradients.  The workspace is at least what
+ * vBlockNormBackwardWorkspace gives for the descriptor, 16-byte aligned, and used by nothing else
+ * until the call's work is done; a smaller one gives vInvalidArgument.  The same call (on buffers
+ * of the same offsets from 16 bytes) gives the same bits. */
+vResult_t vBlockNormBackwardWorkspace(const vBlockNormDesc_t* desc, vcomm_t comm, size_t* bytes);
+vResult_t vAllReduceBlockNormBackward(const vBlockNormDesc_t* desc, const void* const* sendbuffs, const void* hiddenStates,
+                                      const void* block, const float* rstd, const void* postWeight, const void* gate,
+                                      const void* preWeight, const void* gradStream, void* gradResidual,
+                                      void* const* recvbuffs, void* gradPostWeight, void* gradGate, void* gradPreWeight,
+                                      void* workspace, size_t workspaceBytes, vcomm_t comm, cudaStream_t stream);
+
 /* The gradients that a norm is taken over: nTensors tensors on each of nRanks ranks.  A tensor
  * is either split (each rank holds a piece of counts[t] elements: reduce-scattered or
  * tensor-parallel) or replicated (each rank holds all of it: all-reduced).  Any number of
