@@ -22,7 +22,8 @@ LIB = os.path.join(BUILD, "libvcomm.so")
 SOURCES = ["vcomm.cpp", "planner.cpp", "ring_launch.cu", "k_onepass.cu", "k_onepass_small.cu", "k_group.cu", "k_tree.cu", "k_tree_more.cu",
            "k_copy.cu", "k_ring_simple.cu", "k_ring_ll.cu", "k_ring_ll128.cu", "noalloc.cu", "k_tma.cu",
            "operators.cpp", "k_norm.cu", "k_norm_quant.cu", "k_norm_bwd.cu", "k_gradnorm.cu",
-           "block_norm.cpp", "k_block_norm.cu", "k_block_norm_bwd.cu"]
+           "block_norm.cpp", "k_block_norm.cu", "k_block_norm_bwd.cu",
+           "moe.cpp", "k_moe_route.cu", "k_moe_experts.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 

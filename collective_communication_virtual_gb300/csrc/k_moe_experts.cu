@@ -1,0 +1,250 @@
+// k_moe_experts.cu -- the experts' layer of a mixture of experts for a few tokens, the experts split
+// over the ranks.
+//
+//   g = Wgate_e x_t,  u = Wlinear_e x_t,  a = silu(g) u,  silu(g) = g / (1 + exp(-g))
+//   recv_r[t] = sum over the token's chosen experts e of rank r of weight_te Wdown_e a
+//
+// Two launches: the way up (a of every slot, a slot being one choice of one token, into the
+// workspace) and the way down, whose last CTA of a tile of columns adds up every token's slots, in
+// their order, for every rank.  A CTA takes one expert and a tile of output rows, finds the expert's
+// slots in the router's list, and leaves at once if there are none.  A warp takes rows of the weights,
+// one 16-byte vector a lane, against up to eight slots at a time.
+#include "moe.h"
+#include "norm.cuh"
+
+namespace vc {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kGroup = 8;            // slots that a warp takes at once
+constexpr int kRows = 2;             // rows of the weights that it takes at once
+constexpr int kList = 1024;          // slots found before they are worked on
+
+// The slots of expert e, in order, from position `from` on: fills `list` until it may be full, and
+// returns where to go on (>= total: all found).  All threads of the CTA call it.
+__device__ __forceinline__ int find_slots(const int* ids, int total, int e, int from, int* list, int* count) {
+    __shared__ int perWarp[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int n = 0;
+    while (from < total && n + kThreads <= kList) {
+        const int i = from + (int)threadIdx.x;
+        const bool hit = i < total && ids[i] == e;
+        const unsigned in = __ballot_sync(~0u, hit);
+        if (lane == 0) perWarp[warp] = __popc(in);
+        __syncthreads();
+        int at = n;
+        for (int w = 0; w < kWarps; w++) {
+            if (w < warp) at += perWarp[w];
+            n += perWarp[w];
+        }
+        if (hit) list[at + __popc(in & ((1u << lane) - 1))] = i;
+        from += kThreads;
+        __syncthreads();
+    }
+    *count = n;
+    return from;
+}
+
+// A lane's elements of one step along a row: ALIGNED a 16-byte vector from j on, else j + 32 i.
+template <int DT, bool ALIGNED> constexpr int kElems = ALIGNED ? 16 / DTypeOf<DT>::size : 4;
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void load_part(const void* row, int j, int width, float (&f)[kElems<DT, ALIGNED>]) {
+    if constexpr (ALIGNED) {
+        widen_vec<DT>(*reinterpret_cast<const uint4*>((const char*)row + (size_t)j * DTypeOf<DT>::size), f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int e = j + 32 * i;
+            f[i] = 0.0f;
+            if (e >= width) continue;
+            if (DT == kF32) f[i] = ((const float*)row)[e];
+            else f[i] = widen16<DT>(((const uint16_t*)row)[e]);
+        }
+    }
+}
+
+// Dot products of R rows of the weights with n <= G vectors; every lane ends with all of them.
+template <int WT, int XT, bool ALIGNED, int R, int G>
+__device__ __forceinline__ void dots(const char* const (&w)[R], const void* const (&x)[G], int n, int width, float (&acc)[R][G]) {
+    constexpr int E = kElems<WT, ALIGNED>;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int r = 0; r < R; r++)
+#pragma unroll
+        for (int g = 0; g < G; g++) acc[r][g] = 0.0f;
+    for (int j = ALIGNED ? lane * E : lane; j < width; j += ALIGNED ? 32 * E : 128) {
+        float f[R][E];
+#pragma unroll
+        for (int r = 0; r < R; r++) load_part<WT, ALIGNED>(w[r], j, width, f[r]);
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+            if (g >= n) break;
+            float v[E];
+            if constexpr (ALIGNED && WT != kF32 && XT == kF32) {
+                float lo[4], hi[4];
+                load_part<kF32, true>(x[g], j, width, lo);
+                load_part<kF32, true>(x[g], j + 4, width, hi);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    v[i] = lo[i];
+                    v[i + 4] = hi[i];
+                }
+            } else {
+                load_part<XT, ALIGNED>(x[g], j, width, v);
+            }
+#pragma unroll
+            for (int r = 0; r < R; r++)
+#pragma unroll
+                for (int i = 0; i < E; i++) acc[r][g] = fmaf(f[r][i], v[i], acc[r][g]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; r++)
+#pragma unroll
+        for (int g = 0; g < G; g++)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) acc[r][g] += __shfl_xor_sync(~0u, acc[r][g], o);
+}
+
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) k_moe_up(const __grid_constant__ ExpertsArgs a) {
+    pdl_begin();
+    constexpr int ESZ = DTypeOf<DT>::size;
+    __shared__ int list[kList];
+    const int e = (int)blockIdx.y, total = a.rows * a.topK;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (blockIdx.x == 0 && e == 0)
+        for (int i = threadIdx.x; i < (a.hidden + kMoeTile - 1) / kMoeTile; i += kThreads) a.done[i] = 0;
+    const char* base = (const char*)a.up[e / a.share] + (size_t)(e % a.share) * 2 * a.ffn * a.hidden * ESZ;
+    const int f0 = (int)blockIdx.x * kMoeTile, f1 = min(a.ffn, f0 + kMoeTile);
+    for (int from = 0, n; from < total;) {
+        from = find_slots(a.ids, total, e, from, list, &n);
+        for (int g0 = 0; g0 < n; g0 += kGroup) {
+            const int some = min(kGroup, n - g0);
+            const void* x[kGroup];
+#pragma unroll
+            for (int g = 0; g < kGroup; g++)
+                x[g] = (const char*)a.x + (size_t)(list[g0 + min(g, some - 1)] / a.topK) * a.rowStride * ESZ;
+            for (int f = f0 + warp; f < f1; f += kWarps) {
+                const char* const w[kRows] = {base + (size_t)f * a.hidden * ESZ, base + (size_t)(a.ffn + f) * a.hidden * ESZ};
+                float acc[kRows][kGroup];
+                dots<DT, DT, ALIGNED>(w, x, some, a.hidden, acc);
+#pragma unroll
+                for (int g = 0; g < kGroup; g++) {
+                    if (lane != g || g >= some) continue;
+                    a.act[(size_t)list[g0 + g] * a.ffn + f] = acc[0][g] / (1.0f + expf(-acc[0][g])) * acc[1][g];
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Columns [h0, h1) of every rank's output, from all slots' y.
+template <int DT>
+__device__ __forceinline__ void combine(const ExpertsArgs& a, int h0, int h1) {
+    constexpr int ESZ = DTypeOf<DT>::size;
+    const int columns = h1 - h0;
+    for (int i = threadIdx.x; i < a.rows * columns; i += kThreads) {
+        const int t = i / columns, h = h0 + i % columns;
+        const int* ids = a.ids + (size_t)t * a.topK;
+        for (int r = 0; r < a.nRanks; r++) {
+            const int lo = r * a.share, hi = min(a.experts, lo + a.share);
+            float s = 0.0f;
+            for (int k = 0; k < a.topK; k++) {
+                if (ids[k] < lo || ids[k] >= hi) continue;
+                const size_t slot = (size_t)t * a.topK + k;
+                s = fmaf(a.weights[slot], __ldcg(a.y + slot * a.hidden + h), s);
+            }
+            st_elem<ESZ>(a.recv[r], (size_t)t * a.recvStride + h, f32_to_elem<DT>(s));
+        }
+    }
+}
+
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) k_moe_down(const __grid_constant__ ExpertsArgs a) {
+    pdl_begin();
+    constexpr int ESZ = DTypeOf<DT>::size;
+    __shared__ int list[kList];
+    __shared__ unsigned seen[VCOMM_MAX_EXPERTS / 32];
+    __shared__ int last;
+    const int e = (int)blockIdx.y, total = a.rows * a.topK;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int h0 = (int)blockIdx.x * kMoeTile, h1 = min(a.hidden, h0 + kMoeTile);
+    const char* base = (const char*)a.down[e / a.share] + (size_t)(e % a.share) * a.hidden * a.ffn * ESZ;
+    int found = 0;
+    for (int from = 0, n; from < total;) {
+        from = find_slots(a.ids, total, e, from, list, &n);
+        found += n;
+        for (int g0 = 0; g0 < n; g0 += kGroup) {
+            const int some = min(kGroup, n - g0);
+            const void* x[kGroup];
+#pragma unroll
+            for (int g = 0; g < kGroup; g++) x[g] = a.act + (size_t)list[g0 + min(g, some - 1)] * a.ffn;
+            for (int h = h0 + kRows * warp; h < h1; h += kRows * kWarps) {
+                const char* const w[kRows] = {base + (size_t)h * a.ffn * ESZ, base + (size_t)min(h + 1, h1 - 1) * a.ffn * ESZ};
+                float acc[kRows][kGroup];
+                dots<DT, kF32, ALIGNED>(w, x, some, a.ffn, acc);
+#pragma unroll
+                for (int g = 0; g < kGroup; g++) {
+                    if (lane != g || g >= some) continue;
+#pragma unroll
+                    for (int r = 0; r < kRows; r++)
+                        if (h + r < h1) a.y[(size_t)list[g0 + g] * a.hidden + h + r] = acc[r][g];
+                }
+            }
+        }
+        __syncthreads();
+    }
+    // The experts that some slot names; where there are none, the first CTA writes the zeros.
+    for (int i = threadIdx.x; i < VCOMM_MAX_EXPERTS / 32; i += kThreads) seen[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < total; i += kThreads) {
+        const int id = a.ids[i];
+        if (id >= 0 && id < a.experts) atomicOr(&seen[id / 32], 1u << (id % 32));
+    }
+    __syncthreads();
+    int active = 0;
+    for (int i = 0; i < VCOMM_MAX_EXPERTS / 32; i++) active += __popc(seen[i]);
+    if (found == 0 && !(active == 0 && e == 0)) return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = active == 0 || atomicAdd(&a.done[blockIdx.x], 1u) == (unsigned)active - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    combine<DT>(a, h0, h1);
+}
+
+template <int DT, bool ALIGNED>
+cudaError_t experts_launch(const ExpertsArgs& a, cudaStream_t s) {
+    const auto run = [&](auto kernel, int columns) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)((columns + kMoeTile - 1) / kMoeTile), (unsigned)a.experts);
+        cfg.blockDim = dim3(kThreads);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = pdl_enabled() ? 1 : 0;
+        return cudaLaunchKernelEx(&cfg, kernel, a);
+    };
+    const cudaError_t e = run(k_moe_up<DT, ALIGNED>, a.ffn);
+    return e != cudaSuccess ? e : run(k_moe_down<DT, ALIGNED>, a.hidden);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_experts(const ExpertsArgs& a, vDataType_t dt, cudaStream_t s) {
+    switch (dt) {
+    case vFloat32: return a.aligned ? experts_launch<kF32, true>(a, s) : experts_launch<kF32, false>(a, s);
+    case vFloat16: return a.aligned ? experts_launch<kF16, true>(a, s) : experts_launch<kF16, false>(a, s);
+    case vBFloat16: return a.aligned ? experts_launch<kBF16, true>(a, s) : experts_launch<kBF16, false>(a, s);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace vc

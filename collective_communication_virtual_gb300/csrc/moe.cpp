@@ -1,0 +1,178 @@
+// moe.cpp -- entry points of the mixture-of-experts operators.
+#include <cstdio>
+#include <vector>
+
+#include "entry.h"
+#include "moe.h"
+
+namespace {
+
+struct Moe {
+    vMoeDesc_t d;                    // strides filled in
+    int esz;
+    int share;                       // experts of a rank
+    size_t slots;
+};
+
+vResult_t check_moe(const vMoeDesc_t* desc, int nRanks, Moe* m) {
+    if (!desc) return vInvalidArgument;
+    vMoeDesc_t& d = m->d;
+    d = *desc;
+    if (!is_float(d.datatype)) return vInvalidArgument;
+    if (d.routerType != vFloat32 && d.routerType != d.datatype) return vInvalidArgument;
+    if (d.rows > VCOMM_MAX_MOE_ROWS || d.hidden > VCOMM_MAX_HIDDEN || d.ffn > VCOMM_MAX_HIDDEN) return vInvalidArgument;
+    if (d.experts < 1 || d.experts > VCOMM_MAX_EXPERTS) return vInvalidArgument;
+    if (d.topK < 1 || d.topK > VCOMM_MAX_TOPK || d.topK > d.experts) return vInvalidArgument;
+    for (size_t* s : {&d.rowStride, &d.recvStride}) {
+        if (*s == 0) *s = d.hidden;
+        if (*s < d.hidden || *s > ((size_t)1 << 62) / (4 * VCOMM_MAX_MOE_ROWS)) return vInvalidArgument;
+    }
+    m->esz = (int)vc::dtype_size(d.datatype);
+    m->share = (d.experts + nRanks - 1) / nRanks;
+    m->slots = d.rows * (size_t)d.topK;
+    return vSuccess;
+}
+
+// Bytes of the workspace's parts, in their order: act, y, the tiles' counters.
+struct Layout {
+    size_t act, y, done;
+    explicit Layout(const Moe& m)
+        : act((m.slots * m.d.ffn * 4 + 255) / 256 * 256),
+          y((m.slots * m.d.hidden * 4 + 255) / 256 * 256),
+          done((m.d.hidden + vc::kMoeTile - 1) / vc::kMoeTile * 4) {}
+    size_t total() const { return act + y + done + 16; }
+};
+
+vResult_t route(const vMoeDesc_t* desc, const void* x, const void* router, const float* bias, int* ids, float* weights,
+                vcomm_t c, cudaStream_t stream) {
+    CommView v;
+    vResult_t r = comm_view(c, &v);
+    if (r != vSuccess) return r;
+    Moe m;
+    if ((r = check_moe(desc, v.nRanks, &m)) != vSuccess) return r;
+    if (v.grouping) {
+        const vMoeDesc_t d = *desc;
+        return vc::comm_record(c, [=]() {
+            return guarded([&]() { return route(&d, x, router, bias, ids, weights, c, stream); });
+        });
+    }
+    if (m.d.rows == 0) return vSuccess;
+    if (m.d.hidden == 0) return vInvalidArgument;
+    const size_t wsz = vc::dtype_size(m.d.routerType);
+    if (!x || !at(x, m.esz) || !router || !at(router, wsz) || !at(bias, 4)) return vInvalidArgument;
+    if (!ids || !at(ids, 4) || !weights || !at(weights, 4)) return vInvalidArgument;
+    vc::RouteArgs a;
+    a.x = x;
+    a.router = router;
+    a.bias = bias;
+    a.ids = ids;
+    a.weights = weights;
+    a.rowStride = m.d.rowStride;
+    a.rows = (int)m.d.rows;
+    a.hidden = (int)m.d.hidden;
+    a.experts = m.d.experts;
+    a.topK = m.d.topK;
+    a.tokens = a.rows >= 8 ? 8 : a.rows >= 4 ? 4 : a.rows >= 2 ? 2 : 1;
+    // an expert for every warp, as far as a cluster goes
+    a.cluster = 1;
+    while (a.cluster < vc::kRouteCluster && a.cluster * (vc::kRouteThreads / 32) < a.experts) a.cluster *= 2;
+    a.share = (a.experts + a.cluster - 1) / a.cluster;
+    a.routerF32 = m.d.routerType == vFloat32;
+    a.normalize = m.d.normalize != 0;
+    const size_t e = 16 / (size_t)m.esz;
+    a.aligned = m.d.hidden % 8 == 0 && (a.rows == 1 || m.d.rowStride % e == 0) && at(x, 16) && at(router, 16);
+    if (v.debug)
+        std::fprintf(stderr, "vcomm INFO MoeRoute rows=%d hidden=%d experts=%d topK=%d tokens=%d cluster=%d aligned=%d\n", a.rows,
+                     a.hidden, a.experts, a.topK, a.tokens, a.cluster, a.aligned);
+    return comm_launch(c, "moe route", [&]() { return vc::launch_moe_route(a, m.d.datatype, stream); });
+}
+
+vResult_t experts(const vMoeDesc_t* desc, const void* x, const int* ids, const float* weights, const void* const* up,
+                  const void* const* down, void* const* recv, void* workspace, size_t workspaceBytes, vcomm_t c,
+                  cudaStream_t stream) {
+    CommView v;
+    vResult_t r = comm_view(c, &v);
+    if (r != vSuccess) return r;
+    Moe m;
+    if ((r = check_moe(desc, v.nRanks, &m)) != vSuccess) return r;
+    if (v.grouping) {
+        if (!up || !down || !recv) return vInvalidArgument;
+        const vMoeDesc_t d = *desc;
+        const std::vector<const void*> u(up, up + v.nRanks), w(down, down + v.nRanks);
+        const std::vector<void*> o(recv, recv + v.nRanks);
+        return vc::comm_record(c, [=]() {
+            return guarded([&]() {
+                return experts(&d, x, ids, weights, u.data(), w.data(), o.data(), workspace, workspaceBytes, c, stream);
+            });
+        });
+    }
+    if (m.d.rows == 0 || m.d.hidden == 0) return vSuccess;
+    if (m.d.ffn == 0) return vInvalidArgument;
+    if (!x || !at(x, m.esz) || !ids || !at(ids, 4) || !weights || !at(weights, 4) || !up || !down || !recv)
+        return vInvalidArgument;
+    vc::ExpertsArgs a;
+    const size_t e = 16 / (size_t)m.esz;
+    a.aligned = m.d.hidden % e == 0 && m.d.ffn % e == 0 && (m.d.rows == 1 || m.d.rowStride % e == 0) && at(x, 16);
+    for (int k = 0; k < v.nRanks; k++) {
+        const bool holds = k * m.share < m.d.experts;  // else its weights are not looked at
+        if (holds && (!up[k] || !at(up[k], m.esz) || !down[k] || !at(down[k], m.esz))) return vInvalidArgument;
+        if (!recv[k] || !at(recv[k], m.esz)) return vInvalidArgument;
+        a.up[k] = up[k];
+        a.down[k] = down[k];
+        a.recv[k] = recv[k];
+        if (holds) a.aligned = a.aligned && at(up[k], 16) && at(down[k], 16);
+    }
+    const Layout l(m);
+    if (!workspace || !at(workspace, 16) || workspaceBytes < l.total()) return vInvalidArgument;
+    a.x = x;
+    a.ids = ids;
+    a.weights = weights;
+    a.act = (float*)workspace;
+    a.y = (float*)((char*)workspace + l.act);
+    a.done = (unsigned int*)((char*)workspace + l.act + l.y);
+    a.rowStride = m.d.rowStride;
+    a.recvStride = m.d.recvStride;
+    a.rows = (int)m.d.rows;
+    a.hidden = (int)m.d.hidden;
+    a.ffn = (int)m.d.ffn;
+    a.experts = m.d.experts;
+    a.topK = m.d.topK;
+    a.nRanks = v.nRanks;
+    a.share = m.share;
+    if (v.debug)
+        std::fprintf(stderr, "vcomm INFO MoeExperts rows=%d hidden=%d ffn=%d experts=%d topK=%d N=%d aligned=%d\n", a.rows,
+                     a.hidden, a.ffn, a.experts, a.topK, a.nRanks, a.aligned);
+    return comm_launch(c, "moe experts", [&]() { return vc::launch_moe_experts(a, m.d.datatype, stream); });
+}
+
+}  // namespace
+
+extern "C" {
+
+vResult_t vMoeRoute(const vMoeDesc_t* desc, const void* x, const void* routerWeight, const float* bias, int32_t* expertIds,
+                    float* expertWeights, vcomm_t comm, cudaStream_t stream) {
+    Range range("vMoeRoute");
+    return guarded([&]() { return route(desc, x, routerWeight, bias, expertIds, expertWeights, comm, stream); });
+}
+
+vResult_t vMoeExpertsWorkspace(const vMoeDesc_t* desc, vcomm_t comm, size_t* bytes) {
+    CommView v;
+    vResult_t r = comm_view(comm, &v);
+    if (r != vSuccess) return r;
+    Moe m;
+    if ((r = check_moe(desc, v.nRanks, &m)) != vSuccess) return r;
+    if (!bytes) return vInvalidArgument;
+    *bytes = Layout(m).total();
+    return vSuccess;
+}
+
+vResult_t vMoeExperts(const vMoeDesc_t* desc, const void* x, const int32_t* expertIds, const float* expertWeights,
+                      const void* const* upbuffs, const void* const* downbuffs, void* const* recvbuffs, void* workspace,
+                      size_t workspaceBytes, vcomm_t comm, cudaStream_t stream) {
+    Range range("vMoeExperts");
+    return guarded([&]() {
+        return experts(desc, x, expertIds, expertWeights, upbuffs, downbuffs, recvbuffs, workspace, workspaceBytes, comm, stream);
+    });
+}
+
+}  // extern "C"

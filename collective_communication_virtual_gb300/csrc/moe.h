@@ -1,0 +1,49 @@
+// moe.h -- argument blocks and launchers of the mixture-of-experts operators: the router, and the
+// experts' layer for a few tokens.
+#pragma once
+
+#include "operators.h"
+
+namespace vc {
+
+constexpr int kRouteTokens = 8;      // tokens that a cluster of the router's CTAs takes at most
+constexpr int kRouteCluster = 8;
+constexpr int kRouteThreads = 256;
+
+struct RouteArgs {
+    const void* x;
+    const void* router;              // [experts][hidden]
+    const float* bias;               // may be NULL
+    int* ids;                        // [rows][topK]
+    float* weights;
+    size_t rowStride;
+    int rows, hidden, experts, topK;
+    int tokens;                      // of a cluster: 1, 2, 4 or 8
+    int cluster;                     // CTAs that share the experts
+    int share;                       // experts of a CTA
+    int routerF32;
+    int normalize;
+    int aligned;                     // every row of x and of the router starts on 16 bytes and ends with a vector
+};
+cudaError_t launch_moe_route(const RouteArgs& a, vDataType_t dt, cudaStream_t s);
+
+struct ExpertsArgs {
+    const void* up[VCOMM_MAX_RANKS];     // [the rank's experts][2 ffn][hidden]: the gate's rows, then the linear part's
+    const void* down[VCOMM_MAX_RANKS];   // [the rank's experts][hidden][ffn]
+    void* recv[VCOMM_MAX_RANKS];         // [rows][hidden], rank r's part of the sum
+    const void* x;
+    const int* ids;                  // [rows][topK]
+    const float* weights;
+    float* act;                      // workspace: [rows * topK][ffn], what goes into the way down
+    float* y;                        // workspace: [rows * topK][hidden], every slot's output
+    unsigned int* done;              // workspace: experts that have finished a tile of columns
+    size_t rowStride, recvStride;
+    int rows, hidden, ffn, experts, topK;
+    int nRanks;
+    int share;                       // experts of a rank
+    int aligned;                     // every row of x and of the weights starts on 16 bytes and ends with a vector
+};
+constexpr int kMoeTile = 32;         // output columns of a CTA in both launches
+cudaError_t launch_moe_experts(const ExpertsArgs& a, vDataType_t dt, cudaStream_t s);
+
+}  // namespace vc

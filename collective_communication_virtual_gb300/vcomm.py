@@ -75,6 +75,12 @@ class vBlockNormDesc_t(ctypes.Structure):
                 ("residualScale", ctypes.c_float), ("datatype", ctypes.c_int), ("weightType", ctypes.c_int)]
 
 
+class vMoeDesc_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_size_t), ("hidden", ctypes.c_size_t), ("ffn", ctypes.c_size_t), ("experts", ctypes.c_int),
+                ("topK", ctypes.c_int), ("rowStride", ctypes.c_size_t), ("recvStride", ctypes.c_size_t),
+                ("datatype", ctypes.c_int), ("routerType", ctypes.c_int), ("normalize", ctypes.c_int)]
+
+
 _lib = None
 
 _SIGNATURES = {
@@ -127,6 +133,9 @@ _SIGNATURES = {
     "vAllReduceBlockNorm": ([ctypes.c_void_p] * 12, ctypes.c_int),
     "vBlockNormBackwardWorkspace": ([ctypes.c_void_p] * 3, ctypes.c_int),
     "vAllReduceBlockNormBackward": ([ctypes.c_void_p] * 15 + [ctypes.c_size_t] + [ctypes.c_void_p] * 2, ctypes.c_int),
+    "vMoeRoute": ([ctypes.c_void_p] * 8, ctypes.c_int),
+    "vMoeExpertsWorkspace": ([ctypes.c_void_p] * 3, ctypes.c_int),
+    "vMoeExperts": ([ctypes.c_void_p] * 8 + [ctypes.c_size_t] + [ctypes.c_void_p] * 2, ctypes.c_int),
     "vGradListCreate": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_int] + [ctypes.c_void_p] * 5, ctypes.c_int),
     "vGradListDestroy": ([ctypes.c_void_p], ctypes.c_int),
     "vGradNormWorkspace": ([ctypes.c_void_p] * 3, ctypes.c_int),
@@ -527,6 +536,36 @@ def vAllReduceBlockNormBackward(desc, sendbuffs, hidden_states, block, rstd, pos
                                              _addr(grad_stream), _addr(grad_residual), _ptr_array(recvbuffs, n),
                                              _addr(grad_post_weight), _addr(grad_gate), _addr(grad_pre_weight),
                                              *_workspace(workspace), comm, _stream(stream)), "vAllReduceBlockNormBackward")
+
+
+def vMoeDesc(rows: int, hidden: int, ffn: int, experts: int, top_k: int, datatype, router_type=None, normalize: bool = True,
+             row_stride: int = 0, recv_stride: int = 0) -> vMoeDesc_t:
+    """Sizes, strides (in elements, 0 for ``hidden``) and types of a mixture of experts; the router's
+    type is the data's unless ``router_type`` says float32."""
+    dt = _dtype_code(datatype)
+    return vMoeDesc_t(rows, hidden, ffn, experts, top_k, row_stride, recv_stride, dt,
+                      dt if router_type is None else _dtype_code(router_type), int(normalize))
+
+
+def vMoeRoute(desc, x, router_weight, bias, expert_ids, expert_weights, comm, stream=None) -> None:
+    """Every token's best experts (int32) and their weights (fp32); bias may be None."""
+    _check(lib().vMoeRoute(ctypes.addressof(desc), _addr(x), _addr(router_weight), _addr(bias), _addr(expert_ids),
+                           _addr(expert_weights), comm, _stream(stream)), "vMoeRoute")
+
+
+def vMoeExpertsWorkspace(desc, comm) -> int:
+    """Bytes of workspace that vMoeExperts needs for this descriptor."""
+    b = ctypes.c_size_t(0)
+    _check(lib().vMoeExpertsWorkspace(ctypes.addressof(desc), comm, ctypes.addressof(b)), "vMoeExpertsWorkspace")
+    return b.value
+
+
+def vMoeExperts(desc, x, expert_ids, expert_weights, upbuffs, downbuffs, recvbuffs, workspace, comm, stream=None) -> None:
+    """Every rank's experts applied to the tokens that chose them: partial sums, one per rank."""
+    n = _n_ranks(comm)
+    _check(lib().vMoeExperts(ctypes.addressof(desc), _addr(x), _addr(expert_ids), _addr(expert_weights),
+                             _ptr_array(upbuffs, n), _ptr_array(downbuffs, n), _ptr_array(recvbuffs, n),
+                             *_workspace(workspace), comm, _stream(stream)), "vMoeExperts")
 
 
 _dropped_lists: list[int] = []       # handles of lists that lost their last reference

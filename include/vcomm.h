@@ -430,6 +430,53 @@ vResult_t vAllReduceBlockNormBackward(const vBlockNormDesc_t* desc, const void* 
                                       void* const* recvbuffs, void* gradPostWeight, void* gradGate, void* gradPreWeight,
                                       void* workspace, size_t workspaceBytes, vcomm_t comm, cudaStream_t stream);
 
+/* A mixture of experts for a few tokens.  The tokens x are the same on every rank (a norm's output),
+ * so they are passed once; the experts are split over the ranks: with share = ceil(experts /
+ * nRanks), rank r holds experts [r * share, (r + 1) * share), the last ranks fewer or none. */
+#define VCOMM_MAX_MOE_ROWS 1024
+#define VCOMM_MAX_EXPERTS 1024
+#define VCOMM_MAX_TOPK 32
+
+typedef struct {
+    size_t rows;               /* tokens, at most VCOMM_MAX_MOE_ROWS; 0 does nothing */
+    size_t hidden;             /* elements of a token, at most VCOMM_MAX_HIDDEN */
+    size_t ffn;                /* inner width of an expert, at most VCOMM_MAX_HIDDEN */
+    int experts;               /* of all ranks together, at most VCOMM_MAX_EXPERTS */
+    int topK;                  /* experts that a token goes to: at most VCOMM_MAX_TOPK, and experts */
+    size_t rowStride;          /* elements between the rows of x; 0: hidden */
+    size_t recvStride;         /* the same of every receive buffer; 0: hidden */
+    vDataType_t datatype;      /* vFloat32, vFloat16 or vBFloat16: of x, the experts and the outputs */
+    vDataType_t routerType;    /* of the router's weight: datatype or vFloat32 */
+    int normalize;             /* the router's weights add up to 1 over the chosen experts (else over
+                                  all experts) */
+} vMoeDesc_t;
+
+/* The router.  logits = x * routerWeight^T (routerWeight: [experts][hidden], without gaps), score =
+ * logits + bias (fp32, [experts], may be NULL: it takes part in the choice alone).
+ * expertIds[t][k] (int32, [rows][topK]) is the expert with the k-th largest score, ties to the lower
+ * index and a NaN last; expertWeights[t][k] (fp32) = exp(logit of it) / sum of exp(logits), over
+ * the chosen experts or all (normalize).  Where fp32 sums leave open which of two scores is the
+ * larger, their logits are computed anew with twice the digits, so the choice is that of exact
+ * sums but for scores closer than about 2^-45 of their products' magnitudes. */
+vResult_t vMoeRoute(const vMoeDesc_t* desc, const void* x, const void* routerWeight, const float* bias,
+                    int32_t* expertIds, float* expertWeights, vcomm_t comm, cudaStream_t stream);
+
+/* The experts' layer.  upbuffs[r] holds rank r's experts' [2 * ffn][hidden] matrices (the gate's rows
+ * first, then the linear part's), downbuffs[r] their [hidden][ffn] ones, without gaps:
+ *   g = gate_e * x[t],  u = linear_e * x[t],  a = g / (1 + exp(-g)) * u
+ *   recvbuffs[r][t] = sum over k with expertIds[t][k] = e held by rank r of
+ *                     expertWeights[t][k] * (down_e * a)
+ * in the order of k and in fp32, rounded once: the ranks' partial sums, which vAllReduceRmsNorm or
+ * vAllReduceBlockNorm adds up.  A token that goes to no expert of a rank gets zeros there.  An id
+ * outside [0, experts) is no expert (padding); an expert named twice counts twice.  A rank that
+ * holds no expert may pass NULL weights; every recvbuffs entry is written.  Outputs overlap no
+ * input.  The workspace is at least what vMoeExpertsWorkspace gives for the descriptor, 16-byte
+ * aligned, and used by nothing else until the call's work is done. */
+vResult_t vMoeExpertsWorkspace(const vMoeDesc_t* desc, vcomm_t comm, size_t* bytes);
+vResult_t vMoeExperts(const vMoeDesc_t* desc, const void* x, const int32_t* expertIds, const float* expertWeights,
+                      const void* const* upbuffs, const void* const* downbuffs, void* const* recvbuffs,
+                      void* workspace, size_t workspaceBytes, vcomm_t comm, cudaStream_t stream);
+
 /* The gradients that a norm is taken over: nTensors tensors on each of nRanks ranks.  A tensor
  * is either split (each rank holds a piece of counts[t] elements: reduce-scattered or
  * tensor-parallel) or replicated (each rank holds all of it: all-reduced).  Any number of
