@@ -1,0 +1,30 @@
+// sample.h -- argument block and launcher of the sampling from split logits.
+#pragma once
+
+#include "operators.h"
+
+namespace vc {
+
+constexpr int kSampleThreads = 512;
+constexpr int kSampleCluster = 8;
+constexpr int kSampleBins = 2048;
+
+struct SampleArgs {
+    const void* logits[VCOMM_MAX_RANKS];     // rank r: columns [r part, (r + 1) part) of every row
+    int* tokens[VCOMM_MAX_RANKS];            // the nOut outputs that are wanted
+    const float* temperature;                // these four may be NULL
+    const int* topK;
+    const float* topP;
+    const float* minP;
+    const float* uniform;
+    float* logprob;                          // may be NULL
+    size_t stride;                           // elements between rows
+    int rows, vocab, part;
+    int nOut;
+    int cluster;                             // CTAs that share a row
+    int steps;                               // 16-byte vectors of a thread
+    int aligned;                             // every row of every rank starts on 16 bytes
+};
+cudaError_t launch_sample(const SampleArgs& a, vDataType_t dt, cudaStream_t s);
+
+}  // namespace vc

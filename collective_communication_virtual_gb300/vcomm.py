@@ -81,6 +81,11 @@ class vMoeDesc_t(ctypes.Structure):
                 ("datatype", ctypes.c_int), ("routerType", ctypes.c_int), ("normalize", ctypes.c_int)]
 
 
+class vSampleDesc_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_size_t), ("vocab", ctypes.c_size_t), ("part", ctypes.c_size_t), ("stride", ctypes.c_size_t),
+                ("datatype", ctypes.c_int)]
+
+
 _lib = None
 
 _SIGNATURES = {
@@ -136,6 +141,7 @@ _SIGNATURES = {
     "vMoeRoute": ([ctypes.c_void_p] * 8, ctypes.c_int),
     "vMoeExpertsWorkspace": ([ctypes.c_void_p] * 3, ctypes.c_int),
     "vMoeExperts": ([ctypes.c_void_p] * 8 + [ctypes.c_size_t] + [ctypes.c_void_p] * 2, ctypes.c_int),
+    "vSample": ([ctypes.c_void_p] * 11, ctypes.c_int),
     "vGradListCreate": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_int] + [ctypes.c_void_p] * 5, ctypes.c_int),
     "vGradListDestroy": ([ctypes.c_void_p], ctypes.c_int),
     "vGradNormWorkspace": ([ctypes.c_void_p] * 3, ctypes.c_int),
@@ -566,6 +572,20 @@ def vMoeExperts(desc, x, expert_ids, expert_weights, upbuffs, downbuffs, recvbuf
     _check(lib().vMoeExperts(ctypes.addressof(desc), _addr(x), _addr(expert_ids), _addr(expert_weights),
                              _ptr_array(upbuffs, n), _ptr_array(downbuffs, n), _ptr_array(recvbuffs, n),
                              *_workspace(workspace), comm, _stream(stream)), "vMoeExperts")
+
+
+def vSampleDesc(rows: int, vocab: int, datatype, part: int = 0, stride: int = 0) -> vSampleDesc_t:
+    """Sizes of a draw from split logits: ``part`` columns a rank (0: an equal share), rows ``stride``
+    elements apart (0: ``part``)."""
+    return vSampleDesc_t(rows, vocab, part, stride, _dtype_code(datatype))
+
+
+def vSample(desc, logitbuffs, temperature, top_k, top_p, min_p, uniform, tokenbuffs, logprob, comm, stream=None) -> None:
+    """One token a row; temperature, top_k, top_p, min_p, logprob and entries of tokenbuffs may be None."""
+    n = _n_ranks(comm)
+    _check(lib().vSample(ctypes.addressof(desc), _ptr_array(logitbuffs, n), _addr(temperature), _addr(top_k), _addr(top_p),
+                         _addr(min_p), _addr(uniform), _ptr_array(tokenbuffs, n), _addr(logprob), comm, _stream(stream)),
+           "vSample")
 
 
 _dropped_lists: list[int] = []       # handles of lists that lost their last reference

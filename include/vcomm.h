@@ -477,6 +477,38 @@ vResult_t vMoeExperts(const vMoeDesc_t* desc, const void* x, const int32_t* expe
                       const void* const* upbuffs, const void* const* downbuffs, void* const* recvbuffs,
                       void* workspace, size_t workspaceBytes, vcomm_t comm, cudaStream_t stream);
 
+/* One token for every row of logits whose vocabulary is split over the ranks: logitbuffs[r] holds
+ * columns [r * part, (r + 1) * part) of every row, those below vocab.  temperature, topP, minP and
+ * uniform are fp32, topK int32, one value a row, in device memory; all but uniform may be NULL.
+ *   e_i = exp((logit_i - max) / temperature), all filters in the order of the largest e, ties to the
+ *   lower index: the topK first (<= 0: all); of those the shortest run whose sum reaches topP times
+ *   theirs, at least one (topP >= 1 or NaN: all); of those the ones with e_i >= minP, which at most
+ *   leaves the largest (<= 0 or NaN: all).
+ *   token = the first kept index i, in the vocabulary's order, with
+ *           (sum of kept e up to i) > uniform * (sum of kept e)
+ * A temperature that is not above zero takes the largest logit, the first of equals, without a
+ * draw.  uniform lies in [0, 1); other values act as the nearest one, a NaN as 0.  Sums are
+ * taken in units of 2^-44, of e right to 2^-30 of itself, and the same call gives the same tokens.
+ * tokenbuffs[r] (int32, one a row) may be NULL for ranks that want none, but not all; logprob (fp32,
+ * one a row, may be NULL) = log of the token's share of all e before the filters (temperature 1 where
+ * the largest is taken).
+ * Logits of minus infinity and NaN are never drawn; infinite ones share the draw alone.  A row in
+ * which nothing is left gives the token -1 and a NaN. */
+#define VCOMM_MAX_VOCAB 262144
+#define VCOMM_MAX_SAMPLE_ROWS 16777216
+
+typedef struct {
+    size_t rows;               /* at most VCOMM_MAX_SAMPLE_ROWS; 0 does nothing */
+    size_t vocab;              /* tokens to draw from, 1 to VCOMM_MAX_VOCAB */
+    size_t part;               /* columns of a rank; 0: ceil(vocab / nRanks).  A rank all of whose columns
+                                  lie behind vocab may pass a NULL buffer */
+    size_t stride;             /* elements between the rows of every logit buffer; 0: part */
+    vDataType_t datatype;      /* vFloat32, vFloat16 or vBFloat16 */
+} vSampleDesc_t;
+vResult_t vSample(const vSampleDesc_t* desc, const void* const* logitbuffs, const float* temperature,
+                  const int32_t* topK, const float* topP, const float* minP, const float* uniform,
+                  int32_t* const* tokenbuffs, float* logprob, vcomm_t comm, cudaStream_t stream);
+
 /* The gradients that a norm is taken over: nTensors tensors on each of nRanks ranks.  A tensor
  * is either split (each rank holds a piece of counts[t] elements: reduce-scattered or
  * tensor-parallel) or replicated (each rank holds all of it: all-reduced).  Any number of
