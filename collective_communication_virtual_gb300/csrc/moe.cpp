@@ -72,18 +72,19 @@ vResult_t route(const vMoeDesc_t* desc, const void* x, const void* router, const
     a.hidden = (int)m.d.hidden;
     a.experts = m.d.experts;
     a.topK = m.d.topK;
-    a.tokens = a.rows >= 8 ? 8 : a.rows >= 4 ? 4 : a.rows >= 2 ? 2 : 1;
-    // an expert for every warp, as far as a cluster goes
+    // an expert for every warp, or a pass of experts for every CTA, as far as a cluster goes
+    const bool few = a.rows <= vc::kRouteFew;
+    const int each = few ? vc::kRouteThreads / 32 : vc::kRouteTileThreads / 16;
     a.cluster = 1;
-    while (a.cluster < vc::kRouteCluster && a.cluster * (vc::kRouteThreads / 32) < a.experts) a.cluster *= 2;
+    while (a.cluster < (few ? vc::kRouteCluster : vc::kRouteTileCluster) && a.cluster * each < a.experts) a.cluster *= 2;
     a.share = (a.experts + a.cluster - 1) / a.cluster;
     a.routerF32 = m.d.routerType == vFloat32;
     a.normalize = m.d.normalize != 0;
     const size_t e = 16 / (size_t)m.esz;
     a.aligned = m.d.hidden % 8 == 0 && (a.rows == 1 || m.d.rowStride % e == 0) && at(x, 16) && at(router, 16);
     if (v.debug)
-        std::fprintf(stderr, "vcomm INFO MoeRoute rows=%d hidden=%d experts=%d topK=%d tokens=%d cluster=%d aligned=%d\n", a.rows,
-                     a.hidden, a.experts, a.topK, a.tokens, a.cluster, a.aligned);
+        std::fprintf(stderr, "vcomm INFO MoeRoute rows=%d hidden=%d experts=%d topK=%d cluster=%d aligned=%d\n", a.rows,
+                     a.hidden, a.experts, a.topK, a.cluster, a.aligned);
     return comm_launch(c, "moe route", [&]() { return vc::launch_moe_route(a, m.d.datatype, stream); });
 }
 

@@ -6,9 +6,13 @@
 
 namespace vc {
 
-constexpr int kRouteTokens = 8;      // tokens that a cluster of the router's CTAs takes at most
-constexpr int kRouteCluster = 8;
+constexpr int kRouteFew = 4;         // tokens up to which a warp takes an expert's whole row
+constexpr int kRouteTile = 8;        // tokens of a cluster beyond that
+constexpr int kRouteCluster = 8;     // CTAs of a cluster, at most, for a few tokens,
+constexpr int kRouteTileCluster = 4; // and beyond them: larger ones do not fill the SMs at one CTA on each
 constexpr int kRouteThreads = 256;
+constexpr int kRouteTileThreads = 512;
+constexpr int kRouteMaxSmem = 180 * 1024;
 
 struct RouteArgs {
     const void* x;
@@ -18,7 +22,6 @@ struct RouteArgs {
     float* weights;
     size_t rowStride;
     int rows, hidden, experts, topK;
-    int tokens;                      // of a cluster: 1, 2, 4 or 8
     int cluster;                     // CTAs that share the experts
     int share;                       // experts of a CTA
     int routerF32;

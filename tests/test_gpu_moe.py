@@ -58,9 +58,14 @@ def run_route(comm, rows, hidden, experts, k, dtype, wtype, seed, normalize=True
     logits = x.double() @ w.double().t()
     want, share = choose(logits, b, k, normalize)
     assert torch.equal(ids[:rows * k].cpu().view(rows, k).long(), want)
-    # the logits are rounded to fp32 as differences, exp and the quotient add a few u each
+    # the logits are rounded to fp32 as differences, exp and the quotient add a few u each.  The logits
+    # that no choice hangs on are sums of up to 32 products in two fp32 chains: 17 roundings a product,
+    # so up to 17 u of the products' magnitudes off, which add up to at most |x| |w|; a weight depends on
+    # its own logit and on those that it is a share of.  (The first version of this bound left that out:
+    # with logits of 20, sums of 64 products of 1 and more, it allowed 30 u, where they take up 17 * 64.)
     got = weights[:rows * k].cpu().double().view(rows, k)
-    slack = share * R.U32 * (16 + 2 * (logits.gather(1, want) - logits.amax(1, keepdim=True)).abs())
+    sums = 2 * 17 * x.double().norm(dim=1, keepdim=True) * w.double().norm(dim=1).max()
+    slack = share * R.U32 * (16 + 2 * (logits.gather(1, want) - logits.amax(1, keepdim=True)).abs() + sums)
     assert ((got - share).abs() <= slack + 1e-38).all()
     assert (ids[rows * k:] == -7).all() and (weights[rows * k:] == CANARY).all()
 
