@@ -23,7 +23,7 @@ SOURCES = ["vcomm.cpp", "planner.cpp", "ring_launch.cu", "k_onepass.cu", "k_onep
            "k_copy.cu", "k_ring_simple.cu", "k_ring_ll.cu", "k_ring_ll128.cu", "noalloc.cu", "k_tma.cu",
            "operators.cpp", "k_norm.cu", "k_norm_quant.cu", "k_norm_bwd.cu", "k_gradnorm.cu",
            "block_norm.cpp", "k_block_norm.cu", "k_block_norm_bwd.cu",
-           "moe.cpp", "k_moe_route.cu", "k_moe_experts.cu", "sample.cpp", "k_sample.cu"]
+           "moe.cpp", "k_moe_route.cu", "k_moe_experts.cu", "k_moe_tiles.cu", "sample.cpp", "k_sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 

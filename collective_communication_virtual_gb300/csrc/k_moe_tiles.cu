@@ -1,0 +1,462 @@
+// k_moe_tiles.cu -- the experts' layer for a few tokens on the tensor cores: 16-bit types, rows that
+// start on 16 bytes and end with a vector.
+//
+// A tile of 128 rows of an expert's weights is the matrix A of the products, the tokens that chose the
+// expert (up to NT of them) are B, so the weights are read from memory once and a product has as few
+// columns as there are tokens.  Both launches read the weights at the memory's rate; everything else is
+// there to keep it busy: a persistent CTA on every SM, or a cluster of CTAs that split a tile's columns
+// where there are fewer tiles than SMs, walks over tiles of one (expert, tokens) group after another.
+// Eight warps copy the next stages asynchronously, 128 columns each, into the swizzled layout; one
+// thread issues the products; four warps take finished sums out of tensor memory, where two tiles' sums
+// have room.
+//
+// The way up: the tile's rows are 64 of the gate and the 64 of the linear part that belong to them,
+// sixteen and sixteen in turn, so that both sums of an element lie in one warp.  silu(g) u goes into the
+// workspace as two values of the weights' type, the second what the first leaves out, 2^-18 of the value
+// off (bf16), for which the way down makes two products of every tile: in 16 bits alone the result would
+// be as far off again as its own rounding.
+// The way down: every slot's output goes into the workspace in fp32; for few tokens the last warp of a
+// tile of columns adds them up, for more a third launch.
+#include <algorithm>
+
+#include "moe.h"
+#include "norm_stage.cuh"
+#include "tcgen05.cuh"
+
+namespace vc {
+
+namespace {
+
+constexpr int kEpilogueWarps = 4, kProducerWarps = 8;
+constexpr int kIssuer = kEpilogueWarps;                // the warp that issues products
+constexpr int kThreads = 32 * (kEpilogueWarps + 1 + kProducerWarps);
+constexpr int kProducers = 32 * kProducerWarps;
+constexpr int kM = 128;              // rows of a tile
+constexpr int kK = 128;              // columns of a stage: two swizzled halves of 64
+constexpr int kHalfA = kM * 128;     // bytes of a half of A
+constexpr int kMaxStages = 5;
+static_assert(kProducers == 16 * 16, "a producer: one 16-byte chunk of a stage's row, sixteen rows apart");
+
+struct Group {                       // tokens of one expert, at most NT
+    uint16_t expert, first, count;   // first: of its slots in the list
+};
+struct Lists {
+    int count[VCOMM_MAX_EXPERTS];    // slots of an expert, then where the next one goes
+    uint16_t slots[kMoeTileSlots];   // by expert
+    Group groups[VCOMM_MAX_EXPERTS + kMoeTileSlots / 16];
+    int nGroups;
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t sumsFull[2], sumsEmpty[2];
+    uint64_t partFull, partEmpty, drained;
+    uint32_t tmem;
+    int failed;
+    int warpSum[32];
+};
+
+// The slots sorted by expert, and the groups.  All threads.
+template <int NT>
+__device__ __forceinline__ void make_lists(Lists& l, const ExpertsArgs& a) {
+    const int total = a.rows * a.topK, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int e = threadIdx.x; e < a.experts; e += kThreads) l.count[e] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < total; i += kThreads) {
+        const int e = a.ids[i];
+        if (e >= 0 && e < a.experts) atomicAdd(&l.count[e], 1);
+    }
+    __syncthreads();
+    // running sums of slots and of groups, three experts a thread
+    constexpr int PER = (VCOMM_MAX_EXPERTS + kThreads - 1) / kThreads;
+    int slots = 0, groups = 0;
+    for (int i = 0; i < PER; i++) {
+        const int e = (int)threadIdx.x * PER + i;
+        if (e >= a.experts) break;
+        slots += l.count[e];
+        groups += (l.count[e] + NT - 1) / NT;
+    }
+    int run = slots | groups << 16;                    // both below 2^16
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(~0u, run, o);
+        if (lane >= o) run += v;
+    }
+    if (lane == 31) l.warpSum[warp] = run;
+    __syncthreads();
+    int ahead = run - (slots | groups << 16), all = 0;
+    for (int w = 0; w < kThreads / 32; w++) {
+        if (w < warp) ahead += l.warpSum[w];
+        all += l.warpSum[w];
+    }
+    int slot = ahead & 0xFFFF, group = ahead >> 16;
+    for (int i = 0; i < PER; i++) {
+        const int e = (int)threadIdx.x * PER + i;
+        if (e >= a.experts) break;
+        const int n = l.count[e];
+        for (int j = 0; j < n; j += NT) l.groups[group++] = Group{(uint16_t)e, (uint16_t)(slot + j), (uint16_t)min(NT, n - j)};
+        l.count[e] = slot;
+        slot += n;
+    }
+    if (threadIdx.x == 0) l.nGroups = all >> 16;
+    __syncthreads();
+    // in order, so that all CTAs agree on which slots a group of an expert's has
+    if (warp == 0) {
+        for (int i0 = 0; i0 < total; i0 += 32) {
+            const int i = i0 + lane, e = i < total ? a.ids[i] : -1;
+            const bool counts = e >= 0 && e < a.experts;
+            const unsigned same = __match_any_sync(~0u, counts ? e : -1);
+            const int at = counts ? l.count[e] : 0;
+            __syncwarp();
+            if (counts) {
+                l.slots[at + __popc(same & ((1u << lane) - 1))] = (uint16_t)i;
+                if (lane == 31 - __clz((int)same)) l.count[e] = at + __popc(same);
+            }
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void copy_chunk(uint32_t to, const void* from, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_left() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
+// Columns [h0, h1) of every rank's output for tokens [t0, t1), from all slots' y; a thread a column.
+template <int DT>
+__device__ __forceinline__ void combine(const ExpertsArgs& a, int t0, int t1, int h) {
+    constexpr int ESZ = DTypeOf<DT>::size;
+    for (int t = t0; t < t1; t++) {
+        const int* ids = a.ids + (size_t)t * a.topK;
+        for (int r = 0; r < a.nRanks; r++) {
+            const int lo = r * a.share, hi = min(a.experts, lo + a.share);
+            float s = 0.0f;
+            for (int k = 0; k < a.topK; k++) {
+                if (ids[k] < lo || ids[k] >= hi) continue;
+                const size_t slot = (size_t)t * a.topK + k;
+                s = fmaf(a.weights[slot], __ldcg(a.y + slot * a.hidden + h), s);
+            }
+            st_elem<ESZ>(a.recv[r], (size_t)t * a.recvStride + h, f32_to_elem<DT>(s));
+        }
+    }
+}
+
+// UP: the way up, K = hidden, tiles of 64 of the ffn elements; else the way down, K = ffn, tiles of 128
+// columns of the output.
+template <int DT, int NT, bool UP, int STAGES>
+__global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant__ ExpertsArgs a) {
+    constexpr int COPIES = UP ? 1 : 2;                 // of B: the tokens, or both values of silu(g) u
+    constexpr int kHalfB = NT * 128;
+    constexpr int kStage = 2 * kHalfA + 2 * COPIES * kHalfB;
+    extern __shared__ unsigned char raw[];
+    __shared__ Lists l;
+    const uint32_t stages = (smem_at(raw) + 1023u) & ~1023u;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int split = a.split, rank = split > 1 ? (int)cluster_rank() : 0;
+    float* const parts = reinterpret_cast<float*>(raw + (stages - smem_at(raw)) + STAGES * kStage);   // [split - 1][NT][128]
+    // The way up waits for what the calls before wrote, ids and tokens among it, before it lets the way
+    // down start; so that one may read ids and weights at once, and what the way up writes after its wait.
+    if (UP) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        const int tiles = (a.hidden + kM - 1) / kM;
+        if (blockIdx.x == 0)
+            for (int i = threadIdx.x; i < tiles; i += kThreads) a.done[i] = 0;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; i++) {
+            bar_init(&l.full[i], kProducerWarps);
+            bar_init(&l.empty[i], 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            bar_init(&l.sumsFull[i], 1);
+            bar_init(&l.sumsEmpty[i], kEpilogueWarps);
+        }
+        bar_init(&l.partFull, (split - 1) * kEpilogueWarps * 32 + (split == 1));
+        bar_init(&l.partEmpty, kEpilogueWarps);
+        bar_init(&l.drained, 1);
+        l.failed = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kIssuer) tmem_alloc(&l.tmem, NT <= 16 ? 32 : 2 * NT);
+    make_lists<NT>(l, a);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (split > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
+    const uint32_t tmem = l.tmem;
+    const int K = UP ? a.hidden : a.ffn;
+    const int tiles = UP ? (a.ffn + kM / 2 - 1) / (kM / 2) : (a.hidden + kM - 1) / kM;
+    const int units = l.nGroups * tiles;
+    const int first = (int)blockIdx.x / split, step = (int)gridDim.x / split;
+    const int chunks = (K + kK - 1) / kK, chunk0 = rank * chunks / split, chunk1 = (rank + 1) * chunks / split;
+
+    if (warp > kIssuer) {
+        // ---- producers: chunk `c` of rows r0, r0 + 16, ... of a stage
+        const int t = (int)threadIdx.x - 32 * (kIssuer + 1), c = t & 15, r0 = t >> 4;
+        const uint32_t column = (uint32_t)(c >> 3), swizzled = (uint32_t)(((c & 7) ^ (r0 & 7)) << 4);
+        int issued = 0;                                // stages, of which all but the last STAGES - 1 have arrived
+        bool ok = true;
+        // One stage's A, or B.
+        const auto copy_a = [&](int u, int chunk, int at) {
+            const Group g = l.groups[u / tiles];
+            const int m = u % tiles, k = chunk * kK + c * 8;
+            const size_t e = (size_t)(g.expert % a.share);
+            const uint32_t to = stages + (uint32_t)(at * kStage) + column * kHalfA + (uint32_t)r0 * 128 + swizzled;
+            if (UP) {
+                const uint16_t* w = (const uint16_t*)a.up[g.expert / a.share] + e * 2 * a.ffn * K + k;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {          // rows 16 i + r0: sixteen of the gate, sixteen of the linear part
+                    const int f = m * (kM / 2) + (i >> 1) * 16 + r0;
+                    const bool in = f < a.ffn && k < K;
+                    copy_chunk(to + i * 16 * 128, in ? w + ((size_t)(i & 1 ? a.ffn : 0) + f) * K : w - k, in);
+                }
+            } else {
+                const uint16_t* w = (const uint16_t*)a.down[g.expert / a.share] + e * a.hidden * K + k;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int h = m * kM + 16 * i + r0;
+                    const bool in = h < a.hidden && k < K;
+                    copy_chunk(to + i * 16 * 128, in ? w + (size_t)h * K : w - k, in);
+                }
+            }
+        };
+        const auto copy_b = [&](int u, int chunk, int at) {
+            const Group g = l.groups[u / tiles];
+            const int k = chunk * kK + c * 8;
+            const uint32_t to = stages + (uint32_t)(at * kStage) + 2 * kHalfA + column * kHalfB + (uint32_t)r0 * 128 + swizzled;
+            for (int r = r0; r < g.count; r += 16) {
+                const int slot = l.slots[g.first + r];
+                const bool in = k < K;
+                if (UP) {
+                    const uint16_t* x = (const uint16_t*)a.x + (size_t)(slot / a.topK) * a.rowStride;
+                    copy_chunk(to + (r - r0) * 128, in ? x + k : x, in);
+                } else {
+                    const uint16_t* x = (const uint16_t*)a.act + (size_t)slot * 2 * K;
+                    copy_chunk(to + (r - r0) * 128, in ? x + k : x, in);
+                    copy_chunk(to + (r - r0) * 128 + 2 * kHalfB, in ? x + K + k : x, in);
+                }
+            }
+        };
+        const auto arrived = [&](int stage) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) bar_arrive(&l.full[stage % STAGES]);
+        };
+        // The way down: the weights of the first stages need not wait for the way up.
+        int early = 0;
+        if (!UP) {
+            for (int u = first, chunk = chunk0; u < units && early < STAGES; early++) {
+                copy_a(u, chunk, early);
+                if (++chunk == chunk1) {
+                    chunk = chunk0;
+                    u += step;
+                }
+            }
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        }
+        for (int u = first; u < units && ok; u += step) {
+            for (int chunk = chunk0; chunk < chunk1; chunk++) {
+                const int at = issued % STAGES;
+                if (issued >= STAGES) {
+                    ok = __all_sync(~0u, bar_wait(&l.empty[at], (uint32_t)(issued / STAGES - 1) & 1u, &l.failed));
+                    if (!ok) break;
+                }
+                if (issued >= early) copy_a(u, chunk, at);
+                copy_b(u, chunk, at);
+                copies_commit();
+                issued++;
+                if (issued >= STAGES) {
+                    copies_left<STAGES - 1>();
+                    arrived(issued - STAGES);
+                }
+            }
+        }
+        copies_wait();
+        for (int s = max(0, issued - STAGES + 1); s < issued; s++) arrived(s);
+    } else if (warp == kIssuer) {
+        // ---- the issuer
+        if (lane == 0) {
+            int stage = 0, unit = 0;
+            bool ok = true;
+            for (int u = first; u < units && ok; u += step, unit++) {
+                const int n = (l.groups[u / tiles].count + 15) & ~15, buffer = unit & 1;
+                const uint32_t shape = product_shape<DT>(n), d = tmem + (uint32_t)(buffer * NT);
+                if (unit >= 2 && !(ok = bar_wait(&l.sumsEmpty[buffer], (uint32_t)(unit / 2 - 1) & 1u, &l.failed))) break;
+                tmem_fence_after();
+                for (int chunk = chunk0; chunk < chunk1; chunk++, stage++) {
+                    const int at = stage % STAGES;
+                    if (!(ok = bar_wait(&l.full[at], (uint32_t)(stage / STAGES) & 1u, &l.failed))) break;
+                    tmem_fence_after();
+                    const uint32_t sa = stages + (uint32_t)(at * kStage), sb = sa + 2 * kHalfA;
+#pragma unroll
+                    for (int i = 0; i < kK / 16; i++) {
+                        const uint64_t opA = operand(sa + (i >> 2) * kHalfA + (i & 3) * 32);
+#pragma unroll
+                        for (int v = 0; v < COPIES; v++)
+                            multiply(d, opA, operand(sb + v * 2 * kHalfB + (i >> 2) * kHalfB + (i & 3) * 32), shape,
+                                     chunk > chunk0 || i > 0 || v > 0);
+                    }
+                    products_done(&l.empty[at]);
+                }
+                if (ok) products_done(&l.sumsFull[buffer]);
+            }
+            // nothing of this CTA's is under way when its tensor memory is given back
+            products_done(&l.drained);
+            bar_drain(&l.drained, 0, &l.failed);
+        }
+        __syncwarp();
+    } else {
+        // ---- sums out of tensor memory: lane `lane` of warp `warp` has row 32 warp + lane
+        if (!UP) asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int row = warp * 32 + lane;
+        int unit = 0;
+        for (int u = first; u < units; u += step, unit++) {
+            const Group g = l.groups[u / tiles];
+            const int m = u % tiles, buffer = unit & 1;
+            bool ok = bar_wait(&l.sumsFull[buffer], (uint32_t)(unit / 2) & 1u, &l.failed);
+            if (rank > 0 && unit > 0) ok = ok && bar_wait(&l.partEmpty, (uint32_t)(unit - 1) & 1u, &l.failed);
+            if (split > 1 && rank == 0) ok = ok && bar_wait(&l.partFull, (uint32_t)unit & 1u, &l.failed);
+            if (!__all_sync(~0u, ok)) break;
+            tmem_fence_after();
+            for (int j0 = 0; j0 < g.count; j0 += 16) {
+                float v[16];
+                tmem_load(tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)(buffer * NT + j0), v);
+                if (rank > 0) {      // to the first CTA of the cluster
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        st_cluster(parts + ((size_t)(rank - 1) * NT + j0 + j) * kM + row, 0, __float_as_uint(v[j]));
+                    continue;
+                }
+                for (int s = 0; s < split - 1; s++)
+#pragma unroll
+                    for (int j = 0; j < 16; j++) v[j] += parts[((size_t)s * NT + j0 + j) * kM + row];
+                if (UP) {
+                    // lanes 0 to 15 hold the gate's sums, 16 to 31 the linear part's: the first take the
+                    // even columns, the others the odd ones
+                    const int f = m * (kM / 2) + warp * 16 + (lane & 15);
+                    uint16_t* const act = (uint16_t*)a.act;
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float other = __shfl_xor_sync(~0u, lane < 16 ? v[j + 1] : v[j], 16);
+                        const float gate = lane < 16 ? v[j] : other, linear = lane < 16 ? other : v[j + 1];
+                        const int column = j0 + j + (lane >> 4);
+                        if (column >= g.count || f >= a.ffn) continue;
+                        const float x = gate / (1.0f + expf(-gate)) * linear;
+                        const uint16_t hi = narrow16<DT>(x);
+                        const float rest = x - widen16<DT>(hi);
+                        uint16_t* to = act + (size_t)l.slots[g.first + column] * 2 * a.ffn + f;
+                        to[0] = hi;
+                        to[a.ffn] = narrow16<DT>(isfinite(x) ? rest : 0.0f);
+                    }
+                } else {
+                    const int h = m * kM + row;
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        if (j0 + j < g.count && h < a.hidden) a.y[(size_t)l.slots[g.first + j0 + j] * a.hidden + h] = v[j];
+                }
+            }
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&l.sumsEmpty[buffer]);
+            if (rank > 0) bar_arrive_at(&l.partFull, 0);
+            if (split > 1 && rank == 0) {
+                __syncwarp();
+                if (lane > 0 && lane < split) bar_arrive_at(&l.partEmpty, lane);
+            }
+            if (UP || rank > 0 || !a.combineHere) continue;
+            // the last warp of the last group adds up the tile's columns
+            __threadfence();
+            __syncwarp();
+            unsigned before = 0;
+            if (lane == 0) before = atomicAdd(&a.done[m], 1u);
+            if (__shfl_sync(~0u, before, 0) != (unsigned)(kEpilogueWarps * l.nGroups) - 1) continue;
+            __threadfence();
+            for (int h = m * kM + lane; h < min(a.hidden, (m + 1) * kM); h += 32) combine<DT>(a, 0, a.rows, h);
+        }
+        // no expert at all: zeros
+        if (!UP && a.combineHere && l.nGroups == 0)
+            for (int h = (int)blockIdx.x * kM + row; h < a.hidden; h += (int)gridDim.x * kM) combine<DT>(a, 0, a.rows, h);
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == kIssuer) tmem_free(tmem, NT <= 16 ? 32 : 2 * NT);
+    if (threadIdx.x == 0 && l.failed) report_error(a.status, a.statusHost, vTimeout, blockIdx.x, 0, UP ? 0 : 1);
+    if (split > 1) {                                   // another CTA may still arrive here
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
+// Every token's slots added up, for many tokens: a thread a column, a CTA a few tokens.
+constexpr int kCombineThreads = 256, kCombineTokens = 2;
+template <int DT>
+__global__ void __launch_bounds__(kCombineThreads) k_moe_combine(const __grid_constant__ ExpertsArgs a) {
+    pdl_begin();
+    const int h = (int)blockIdx.x * kCombineThreads + (int)threadIdx.x, t0 = (int)blockIdx.y * kCombineTokens;
+    if (h < a.hidden) combine<DT>(a, t0, min(a.rows, t0 + kCombineTokens), h);
+}
+
+template <int DT, int NT, bool UP, int STAGES>
+cudaError_t tiles_launch(const ExpertsArgs& a, const MoeTiles& t, cudaStream_t s) {
+    const auto kernel = k_moe_tiles<DT, NT, UP, STAGES>;
+    constexpr int stage = 2 * kHalfA + (UP ? 1 : 2) * 2 * NT * 128;
+    constexpr int parts = NT == 16 ? (kMoeMaxSplit - 1) * NT * kM * 4 : 0;
+    constexpr int bytes = STAGES * stage + parts + 1024;
+    static_assert(bytes + (int)sizeof(Lists) <= 227 * 1024, "shared memory of a CTA");
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    ExpertsArgs b = a;
+    b.split = UP ? t.splitUp : t.splitDown;
+    b.combineHere = t.combineHere;
+    NormShape sh = {};
+    sh.threads = kThreads;
+    sh.cluster = b.split;
+    return norm_launch(kernel, (unsigned)(UP ? t.gridUp : t.gridDown), sh, bytes, s, b);
+}
+template <int DT>
+cudaError_t tiles_dt(const ExpertsArgs& a, const MoeTiles& t, cudaStream_t s) {
+    cudaError_t e;
+    switch (t.tokens) {
+    case 16:
+        e = tiles_launch<DT, 16, true, 5>(a, t, s);
+        if (e == cudaSuccess) e = tiles_launch<DT, 16, false, 4>(a, t, s);
+        break;
+    case 32:
+        e = tiles_launch<DT, 32, true, 5>(a, t, s);
+        if (e == cudaSuccess) e = tiles_launch<DT, 32, false, 4>(a, t, s);
+        break;
+    default:
+        e = tiles_launch<DT, 64, true, 4>(a, t, s);
+        if (e == cudaSuccess) e = tiles_launch<DT, 64, false, 3>(a, t, s);
+        break;
+    }
+    if (e != cudaSuccess || t.combineHere) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.hidden + kCombineThreads - 1) / kCombineThreads),
+                       (unsigned)((a.rows + kCombineTokens - 1) / kCombineTokens));
+    cfg.blockDim = dim3(kCombineThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k_moe_combine<DT>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_tiles(const ExpertsArgs& a, const MoeTiles& t, vDataType_t dt, cudaStream_t s) {
+    switch (dt) {
+    case vFloat16: return tiles_dt<kF16>(a, t, s);
+    case vBFloat16: return tiles_dt<kBF16>(a, t, s);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace vc

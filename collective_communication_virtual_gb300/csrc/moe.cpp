@@ -43,6 +43,34 @@ struct Layout {
     size_t total() const { return act + y + done + 16; }
 };
 
+// Shapes of the tensor core launches.
+vc::MoeTiles moe_tiles(const vc::ExpertsArgs& a, int smCount) {
+    vc::MoeTiles t = {};
+    const int slots = a.rows * a.topK;
+    // Most experts' tokens in one group: a second one reads the expert's weights again.
+    const double mean = (double)slots / a.experts;
+    t.tokens = a.rows <= 16 || mean <= 6 ? 16 : a.rows <= 32 || mean <= 18 ? 32 : 64;
+    const int groups = std::min(a.experts, slots);
+    const auto shape = [&](int tiles, int columns, int* split, int* grid) {
+        // rounds of tiles by the stages of one, and one more for a sum that is put together
+        const int chunks = (columns + 127) / 128;
+        double least = 0;
+        for (const int s : {1, 2, 4}) {
+            if (s > 1 && (t.tokens > 16 || s > chunks)) break;
+            const int clusters = std::max(1, smCount / s);
+            const double cost = (double)((groups * tiles + clusters - 1) / clusters) * ((double)((chunks + s - 1) / s) + (s > 1));
+            if (s > 1 && cost >= least) continue;
+            least = cost;
+            *split = s;
+            *grid = std::min(clusters, std::max(1, (groups + slots / t.tokens) * tiles)) * s;
+        }
+    };
+    shape((a.ffn + 63) / 64, a.hidden, &t.splitUp, &t.gridUp);
+    shape((a.hidden + 127) / 128, a.ffn, &t.splitDown, &t.gridDown);
+    t.combineHere = a.rows <= 4;
+    return t;
+}
+
 vResult_t route(const vMoeDesc_t* desc, const void* x, const void* router, const float* bias, int* ids, float* weights,
                 vcomm_t c, cudaStream_t stream) {
     CommView v;
@@ -140,6 +168,17 @@ vResult_t experts(const vMoeDesc_t* desc, const void* x, const int* ids, const f
     a.topK = m.d.topK;
     a.nRanks = v.nRanks;
     a.share = m.share;
+    a.split = 1;
+    a.combineHere = 1;
+    a.status = v.status;
+    a.statusHost = v.statusHost;
+    if (a.aligned && m.esz == 2 && m.slots <= (size_t)vc::kMoeTileSlots) {
+        const vc::MoeTiles t = moe_tiles(a, v.smCount);
+        if (v.debug)
+            std::fprintf(stderr, "vcomm INFO MoeExperts rows=%d hidden=%d ffn=%d experts=%d topK=%d N=%d tokens=%d split=%d,%d grid=%d,%d\n",
+                         a.rows, a.hidden, a.ffn, a.experts, a.topK, a.nRanks, t.tokens, t.splitUp, t.splitDown, t.gridUp, t.gridDown);
+        return vc::comm_launch_tracked(c, "moe experts", stream, [&]() { return vc::launch_moe_tiles(a, t, m.d.datatype, stream); });
+    }
     if (v.debug)
         std::fprintf(stderr, "vcomm INFO MoeExperts rows=%d hidden=%d ffn=%d experts=%d topK=%d N=%d aligned=%d\n", a.rows,
                      a.hidden, a.ffn, a.experts, a.topK, a.nRanks, a.aligned);

@@ -45,8 +45,23 @@ struct ExpertsArgs {
     int nRanks;
     int share;                       // experts of a rank
     int aligned;                     // every row of x and of the weights starts on 16 bytes and ends with a vector
+    int split;                       // tensor cores: CTAs of a cluster that share a tile's columns
+    int combineHere;                 // the same: the way down adds up the slots
+    Status* status;                  // device copy
+    volatile Status* statusHost;     // pinned mirror
 };
 constexpr int kMoeTile = 32;         // output columns of a CTA in both launches
 cudaError_t launch_moe_experts(const ExpertsArgs& a, vDataType_t dt, cudaStream_t s);
+
+// The same on the tensor cores.
+constexpr int kMoeTileSlots = 4096;  // rows * topK, at most
+constexpr int kMoeMaxSplit = 4;
+struct MoeTiles {
+    int tokens;                      // of a tile: 16, 32 or 64
+    int splitUp, splitDown;          // CTAs of a cluster that share a tile's columns: 1, 2 or 4
+    int gridUp, gridDown;
+    int combineHere;                 // few tokens: no third launch
+};
+cudaError_t launch_moe_tiles(const ExpertsArgs& a, const MoeTiles& t, vDataType_t dt, cudaStream_t s);
 
 }  // namespace vc

@@ -17,6 +17,8 @@ struct CommView {
     int smCount;
     bool debug;
     bool grouping;                   // between vcommGroupStart and vcommGroupEnd
+    Status* status;                  // where a kernel whose bounded wait runs out says so: the device's
+    Status* statusHost;              // copy and the pinned mirror, both by device address
 };
 // vInvalidArgument for a bad handle, the sticky error if there is one, else vSuccess.
 vResult_t comm_view(vcomm_t c, CommView* v);
@@ -24,6 +26,8 @@ vResult_t comm_view(vcomm_t c, CommView* v);
 vResult_t comm_record(vcomm_t c, std::function<vResult_t()> call);
 // Run `launch` with the communicator's device and launch mode, and take note of its error.
 vResult_t comm_launch(vcomm_t c, const char* what, const std::function<cudaError_t()>& launch);
+// The same for a kernel that may write the communicator's status, which vcommDestroy waits for.
+vResult_t comm_launch_tracked(vcomm_t c, const char* what, cudaStream_t stream, const std::function<cudaError_t()>& launch);
 
 size_t dtype_size(int dt);           // 0 for a type that is none
 

@@ -546,6 +546,8 @@ vResult_t comm_view(vcomm_t c, CommView* v) {
     v->smCount = c->smCount;
     v->debug = c->cfg.debug;
     v->grouping = c->groupDepth > 0;
+    v->status = c->statusDev;
+    v->statusHost = c->statusHostDev;
     return vSuccess;
 }
 
@@ -560,6 +562,12 @@ vResult_t comm_launch(vcomm_t c, const char* what, const std::function<cudaError
     DeviceGuard g(c);
     if (!g.ok) return vUnhandledCudaError;
     return finish_launch(c, launch(), nullptr, what);
+}
+
+vResult_t comm_launch_tracked(vcomm_t c, const char* what, cudaStream_t stream, const std::function<cudaError_t()>& launch) {
+    DeviceGuard g(c);
+    if (!g.ok) return vUnhandledCudaError;
+    return finish_launch(c, launch(), stream, what, true);
 }
 
 }  // namespace vc
