@@ -17,8 +17,6 @@
 // be as far off again as its own rounding.
 // The way down: every slot's output goes into the workspace in fp32; for few tokens the last warp of a
 // tile of columns adds them up, for more a third launch.
-#include <algorithm>
-
 #include "moe.h"
 #include "norm_stage.cuh"
 #include "tcgen05.cuh"
@@ -34,29 +32,50 @@ constexpr int kProducers = 32 * kProducerWarps;
 constexpr int kM = 128;              // rows of a tile
 constexpr int kK = 128;              // columns of a stage: two swizzled halves of 64
 constexpr int kHalfA = kM * 128;     // bytes of a half of A
-constexpr int kMaxStages = 5;
 static_assert(kProducers == 16 * 16, "a producer: one 16-byte chunk of a stage's row, sixteen rows apart");
 
-struct Group {                       // tokens of one expert, at most NT
-    uint16_t expert, first, count;   // first: of its slots in the list
-};
-struct Lists {
-    int count[VCOMM_MAX_EXPERTS];    // slots of an expert, then where the next one goes
-    uint16_t slots[kMoeTileSlots];   // by expert
-    Group groups[VCOMM_MAX_EXPERTS + kMoeTileSlots / 16];
-    int nGroups;
-    uint64_t full[kMaxStages], empty[kMaxStages];
+struct Shared {
+    uint64_t full[kMoeMaxStages], empty[kMoeMaxStages];
     uint64_t sumsFull[2], sumsEmpty[2];
     uint64_t partFull, partEmpty, drained;
     uint32_t tmem;
-    int failed;
+    int failed, nGroups;
     int warpSum[32];
+};
+// In dynamic shared memory, as long as the call needs them.
+struct Lists {
+    int* count;                      // slots of an expert, then where the next one goes
+    uint16_t* slots;                 // by expert
+    MoeGroup* groups;
 };
 
 // The slots sorted by expert, and the groups.  All threads.
 template <int NT>
-__device__ __forceinline__ void make_lists(Lists& l, const ExpertsArgs& a) {
+__device__ __forceinline__ void make_lists(Shared& sh, const Lists& l, const ExpertsArgs& a) {
     const int total = a.rows * a.topK, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (total <= 32 && NT >= 16) {   // by one warp, experts in the order of their first slots
+        if (warp == 0) {
+            const int e = lane < total ? a.ids[lane] : -1;
+            const bool counts = e >= 0 && e < a.experts;
+            const unsigned same = __match_any_sync(~0u, counts ? e : -1), below = (1u << lane) - 1;
+            const bool leads = counts && (same & below) == 0;
+            const int n = __popc(same), mine = leads ? n | (n + NT - 1) / NT << 16 : 0;    // slots and groups
+            int run = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(~0u, run, o);
+                if (lane >= o) run += v;
+            }
+            const int first = __shfl_sync(~0u, run - mine, __ffs(same) - 1) & 0xFFFF;
+            if (counts) l.slots[first + __popc(same & below)] = (uint16_t)lane;
+            if (leads)
+                for (int j = 0; j < n; j += NT)
+                    l.groups[((run - mine) >> 16) + j / NT] = MoeGroup{(uint16_t)e, (uint16_t)(first + j), (uint16_t)min(NT, n - j)};
+            if (lane == 31) sh.nGroups = run >> 16;
+        }
+        __syncthreads();
+        return;
+    }
     for (int e = threadIdx.x; e < a.experts; e += kThreads) l.count[e] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < total; i += kThreads) {
@@ -73,29 +92,29 @@ __device__ __forceinline__ void make_lists(Lists& l, const ExpertsArgs& a) {
         slots += l.count[e];
         groups += (l.count[e] + NT - 1) / NT;
     }
-    int run = slots | groups << 16;                    // both below 2^16
+    int run = slots | groups << 16;                    // both below 2^15
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(~0u, run, o);
         if (lane >= o) run += v;
     }
-    if (lane == 31) l.warpSum[warp] = run;
+    if (lane == 31) sh.warpSum[warp] = run;
     __syncthreads();
     int ahead = run - (slots | groups << 16), all = 0;
     for (int w = 0; w < kThreads / 32; w++) {
-        if (w < warp) ahead += l.warpSum[w];
-        all += l.warpSum[w];
+        if (w < warp) ahead += sh.warpSum[w];
+        all += sh.warpSum[w];
     }
     int slot = ahead & 0xFFFF, group = ahead >> 16;
     for (int i = 0; i < PER; i++) {
         const int e = (int)threadIdx.x * PER + i;
         if (e >= a.experts) break;
         const int n = l.count[e];
-        for (int j = 0; j < n; j += NT) l.groups[group++] = Group{(uint16_t)e, (uint16_t)(slot + j), (uint16_t)min(NT, n - j)};
+        for (int j = 0; j < n; j += NT) l.groups[group++] = MoeGroup{(uint16_t)e, (uint16_t)(slot + j), (uint16_t)min(NT, n - j)};
         l.count[e] = slot;
         slot += n;
     }
-    if (threadIdx.x == 0) l.nGroups = all >> 16;
+    if (threadIdx.x == 0) sh.nGroups = all >> 16;
     __syncthreads();
     // in order, so that all CTAs agree on which slots a group of an expert's has
     if (warp == 0) {
@@ -118,41 +137,85 @@ __device__ __forceinline__ void make_lists(Lists& l, const ExpertsArgs& a) {
 __device__ __forceinline__ void copy_chunk(uint32_t to, const void* from, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
 }
-template <int N>
-__device__ __forceinline__ void copies_left() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
-// Columns [h0, h1) of every rank's output for tokens [t0, t1), from all slots' y; a thread a column.
+// Columns [h, h + 4) of every rank's output for token t, from its slots' y.  What up to eight slots need is
+// loaded together, whether it counts or not: the wait for memory is most of this.
 template <int DT>
-__device__ __forceinline__ void combine(const ExpertsArgs& a, int t0, int t1, int h) {
-    constexpr int ESZ = DTypeOf<DT>::size;
-    for (int t = t0; t < t1; t++) {
-        const int* ids = a.ids + (size_t)t * a.topK;
-        for (int r = 0; r < a.nRanks; r++) {
-            const int lo = r * a.share, hi = min(a.experts, lo + a.share);
-            float s = 0.0f;
-            for (int k = 0; k < a.topK; k++) {
-                if (ids[k] < lo || ids[k] >= hi) continue;
-                const size_t slot = (size_t)t * a.topK + k;
-                s = fmaf(a.weights[slot], __ldcg(a.y + slot * a.hidden + h), s);
-            }
-            st_elem<ESZ>(a.recv[r], (size_t)t * a.recvStride + h, f32_to_elem<DT>(s));
+__device__ __forceinline__ void combine(const ExpertsArgs& a, int t, int h) {
+    constexpr int ESZ = DTypeOf<DT>::size, UN = 8;
+    static_assert(ESZ == 2, "the tensor cores' types");
+    const auto put = [&](int r, const float (&s)[4]) {
+        uint16_t* to = (uint16_t*)a.recv[r] + (size_t)t * a.recvStride + h;
+        if (a.recvAligned) {
+            *reinterpret_cast<uint2*>(to) = make_uint2(narrow16<DT>(s[0]) | (uint32_t)narrow16<DT>(s[1]) << 16,
+                                                       narrow16<DT>(s[2]) | (uint32_t)narrow16<DT>(s[3]) << 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; j++) to[j] = narrow16<DT>(s[j]);
         }
+    };
+    const auto add = [&](int k0, int k, float4& y, float& w, int& r) {
+        const size_t slot = (size_t)t * a.topK + min(k0 + k, a.topK - 1);
+        const int e = a.ids[slot];
+        w = a.weights[slot];
+        y = __ldcg(reinterpret_cast<const float4*>(a.y + slot * a.hidden + h));
+        r = k0 + k < a.topK && e >= 0 && e < a.experts ? e / a.share : -1;
+    };
+    if (a.topK <= UN) {
+        float4 y[UN];
+        float w[UN];
+        int rank[UN];
+#pragma unroll
+        for (int k = 0; k < UN; k++) add(0, k, y[k], w[k], rank[k]);
+        for (int r = 0; r < a.nRanks; r++) {
+            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < UN; k++) {
+                if (rank[k] != r) continue;
+                s[0] = fmaf(w[k], y[k].x, s[0]);
+                s[1] = fmaf(w[k], y[k].y, s[1]);
+                s[2] = fmaf(w[k], y[k].z, s[2]);
+                s[3] = fmaf(w[k], y[k].w, s[3]);
+            }
+            put(r, s);
+        }
+        return;
+    }
+    for (int r = 0; r < a.nRanks; r++) {
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = 0; k < a.topK; k++) {
+            float4 y;
+            float w;
+            int rank;
+            add(0, k, y, w, rank);
+            if (rank != r) continue;
+            s[0] = fmaf(w, y.x, s[0]);
+            s[1] = fmaf(w, y.y, s[1]);
+            s[2] = fmaf(w, y.z, s[2]);
+            s[3] = fmaf(w, y.w, s[3]);
+        }
+        put(r, s);
     }
 }
 
 // UP: the way up, K = hidden, tiles of 64 of the ffn elements; else the way down, K = ffn, tiles of 128
 // columns of the output.
-template <int DT, int NT, bool UP, int STAGES>
+template <int DT, int NT, bool UP>
 __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant__ ExpertsArgs a) {
     constexpr int COPIES = UP ? 1 : 2;                 // of B: the tokens, or both values of silu(g) u
     constexpr int kHalfB = NT * 128;
     constexpr int kStage = 2 * kHalfA + 2 * COPIES * kHalfB;
     extern __shared__ unsigned char raw[];
-    __shared__ Lists l;
+    __shared__ Shared sh;
     const uint32_t stages = (smem_at(raw) + 1023u) & ~1023u;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int split = a.split, rank = split > 1 ? (int)cluster_rank() : 0;
-    float* const parts = reinterpret_cast<float*>(raw + (stages - smem_at(raw)) + STAGES * kStage);   // [split - 1][NT][128]
+    const int nStages = a.stages;
+    float* const parts = reinterpret_cast<float*>(raw + (stages - smem_at(raw)) + nStages * kStage);   // [split - 1][NT][128]
+    Lists l;
+    l.count = reinterpret_cast<int*>(parts + (split - 1) * NT * kM);
+    l.groups = reinterpret_cast<MoeGroup*>(l.count + a.experts);
+    l.slots = reinterpret_cast<uint16_t*>(l.groups + moe_groups(a.experts, a.rows * a.topK, NT));
     // The way up waits for what the calls before wrote, ids and tokens among it, before it lets the way
     // down start; so that one may read ids and weights at once, and what the way up writes after its wait.
     if (UP) {
@@ -163,22 +226,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
             for (int i = threadIdx.x; i < tiles; i += kThreads) a.done[i] = 0;
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < STAGES; i++) {
-            bar_init(&l.full[i], kProducerWarps);
-            bar_init(&l.empty[i], 1);
+        for (int i = 0; i < nStages; i++) {
+            bar_init(&sh.full[i], kProducers);
+            bar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < 2; i++) {
-            bar_init(&l.sumsFull[i], 1);
-            bar_init(&l.sumsEmpty[i], kEpilogueWarps);
+            bar_init(&sh.sumsFull[i], 1);
+            bar_init(&sh.sumsEmpty[i], kEpilogueWarps);
         }
-        bar_init(&l.partFull, (split - 1) * kEpilogueWarps * 32 + (split == 1));
-        bar_init(&l.partEmpty, kEpilogueWarps);
-        bar_init(&l.drained, 1);
-        l.failed = 0;
+        bar_init(&sh.partFull, (split - 1) * kEpilogueWarps * 32 + (split == 1));
+        bar_init(&sh.partEmpty, kEpilogueWarps);
+        bar_init(&sh.drained, 1);
+        sh.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kIssuer) tmem_alloc(&l.tmem, NT <= 16 ? 32 : 2 * NT);
-    make_lists<NT>(l, a);
+    if (warp == kIssuer) tmem_alloc(&sh.tmem, NT <= 16 ? 32 : 2 * NT);
+    make_lists<NT>(sh, l, a);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -186,10 +249,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
         cluster_arrive();
         cluster_wait();
     }
-    const uint32_t tmem = l.tmem;
+    const uint32_t tmem = sh.tmem;
     const int K = UP ? a.hidden : a.ffn;
     const int tiles = UP ? (a.ffn + kM / 2 - 1) / (kM / 2) : (a.hidden + kM - 1) / kM;
-    const int units = l.nGroups * tiles;
+    const int units = sh.nGroups * tiles;
     const int first = (int)blockIdx.x / split, step = (int)gridDim.x / split;
     const int chunks = (K + kK - 1) / kK, chunk0 = rank * chunks / split, chunk1 = (rank + 1) * chunks / split;
 
@@ -197,11 +260,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
         // ---- producers: chunk `c` of rows r0, r0 + 16, ... of a stage
         const int t = (int)threadIdx.x - 32 * (kIssuer + 1), c = t & 15, r0 = t >> 4;
         const uint32_t column = (uint32_t)(c >> 3), swizzled = (uint32_t)(((c & 7) ^ (r0 & 7)) << 4);
-        int issued = 0;                                // stages, of which all but the last STAGES - 1 have arrived
         bool ok = true;
         // One stage's A, or B.
         const auto copy_a = [&](int u, int chunk, int at) {
-            const Group g = l.groups[u / tiles];
+            const MoeGroup g = l.groups[u / tiles];
             const int m = u % tiles, k = chunk * kK + c * 8;
             const size_t e = (size_t)(g.expert % a.share);
             const uint32_t to = stages + (uint32_t)(at * kStage) + column * kHalfA + (uint32_t)r0 * 128 + swizzled;
@@ -224,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
             }
         };
         const auto copy_b = [&](int u, int chunk, int at) {
-            const Group g = l.groups[u / tiles];
+            const MoeGroup g = l.groups[u / tiles];
             const int k = chunk * kK + c * 8;
             const uint32_t to = stages + (uint32_t)(at * kStage) + 2 * kHalfA + column * kHalfB + (uint32_t)r0 * 128 + swizzled;
             for (int r = r0; r < g.count; r += 16) {
@@ -240,15 +302,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
                 }
             }
         };
-        const auto arrived = [&](int stage) {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) bar_arrive(&l.full[stage % STAGES]);
-        };
         // The way down: the weights of the first stages need not wait for the way up.
         int early = 0;
         if (!UP) {
-            for (int u = first, chunk = chunk0; u < units && early < STAGES; early++) {
+            for (int u = first, chunk = chunk0; u < units && early < nStages; early++) {
                 copy_a(u, chunk, early);
                 if (++chunk == chunk1) {
                     chunk = chunk0;
@@ -258,38 +315,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
             asm volatile("griddepcontrol.wait;" ::: "memory");
             asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         }
+        int at = 0;
+        uint32_t round = 0;                            // times that all stages have been filled
         for (int u = first; u < units && ok; u += step) {
             for (int chunk = chunk0; chunk < chunk1; chunk++) {
-                const int at = issued % STAGES;
-                if (issued >= STAGES) {
-                    ok = __all_sync(~0u, bar_wait(&l.empty[at], (uint32_t)(issued / STAGES - 1) & 1u, &l.failed));
+                if (round > 0) {
+                    ok = __all_sync(~0u, bar_wait(&sh.empty[at], (round - 1) & 1u, &sh.failed));
                     if (!ok) break;
                 }
-                if (issued >= early) copy_a(u, chunk, at);
+                if (early > 0) early--;
+                else copy_a(u, chunk, at);
                 copy_b(u, chunk, at);
-                copies_commit();
-                issued++;
-                if (issued >= STAGES) {
-                    copies_left<STAGES - 1>();
-                    arrived(issued - STAGES);
+                // arrives when this thread's copies are there; the issuer makes them visible to its products (a
+                // fence here would wait for the stages under way: 816 us for the way up of 64 x 4096 x 1536, 499)
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_at(&sh.full[at])) : "memory");
+                if (++at == nStages) {
+                    at = 0;
+                    round++;
                 }
             }
         }
-        copies_wait();
-        for (int s = max(0, issued - STAGES + 1); s < issued; s++) arrived(s);
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == kIssuer) {
         // ---- the issuer
         if (lane == 0) {
-            int stage = 0, unit = 0;
+            int at = 0, unit = 0;
+            uint32_t round = 0;
             bool ok = true;
             for (int u = first; u < units && ok; u += step, unit++) {
                 const int n = (l.groups[u / tiles].count + 15) & ~15, buffer = unit & 1;
                 const uint32_t shape = product_shape<DT>(n), d = tmem + (uint32_t)(buffer * NT);
-                if (unit >= 2 && !(ok = bar_wait(&l.sumsEmpty[buffer], (uint32_t)(unit / 2 - 1) & 1u, &l.failed))) break;
+                if (unit >= 2 && !(ok = bar_wait(&sh.sumsEmpty[buffer], (uint32_t)(unit / 2 - 1) & 1u, &sh.failed))) break;
                 tmem_fence_after();
-                for (int chunk = chunk0; chunk < chunk1; chunk++, stage++) {
-                    const int at = stage % STAGES;
-                    if (!(ok = bar_wait(&l.full[at], (uint32_t)(stage / STAGES) & 1u, &l.failed))) break;
+                for (int chunk = chunk0; chunk < chunk1; chunk++) {
+                    if (!(ok = bar_wait(&sh.full[at], round & 1u, &sh.failed))) break;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     tmem_fence_after();
                     const uint32_t sa = stages + (uint32_t)(at * kStage), sb = sa + 2 * kHalfA;
 #pragma unroll
@@ -300,13 +360,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
                             multiply(d, opA, operand(sb + v * 2 * kHalfB + (i >> 2) * kHalfB + (i & 3) * 32), shape,
                                      chunk > chunk0 || i > 0 || v > 0);
                     }
-                    products_done(&l.empty[at]);
+                    products_done(&sh.empty[at]);
+                    if (++at == nStages) {
+                        at = 0;
+                        round++;
+                    }
                 }
-                if (ok) products_done(&l.sumsFull[buffer]);
+                if (ok) products_done(&sh.sumsFull[buffer]);
             }
             // nothing of this CTA's is under way when its tensor memory is given back
-            products_done(&l.drained);
-            bar_drain(&l.drained, 0, &l.failed);
+            products_done(&sh.drained);
+            bar_drain(&sh.drained, 0, &sh.failed);
         }
         __syncwarp();
     } else {
@@ -315,11 +379,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
         const int row = warp * 32 + lane;
         int unit = 0;
         for (int u = first; u < units; u += step, unit++) {
-            const Group g = l.groups[u / tiles];
+            const MoeGroup g = l.groups[u / tiles];
             const int m = u % tiles, buffer = unit & 1;
-            bool ok = bar_wait(&l.sumsFull[buffer], (uint32_t)(unit / 2) & 1u, &l.failed);
-            if (rank > 0 && unit > 0) ok = ok && bar_wait(&l.partEmpty, (uint32_t)(unit - 1) & 1u, &l.failed);
-            if (split > 1 && rank == 0) ok = ok && bar_wait(&l.partFull, (uint32_t)unit & 1u, &l.failed);
+            bool ok = bar_wait(&sh.sumsFull[buffer], (uint32_t)(unit / 2) & 1u, &sh.failed);
+            if (rank > 0 && unit > 0) ok = ok && bar_wait(&sh.partEmpty, (uint32_t)(unit - 1) & 1u, &sh.failed);
+            if (split > 1 && rank == 0) ok = ok && bar_wait(&sh.partFull, (uint32_t)unit & 1u, &sh.failed);
             if (!__all_sync(~0u, ok)) break;
             tmem_fence_after();
             for (int j0 = 0; j0 < g.count; j0 += 16) {
@@ -361,11 +425,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
             }
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(&l.sumsEmpty[buffer]);
-            if (rank > 0) bar_arrive_at(&l.partFull, 0);
+            if (lane == 0) bar_arrive(&sh.sumsEmpty[buffer]);
+            if (rank > 0) bar_arrive_at(&sh.partFull, 0);
             if (split > 1 && rank == 0) {
                 __syncwarp();
-                if (lane > 0 && lane < split) bar_arrive_at(&l.partEmpty, lane);
+                if (lane > 0 && lane < split) bar_arrive_at(&sh.partEmpty, lane);
             }
             if (UP || rank > 0 || !a.combineHere) continue;
             // the last warp of the last group adds up the tile's columns
@@ -373,72 +437,65 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
             __syncwarp();
             unsigned before = 0;
             if (lane == 0) before = atomicAdd(&a.done[m], 1u);
-            if (__shfl_sync(~0u, before, 0) != (unsigned)(kEpilogueWarps * l.nGroups) - 1) continue;
+            if (__shfl_sync(~0u, before, 0) != (unsigned)(kEpilogueWarps * sh.nGroups) - 1) continue;
             __threadfence();
-            for (int h = m * kM + lane; h < min(a.hidden, (m + 1) * kM); h += 32) combine<DT>(a, 0, a.rows, h);
+            if (m * kM + 4 * lane < a.hidden)
+                for (int t = 0; t < a.rows; t++) combine<DT>(a, t, m * kM + 4 * lane);
         }
         // no expert at all: zeros
-        if (!UP && a.combineHere && l.nGroups == 0)
-            for (int h = (int)blockIdx.x * kM + row; h < a.hidden; h += (int)gridDim.x * kM) combine<DT>(a, 0, a.rows, h);
+        if (!UP && a.combineHere && sh.nGroups == 0)
+            for (int h = ((int)blockIdx.x * kM + row) * 4; h < a.hidden; h += (int)gridDim.x * kM * 4)
+                for (int t = 0; t < a.rows; t++) combine<DT>(a, t, h);
     }
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     if (warp == kIssuer) tmem_free(tmem, NT <= 16 ? 32 : 2 * NT);
-    if (threadIdx.x == 0 && l.failed) report_error(a.status, a.statusHost, vTimeout, blockIdx.x, 0, UP ? 0 : 1);
+    if (threadIdx.x == 0 && sh.failed) report_error(a.status, a.statusHost, vTimeout, blockIdx.x, 0, UP ? 0 : 1);
     if (split > 1) {                                   // another CTA may still arrive here
         cluster_arrive();
         cluster_wait();
     }
 }
 
-// Every token's slots added up, for many tokens: a thread a column, a CTA a few tokens.
-constexpr int kCombineThreads = 256, kCombineTokens = 2;
+// Every token's slots added up, for many tokens: a thread four columns of a token.
+constexpr int kCombineThreads = 128;
 template <int DT>
 __global__ void __launch_bounds__(kCombineThreads) k_moe_combine(const __grid_constant__ ExpertsArgs a) {
     pdl_begin();
-    const int h = (int)blockIdx.x * kCombineThreads + (int)threadIdx.x, t0 = (int)blockIdx.y * kCombineTokens;
-    if (h < a.hidden) combine<DT>(a, t0, min(a.rows, t0 + kCombineTokens), h);
+    const int h = 4 * ((int)blockIdx.x * kCombineThreads + (int)threadIdx.x);
+    if (h < a.hidden) combine<DT>(a, (int)blockIdx.y, h);
 }
 
-template <int DT, int NT, bool UP, int STAGES>
+template <int DT, int NT, bool UP>
 cudaError_t tiles_launch(const ExpertsArgs& a, const MoeTiles& t, cudaStream_t s) {
-    const auto kernel = k_moe_tiles<DT, NT, UP, STAGES>;
-    constexpr int stage = 2 * kHalfA + (UP ? 1 : 2) * 2 * NT * 128;
-    constexpr int parts = NT == 16 ? (kMoeMaxSplit - 1) * NT * kM * 4 : 0;
-    constexpr int bytes = STAGES * stage + parts + 1024;
-    static_assert(bytes + (int)sizeof(Lists) <= 227 * 1024, "shared memory of a CTA");
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const auto kernel = k_moe_tiles<DT, NT, UP>;
+    // one value for every launch, as host threads share the kernel's limit
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoeMaxSmem);
     if (e != cudaSuccess) return e;
     ExpertsArgs b = a;
     b.split = UP ? t.splitUp : t.splitDown;
+    b.stages = UP ? t.stagesUp : t.stagesDown;
     b.combineHere = t.combineHere;
     NormShape sh = {};
     sh.threads = kThreads;
     sh.cluster = b.split;
-    return norm_launch(kernel, (unsigned)(UP ? t.gridUp : t.gridDown), sh, bytes, s, b);
+    return norm_launch(kernel, (unsigned)(UP ? t.gridUp : t.gridDown), sh,
+                       (size_t)moe_tiles_smem(a.experts, a.rows * a.topK, NT, UP, b.split, b.stages), s, b);
+}
+template <int DT, int NT>
+cudaError_t tiles_both(const ExpertsArgs& a, const MoeTiles& t, cudaStream_t s) {
+    const cudaError_t e = tiles_launch<DT, NT, true>(a, t, s);
+    return e != cudaSuccess ? e : tiles_launch<DT, NT, false>(a, t, s);
 }
 template <int DT>
 cudaError_t tiles_dt(const ExpertsArgs& a, const MoeTiles& t, cudaStream_t s) {
-    cudaError_t e;
-    switch (t.tokens) {
-    case 16:
-        e = tiles_launch<DT, 16, true, 5>(a, t, s);
-        if (e == cudaSuccess) e = tiles_launch<DT, 16, false, 4>(a, t, s);
-        break;
-    case 32:
-        e = tiles_launch<DT, 32, true, 5>(a, t, s);
-        if (e == cudaSuccess) e = tiles_launch<DT, 32, false, 4>(a, t, s);
-        break;
-    default:
-        e = tiles_launch<DT, 64, true, 4>(a, t, s);
-        if (e == cudaSuccess) e = tiles_launch<DT, 64, false, 3>(a, t, s);
-        break;
-    }
+    const cudaError_t e = t.tokens == 16   ? tiles_both<DT, 16>(a, t, s)
+                          : t.tokens == 32 ? tiles_both<DT, 32>(a, t, s)
+                                           : tiles_both<DT, 64>(a, t, s);
     if (e != cudaSuccess || t.combineHere) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.hidden + kCombineThreads - 1) / kCombineThreads),
-                       (unsigned)((a.rows + kCombineTokens - 1) / kCombineTokens));
+    cfg.gridDim = dim3((unsigned)((a.hidden + 4 * kCombineThreads - 1) / (4 * kCombineThreads)), (unsigned)a.rows);
     cfg.blockDim = dim3(kCombineThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -67,6 +67,17 @@ vc::MoeTiles moe_tiles(const vc::ExpertsArgs& a, int smCount) {
     };
     shape((a.ffn + 63) / 64, a.hidden, &t.splitUp, &t.gridUp);
     shape((a.hidden + 127) / 128, a.ffn, &t.splitDown, &t.gridDown);
+    const auto stages = [&](bool up, int bytes) {
+        int n = 2;
+        while (n < vc::kMoeMaxStages &&
+               vc::moe_tiles_smem(a.experts, slots, t.tokens, up, up ? t.splitUp : t.splitDown, n + 1) <= bytes) n++;
+        return n;
+    };
+    // A tile or two a CTA: both launches' CTAs on an SM, so that the second's first weights are on their
+    // way while the first still runs.
+    const bool few = groups * ((a.ffn + 63) / 64) * t.splitUp <= 2 * t.gridUp && t.tokens == 16;
+    t.stagesUp = stages(true, few ? 124 * 1024 : vc::kMoeMaxSmem);
+    t.stagesDown = stages(false, few ? 100 * 1024 : vc::kMoeMaxSmem);
     t.combineHere = a.rows <= 4;
     return t;
 }
@@ -142,6 +153,7 @@ vResult_t experts(const vMoeDesc_t* desc, const void* x, const int* ids, const f
     vc::ExpertsArgs a;
     const size_t e = 16 / (size_t)m.esz;
     a.aligned = m.d.hidden % e == 0 && m.d.ffn % e == 0 && (m.d.rows == 1 || m.d.rowStride % e == 0) && at(x, 16);
+    a.recvAligned = m.d.rows == 1 || m.d.recvStride * m.esz % 8 == 0;
     for (int k = 0; k < v.nRanks; k++) {
         const bool holds = k * m.share < m.d.experts;  // else its weights are not looked at
         if (holds && (!up[k] || !at(up[k], m.esz) || !down[k] || !at(down[k], m.esz))) return vInvalidArgument;
@@ -149,6 +161,7 @@ vResult_t experts(const vMoeDesc_t* desc, const void* x, const int* ids, const f
         a.up[k] = up[k];
         a.down[k] = down[k];
         a.recv[k] = recv[k];
+        a.recvAligned = a.recvAligned && at(recv[k], 8);
         if (holds) a.aligned = a.aligned && at(up[k], 16) && at(down[k], 16);
     }
     const Layout l(m);

@@ -45,7 +45,9 @@ struct ExpertsArgs {
     int nRanks;
     int share;                       // experts of a rank
     int aligned;                     // every row of x and of the weights starts on 16 bytes and ends with a vector
+    int recvAligned;                 // every row of the outputs starts on 8 bytes
     int split;                       // tensor cores: CTAs of a cluster that share a tile's columns
+    int stages;                      // the same: stages of a CTA
     int combineHere;                 // the same: the way down adds up the slots
     Status* status;                  // device copy
     volatile Status* statusHost;     // pinned mirror
@@ -55,11 +57,28 @@ cudaError_t launch_moe_experts(const ExpertsArgs& a, vDataType_t dt, cudaStream_
 
 // The same on the tensor cores.
 constexpr int kMoeTileSlots = 4096;  // rows * topK, at most
-constexpr int kMoeMaxSplit = 4;
+constexpr int kMoeMaxStages = 8;
+constexpr int kMoeMaxSmem = 225 * 1024;
+struct MoeGroup {                    // tokens of one expert, as many as a tile takes
+    uint16_t expert, first, count;   // first: of its slots in the list
+};
+#if defined(__CUDACC__)
+__host__ __device__
+#endif
+constexpr int moe_groups(int experts, int slots, int tokens) {
+    return (experts < slots ? experts : slots) + slots / tokens;
+}
+// Dynamic shared memory of a CTA: stages, the sums of the other CTAs of a cluster, and the lists.
+constexpr int moe_stage_bytes(int tokens, bool up) { return 128 * 256 + (up ? 1 : 2) * tokens * 256; }
+constexpr int moe_tiles_smem(int experts, int slots, int tokens, bool up, int split, int stages) {
+    return 1024 + stages * moe_stage_bytes(tokens, up) + (split - 1) * tokens * 128 * 4 + experts * 4 +
+           moe_groups(experts, slots, tokens) * (int)sizeof(MoeGroup) + slots * 2;
+}
 struct MoeTiles {
     int tokens;                      // of a tile: 16, 32 or 64
     int splitUp, splitDown;          // CTAs of a cluster that share a tile's columns: 1, 2 or 4
     int gridUp, gridDown;
+    int stagesUp, stagesDown;
     int combineHere;                 // few tokens: no third launch
 };
 cudaError_t launch_moe_tiles(const ExpertsArgs& a, const MoeTiles& t, vDataType_t dt, cudaStream_t s);
