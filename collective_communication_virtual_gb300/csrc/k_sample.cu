@@ -16,8 +16,9 @@
 // The draw is a comparison of sums, so these are exact: a weight is a 64-bit integer, 2^44 e, right to
 // 2^-30 of itself, and the order of additions does not matter.
 //
-// A row is read once, into the shared memory of a cluster's CTAs, which exchange maxima, histograms
-// and sums there.
+// A row is read once, into the shared memory of a cluster's CTAs, which exchange maxima and sums there.
+// What is above the bounds, where it is few, goes to the first of them, which decides alone, without the
+// cluster's barriers (more than a microsecond each); else all decide together.
 #include "norm_stage.cuh"
 #include "sample.h"
 
@@ -27,7 +28,9 @@ namespace {
 
 constexpr int kWarps = kSampleThreads / 32;
 constexpr int kFix = 44;             // weights in units of 2^-44
+constexpr int kLevels = 4;           // groups of values by lanes: 32, 16, 8 and 1 of them
 typedef unsigned long long u64;
+constexpr int kWords = 4;            // that the CTAs of a cluster exchange at a time
 
 // 2^31 2^(k / 32), rounded
 __constant__ uint32_t kPowers[32] = {
@@ -39,11 +42,11 @@ __constant__ uint32_t kPowers[32] = {
 struct Shared {
     uint32_t powers[32];
     float max[kWarps];
-    float low[3][kWarps];            // smallest maximum of a warp, of its 8-lane groups, of its lanes
+    float low[kLevels][kWarps];      // smallest maximum of the groups of a level
     u64 warp[2][kWarps];
-    u64 box[2][kSampleCluster][4];   // one line a CTA, written by all CTAs of the cluster
+    u64 box[2][kSampleCluster][kWords];      // one line a CTA, written by all CTAs of the cluster
     u64 found[2][3];                 // bin, what lies before it, what lies in it
-    u64 target;
+    u64 target, left, total;
     int owner;
 };
 
@@ -68,8 +71,8 @@ __device__ __forceinline__ uint32_t ld_cluster(const void* local, unsigned rank)
 }
 // Every CTA's four words in box[.][its rank] of every CTA.  Called by all threads; `mine` is the same
 // in all.  Two boxes in turn: a CTA writes one again only when all have met since it was read.
-__device__ __forceinline__ const u64 (*exchange(Shared& sh, Team& team, const u64 (&mine)[4]))[4] {
-    u64(*box)[4] = sh.box[team.flip];
+__device__ __forceinline__ const u64 (*exchange(Shared& sh, Team& team, const u64 (&mine)[kWords]))[kWords] {
+    u64(*box)[kWords] = sh.box[team.flip];
     team.flip ^= 1;
     if (team.size == 1) {
         __syncthreads();
@@ -149,22 +152,45 @@ struct Weights {
     }
 };
 
-// A CTA's columns in shared memory: vector `step * 32 + lane` of a warp's run.
+// Values in shared memory, cut into runs of `steps` times 32 vectors, one a warp.
 template <int DT>
 struct Columns {
     static constexpr int E = kVecElems<DT>;
     uint32_t base;                   // the thread's first vector
-    int first, steps;                // its first column within the CTA
+    int first, steps;                // its first value's number
     __device__ __forceinline__ Columns(uint32_t smem, int n) : steps(n) {
         const int vec = (int)(threadIdx.x >> 5) * 32 * n + (int)(threadIdx.x & 31);
         base = smem + (uint32_t)vec * 16u;
         first = vec * E;
     }
-    // Values of a step; a NaN counts as minus infinity.
-    __device__ __forceinline__ void get(int step, float (&f)[E]) const {
-        widen_vec<DT>(ld_smem(base + (uint32_t)step * 512u), f);
-#pragma unroll
-        for (int j = 0; j < E; j++) f[j] = f[j] == f[j] ? f[j] : -INFINITY;
+    __device__ __forceinline__ uint32_t at(int step) const { return base + (uint32_t)step * 512u; }
+    __device__ __forceinline__ void get(int step, float (&f)[E]) const { widen_vec<DT>(ld_smem(at(step)), f); }
+    // The largest of a step's values, by pairs in the 16-bit types.
+    __device__ __forceinline__ float largest(int step) const { return largest_of(ld_smem(at(step))); }
+    static __device__ __forceinline__ float largest_of(const uint4& v) {
+        if (DT == kF32)
+            return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+        const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+        return fmaxf(widen16<DT == kF32 ? kBF16 : DT>((uint16_t)m), widen16<DT == kF32 ? kBF16 : DT>((uint16_t)(m >> 16)));
+    }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        if (DT == kBF16) {
+            const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+            return *reinterpret_cast<const uint32_t*>(&r);
+        }
+        const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    // Whether a vector may hold a NaN: its sums are one then (infinities of both signs give one too).
+    static __device__ __forceinline__ bool suspect(const uint4& v) {
+        if (DT == kF32) {
+            const float t = (__uint_as_float(v.x) + __uint_as_float(v.y)) + (__uint_as_float(v.z) + __uint_as_float(v.w));
+            return t != t;
+        }
+        const uint32_t t = op_word<DT == kF32 ? kBF16 : DT, kSum>(op_word<DT == kF32 ? kBF16 : DT, kSum>(v.x, v.y),
+                                                                   op_word<DT == kF32 ? kBF16 : DT, kSum>(v.z, v.w));
+        const float a = widen16<DT == kF32 ? kBF16 : DT>((uint16_t)t), b = widen16<DT == kF32 ? kBF16 : DT>((uint16_t)(t >> 16));
+        return a != a || b != b;
     }
 };
 
@@ -202,10 +228,10 @@ __device__ __forceinline__ void load_columns(const SampleArgs& a, int row, int c
 // The distance d from the largest key at which the running count (or, BY_MASS, the running sum of
 // weights) reaches `target`: *before is what lies before d.  Looks at distances of at most `most`.
 // False where all of them together do not reach it.
-template <int DT, bool BY_MASS>
-__device__ bool search(Shared& sh, Team& team, uint32_t* hist, const Columns<DT>& cols, const Weights& w, uint32_t keyTop,
+template <int DT, bool BY_MASS, typename Cols>
+__device__ bool search(Shared& sh, Team& team, uint32_t* hist, const Cols& cols, const Weights& w, uint32_t keyTop,
                        uint32_t most, u64 target, uint32_t* at, u64* before) {
-    constexpr int E = kVecElems<DT>;
+    constexpr int E = Cols::E;
     uint32_t* const low = hist;                        // counts, or the sums' low words
     uint32_t* const high = hist + kSampleBins;
     const int slice = kSampleBins / team.size, per = max(1, slice / kSampleThreads);
@@ -269,8 +295,8 @@ __device__ bool search(Shared& sh, Team& team, uint32_t* hist, const Columns<DT>
             if (i < warp) ahead += sh.warp[0][i];
             all += sh.warp[0][i];
         }
-        const u64 mine[4] = {all, 0, 0, 0};
-        const u64(*box)[4] = exchange(sh, team, mine);
+        const u64 mine[kWords] = {all, 0, 0, 0};
+        const u64(*box)[kWords] = exchange(sh, team, mine);
         u64 total = below;
         ahead += below;
         for (int c = 0; c < team.size; c++) {
@@ -304,143 +330,63 @@ __device__ bool search(Shared& sh, Team& team, uint32_t* hist, const Columns<DT>
     return true;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kSampleThreads) k_sample(const __grid_constant__ SampleArgs a) {
-    pdl_begin();
-    constexpr int E = kVecElems<DT>;
-    extern __shared__ __align__(16) unsigned char dynamic[];
-    __shared__ Shared sh;
-    uint32_t* const hist = reinterpret_cast<uint32_t*>(dynamic);
-    const uint32_t values = (uint32_t)__cvta_generic_to_shared(dynamic) + 2 * kSampleBins * 4;
+// What the filters of a row ask for.
+struct Filters {
+    float heat, p, least;
+    int k;                           // vocab: no limit
+    bool greedy, limited, nucleus;
+};
+
+// The exact sum of all weights.
+template <typename Cols>
+__device__ u64 exact_sum(Shared& sh, Team& team, const Cols& cols, const Weights& w) {
+    u64 s = 0, none = 0;
+    for (int i = 0; i < cols.steps; i++) {
+        float f[Cols::E];
+        cols.get(i, f);
+#pragma unroll
+        for (int j = 0; j < Cols::E; j++) s += w.fixed(f[j]);
+    }
+    block_sums(sh, s, none);
+    const u64 mine[kWords] = {s, 0, 0, 0};
+    const u64(*box)[kWords] = exchange(sh, team, mine);
+    u64 all = 0;
+    for (int c = 0; c < team.size; c++) all += box[c][0];
+    return all;
+}
+
+// The smallest value of weight `e`, with room for the roundings.
+__device__ __forceinline__ float value_at(const Weights& w, float e) {
+    const float x = w.top + (__log2f(e) - 0.01f) / w.ch;
+    return x - 1e-5f * fabsf(x) - 1e-5f * fabsf(w.top);
+}
+
+// The token, from values that hold all that may be kept: none below kBound counts for topK, none below
+// pBound for topP.  exact: the sum of all weights where topP is a share of it, else 0; total: of the
+// weights before the filters, 0 where it is not known yet.  token_of gives a value's token.
+template <int DT, typename Cols, typename TokenOf>
+__device__ __forceinline__ void decide(const SampleArgs& a, const Filters& q, Shared& sh, Team& team, uint32_t* hist, const Cols& cols,
+                                       const Weights& w, float kBound, float pBound, u64 exact, u64 total, int row, TokenOf token_of) {
+    constexpr int E = Cols::E;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Team team;
-    team.size = a.cluster;
-    team.rank = a.cluster > 1 ? (int)cluster_rank() : 0;
-    team.flip = team.flipFound = 0;
-    const int row = (int)(blockIdx.x / (unsigned)a.cluster);
-    const int columns = a.steps * kSampleThreads * E, c0 = team.rank * columns;
-    if (threadIdx.x < 32) sh.powers[threadIdx.x] = kPowers[threadIdx.x];
-    const float heat = a.temperature ? a.temperature[row] : 1.0f;
-    const bool greedy = !(heat > 0.0f);
-    int k = greedy ? 1 : a.topK ? a.topK[row] : 0;
-    if (k <= 0 || k >= a.vocab) k = a.vocab;           // no limit
-    const float p = a.topP && !greedy ? a.topP[row] : 1.0f;
-    const float least = a.minP && !greedy ? a.minP[row] : 0.0f;
-    load_columns<DT>(a, row, c0, columns, values);
-    const Columns<DT> cols(values, a.steps);
-
-    // The largest value, and for topK the smallest maximum of disjoint groups.
-    float top = -INFINITY;
-    for (int s = 0; s < cols.steps; s++) {
-        float f[E];
-        cols.get(s, f);
-#pragma unroll
-        for (int j = 0; j < E; j++) top = fmaxf(top, f[j]);
-    }
-    float low[3];
-    low[2] = top;
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    low[1] = top;
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
-    low[0] = top;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        low[1] = fminf(low[1], __shfl_xor_sync(~0u, low[1], o));
-        low[2] = fminf(low[2], __shfl_xor_sync(~0u, low[2], o));
-    }
-    if (lane == 0) {
-        sh.max[warp] = top;
-        for (int i = 0; i < 3; i++) sh.low[i][warp] = low[i];
-    }
-    if (team.size > 1) meet(team);                     // every CTA of the cluster has started
-    else __syncthreads();
-    for (int i = 0; i < kWarps; i++) {
-        top = fmaxf(top, sh.max[i]);
-        for (int g = 0; g < 3; g++) low[g] = fminf(low[g], sh.low[g][i]);
-    }
-    {
-        const u64 mine[4] = {__float_as_uint(top), __float_as_uint(low[0]), __float_as_uint(low[1]), __float_as_uint(low[2])};
-        const u64(*box)[4] = exchange(sh, team, mine);
-        for (int c = 0; c < team.size; c++) {
-            top = fmaxf(top, __uint_as_float((uint32_t)box[c][0]));
-            for (int g = 0; g < 3; g++) low[g] = fminf(low[g], __uint_as_float((uint32_t)box[c][1 + g]));
-        }
-    }
-    if (top == -INFINITY) {                            // nothing to draw from
-        if (threadIdx.x == 0 && team.rank == 0) {
-            for (int o = 0; o < a.nOut; o++) a.tokens[o][row] = -1;
-            if (a.logprob) a.logprob[row] = __int_as_float(0x7FFFFFFF);
-        }
-        return;
-    }
-
-    Weights w;
-    w.top = top;
-    w.powers = sh.powers;
-    {
-        // log2(e) / temperature and what its rounding lost, kept off zero and infinity
-        const float t = greedy ? 1.0f : heat, l2e = 1.44269504088896341f, l2eLow = 1.9259629911266175e-8f;
-        const float r = __frcp_rn(t), c = __fmul_rn(l2e, r);
-        w.ch = fminf(fmaxf(c, 1.17549435e-38f), 3.40282347e38f);
-        w.cl = (__fmaf_rn(-c, t, l2e) + l2eLow) * r;
-        if (w.ch != c || !(fabsf(w.cl) <= 1e-6f * c)) w.cl = 0.0f;
-    }
+    const float top = w.top;
     const uint32_t keyTop = key_of<DT>(top);
     // Distance of the smallest value that a value of at least x can have.
     const auto distance = [&](float x) { return x >= top ? 0u : keyTop - key_of<DT>(fmaxf(x, -3.40282347e38f)); };
-    const bool limited = k < a.vocab, nucleus = p < 1.0f && k > 1;
-    // The smallest value of weight `e`, with room for the roundings.
-    const auto value_at = [&](float e) {
-        const float x = top + (__log2f(e) - 0.01f) / w.ch;
-        return x - 1e-5f * fabsf(x) - 1e-5f * fabsf(top);
-    };
 
-    // The sum of all weights: exactly, where topP is a share of it, or the draw goes through all.
-    u64 total = 0, exact = 0;
-    const auto sum_all = [&](bool exactly) {
-        u64 s = 0, none = 0;
-        for (int i = 0; i < cols.steps; i++) {
-            float f[E];
-            cols.get(i, f);
-            if (exactly) {
-#pragma unroll
-                for (int j = 0; j < E; j++) s += w.fixed(f[j]);
-            } else {
-                float part = 0.0f;
-#pragma unroll
-                for (int j = 0; j < E; j++) {          // the largest apart: what is beside them may be small
-                    part += f[j] == top ? 0.0f : w.rough(f[j]);
-                    s += f[j] == top ? 1ull << kFix : 0ull;
-                }
-                s += __float2ull_rn(part * (float)(1ull << kFix));
-            }
-        }
-        block_sums(sh, s, none);
-        const u64 mine[4] = {s, 0, 0, 0};
-        const u64(*box)[4] = exchange(sh, team, mine);
-        u64 all = 0;
-        for (int c = 0; c < team.size; c++) all += box[c][0];
-        return all;
-    };
-    if (limited || least > 0.0f || !nucleus) total = sum_all(false);
-
-    // What is kept: distances below `edge`, and the first `ties` columns at it.
+    // What is kept: distances below `edge`, and the first `ties` values at it.
     uint32_t edge = 0xFFFFFFFFu;
     u64 ties = 0, before = 0;
     bool cut = false;
-    if (k == 1) {                    // the first of the largest
+    if (q.k == 1) {                  // the first of the largest
         edge = 0;
         ties = 1;
         cut = true;
-    } else if (limited) {
-        const int groups = team.size * kWarps;
-        const float bound = k <= groups ? low[0] : k <= 4 * groups ? low[1] : k <= 32 * groups ? low[2] : -INFINITY;
-        cut = search<DT, false>(sh, team, hist, cols, w, keyTop, distance(bound), (u64)k, &edge, &before);
-        if (cut) ties = (u64)k - before;
+    } else if (q.limited) {
+        cut = search<DT, false>(sh, team, hist, cols, w, keyTop, distance(kBound), (u64)q.k, &edge, &before);
+        if (cut) ties = (u64)q.k - before;
     }
-    if (nucleus) {
+    if (q.nucleus) {
         uint32_t most;
         if (cut) {                   // the sum of the topK
             u64 s = 0, none = 0;
@@ -452,17 +398,16 @@ __global__ void __launch_bounds__(kSampleThreads) k_sample(const __grid_constant
                     if (keyTop - key_of<DT>(f[j]) < edge) s += w.fixed(f[j]);
             }
             block_sums(sh, s, none);
-            const u64 mine[4] = {s, 0, 0, 0};
-            const u64(*box)[4] = exchange(sh, team, mine);
+            const u64 mine[kWords] = {s, 0, 0, 0};
+            const u64(*box)[kWords] = exchange(sh, team, mine);
             exact = ties * w.fixed(value_of<DT>(keyTop - edge));
             for (int c = 0; c < team.size; c++) exact += box[c][0];
             most = edge;
-        } else {                     // weights below (1 - p) of the mean are outside, all of them together
-            exact = sum_all(true);
-            if (total == 0) total = exact;
-            most = distance(value_at((1.0f - fmaxf(p, 0.0f)) * 0.99f * ((float)exact * 0x1p-44f) / (float)a.vocab));
+        } else {
+            if (q.limited) exact = exact_sum(sh, team, cols, w);     // fewer than topK
+            most = distance(pBound);
         }
-        const u64 goal = max(1ull, (u64)ceil((double)fmaxf(p, 0.0f) * (double)exact));
+        const u64 goal = max(1ull, (u64)ceil((double)fmaxf(q.p, 0.0f) * (double)exact));
         uint32_t at;
         if (search<DT, true>(sh, team, hist, cols, w, keyTop, most, goal, &at, &before)) {
             const u64 one = max(1ull, w.fixed(value_of<DT>(keyTop - at)));
@@ -472,9 +417,8 @@ __global__ void __launch_bounds__(kSampleThreads) k_sample(const __grid_constant
             cut = true;
         }
     }
-    if (total == 0) total = exact;
-    const u64 floorWeight = least > 0.0f ? (u64)ceil((double)fminf(least, 1.0f) * (double)(1ull << kFix)) : 0;
-    const float floorValue = floorWeight ? value_at(fminf(least, 1.0f)) : -INFINITY;
+    const u64 floorWeight = q.least > 0.0f ? (u64)ceil((double)fminf(q.least, 1.0f) * (double)(1ull << kFix)) : 0;
+    const float floorValue = floorWeight ? value_at(w, fminf(q.least, 1.0f)) : -INFINITY;
 
     // Weights kept by every warp, its ties at the edge aside.
     u64 atEdge = cut ? w.fixed(value_of<DT>(keyTop - edge)) : 0;
@@ -486,8 +430,11 @@ __global__ void __launch_bounds__(kSampleThreads) k_sample(const __grid_constant
         const u64 v = w.fixed(x);
         return v >= floorWeight ? v : 0ull;
     };
+    // What lies below this is not kept, and no tie.
+    const float bottom = fmaxf(cut ? value_of<DT>(keyTop - edge) : -INFINITY, floorValue);
     u64 sum = 0, count = 0;
     for (int s = 0; s < cols.steps; s++) {
+        if (cols.largest(s) < bottom) continue;
         float f[E];
         cols.get(s, f);
 #pragma unroll
@@ -499,8 +446,8 @@ __global__ void __launch_bounds__(kSampleThreads) k_sample(const __grid_constant
     }
     u64 blockSum = sum, blockCount = count;
     block_sums(sh, blockSum, blockCount);              // leaves every warp's sums in sh.warp
-    const u64 mine[4] = {blockSum, blockCount, 0, 0};
-    const u64(*box)[4] = exchange(sh, team, mine);
+    const u64 mine[kWords] = {blockSum, blockCount, 0, 0};
+    const u64(*box)[kWords] = exchange(sh, team, mine);
     // From here on nothing touches another CTA's memory.
     if (threadIdx.x == 0) {
         u64 all = 0, ahead = 0, left = ties, leftHere = ties;
@@ -517,12 +464,13 @@ __global__ void __launch_bounds__(kSampleThreads) k_sample(const __grid_constant
         u64 goal = u > 0.0f ? (u64)((double)u * (double)all) : 0;
         goal = min(goal, all - 1);
         sh.owner = -1;
+        sh.total = total ? total : all;
         for (int i = 0; i < kWarps && goal >= ahead; i++) {
             const u64 n = min(leftHere, sh.warp[1][i]), here = sh.warp[0][i] + n * atEdge;
             if (goal < ahead + here) {
                 sh.owner = i;
                 sh.target = goal - ahead;
-                sh.box[0][0][0] = leftHere;            // nobody reads the boxes any more but this thread
+                sh.left = leftHere;
                 break;
             }
             ahead += here;
@@ -532,8 +480,8 @@ __global__ void __launch_bounds__(kSampleThreads) k_sample(const __grid_constant
     __syncthreads();
     if (warp != sh.owner) return;
 
-    // The warp whose columns hold the token goes through them in order.
-    u64 goal = sh.target, left = sh.box[0][0][0];
+    // The warp whose values hold the token goes through them in order.
+    u64 goal = sh.target, left = sh.left;
     for (int s = 0; s < cols.steps; s++) {
         float f[E];
         cols.get(s, f);
@@ -545,6 +493,7 @@ __global__ void __launch_bounds__(kSampleThreads) k_sample(const __grid_constant
             own += v[j];
             n += tie[j];
         }
+        if (!__any_sync(~0u, own + n != 0)) continue;
         u64 runTies = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -579,11 +528,11 @@ __global__ void __launch_bounds__(kSampleThreads) k_sample(const __grid_constant
                     x = f[j];
                 }
             }
-            const int token = c0 + cols.first + s * 32 * E + pick;
+            const int token = token_of(cols.first + s * 32 * E + pick);
             for (int o = 0; o < a.nOut; o++) a.tokens[o][row] = token;
             if (a.logprob) {
-                const float z = x == top ? 0.0f : greedy ? x - top : (x - top) / heat;
-                a.logprob[row] = z - log1pf((float)(total - (1ull << kFix)) * 0x1p-44f);
+                const float z = x == top ? 0.0f : q.greedy ? x - top : (x - top) / q.heat;
+                a.logprob[row] = z - log1pf((float)(sh.total - (1ull << kFix)) * 0x1p-44f);
             }
         }
         if (__any_sync(~0u, here)) return;
@@ -593,11 +542,222 @@ __global__ void __launch_bounds__(kSampleThreads) k_sample(const __grid_constant
 }
 
 template <int DT>
+__global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_constant__ SampleArgs a) {
+    pdl_begin();
+    constexpr int E = kVecElems<DT>;
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    __shared__ Shared sh;
+    uint32_t* const hist = reinterpret_cast<uint32_t*>(dynamic);
+    float* const listValues = reinterpret_cast<float*>(hist + 2 * kSampleBins);
+    int* const listTokens = reinterpret_cast<int*>(listValues + kSampleList);
+    const uint32_t values = (uint32_t)__cvta_generic_to_shared(listTokens + kSampleList);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Team team;
+    team.size = a.cluster;
+    team.rank = a.cluster > 1 ? (int)cluster_rank() : 0;
+    team.flip = team.flipFound = 0;
+    const int row = (int)(blockIdx.x / (unsigned)a.cluster);
+    const int columns = a.steps * kSampleThreads * E, c0 = team.rank * columns;
+    if (threadIdx.x < 32) sh.powers[threadIdx.x] = kPowers[threadIdx.x];
+    Filters q;
+    q.heat = a.temperature ? a.temperature[row] : 1.0f;
+    q.greedy = !(q.heat > 0.0f);
+    q.k = q.greedy ? 1 : a.topK ? a.topK[row] : 0;
+    if (q.k <= 0 || q.k >= a.vocab) q.k = a.vocab;
+    q.p = a.topP && !q.greedy ? a.topP[row] : 1.0f;
+    q.least = a.minP && !q.greedy ? a.minP[row] : 0.0f;
+    q.limited = q.k < a.vocab;
+    q.nucleus = q.p < 1.0f && q.k > 1;
+    load_columns<DT>(a, row, c0, columns, values);
+    const Columns<DT> cols(values, a.steps);
+
+    // The largest value, and for topK the smallest maximum of disjoint groups.  A NaN counts as minus
+    // infinity, and is overwritten by it.
+    float top = -INFINITY;
+    for (int s = 0; s < cols.steps; s++) {
+        const uint4 v = ld_smem(cols.at(s));
+        float m = cols.largest_of(v);
+        if (cols.suspect(v)) {
+            float f[E];
+            widen_vec<DT>(v, f);
+            m = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < E; j++) {
+                f[j] = f[j] == f[j] ? f[j] : -INFINITY;
+                m = fmaxf(m, f[j]);
+            }
+            st_smem(cols.at(s), narrow_vec<DT>(f));
+        }
+        top = fmaxf(top, m);
+    }
+    float low[kLevels];
+    low[3] = top;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    low[2] = top;
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+    low[1] = top;
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+    low[0] = top;
+    low[1] = fminf(low[1], __shfl_xor_sync(~0u, low[1], 16));
+    low[2] = fminf(low[2], __shfl_xor_sync(~0u, low[2], 16));
+    low[2] = fminf(low[2], __shfl_xor_sync(~0u, low[2], 8));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) low[3] = fminf(low[3], __shfl_xor_sync(~0u, low[3], o));
+    if (lane == 0) {
+        sh.max[warp] = top;
+        for (int i = 0; i < kLevels; i++) sh.low[i][warp] = low[i];
+    }
+    meet(team);                                        // every CTA of the cluster has started
+    for (int i = 0; i < kWarps; i++) top = fmaxf(top, sh.max[i]);
+    // the level whose groups are at least k
+    const int groups = team.size * kWarps;
+    const int level = q.k <= groups ? 0 : q.k <= 2 * groups ? 1 : q.k <= 4 * groups ? 2 : 3;
+    float kBound = INFINITY;
+    for (int i = 0; i < kWarps; i++) kBound = fminf(kBound, sh.low[level][i]);
+    {
+        const u64 mine[kWords] = {__float_as_uint(top), __float_as_uint(kBound), 0, 0};
+        const u64(*box)[kWords] = exchange(sh, team, mine);
+        for (int c = 0; c < team.size; c++) {
+            top = fmaxf(top, __uint_as_float((uint32_t)box[c][0]));
+            kBound = fminf(kBound, __uint_as_float((uint32_t)box[c][1]));
+        }
+        if (q.k > 32 * groups) kBound = -INFINITY;
+    }
+    if (top == -INFINITY) {                            // nothing to draw from
+        if (threadIdx.x == 0 && team.rank == 0) {
+            for (int o = 0; o < a.nOut; o++) a.tokens[o][row] = -1;
+            if (a.logprob) a.logprob[row] = __int_as_float(0x7FFFFFFF);
+        }
+        return;
+    }
+
+    Weights w;
+    w.top = top;
+    w.powers = sh.powers;
+    {
+        // log2(e) / temperature and what its rounding lost, kept off zero and infinity
+        const float t = q.greedy ? 1.0f : q.heat, l2e = 1.44269504088896341f, l2eLow = 1.9259629911266175e-8f;
+        const float r = __frcp_rn(t), c = __fmul_rn(l2e, r);
+        w.ch = fminf(fmaxf(c, 1.17549435e-38f), 3.40282347e38f);
+        w.cl = (__fmaf_rn(-c, t, l2e) + l2eLow) * r;
+        if (w.ch != c || !(fabsf(w.cl) <= 1e-6f * c)) w.cl = 0.0f;
+    }
+
+    // All that may be kept is at least `bound`: topK's is known, topP's follows from the sum of all weights
+    // (those below (1 - p) of the mean are outside it, all of them together), minP's is a weight.
+    u64 exact = 0, total = 0;
+    float bound = -INFINITY, pBound = -INFINITY;
+    if (q.k == 1) {
+        bound = kBound = top;
+    } else if (q.limited) {
+        bound = kBound;
+    } else if (q.nucleus) {
+        total = exact = exact_sum(sh, team, cols, w);
+        bound = pBound = value_at(w, (1.0f - fmaxf(q.p, 0.0f)) * 0.99f * ((float)exact * 0x1p-44f) / (float)a.vocab);
+    }
+    if (!q.nucleus && q.least > 0.0f) bound = fmaxf(bound, value_at(w, fminf(q.least, 1.0f)));
+    if (!(bound <= top)) bound = bound > top ? top : -INFINITY;
+
+    // The sum of all weights where it is not exact yet, and what is above the bound.
+    const bool filtered = q.limited || q.nucleus || q.least > 0.0f;
+    u64 sum = 0, count = 0;
+    if (filtered) {
+        for (int s = 0; s < cols.steps; s++) {
+            const uint4 v = ld_smem(cols.at(s));
+            const float m = cols.largest_of(v);
+            if (total && m < bound) continue;
+            float f[E];
+            widen_vec<DT>(v, f);
+            if (!total) {
+                float part = 0.0f;
+                if (m == top) {      // the largest apart: what is beside them may be small
+#pragma unroll
+                    for (int j = 0; j < E; j++) {
+                        part += f[j] == top ? 0.0f : w.rough(f[j]);
+                        sum += f[j] == top ? 1ull << kFix : 0ull;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < E; j++) part += w.rough(f[j]);
+                }
+                sum += __float2ull_rn(part * (float)(1ull << kFix));
+            }
+            if (m < bound) continue;
+#pragma unroll
+            for (int j = 0; j < E; j++) count += f[j] >= bound;
+        }
+        u64 blockSum = sum, blockCount = count;
+        block_sums(sh, blockSum, blockCount);          // leaves every warp's sums in sh.warp
+        const u64 mine[kWords] = {blockSum, blockCount, 0, 0};
+        const u64(*box)[kWords] = exchange(sh, team, mine);
+        u64 all = 0, ahead = 0, few = 0;
+        for (int c = 0; c < team.size; c++) {
+            all += box[c][0];
+            if (c < team.rank) ahead += box[c][1];
+            few += box[c][1];
+        }
+        if (!total) total = all;
+        if (few <= (u64)kSampleList) {
+            // to the first CTA's list, in order
+            int at = (int)ahead;
+            for (int i = 0; i < warp; i++) at += (int)sh.warp[1][i];
+            for (int s = 0; s < cols.steps; s++) {
+                const uint4 v = ld_smem(cols.at(s));
+                const bool any = cols.largest_of(v) >= bound;
+                if (!__any_sync(~0u, any)) continue;
+                float f[E];
+                widen_vec<DT>(v, f);
+                int n = 0;
+                if (any) {
+#pragma unroll
+                    for (int j = 0; j < E; j++) n += f[j] >= bound;
+                }
+                int run = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(~0u, run, o);
+                    if (lane >= o) run += x;
+                }
+                int to = at + run - n;
+                if (any) {
+#pragma unroll
+                    for (int j = 0; j < E; j++) {
+                        if (!(f[j] >= bound)) continue;
+                        const int token = c0 + cols.first + s * 32 * E + j;
+                        if (team.size == 1) {
+                            listValues[to] = f[j];
+                            listTokens[to] = token;
+                        } else {
+                            st_cluster(listValues + to, 0, __float_as_uint(f[j]));
+                            st_cluster(listTokens + to, 0, (uint32_t)token);
+                        }
+                        to++;
+                    }
+                }
+                at += __shfl_sync(~0u, run, 31);
+            }
+            meet(team);
+            if (team.rank != 0) return;
+            constexpr int each = kSampleThreads * kVecElems<kF32>;
+            const int steps = ((int)few + each - 1) / each;
+            for (int i = (int)few + (int)threadIdx.x; i < steps * each; i += kSampleThreads) listValues[i] = -INFINITY;
+            __syncthreads();
+            Team alone = {0, 1, 0, 0};
+            const Columns<kF32> list((uint32_t)__cvta_generic_to_shared(listValues), steps);
+            decide<DT>(a, q, sh, alone, hist, list, w, kBound, pBound, exact, total, row, [&](int i) { return listTokens[i]; });
+            return;
+        }
+    }
+    decide<DT>(a, q, sh, team, hist, cols, w, kBound, pBound, exact, total, row, [&](int i) { return c0 + i; });
+}
+
+template <int DT>
 cudaError_t sample_launch(const SampleArgs& a, cudaStream_t s) {
-    const size_t smem = 2 * kSampleBins * 4 + (size_t)a.steps * kSampleThreads * 16;
+    const size_t smem = 2 * kSampleBins * 4 + kSampleList * 8 + (size_t)a.steps * kSampleThreads * 16;
     if (smem > 32 * 1024) {
         // one value for every launch, as host threads share the kernel's limit
-        const cudaError_t e = cudaFuncSetAttribute(k_sample<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+        const cudaError_t e = cudaFuncSetAttribute(k_sample<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 184 * 1024);
         if (e != cudaSuccess) return e;
     }
     NormShape sh = {};

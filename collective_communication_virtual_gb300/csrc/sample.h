@@ -8,6 +8,7 @@ namespace vc {
 constexpr int kSampleThreads = 512;
 constexpr int kSampleCluster = 8;
 constexpr int kSampleBins = 2048;
+constexpr int kSampleList = 4096;    // values above a row's bound that one CTA takes
 
 struct SampleArgs {
     const void* logits[VCOMM_MAX_RANKS];     // rank r: columns [r part, (r + 1) part) of every row
