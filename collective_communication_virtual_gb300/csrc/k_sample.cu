@@ -19,6 +19,9 @@
 // A row is read once, into the shared memory of a cluster's CTAs, which exchange maxima and sums there.
 // What is above the bounds, where it is few, goes to the first of them, which decides alone, without the
 // cluster's barriers (more than a microsecond each); else all decide together.
+//
+// A row's part on a rank is read by whole 16-byte blocks, wherever it starts; what a block holds besides
+// counts as minus infinity.
 #include "norm_stage.cuh"
 #include "sample.h"
 
@@ -28,7 +31,6 @@ namespace {
 
 constexpr int kWarps = kSampleThreads / 32;
 constexpr int kFix = 44;             // weights in units of 2^-44
-constexpr int kLevels = 4;           // groups of values by lanes: 32, 16, 8 and 1 of them
 typedef unsigned long long u64;
 constexpr int kWords = 4;            // that the CTAs of a cluster exchange at a time
 
@@ -41,8 +43,11 @@ __constant__ uint32_t kPowers[32] = {
 
 struct Shared {
     uint32_t powers[32];
-    float max[kWarps];
-    float low[kLevels][kWarps];      // smallest maximum of the groups of a level
+    float max[kWarps], low[kWarps];  // the largest value, and the smallest maximum of groups of lanes
+    // the row's parts: the first block, the elements before the part in it, their number, and the blocks
+    // of the parts before
+    const uint4* part[VCOMM_MAX_RANKS];
+    int shift[VCOMM_MAX_RANKS], length[VCOMM_MAX_RANKS], blocks[VCOMM_MAX_RANKS + 1];
     u64 warp[2][kWarps];
     u64 box[2][kSampleCluster][kWords];      // one line a CTA, written by all CTAs of the cluster
     u64 found[2][3];                 // bin, what lies before it, what lies in it
@@ -128,7 +133,20 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 struct Weights {
     float top, ch, cl;               // ch + cl = log2(e) / temperature
     const uint32_t* powers;
-    __device__ __forceinline__ float rough(float x) const { return exp2f((x - top) * ch); }
+    // The sum of E values' e, none of them the top's: 2^-20 off or so, and 0 below 2^-126.
+    template <int E>
+    __device__ __forceinline__ float rough(const float (&f)[E]) const {
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < E; j += 2) {
+            const float2 z = mul2(add2(make_float2(f[j], f[j + 1]), make_float2(-top, -top)), make_float2(ch, ch));
+            float2 e;
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(z.x));
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(z.y));
+            sum = add2(sum, e);
+        }
+        return sum.x + sum.y;
+    }
     // 2^44 e, as an integer: the difference and its product with ch + cl with their rounding errors,
     // 2^(k/32) from a table and 2^g, |g| <= 1/64, from its series.
     __device__ __forceinline__ u64 fixed(float x) const {
@@ -152,26 +170,21 @@ struct Weights {
     }
 };
 
-// Values in shared memory, cut into runs of `steps` times 32 vectors, one a warp.
+// 16-byte vectors of values.
 template <int DT>
-struct Columns {
+struct Vec {
     static constexpr int E = kVecElems<DT>;
-    uint32_t base;                   // the thread's first vector
-    int first, steps;                // its first value's number
-    __device__ __forceinline__ Columns(uint32_t smem, int n) : steps(n) {
-        const int vec = (int)(threadIdx.x >> 5) * 32 * n + (int)(threadIdx.x & 31);
-        base = smem + (uint32_t)vec * 16u;
-        first = vec * E;
+    static constexpr int T = DT == kF32 ? kBF16 : DT;  // for what is only called with 16-bit types
+    static __device__ __forceinline__ uint4 none() {
+        const uint32_t w = DT == kF32 ? 0xFF800000u : DT == kBF16 ? 0xFF80FF80u : 0xFC00FC00u;
+        return make_uint4(w, w, w, w);
     }
-    __device__ __forceinline__ uint32_t at(int step) const { return base + (uint32_t)step * 512u; }
-    __device__ __forceinline__ void get(int step, float (&f)[E]) const { widen_vec<DT>(ld_smem(at(step)), f); }
-    // The largest of a step's values, by pairs in the 16-bit types.
-    __device__ __forceinline__ float largest(int step) const { return largest_of(ld_smem(at(step))); }
-    static __device__ __forceinline__ float largest_of(const uint4& v) {
+    // The largest value, by pairs in the 16-bit types.
+    static __device__ __forceinline__ float largest(const uint4& v) {
         if (DT == kF32)
             return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
         const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
-        return fmaxf(widen16<DT == kF32 ? kBF16 : DT>((uint16_t)m), widen16<DT == kF32 ? kBF16 : DT>((uint16_t)(m >> 16)));
+        return fmaxf(widen16<T>((uint16_t)m), widen16<T>((uint16_t)(m >> 16)));
     }
     static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
         if (DT == kBF16) {
@@ -181,47 +194,111 @@ struct Columns {
         const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
         return *reinterpret_cast<const uint32_t*>(&r);
     }
-    // Whether a vector may hold a NaN: its sums are one then (infinities of both signs give one too).
+    // Whether there may be a NaN: the sums are one then (infinities of both signs give one too).
     static __device__ __forceinline__ bool suspect(const uint4& v) {
         if (DT == kF32) {
             const float t = (__uint_as_float(v.x) + __uint_as_float(v.y)) + (__uint_as_float(v.z) + __uint_as_float(v.w));
             return t != t;
         }
-        const uint32_t t = op_word<DT == kF32 ? kBF16 : DT, kSum>(op_word<DT == kF32 ? kBF16 : DT, kSum>(v.x, v.y),
-                                                                   op_word<DT == kF32 ? kBF16 : DT, kSum>(v.z, v.w));
-        const float a = widen16<DT == kF32 ? kBF16 : DT>((uint16_t)t), b = widen16<DT == kF32 ? kBF16 : DT>((uint16_t)(t >> 16));
+        const uint32_t t = op_word<T, kSum>(op_word<T, kSum>(v.x, v.y), op_word<T, kSum>(v.z, v.w));
+        const float a = widen16<T>((uint16_t)t), b = widen16<T>((uint16_t)(t >> 16));
         return a != a || b != b;
+    }
+    // Values before `from` and from `to` on, and NaNs, become minus infinity.
+    static __device__ __noinline__ uint4 only(const uint4& v, int from, int to) {
+        float f[E];
+        widen_vec<DT>(v, f);
+#pragma unroll
+        for (int j = 0; j < E; j++) f[j] = j >= from && j < to && f[j] == f[j] ? f[j] : -INFINITY;
+        return narrow_vec<DT>(f);
     }
 };
 
-// The CTA's columns [c0, c1) of a row into shared memory, minus infinity behind them.
+// The parts of a row.  All threads.
 template <int DT>
-__device__ __forceinline__ void load_columns(const SampleArgs& a, int row, int c0, int columns, uint32_t smem) {
+__device__ __forceinline__ void find_parts(const SampleArgs& a, Shared& sh, int row) {
     constexpr int E = kVecElems<DT>, ESZ = DTypeOf<DT>::size;
-    const int c1 = min(a.vocab, c0 + columns);
-    const uint32_t none = DT == kF32 ? 0xFF800000u : DT == kBF16 ? 0xFF80u : 0xFC00u;
-    const auto put = [&](int i, uint32_t v) {
-        if (ESZ == 4) asm volatile("st.shared.u32 [%0], %1;" :: "r"(smem + 4u * i), "r"(v) : "memory");
-        else asm volatile("st.shared.u16 [%0], %1;" :: "r"(smem + 2u * i), "h"((uint16_t)v) : "memory");
-    };
-    for (int i = max(0, c1 - c0) + (int)threadIdx.x; i < columns; i += kSampleThreads) put(i, none);
-    for (int lo = c0; lo < c1;) {
-        const int r = lo / a.part, hi = min(c1, (r + 1) * a.part);
-        const char* from = (const char*)a.logits[r] + ((size_t)row * a.stride + (lo - r * a.part)) * ESZ;
-        int done = 0;
-        if (a.aligned) {             // lo is a multiple of E, as a part is
-            const int whole = (hi - lo) / E;
-            for (int i = threadIdx.x; i < whole; i += kSampleThreads)
-                copy_block_async(smem + (uint32_t)(lo - c0) * ESZ + 16u * i, from + (size_t)i * 16);
-            done = whole * E;
+    if (threadIdx.x < 32) {
+        int ahead = 0;
+        for (int r0 = 0; r0 < a.nParts; r0 += 32) {
+            const int r = r0 + (int)threadIdx.x;
+            int n = 0;
+            if (r < a.nParts) {
+                const uintptr_t p = (uintptr_t)a.logits[r] + (size_t)row * a.stride * ESZ;
+                const int shift = (int)(p & 15u) / ESZ, length = min(a.part, a.vocab - r * a.part);
+                sh.part[r] = reinterpret_cast<const uint4*>(p & ~(uintptr_t)15);
+                sh.shift[r] = shift;
+                sh.length[r] = length;
+                n = (shift + length + E - 1) / E;
+            }
+            int run = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(~0u, run, o);
+                if ((int)threadIdx.x >= o) run += v;
+            }
+            if (r < a.nParts) sh.blocks[r + 1] = ahead + run;
+            ahead += __shfl_sync(~0u, run, 31);
         }
-#pragma unroll 4
-        for (int i = done + (int)threadIdx.x; i < hi - lo; i += kSampleThreads)
-            put(lo - c0 + i, ESZ == 4 ? ((const uint32_t*)from)[i] : (uint32_t)((const uint16_t*)from)[i]);
-        lo = hi;
+        if (threadIdx.x == 0) sh.blocks[0] = 0;
+    }
+    __syncthreads();
+}
+// The part that holds a block, from part r on.
+__device__ __forceinline__ int part_of(const Shared& sh, int block, int r) {
+    while (block >= sh.blocks[r + 1]) r++;
+    return r;
+}
+// Values in shared memory.  A warp has the vectors from `begin` on, every 32nd of them a lane.
+template <int DT>
+struct Columns {
+    static constexpr int E = kVecElems<DT>, kType = DT;
+    using V = Vec<DT>;
+    uint32_t at;                     // the thread's first vector
+    int first, left, steps;          // its number, the vectors from it to the run's end, the steps of the warp
+    __device__ __forceinline__ Columns(uint32_t smem, int begin, int end) {
+        const int lane = (int)threadIdx.x & 31;
+        at = smem + (uint32_t)(begin + lane) * 16u;
+        first = begin + lane;
+        left = end - first;
+        steps = (end - begin + 31) / 32;
+    }
+    __device__ __forceinline__ uint4 raw(int step) const { return step * 32 < left ? ld_smem(at + (uint32_t)step * 512u) : V::none(); }
+    __device__ __forceinline__ void put(int step, const uint4& v) const { st_smem(at + (uint32_t)step * 512u, v); }
+    __device__ __forceinline__ void get(int step, float (&f)[E]) const { widen_vec<DT>(raw(step), f); }
+    // f(step, vector) for all steps of the warp, by all lanes
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
+#pragma unroll 2
+        for (int s = 0; s < steps; s++) f(s, raw(s));
+    }
+};
+
+// Blocks [c0, c1) of a row into shared memory.
+template <int DT>
+__device__ __forceinline__ void load_blocks(const Shared& sh, int parts, int c0, int c1, uint32_t smem) {
+    constexpr int E = kVecElems<DT>;
+    for (int r = 0; r < parts; r++) {
+        const int lo = max(c0, sh.blocks[r]), hi = min(c1, sh.blocks[r + 1]);
+        const uint4* from = sh.part[r] + (lo - sh.blocks[r]);
+        for (int i = threadIdx.x; i < hi - lo; i += kSampleThreads)
+            copy_block_async(smem + 16u * (lo - c0 + i), reinterpret_cast<const char*>(from + i));
     }
     copies_commit();
     copies_wait();
+    __syncthreads();
+    // what the first and the last block of a part hold besides it
+    if ((int)threadIdx.x < parts) {
+        const int r = threadIdx.x, first = sh.blocks[r], last = sh.blocks[r + 1] - 1;
+        const auto cut = [&](int b) {
+            if (b < c0 || b >= c1) return;
+            const int at = (b - first) * E - sh.shift[r];        // the first value's place in its part
+            const uint32_t p = smem + 16u * (b - c0);
+            st_smem(p, Vec<DT>::only(ld_smem(p), -at, sh.length[r] - at));
+        };
+        cut(first);
+        if (last > first) cut(last);
+    }
     __syncthreads();
 }
 
@@ -242,9 +319,9 @@ __device__ bool search(Shared& sh, Team& team, uint32_t* hist, const Cols& cols,
         const bool masses = BY_MASS && shift > 0;      // a bin of one value needs counts alone
         for (int i = threadIdx.x; i < kSampleBins * (masses ? 2 : 1); i += kSampleThreads) hist[i] = 0;
         __syncthreads();
-        for (int s = 0; s < cols.steps; s++) {
+        cols.each([&](int, const uint4& v) {
             float f[E];
-            cols.get(s, f);
+            widen_vec<Cols::kType>(v, f);
 #pragma unroll
             for (int j = 0; j < E; j++) {
                 const uint32_t d = keyTop - key_of<DT>(f[j]);
@@ -253,13 +330,13 @@ __device__ bool search(Shared& sh, Team& team, uint32_t* hist, const Cols& cols,
                 if (!masses) {
                     atomicAdd(&low[bin], 1u);
                 } else {
-                    const u64 v = w.fixed(f[j]);
-                    const uint32_t old = atomicAdd(&low[bin], (uint32_t)v);
-                    const uint32_t carry = (uint32_t)(v >> 32) + (old + (uint32_t)v < old ? 1u : 0u);
+                    const u64 e = w.fixed(f[j]);
+                    const uint32_t old = atomicAdd(&low[bin], (uint32_t)e);
+                    const uint32_t carry = (uint32_t)(e >> 32) + (old + (uint32_t)e < old ? 1u : 0u);
                     if (carry) atomicAdd(&high[bin], carry);
                 }
             }
-        }
+        });
         meet(team);
         // This CTA's share of the bins, over all CTAs.
         u64 val[4], sum = 0;
@@ -341,12 +418,12 @@ struct Filters {
 template <typename Cols>
 __device__ u64 exact_sum(Shared& sh, Team& team, const Cols& cols, const Weights& w) {
     u64 s = 0, none = 0;
-    for (int i = 0; i < cols.steps; i++) {
+    cols.each([&](int, const uint4& v) {
         float f[Cols::E];
-        cols.get(i, f);
+        widen_vec<Cols::kType>(v, f);
 #pragma unroll
         for (int j = 0; j < Cols::E; j++) s += w.fixed(f[j]);
-    }
+    });
     block_sums(sh, s, none);
     const u64 mine[kWords] = {s, 0, 0, 0};
     const u64(*box)[kWords] = exchange(sh, team, mine);
@@ -390,13 +467,13 @@ __device__ __forceinline__ void decide(const SampleArgs& a, const Filters& q, Sh
         uint32_t most;
         if (cut) {                   // the sum of the topK
             u64 s = 0, none = 0;
-            for (int i = 0; i < cols.steps; i++) {
+            cols.each([&](int, const uint4& v) {
                 float f[E];
-                cols.get(i, f);
+                widen_vec<Cols::kType>(v, f);
 #pragma unroll
                 for (int j = 0; j < E; j++)
                     if (keyTop - key_of<DT>(f[j]) < edge) s += w.fixed(f[j]);
-            }
+            });
             block_sums(sh, s, none);
             const u64 mine[kWords] = {s, 0, 0, 0};
             const u64(*box)[kWords] = exchange(sh, team, mine);
@@ -433,17 +510,17 @@ __device__ __forceinline__ void decide(const SampleArgs& a, const Filters& q, Sh
     // What lies below this is not kept, and no tie.
     const float bottom = fmaxf(cut ? value_of<DT>(keyTop - edge) : -INFINITY, floorValue);
     u64 sum = 0, count = 0;
-    for (int s = 0; s < cols.steps; s++) {
-        if (cols.largest(s) < bottom) continue;
+    cols.each([&](int, const uint4& v) {
+        if (Cols::V::largest(v) < bottom) return;
         float f[E];
-        cols.get(s, f);
+        widen_vec<Cols::kType>(v, f);
 #pragma unroll
         for (int j = 0; j < E; j++) {
             bool tie;
             sum += kept(f[j], &tie);
             count += tie;
         }
-    }
+    });
     u64 blockSum = sum, blockCount = count;
     block_sums(sh, blockSum, blockCount);              // leaves every warp's sums in sh.warp
     const u64 mine[kWords] = {blockSum, blockCount, 0, 0};
@@ -528,7 +605,7 @@ __device__ __forceinline__ void decide(const SampleArgs& a, const Filters& q, Sh
                     x = f[j];
                 }
             }
-            const int token = token_of(cols.first + s * 32 * E + pick);
+            const int token = token_of((cols.first + s * 32) * E + pick);
             for (int o = 0; o < a.nOut; o++) a.tokens[o][row] = token;
             if (a.logprob) {
                 const float z = x == top ? 0.0f : q.greedy ? x - top : (x - top) / q.heat;
@@ -541,80 +618,34 @@ __device__ __forceinline__ void decide(const SampleArgs& a, const Filters& q, Sh
     }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_constant__ SampleArgs a) {
-    pdl_begin();
-    constexpr int E = kVecElems<DT>;
-    extern __shared__ __align__(16) unsigned char dynamic[];
-    __shared__ Shared sh;
-    uint32_t* const hist = reinterpret_cast<uint32_t*>(dynamic);
-    float* const listValues = reinterpret_cast<float*>(hist + 2 * kSampleBins);
-    int* const listTokens = reinterpret_cast<int*>(listValues + kSampleList);
-    const uint32_t values = (uint32_t)__cvta_generic_to_shared(listTokens + kSampleList);
+// From a row's values to its token.  top is this thread's largest value.
+template <int DT, typename Cols, typename TokenOf>
+__device__ __forceinline__ void draw(const SampleArgs& a, const Filters& q, Shared& sh, Team& team, uint32_t* hist,
+                                     float* listValues, int* listTokens, const Cols& cols, float top, int row, TokenOf token_of) {
+    constexpr int E = Cols::E;
+    using V = typename Cols::V;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Team team;
-    team.size = a.cluster;
-    team.rank = a.cluster > 1 ? (int)cluster_rank() : 0;
-    team.flip = team.flipFound = 0;
-    const int row = (int)(blockIdx.x / (unsigned)a.cluster);
-    const int columns = a.steps * kSampleThreads * E, c0 = team.rank * columns;
-    if (threadIdx.x < 32) sh.powers[threadIdx.x] = kPowers[threadIdx.x];
-    Filters q;
-    q.heat = a.temperature ? a.temperature[row] : 1.0f;
-    q.greedy = !(q.heat > 0.0f);
-    q.k = q.greedy ? 1 : a.topK ? a.topK[row] : 0;
-    if (q.k <= 0 || q.k >= a.vocab) q.k = a.vocab;
-    q.p = a.topP && !q.greedy ? a.topP[row] : 1.0f;
-    q.least = a.minP && !q.greedy ? a.minP[row] : 0.0f;
-    q.limited = q.k < a.vocab;
-    q.nucleus = q.p < 1.0f && q.k > 1;
-    load_columns<DT>(a, row, c0, columns, values);
-    const Columns<DT> cols(values, a.steps);
-
-    // The largest value, and for topK the smallest maximum of disjoint groups.  A NaN counts as minus
-    // infinity, and is overwritten by it.
-    float top = -INFINITY;
-    for (int s = 0; s < cols.steps; s++) {
-        const uint4 v = ld_smem(cols.at(s));
-        float m = cols.largest_of(v);
-        if (cols.suspect(v)) {
-            float f[E];
-            widen_vec<DT>(v, f);
-            m = -INFINITY;
+    // The largest value, and for topK the smallest maximum of at least k disjoint groups, of as many lanes
+    // each as leave that many.
+    const int groups = team.size * kWarps;
+    int lanes = 32;
+    while (lanes > 1 && q.k > groups * (32 / lanes)) lanes >>= 1;
+    float kBound = top;
 #pragma unroll
-            for (int j = 0; j < E; j++) {
-                f[j] = f[j] == f[j] ? f[j] : -INFINITY;
-                m = fmaxf(m, f[j]);
-            }
-            st_smem(cols.at(s), narrow_vec<DT>(f));
-        }
-        top = fmaxf(top, m);
+    for (int o = 1; o < 32; o <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        const float other = __shfl_xor_sync(~0u, kBound, o);
+        kBound = o < lanes ? fmaxf(kBound, other) : fminf(kBound, other);
     }
-    float low[kLevels];
-    low[3] = top;
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    low[2] = top;
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
-    low[1] = top;
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
-    low[0] = top;
-    low[1] = fminf(low[1], __shfl_xor_sync(~0u, low[1], 16));
-    low[2] = fminf(low[2], __shfl_xor_sync(~0u, low[2], 16));
-    low[2] = fminf(low[2], __shfl_xor_sync(~0u, low[2], 8));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) low[3] = fminf(low[3], __shfl_xor_sync(~0u, low[3], o));
     if (lane == 0) {
         sh.max[warp] = top;
-        for (int i = 0; i < kLevels; i++) sh.low[i][warp] = low[i];
+        sh.low[warp] = kBound;
     }
     meet(team);                                        // every CTA of the cluster has started
-    for (int i = 0; i < kWarps; i++) top = fmaxf(top, sh.max[i]);
-    // the level whose groups are at least k
-    const int groups = team.size * kWarps;
-    const int level = q.k <= groups ? 0 : q.k <= 2 * groups ? 1 : q.k <= 4 * groups ? 2 : 3;
-    float kBound = INFINITY;
-    for (int i = 0; i < kWarps; i++) kBound = fminf(kBound, sh.low[level][i]);
+    for (int i = 0; i < kWarps; i++) {
+        top = fmaxf(top, sh.max[i]);
+        kBound = fminf(kBound, sh.low[i]);
+    }
     {
         const u64 mine[kWords] = {__float_as_uint(top), __float_as_uint(kBound), 0, 0};
         const u64(*box)[kWords] = exchange(sh, team, mine);
@@ -663,30 +694,27 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     const bool filtered = q.limited || q.nucleus || q.least > 0.0f;
     u64 sum = 0, count = 0;
     if (filtered) {
-        for (int s = 0; s < cols.steps; s++) {
-            const uint4 v = ld_smem(cols.at(s));
-            const float m = cols.largest_of(v);
-            if (total && m < bound) continue;
+        cols.each([&](int, const uint4& v) {
+            const float m = V::largest(v);
+            if (total && m < bound) return;
             float f[E];
             widen_vec<DT>(v, f);
             if (!total) {
-                float part = 0.0f;
                 if (m == top) {      // the largest apart: what is beside them may be small
 #pragma unroll
                     for (int j = 0; j < E; j++) {
-                        part += f[j] == top ? 0.0f : w.rough(f[j]);
                         sum += f[j] == top ? 1ull << kFix : 0ull;
+                        f[j] = f[j] == top ? -INFINITY : f[j];
                     }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < E; j++) part += w.rough(f[j]);
                 }
+                const float part = w.rough(f);
                 sum += __float2ull_rn(part * (float)(1ull << kFix));
             }
-            if (m < bound) continue;
+            if (m < bound) return;
+            widen_vec<DT>(v, f);
 #pragma unroll
             for (int j = 0; j < E; j++) count += f[j] >= bound;
-        }
+        });
         u64 blockSum = sum, blockCount = count;
         block_sums(sh, blockSum, blockCount);          // leaves every warp's sums in sh.warp
         const u64 mine[kWords] = {blockSum, blockCount, 0, 0};
@@ -702,10 +730,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
             // to the first CTA's list, in order
             int at = (int)ahead;
             for (int i = 0; i < warp; i++) at += (int)sh.warp[1][i];
-            for (int s = 0; s < cols.steps; s++) {
-                const uint4 v = ld_smem(cols.at(s));
-                const bool any = cols.largest_of(v) >= bound;
-                if (!__any_sync(~0u, any)) continue;
+            cols.each([&](int s, const uint4& v) {
+                const bool any = V::largest(v) >= bound;
+                if (!__any_sync(~0u, any)) return;
                 float f[E];
                 widen_vec<DT>(v, f);
                 int n = 0;
@@ -724,46 +751,100 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
 #pragma unroll
                     for (int j = 0; j < E; j++) {
                         if (!(f[j] >= bound)) continue;
-                        const int token = c0 + cols.first + s * 32 * E + j;
+                        const int number = (cols.first + s * 32) * E + j;
                         if (team.size == 1) {
                             listValues[to] = f[j];
-                            listTokens[to] = token;
+                            listTokens[to] = number;
                         } else {
                             st_cluster(listValues + to, 0, __float_as_uint(f[j]));
-                            st_cluster(listTokens + to, 0, (uint32_t)token);
+                            st_cluster(listTokens + to, 0, (uint32_t)number | (uint32_t)team.rank << 28);
                         }
                         to++;
                     }
                 }
                 at += __shfl_sync(~0u, run, 31);
-            }
+            });
             meet(team);
             if (team.rank != 0) return;
-            constexpr int each = kSampleThreads * kVecElems<kF32>;
-            const int steps = ((int)few + each - 1) / each;
-            for (int i = (int)few + (int)threadIdx.x; i < steps * each; i += kSampleThreads) listValues[i] = -INFINITY;
+            constexpr int LE = kVecElems<kF32>;
+            const int vecs = ((int)few + LE - 1) / LE;
+            if ((int)threadIdx.x < vecs * LE - (int)few) listValues[few + threadIdx.x] = -INFINITY;
             __syncthreads();
             Team alone = {0, 1, 0, 0};
-            const Columns<kF32> list((uint32_t)__cvta_generic_to_shared(listValues), steps);
-            decide<DT>(a, q, sh, alone, hist, list, w, kBound, pBound, exact, total, row, [&](int i) { return listTokens[i]; });
+            const Columns<kF32> list((uint32_t)__cvta_generic_to_shared(listValues), vecs * warp / kWarps, vecs * (warp + 1) / kWarps);
+            decide<DT>(a, q, sh, alone, hist, list, w, kBound, pBound, exact, total, row, [&](int i) {
+                const int v = listTokens[i];
+                return token_of(v & 0x0FFFFFFF, v >> 28);
+            });
             return;
         }
     }
-    decide<DT>(a, q, sh, team, hist, cols, w, kBound, pBound, exact, total, row, [&](int i) { return c0 + i; });
+    decide<DT>(a, q, sh, team, hist, cols, w, kBound, pBound, exact, total, row, [&](int i) { return token_of(i, team.rank); });
+}
+
+__device__ __forceinline__ Filters filters_of(const SampleArgs& a, int row) {
+    Filters q;
+    q.heat = a.temperature ? a.temperature[row] : 1.0f;
+    q.greedy = !(q.heat > 0.0f);
+    q.k = q.greedy ? 1 : a.topK ? a.topK[row] : 0;
+    if (q.k <= 0 || q.k >= a.vocab) q.k = a.vocab;
+    q.p = a.topP && !q.greedy ? a.topP[row] : 1.0f;
+    q.least = a.minP && !q.greedy ? a.minP[row] : 0.0f;
+    q.limited = q.k < a.vocab;
+    q.nucleus = q.p < 1.0f && q.k > 1;
+    return q;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_constant__ SampleArgs a) {
+    pdl_begin();
+    constexpr int E = kVecElems<DT>;
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    __shared__ Shared sh;
+    uint32_t* const hist = reinterpret_cast<uint32_t*>(dynamic);
+    float* const listValues = reinterpret_cast<float*>(hist + 2 * kSampleBins);
+    int* const listTokens = reinterpret_cast<int*>(listValues + kSampleList);
+    const uint32_t values = (uint32_t)__cvta_generic_to_shared(listTokens + kSampleList);
+    Team team;
+    team.size = a.cluster;
+    team.rank = a.cluster > 1 ? (int)cluster_rank() : 0;
+    team.flip = team.flipFound = 0;
+    const int row = (int)(blockIdx.x / (unsigned)team.size), warp = (int)threadIdx.x >> 5;
+    if (threadIdx.x < 32) sh.powers[threadIdx.x] = kPowers[threadIdx.x];
+    const Filters q = filters_of(a, row);
+    find_parts<DT>(a, sh, row);
+    // every warp of the cluster the same share of the blocks, so that none is without a value
+    const int total = sh.blocks[a.nParts], warps = team.size * kWarps;
+    const auto share = [&](int w) { return (int)((long long)total * w / warps); };
+    const int c0 = share(team.rank * kWarps), c1 = share((team.rank + 1) * kWarps);
+    load_blocks<DT>(sh, a.nParts, c0, c1, values);
+    const Columns<DT> cols(values, share(team.rank * kWarps + warp) - c0, share(team.rank * kWarps + warp + 1) - c0);
+    // a NaN counts as minus infinity, and is overwritten by it
+    float top = -INFINITY;
+    cols.each([&](int s, uint4 v) {
+        if (Vec<DT>::suspect(v)) {
+            v = Vec<DT>::only(v, 0, E);
+            if (s * 32 < cols.left) cols.put(s, v);
+        }
+        top = fmaxf(top, Vec<DT>::largest(v));
+    });
+    draw<DT>(a, q, sh, team, hist, listValues, listTokens, cols, top, row, [&](int number, int rank) {
+        const int block = number / E + share(rank * kWarps), r = part_of(sh, block, 0);
+        return r * a.part + (block - sh.blocks[r]) * E - sh.shift[r] + number % E;
+    });
 }
 
 template <int DT>
 cudaError_t sample_launch(const SampleArgs& a, cudaStream_t s) {
-    const size_t smem = 2 * kSampleBins * 4 + kSampleList * 8 + (size_t)a.steps * kSampleThreads * 16;
-    if (smem > 32 * 1024) {
-        // one value for every launch, as host threads share the kernel's limit
-        const cudaError_t e = cudaFuncSetAttribute(k_sample<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 184 * 1024);
-        if (e != cudaSuccess) return e;
-    }
+    const auto kernel = k_sample<DT>;
+    // one value for every launch, as host threads share the kernel's limit
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSampleMaxSmem);
+    if (e != cudaSuccess) return e;
     NormShape sh = {};
     sh.threads = kSampleThreads;
     sh.cluster = a.cluster;
-    return norm_launch(k_sample<DT>, (unsigned)a.rows * (unsigned)a.cluster, sh, smem, s, a);
+    const size_t smem = 2 * kSampleBins * 4 + kSampleList * 8 + (size_t)a.blocks * 16;
+    return norm_launch(kernel, (unsigned)a.rows * (unsigned)sh.cluster, sh, smem, s, a);
 }
 
 }  // namespace

@@ -38,13 +38,12 @@ vResult_t sample(const vSampleDesc_t* desc, const void* const* logits, const flo
                           (const void*)uniform, (const void*)logprob})
         if (!at(p, 4)) return vInvalidArgument;
     vc::SampleArgs a;
-    a.aligned = d.part % e == 0 && (d.rows == 1 || d.stride % e == 0);
-    a.nOut = 0;
+    a.nOut = a.nParts = 0;
     for (int k = 0; k < v.nRanks; k++) {
         a.logits[k] = logits[k];
         if (k * d.part < d.vocab) {                    // else it holds no column that counts
             if (!logits[k] || !at(logits[k], esz)) return vInvalidArgument;
-            a.aligned = a.aligned && at(logits[k], 16);
+            a.nParts++;
         }
         if (!tokens[k]) continue;
         if (!at(tokens[k], 4)) return vInvalidArgument;
@@ -61,14 +60,17 @@ vResult_t sample(const vSampleDesc_t* desc, const void* const* logits, const flo
     a.rows = (int)d.rows;
     a.vocab = (int)d.vocab;
     a.part = (int)d.part;
-    const size_t each = vc::kSampleThreads * e;        // columns of a step
+    // Blocks of a row, at most: a part may begin and end inside one.  As many CTAs as leave a thread four
+    // of them while SMs are idle; of more rows than SMs, as leave two CTAs an SM.
+    const size_t blocks = d.vocab / e + 2 * (size_t)a.nParts;
+    const auto each = [&]() { return (blocks + a.cluster - 1) / a.cluster + 1; };
     a.cluster = 1;
-    const auto steps = [&]() { return (int)((d.vocab + each * a.cluster - 1) / (each * a.cluster)); };
-    while (a.cluster < vc::kSampleCluster && steps() > 1 && (steps() > 4 || d.rows * a.cluster < (size_t)v.smCount)) a.cluster *= 2;
-    a.steps = steps();
+    while (a.cluster < vc::kSampleCluster &&
+           (each() * 16 > vc::kSamplePair || (each() > vc::kSampleThreads && d.rows * a.cluster < (size_t)v.smCount))) a.cluster *= 2;
+    a.blocks = (int)each();
     if (v.debug)
-        std::fprintf(stderr, "vcomm INFO Sample rows=%d vocab=%d dt=%d N=%d cluster=%d steps=%d aligned=%d\n", a.rows, a.vocab,
-                     (int)d.datatype, v.nRanks, a.cluster, a.steps, a.aligned);
+        std::fprintf(stderr, "vcomm INFO Sample rows=%d vocab=%d dt=%d N=%d cluster=%d blocks=%d\n", a.rows, a.vocab,
+                     (int)d.datatype, v.nRanks, a.cluster, a.blocks);
     return comm_launch(c, "sample", [&]() { return vc::launch_sample(a, d.datatype, stream); });
 }
 

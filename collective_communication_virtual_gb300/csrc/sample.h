@@ -8,7 +8,9 @@ namespace vc {
 constexpr int kSampleThreads = 512;
 constexpr int kSampleCluster = 8;
 constexpr int kSampleBins = 2048;
-constexpr int kSampleList = 4096;    // values above a row's bound that one CTA takes
+constexpr int kSampleMaxSmem = 192 * 1024;
+constexpr int kSamplePair = 72 * 1024;   // bytes of a row that leave an SM room for two CTAs
+constexpr int kSampleList = 2560;    // values above a row's bound that one CTA takes
 
 struct SampleArgs {
     const void* logits[VCOMM_MAX_RANKS];     // rank r: columns [r part, (r + 1) part) of every row
@@ -21,10 +23,10 @@ struct SampleArgs {
     float* logprob;                          // may be NULL
     size_t stride;                           // elements between rows
     int rows, vocab, part;
+    int nParts;                              // ranks that hold columns below vocab
     int nOut;
     int cluster;                             // CTAs that share a row
-    int steps;                               // 16-byte vectors of a thread
-    int aligned;                             // every row of every rank starts on 16 bytes
+    int blocks;                              // 16-byte blocks of it that a CTA has at most
 };
 cudaError_t launch_sample(const SampleArgs& a, vDataType_t dt, cudaStream_t s);
 
