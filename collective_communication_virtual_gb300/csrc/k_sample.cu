@@ -11,7 +11,8 @@
 // their order, and a histogram of their distances from the largest, 2048 bins at a time, is refined
 // until a bin is one value.  Bounds that cost nothing keep most logits out of the histograms: the
 // topK-th largest is at least the smallest of topK disjoint groups' maxima, and weights below a share
-// of the sum that all of them together could not fill lie outside topP.
+// of the sum that all of them together could not fill lie outside topP.  Where few logits are left, they
+// are held in registers and the value is found by halving its range.
 //
 // The draw is a comparison of sums, so these are exact: a weight is a 64-bit integer, 2^44 e, right to
 // 2^-30 of itself, and the order of additions does not matter.
@@ -51,6 +52,8 @@ struct Shared {
     u64 warp[2][kWarps];
     u64 box[2][kSampleCluster][kWords];      // one line a CTA, written by all CTAs of the cluster
     u64 found[2][3];                 // bin, what lies before it, what lies in it
+    int count[2][kWarps];
+    unsigned mass[2][3][kWarps];
     u64 target, left, total;
     int owner;
 };
@@ -407,6 +410,19 @@ __device__ bool search(Shared& sh, Team& team, uint32_t* hist, const Cols& cols,
     return true;
 }
 
+// x times f, f below 1, rounded down, or up: a product of 24 by 64 bits.
+__device__ __forceinline__ u64 share_of(u64 x, float f, bool up) {
+    if (!(f > 0.0f)) return 0;
+    const uint32_t b = __float_as_uint(f), e = b >> 23;
+    const u64 m = e ? (b & 0x7FFFFFu) | 0x800000u : b & 0x7FFFFFu;
+    const int down = 150 - (int)max(e, 1u);            // 24 or more
+    const u64 lo = x * m, hi = __umul64hi(x, m);
+    if (down >= 128) return up;
+    const u64 whole = down >= 64 ? hi >> (down - 64) : hi << (64 - down) | lo >> down;
+    const u64 rest = down >= 64 ? lo | (down > 64 ? hi << (128 - down) : 0) : lo << (64 - down);
+    return whole + (up && rest ? 1 : 0);
+}
+
 // What the filters of a row ask for.
 struct Filters {
     float heat, p, least;
@@ -484,7 +500,7 @@ __device__ __forceinline__ void decide(const SampleArgs& a, const Filters& q, Sh
             if (q.limited) exact = exact_sum(sh, team, cols, w);     // fewer than topK
             most = distance(pBound);
         }
-        const u64 goal = max(1ull, (u64)ceil((double)fmaxf(q.p, 0.0f) * (double)exact));
+        const u64 goal = max(1ull, share_of(exact, q.p, true));
         uint32_t at;
         if (search<DT, true>(sh, team, hist, cols, w, keyTop, most, goal, &at, &before)) {
             const u64 one = max(1ull, w.fixed(value_of<DT>(keyTop - at)));
@@ -494,7 +510,7 @@ __device__ __forceinline__ void decide(const SampleArgs& a, const Filters& q, Sh
             cut = true;
         }
     }
-    const u64 floorWeight = q.least > 0.0f ? (u64)ceil((double)fminf(q.least, 1.0f) * (double)(1ull << kFix)) : 0;
+    const u64 floorWeight = q.least >= 1.0f ? 1ull << kFix : share_of(1ull << kFix, q.least, true);
     const float floorValue = floorWeight ? value_at(w, fminf(q.least, 1.0f)) : -INFINITY;
 
     // Weights kept by every warp, its ties at the edge aside.
@@ -538,8 +554,7 @@ __device__ __forceinline__ void decide(const SampleArgs& a, const Filters& q, Sh
             left -= n;
         }
         const float u = a.uniform[row];
-        u64 goal = u > 0.0f ? (u64)((double)u * (double)all) : 0;
-        goal = min(goal, all - 1);
+        const u64 goal = u >= 1.0f ? all - 1 : share_of(all, u, false);
         sh.owner = -1;
         sh.total = total ? total : all;
         for (int i = 0; i < kWarps && goal >= ahead; i++) {
@@ -615,6 +630,170 @@ __device__ __forceinline__ void decide(const SampleArgs& a, const Filters& q, Sh
         if (__any_sync(~0u, here)) return;
         goal -= __shfl_sync(~0u, run, 31);
         left -= min(left, __shfl_sync(~0u, runTies, 31));
+    }
+}
+
+// A list's values, kPer a thread in their order.
+constexpr int kPer = kSampleList / kSampleThreads;
+static_assert(kPer * kSampleThreads == kSampleList, "the list is shared out");
+
+// The CTA's sum, in every thread; `buffer` alternates from call to call.
+__device__ __forceinline__ int block_count(Shared& sh, int v, int& buffer) {
+    v = __reduce_add_sync(~0u, v);
+    if ((threadIdx.x & 31) == 0) sh.count[buffer][threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int w = (int)threadIdx.x & 31;
+    v = __reduce_add_sync(~0u, w < kWarps ? sh.count[buffer][w] : 0);
+    buffer ^= 1;
+    return v;
+}
+// The same of numbers below 2^45 (at most kSampleList of them): three sums of 15 bits each.
+__device__ __forceinline__ u64 block_mass(Shared& sh, const unsigned (&part)[3], int& buffer) {
+    unsigned v[3];
+#pragma unroll
+    for (int i = 0; i < 3; i++) {
+        v[i] = __reduce_add_sync(~0u, part[i]);
+        if ((threadIdx.x & 31) == 0) sh.mass[buffer][i][threadIdx.x >> 5] = v[i];
+    }
+    __syncthreads();
+    const int w = (int)threadIdx.x & 31;
+    u64 sum = 0;
+#pragma unroll
+    for (int i = 0; i < 3; i++) sum += (u64)__reduce_add_sync(~0u, w < kWarps ? sh.mass[buffer][i][w] : 0u) << (15 * i);
+    buffer ^= 1;
+    return sum;
+}
+__device__ __forceinline__ void add_mass(unsigned (&part)[3], u64 v) {
+#pragma unroll
+    for (int i = 0; i < 3; i++) part[i] += (unsigned)(v >> (15 * i)) & 0x7FFFu;
+}
+
+// As decide(), by one CTA, of the `few` values of its list, of which none is further than `most` from the top.
+template <int DT, typename TokenOf>
+__device__ __forceinline__ void decide_list(const SampleArgs& a, const Filters& q, Shared& sh, const float* values, int few,
+                                            const Weights& w, uint32_t most, u64 exact, u64 total, int row, TokenOf token_of) {
+    const float top = w.top;
+    const uint32_t keyTop = key_of<DT>(top);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = (int)threadIdx.x * kPer;
+    uint32_t d[kPer];
+    u64 v[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; j++) d[j] = first + j < few ? keyTop - key_of<DT>(values[first + j]) : 0xFFFFFFFFu;
+    int buffer = 0;
+    // What is kept: distances below `edge`, and the first `ties` values at it.
+    uint32_t edge = most;
+    u64 ties = ~0ull;
+    if (q.limited && few >= q.k) {
+        uint32_t lo = 0;             // fewer than k are nearer than lo: `below` of them
+        int below = 0;
+        while (lo < edge) {
+            const uint32_t mid = lo + (edge - lo) / 2;
+            int n = 0;
+#pragma unroll
+            for (int j = 0; j < kPer; j++) n += d[j] <= mid;
+            n = block_count(sh, n, buffer);
+            if (n >= q.k) {
+                edge = mid;
+            } else {
+                lo = mid + 1;
+                below = n;
+            }
+        }
+        ties = (u64)(q.k - below);
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; j++) v[j] = d[j] <= edge ? w.fixed(values[first + j]) : 0;
+    if (q.nucleus) {
+        if (q.limited) {             // the sum of the topK
+            unsigned part[3] = {};
+#pragma unroll
+            for (int j = 0; j < kPer; j++)
+                if (d[j] < edge || ties == ~0ull) add_mass(part, v[j]);
+            exact = block_mass(sh, part, buffer);
+            if (ties != ~0ull) exact += ties * w.fixed(value_of<DT>(keyTop - edge));
+        }
+        const u64 goal = max(1ull, share_of(exact, q.p, true));
+        uint32_t lo = 0, hi = edge;
+        u64 before = 0;              // the sum of what is nearer than lo, less than the goal
+        while (lo < hi) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            unsigned part[3] = {};
+#pragma unroll
+            for (int j = 0; j < kPer; j++)
+                if (d[j] <= mid) add_mass(part, v[j]);
+            const u64 sum = block_mass(sh, part, buffer);
+            if (sum >= goal) {
+                hi = mid;
+            } else {
+                lo = mid + 1;
+                before = sum;
+            }
+        }
+        const u64 one = max(1ull, w.fixed(value_of<DT>(keyTop - hi))), n = (goal - before + one - 1) / one;
+        ties = hi == edge ? min(ties, n) : n;
+        edge = hi;
+    }
+    const u64 floorWeight = q.least >= 1.0f ? 1ull << kFix : share_of(1ull << kFix, q.least, true);
+    u64 sum = 0, atEdge = w.fixed(value_of<DT>(keyTop - edge));
+    if (atEdge < floorWeight) atEdge = 0;
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; j++) {
+        n += d[j] == edge;
+        v[j] = d[j] < edge && v[j] >= floorWeight ? v[j] : 0;
+        sum += v[j];
+    }
+    // The ties before this thread's, then what is kept before it.
+    int runTies = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(~0u, runTies, o);
+        if (lane >= o) runTies += x;
+    }
+    __syncthreads();
+    if (lane == 31) sh.count[0][warp] = runTies;
+    __syncthreads();
+    runTies -= n;
+    for (int i = 0; i < warp; i++) runTies += sh.count[0][i];
+    int mineLeft = (int)(ties > (u64)runTies ? min(ties - (u64)runTies, (u64)n) : 0);
+    sum += (u64)mineLeft * atEdge;
+    u64 run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 x = __shfl_up_sync(~0u, run, o);
+        if (lane >= o) run += x;
+    }
+    if (lane == 31) sh.warp[0][warp] = run;
+    __syncthreads();
+    u64 all = 0, ahead = run - sum;
+    for (int i = 0; i < kWarps; i++) {
+        if (i < warp) ahead += sh.warp[0][i];
+        all += sh.warp[0][i];
+    }
+    const float u = a.uniform[row];
+    const u64 goal = u >= 1.0f ? all - 1 : share_of(all, u, false);
+    if (goal < ahead || goal >= ahead + sum) return;
+    int pick = 0;
+    bool done = false;
+#pragma unroll
+    for (int j = 0; j < kPer; j++) {
+        u64 e = v[j];
+        if (d[j] == edge && mineLeft > 0) {
+            mineLeft--;
+            e = atEdge;
+        }
+        ahead += e;
+        if (!done && goal < ahead) {
+            done = true;
+            pick = j;
+        }
+    }
+    const int token = token_of(first + pick);
+    const float x = values[first + pick];
+    for (int o = 0; o < a.nOut; o++) a.tokens[o][row] = token;
+    if (a.logprob) {
+        const float z = x == top ? 0.0f : q.greedy ? x - top : (x - top) / q.heat;
+        a.logprob[row] = z - log1pf((float)(total - (1ull << kFix)) * 0x1p-44f);
     }
 }
 
@@ -766,13 +945,8 @@ __device__ __forceinline__ void draw(const SampleArgs& a, const Filters& q, Shar
             });
             meet(team);
             if (team.rank != 0) return;
-            constexpr int LE = kVecElems<kF32>;
-            const int vecs = ((int)few + LE - 1) / LE;
-            if ((int)threadIdx.x < vecs * LE - (int)few) listValues[few + threadIdx.x] = -INFINITY;
-            __syncthreads();
-            Team alone = {0, 1, 0, 0};
-            const Columns<kF32> list((uint32_t)__cvta_generic_to_shared(listValues), vecs * warp / kWarps, vecs * (warp + 1) / kWarps);
-            decide<DT>(a, q, sh, alone, hist, list, w, kBound, pBound, exact, total, row, [&](int i) {
+            const uint32_t most = bound >= top ? 0u : key_of<DT>(top) - key_of<DT>(fmaxf(bound, -3.40282347e38f));
+            decide_list<DT>(a, q, sh, listValues, (int)few, w, most, exact, total, row, [&](int i) {
                 const int v = listTokens[i];
                 return token_of(v & 0x0FFFFFFF, v >> 28);
             });
