@@ -12,7 +12,8 @@
 // until a bin is one value.  Bounds that cost nothing keep most logits out of the histograms: the
 // topK-th largest is at least the smallest of topK disjoint groups' maxima, and weights below a share
 // of the sum that all of them together could not fill lie outside topP.  Where few logits are left, they
-// are held in registers and the value is found by halving its range.
+// are held in registers and the value is found by halving its range, or, of at most 256, every one's
+// place and what is kept before it by comparing it with all others.
 //
 // The draw is a comparison of sums, so these are exact: a weight is a 64-bit integer, 2^44 e, right to
 // 2^-30 of itself, and the order of additions does not matter.
@@ -42,7 +43,14 @@ __constant__ uint32_t kPowers[32] = {
     3037000500u, 3103502151u, 3171459999u, 3240905930u, 3311872529u, 3384393094u, 3458501653u, 3534232978u,
     3611622603u, 3690706840u, 3771522796u, 3854108391u, 3938502376u, 4024744348u, 4112874773u, 4202935003u};
 
+constexpr int kSampleFew = 256;      // values that are compared with one another
+struct alignas(16) FewValue {
+    uint32_t d;                      // distance from the top
+    int at;                          // place in the list
+    u64 v;                           // weight
+};
 struct Shared {
+    FewValue few[kSampleFew];
     uint32_t powers[32];
     float max[kWarps], low[kWarps];  // the largest value, and the smallest maximum of groups of lanes
     // the row's parts: the first block, the elements before the part in it, their number, and the blocks
@@ -668,6 +676,85 @@ __device__ __forceinline__ void add_mass(unsigned (&part)[3], u64 v) {
     for (int i = 0; i < 3; i++) part[i] += (unsigned)(v >> (15 * i)) & 0x7FFFu;
 }
 
+// As decide(), by one CTA, of the `n` values of its list that are no further than `most` from the top, each
+// thread's distances in d.
+template <int DT, typename TokenOf>
+__device__ __forceinline__ void decide_few(const SampleArgs& a, const Filters& q, Shared& sh, const float* values, const uint32_t (&d)[kPer],
+                                           uint32_t most, int n, const Weights& w, u64 exact, u64 total, int row, TokenOf token_of) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = (int)threadIdx.x * kPer;
+    // in their order, one a thread
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; j++) mine += d[j] <= most;
+    int to = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(~0u, to, o);
+        if (lane >= o) to += x;
+    }
+    __syncthreads();
+    if (lane == 31) sh.count[0][warp] = to;
+    __syncthreads();
+    to -= mine;
+    for (int i = 0; i < warp; i++) to += sh.count[0][i];
+#pragma unroll
+    for (int j = 0; j < kPer; j++)
+        if (d[j] <= most) sh.few[to++] = FewValue{d[j], first + j, w.fixed(values[first + j])};
+    __syncthreads();
+    // its place, and the sum of what lies before it and of all, in the order of the filters
+    const int i = threadIdx.x;
+    FewValue own = {0xFFFFFFFFu, 0, 0};
+    int place = 0;
+    u64 before = 0;
+    if (i < n) own = sh.few[i];
+    if (warp * 32 < n) {
+#pragma unroll 4
+        for (int j = 0; j < n; j++) {
+            const FewValue other = sh.few[j];
+            if (other.d < own.d + (j < i)) {
+                place++;
+                before += other.v;
+            }
+        }
+    }
+    bool keep = i < n && place < q.k;
+    if (q.nucleus) {
+        if (q.limited) {             // the sum of the topK
+            if (keep && (place == q.k - 1 || place == n - 1)) sh.total = before + own.v;
+            __syncthreads();
+            exact = sh.total;
+        }
+        keep = keep && before < max(1ull, share_of(exact, q.p, true));
+    }
+    const u64 floorWeight = q.least >= 1.0f ? 1ull << kFix : share_of(1ull << kFix, q.least, true);
+    const u64 sum = keep && own.v >= floorWeight ? own.v : 0;
+    u64 run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 x = __shfl_up_sync(~0u, run, o);
+        if (lane >= o) run += x;
+    }
+    if (lane == 31) sh.warp[0][warp] = run;
+    __syncthreads();
+    u64 all = 0, ahead = run - sum;
+#pragma unroll
+    for (int k = 0; k < kSampleFew / 32; k++) {
+        const u64 x = sh.warp[0][k];
+        if (k < warp) ahead += x;
+        all += x;
+    }
+    const float u = a.uniform[row];
+    const u64 goal = u >= 1.0f ? all - 1 : share_of(all, u, false);
+    if (goal < ahead || goal >= ahead + sum) return;
+    const float x = values[own.at];
+    const int token = token_of(own.at);
+    for (int o = 0; o < a.nOut; o++) a.tokens[o][row] = token;
+    if (a.logprob) {
+        const float z = x == w.top ? 0.0f : q.greedy ? x - w.top : (x - w.top) / q.heat;
+        a.logprob[row] = z - log1pf((float)(total - (1ull << kFix)) * 0x1p-44f);
+    }
+}
+
 // As decide(), by one CTA, of the `few` values of its list, of which none is further than `most` from the top.
 template <int DT, typename TokenOf>
 __device__ __forceinline__ void decide_list(const SampleArgs& a, const Filters& q, Shared& sh, const float* values, int few,
@@ -680,6 +767,28 @@ __device__ __forceinline__ void decide_list(const SampleArgs& a, const Filters& 
 #pragma unroll
     for (int j = 0; j < kPer; j++) d[j] = first + j < few ? keyTop - key_of<DT>(values[first + j]) : 0xFFFFFFFFu;
     int buffer = 0;
+    // Few enough to compare all with all: those up to a distance that leaves at least k.
+    if (few <= kSampleFew || (q.limited && q.k <= kSampleFew)) {
+        uint32_t lo = 0, hi = most;  // up to hi there are `n`, at least k of them where there are k
+        int n = few;
+        while (n > kSampleFew && lo < hi) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            int c = 0;
+#pragma unroll
+            for (int j = 0; j < kPer; j++) c += d[j] <= mid;
+            c = block_count(sh, c, buffer);
+            if (c >= q.k) {
+                hi = mid;
+                n = c;
+            } else {
+                lo = mid + 1;
+            }
+        }
+        if (n <= kSampleFew) {
+            decide_few<DT>(a, q, sh, values, d, hi, n, w, exact, total, row, token_of);
+            return;
+        }
+    }
     // What is kept: distances below `edge`, and the first `ties` values at it.
     uint32_t edge = most;
     u64 ties = ~0ull;
