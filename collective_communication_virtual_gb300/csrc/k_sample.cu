@@ -51,6 +51,8 @@ struct alignas(16) FewValue {
 };
 struct Shared {
     FewValue few[kSampleFew];
+    int place[3][kSampleFew];
+    u64 before[3][kSampleFew];
     uint32_t powers[32];
     float max[kWarps], low[kWarps];  // the largest value, and the smallest maximum of groups of lanes
     // the row's parts: the first block, the elements before the part in it, their number, and the blocks
@@ -63,7 +65,7 @@ struct Shared {
     int count[2][kWarps];
     unsigned mass[2][3][kWarps];
     u64 target, left, total;
-    int owner;
+    int owner, settled;
 };
 
 // What the exchanges between the CTAs of a cluster need.
@@ -260,57 +262,63 @@ __device__ __forceinline__ int part_of(const Shared& sh, int block, int r) {
     while (block >= sh.blocks[r + 1]) r++;
     return r;
 }
-// Values in shared memory.  A warp has the vectors from `begin` on, every 32nd of them a lane.
+// Values in shared memory.  A warp has a run of blocks, each lane an equal share of them one behind the
+// other, so that a lane's values follow those of the lanes before; the lanes lie an odd number of
+// vectors apart, so that eight lanes' 16-byte loads touch all banks.
 template <int DT>
 struct Columns {
     static constexpr int E = kVecElems<DT>, kType = DT;
     using V = Vec<DT>;
     uint32_t at;                     // the thread's first vector
-    int first, left, steps;          // its number, the vectors from it to the run's end, the steps of the warp
-    __device__ __forceinline__ Columns(uint32_t smem, int begin, int end) {
+    int first, count;                // its number, and how many there are
+    __device__ __forceinline__ Columns(uint32_t smem, int begin, int end, int each) {
         const int lane = (int)threadIdx.x & 31;
-        at = smem + (uint32_t)(begin + lane) * 16u;
-        first = begin + lane;
-        left = end - first;
-        steps = (end - begin + 31) / 32;
+        at = smem + (uint32_t)(threadIdx.x * (unsigned)(each | 1)) * 16u;
+        first = (end - begin) * lane / 32;
+        count = (end - begin) * (lane + 1) / 32 - first;
+        first += begin;
     }
-    __device__ __forceinline__ uint4 raw(int step) const { return step * 32 < left ? ld_smem(at + (uint32_t)step * 512u) : V::none(); }
-    __device__ __forceinline__ void put(int step, const uint4& v) const { st_smem(at + (uint32_t)step * 512u, v); }
-    __device__ __forceinline__ void get(int step, float (&f)[E]) const { widen_vec<DT>(raw(step), f); }
-    // f(step, vector) for all steps of the warp, by all lanes
+    __device__ __forceinline__ uint4 raw(int k) const { return ld_smem(at + (uint32_t)k * 16u); }
+    __device__ __forceinline__ void put(int k, const uint4& v) const { st_smem(at + (uint32_t)k * 16u, v); }
+    // f(number of the vector, vector) for all of the thread's
     template <typename F>
     __device__ __forceinline__ void each(F f) const {
 #pragma unroll 2
-        for (int s = 0; s < steps; s++) f(s, raw(s));
+        for (int k = 0; k < count; k++) f(k, raw(k));
     }
 };
 
-// Blocks [c0, c1) of a row into shared memory.
+// The warp's blocks [begin, end) of a row into shared memory, by the warp.
 template <int DT>
-__device__ __forceinline__ void load_blocks(const Shared& sh, int parts, int c0, int c1, uint32_t smem) {
+__device__ __forceinline__ void load_blocks(const Shared& sh, int parts, int begin, int end, int each, uint32_t smem) {
     constexpr int E = kVecElems<DT>;
-    for (int r = 0; r < parts; r++) {
-        const int lo = max(c0, sh.blocks[r]), hi = min(c1, sh.blocks[r + 1]);
-        const uint4* from = sh.part[r] + (lo - sh.blocks[r]);
-        for (int i = threadIdx.x; i < hi - lo; i += kSampleThreads)
-            copy_block_async(smem + 16u * (lo - c0 + i), reinterpret_cast<const char*>(from + i));
+    const int lane = (int)threadIdx.x & 31, stride = each | 1;
+    const uint32_t base = smem + (threadIdx.x & ~31u) * (unsigned)stride * 16u;
+    const int run = end - begin;
+    const auto slot = [&](int i) {
+        const int owner = (32 * (i + 1) - 1) / run;    // the lane l with run l / 32 <= i < run (l + 1) / 32
+        return base + (uint32_t)(owner * stride + i - run * owner / 32) * 16u;
+    };
+    for (int i = lane, r = 0; i < run; i += 32) {
+        r = part_of(sh, begin + i, r);
+        copy_block_async(slot(i), reinterpret_cast<const char*>(sh.part[r] + (begin + i - sh.blocks[r])));
     }
     copies_commit();
     copies_wait();
-    __syncthreads();
+    __syncwarp();
     // what the first and the last block of a part hold besides it
-    if ((int)threadIdx.x < parts) {
-        const int r = threadIdx.x, first = sh.blocks[r], last = sh.blocks[r + 1] - 1;
+    for (int r = lane; r < parts; r += 32) {
+        const int first = sh.blocks[r], last = sh.blocks[r + 1] - 1;
         const auto cut = [&](int b) {
-            if (b < c0 || b >= c1) return;
+            if (b < begin || b >= end) return;
             const int at = (b - first) * E - sh.shift[r];        // the first value's place in its part
-            const uint32_t p = smem + 16u * (b - c0);
+            const uint32_t p = slot(b - begin);
             st_smem(p, Vec<DT>::only(ld_smem(p), -at, sh.length[r] - at));
         };
         cut(first);
         if (last > first) cut(last);
     }
-    __syncthreads();
+    __syncwarp();
 }
 
 // The distance d from the largest key at which the running count (or, BY_MASS, the running sum of
@@ -549,95 +557,65 @@ __device__ __forceinline__ void decide(const SampleArgs& a, const Filters& q, Sh
     block_sums(sh, blockSum, blockCount);              // leaves every warp's sums in sh.warp
     const u64 mine[kWords] = {blockSum, blockCount, 0, 0};
     const u64(*box)[kWords] = exchange(sh, team, mine);
-    // From here on nothing touches another CTA's memory.
-    if (threadIdx.x == 0) {
-        u64 all = 0, ahead = 0, left = ties, leftHere = ties;
+    // From here on nothing touches another CTA's memory.  What is kept before this warp, and of its ties.
+    u64 all = 0, ahead = 0, left = ties;
+    {
+        u64 rest = ties;
         for (int c = 0; c < team.size; c++) {
-            const u64 n = min(left, box[c][1]);
+            const u64 n = min(rest, box[c][1]);
             if (c == team.rank) {
                 ahead = all;
-                leftHere = left;
+                left = rest;
             }
             all += box[c][0] + n * atEdge;
+            rest -= n;
+        }
+        for (int i = 0; i < warp; i++) {
+            const u64 n = min(left, sh.warp[1][i]);
+            ahead += sh.warp[0][i] + n * atEdge;
             left -= n;
         }
-        const float u = a.uniform[row];
-        const u64 goal = u >= 1.0f ? all - 1 : share_of(all, u, false);
-        sh.owner = -1;
-        sh.total = total ? total : all;
-        for (int i = 0; i < kWarps && goal >= ahead; i++) {
-            const u64 n = min(leftHere, sh.warp[1][i]), here = sh.warp[0][i] + n * atEdge;
-            if (goal < ahead + here) {
-                sh.owner = i;
-                sh.target = goal - ahead;
-                sh.left = leftHere;
-                break;
-            }
-            ahead += here;
-            leftHere -= n;
-        }
     }
-    __syncthreads();
-    if (warp != sh.owner) return;
-
-    // The warp whose values hold the token goes through them in order.
-    u64 goal = sh.target, left = sh.left;
-    for (int s = 0; s < cols.steps; s++) {
+    const float u = a.uniform[row];
+    const u64 goal = u >= 1.0f ? all - 1 : share_of(all, u, false);
+    // The ties before this thread's, then what is kept before it.
+    u64 runTies = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 x = __shfl_up_sync(~0u, runTies, o);
+        if (lane >= o) runTies += x;
+    }
+    left -= min(left, runTies - count);
+    sum += min(left, count) * atEdge;
+    u64 run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 x = __shfl_up_sync(~0u, run, o);
+        if (lane >= o) run += x;
+    }
+    ahead += run - sum;
+    if (goal < ahead || goal >= ahead + sum) return;
+    // The thread whose values hold the token goes through them in order.
+    for (int k = 0; k < cols.count; k++) {
         float f[E];
-        cols.get(s, f);
-        u64 v[E], own = 0, n = 0;
-        bool tie[E];
-#pragma unroll
+        widen_vec<Cols::kType>(cols.raw(k), f);
         for (int j = 0; j < E; j++) {
-            v[j] = kept(f[j], &tie[j]);
-            own += v[j];
-            n += tie[j];
-        }
-        if (!__any_sync(~0u, own + n != 0)) continue;
-        u64 runTies = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 x = __shfl_up_sync(~0u, runTies, o);
-            if (lane >= o) runTies += x;
-        }
-        u64 mineLeft = left - min(left, runTies - n);  // ties that may still be kept, from this lane on
-        own += min(mineLeft, n) * atEdge;
-        u64 run = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 x = __shfl_up_sync(~0u, run, o);
-            if (lane >= o) run += x;
-        }
-        const bool here = goal >= run - own && goal < run;
-        if (here) {
-            u64 ahead = run - own;
-            int pick = 0;
-            float x = f[0];
-            bool done = false;
-#pragma unroll
-            for (int j = 0; j < E; j++) {
-                u64 e = v[j];
-                if (tie[j] && mineLeft > 0) {
-                    mineLeft--;
-                    e = atEdge;
-                }
-                ahead += e;
-                if (!done && goal < ahead) {
-                    done = true;
-                    pick = j;
-                    x = f[j];
-                }
+            bool tie;
+            u64 e = kept(f[j], &tie);
+            if (tie && left > 0) {
+                left--;
+                e = atEdge;
             }
-            const int token = token_of((cols.first + s * 32) * E + pick);
+            ahead += e;
+            if (goal >= ahead) continue;
+            const int token = token_of((cols.first + k) * E + j);
             for (int o = 0; o < a.nOut; o++) a.tokens[o][row] = token;
             if (a.logprob) {
-                const float z = x == top ? 0.0f : q.greedy ? x - top : (x - top) / q.heat;
-                a.logprob[row] = z - log1pf((float)(sh.total - (1ull << kFix)) * 0x1p-44f);
+                const float x = f[j], z = x == top ? 0.0f : q.greedy ? x - top : (x - top) / q.heat;
+                a.logprob[row] = z - log1pf((float)((total ? total : all) - (1ull << kFix)) * 0x1p-44f);
             }
+            return;
         }
-        if (__any_sync(~0u, here)) return;
-        goal -= __shfl_sync(~0u, run, 31);
-        left -= min(left, __shfl_sync(~0u, runTies, 31));
     }
 }
 
@@ -679,8 +657,9 @@ __device__ __forceinline__ void add_mass(unsigned (&part)[3], u64 v) {
 // As decide(), by one CTA, of the `n` values of its list that are no further than `most` from the top, each
 // thread's distances in d.
 template <int DT, typename TokenOf>
-__device__ __forceinline__ void decide_few(const SampleArgs& a, const Filters& q, Shared& sh, const float* values, const uint32_t (&d)[kPer],
-                                           uint32_t most, int n, const Weights& w, u64 exact, u64 total, int row, TokenOf token_of) {
+__device__ __forceinline__ bool decide_few(const SampleArgs& a, const Filters& q, Shared& sh, const float* values, const uint32_t (&d)[kPer],
+                                           uint32_t most, int n, const Weights& w, u64 least, u64 exact, u64 total, int row,
+                                           TokenOf token_of) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = (int)threadIdx.x * kPer;
     // in their order, one a thread
     int mine = 0;
@@ -701,15 +680,17 @@ __device__ __forceinline__ void decide_few(const SampleArgs& a, const Filters& q
     for (int j = 0; j < kPer; j++)
         if (d[j] <= most) sh.few[to++] = FewValue{d[j], first + j, w.fixed(values[first + j])};
     __syncthreads();
-    // its place, and the sum of what lies before it and of all, in the order of the filters
-    const int i = threadIdx.x;
+    // its place, and the sum of what lies before it, in the order of the filters; two or four threads a
+    // value, each of which compares it with its share of all
+    const int ways = n <= kSampleThreads / 4 ? 4 : 2, span = kSampleThreads / ways;
+    const int i = (int)threadIdx.x % span, way = (int)threadIdx.x / span;
     FewValue own = {0xFFFFFFFFu, 0, 0};
     int place = 0;
     u64 before = 0;
     if (i < n) own = sh.few[i];
-    if (warp * 32 < n) {
+    if (i / 32 * 32 < n) {
 #pragma unroll 4
-        for (int j = 0; j < n; j++) {
+        for (int j = n * way / ways; j < n * (way + 1) / ways; j++) {
             const FewValue other = sh.few[j];
             if (other.d < own.d + (j < i)) {
                 place++;
@@ -717,14 +698,25 @@ __device__ __forceinline__ void decide_few(const SampleArgs& a, const Filters& q
             }
         }
     }
-    bool keep = i < n && place < q.k;
+    if (way > 0) {
+        sh.place[way - 1][i] = place;
+        sh.before[way - 1][i] = before;
+    }
+    __syncthreads();
+    if (way > 0) own = FewValue{0xFFFFFFFFu, 0, 0};
+    for (int k = 0; k < (way == 0 ? ways - 1 : 0); k++) {
+        place += sh.place[k][i];
+        before += sh.before[k][i];
+    }
+    bool keep = way == 0 && i < n && place < q.k;
     if (q.nucleus) {
         if (q.limited) {             // the sum of the topK
             if (keep && (place == q.k - 1 || place == n - 1)) sh.total = before + own.v;
             __syncthreads();
-            exact = sh.total;
+            least = exact = sh.total;
         }
         keep = keep && before < max(1ull, share_of(exact, q.p, true));
+        if (least != exact && __syncthreads_or(keep && before >= max(1ull, share_of(least, q.p, true)))) return false;
     }
     const u64 floorWeight = q.least >= 1.0f ? 1ull << kFix : share_of(1ull << kFix, q.least, true);
     const u64 sum = keep && own.v >= floorWeight ? own.v : 0;
@@ -745,7 +737,7 @@ __device__ __forceinline__ void decide_few(const SampleArgs& a, const Filters& q
     }
     const float u = a.uniform[row];
     const u64 goal = u >= 1.0f ? all - 1 : share_of(all, u, false);
-    if (goal < ahead || goal >= ahead + sum) return;
+    if (goal < ahead || goal >= ahead + sum) return true;
     const float x = values[own.at];
     const int token = token_of(own.at);
     for (int o = 0; o < a.nOut; o++) a.tokens[o][row] = token;
@@ -753,12 +745,15 @@ __device__ __forceinline__ void decide_few(const SampleArgs& a, const Filters& q
         const float z = x == w.top ? 0.0f : q.greedy ? x - w.top : (x - w.top) / q.heat;
         a.logprob[row] = z - log1pf((float)(total - (1ull << kFix)) * 0x1p-44f);
     }
+    return true;
 }
 
 // As decide(), by one CTA, of the `few` values of its list, of which none is further than `most` from the top.
+// The sum that topP is a share of lies between `least` and `exact`: false where that leaves open what is kept.
 template <int DT, typename TokenOf>
-__device__ __forceinline__ void decide_list(const SampleArgs& a, const Filters& q, Shared& sh, const float* values, int few,
-                                            const Weights& w, uint32_t most, u64 exact, u64 total, int row, TokenOf token_of) {
+__device__ __forceinline__ bool decide_list(const SampleArgs& a, const Filters& q, Shared& sh, const float* values, int few,
+                                            const Weights& w, uint32_t most, u64 least, u64 exact, u64 total, int row,
+                                            TokenOf token_of) {
     const float top = w.top;
     const uint32_t keyTop = key_of<DT>(top);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = (int)threadIdx.x * kPer;
@@ -766,33 +761,46 @@ __device__ __forceinline__ void decide_list(const SampleArgs& a, const Filters& 
     u64 v[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; j++) d[j] = first + j < few ? keyTop - key_of<DT>(values[first + j]) : 0xFFFFFFFFu;
-    int buffer = 0;
-    // Few enough to compare all with all: those up to a distance that leaves at least k.
-    if (few <= kSampleFew || (q.limited && q.k <= kSampleFew)) {
-        uint32_t lo = 0, hi = most;  // up to hi there are `n`, at least k of them where there are k
-        int n = few;
-        while (n > kSampleFew && lo < hi) {
-            const uint32_t mid = lo + (hi - lo) / 2;
-            int c = 0;
+    int buffer = 0, within = 0;      // minus infinities are in the list where there is no bound
 #pragma unroll
-            for (int j = 0; j < kPer; j++) c += d[j] <= mid;
-            c = block_count(sh, c, buffer);
-            if (c >= q.k) {
-                hi = mid;
-                n = c;
-            } else {
-                lo = mid + 1;
+    for (int j = 0; j < kPer; j++) within += d[j] <= most;
+    within = block_count(sh, within, buffer);
+    // Few enough to compare all with all: those up to a distance that leaves at least k, or, of topP's
+    // weights, rounded down to units of 2^-20, more than the goal.
+    const bool byMass = q.nucleus && !q.limited;
+    if (within <= kSampleFew || byMass || (q.limited && q.k <= kSampleFew)) {
+        uint32_t lo = 0, hi = most;  // up to hi there are `n`, at least k of them where there are k
+        int n = within;
+        if (n > kSampleFew) {
+            unsigned weight[kPer];
+#pragma unroll
+            for (int j = 0; j < kPer; j++) weight[j] = byMass && d[j] <= most ? (unsigned)(w.fixed(values[first + j]) >> (kFix - 20)) : 0u;
+            const u64 goal = (share_of(exact, q.p, true) >> (kFix - 20)) + 1;
+            while (n > kSampleFew && lo < hi) {
+                const uint32_t mid = lo + (hi - lo) / 2;
+                int c = 0;
+                unsigned sum = 0;
+#pragma unroll
+                for (int j = 0; j < kPer; j++) {
+                    c += d[j] <= mid;
+                    sum += d[j] <= mid ? weight[j] : 0u;
+                }
+                c = block_count(sh, c, buffer);
+                if (byMass ? (unsigned)block_count(sh, (int)sum, buffer) >= goal : c >= q.k) {
+                    hi = mid;
+                    n = c;
+                } else {
+                    lo = mid + 1;
+                }
             }
         }
-        if (n <= kSampleFew) {
-            decide_few<DT>(a, q, sh, values, d, hi, n, w, exact, total, row, token_of);
-            return;
-        }
+        if (n <= kSampleFew)
+            return decide_few<DT>(a, q, sh, values, d, hi, n, w, least, exact, total, row, token_of);
     }
     // What is kept: distances below `edge`, and the first `ties` values at it.
     uint32_t edge = most;
     u64 ties = ~0ull;
-    if (q.limited && few >= q.k) {
+    if (q.limited && within >= q.k) {
         uint32_t lo = 0;             // fewer than k are nearer than lo: `below` of them
         int below = 0;
         while (lo < edge) {
@@ -820,6 +828,7 @@ __device__ __forceinline__ void decide_list(const SampleArgs& a, const Filters& 
                 if (d[j] < edge || ties == ~0ull) add_mass(part, v[j]);
             exact = block_mass(sh, part, buffer);
             if (ties != ~0ull) exact += ties * w.fixed(value_of<DT>(keyTop - edge));
+            least = exact;
         }
         const u64 goal = max(1ull, share_of(exact, q.p, true));
         uint32_t lo = 0, hi = edge;
@@ -839,6 +848,7 @@ __device__ __forceinline__ void decide_list(const SampleArgs& a, const Filters& 
             }
         }
         const u64 one = max(1ull, w.fixed(value_of<DT>(keyTop - hi))), n = (goal - before + one - 1) / one;
+        if (least != exact && max(1ull, share_of(least, q.p, true)) <= before + (n - 1) * one) return false;
         ties = hi == edge ? min(ties, n) : n;
         edge = hi;
     }
@@ -881,7 +891,7 @@ __device__ __forceinline__ void decide_list(const SampleArgs& a, const Filters& 
     }
     const float u = a.uniform[row];
     const u64 goal = u >= 1.0f ? all - 1 : share_of(all, u, false);
-    if (goal < ahead || goal >= ahead + sum) return;
+    if (goal < ahead || goal >= ahead + sum) return true;
     int pick = 0;
     bool done = false;
 #pragma unroll
@@ -904,6 +914,7 @@ __device__ __forceinline__ void decide_list(const SampleArgs& a, const Filters& 
         const float z = x == top ? 0.0f : q.greedy ? x - top : (x - top) / q.heat;
         a.logprob[row] = z - log1pf((float)(total - (1ull << kFix)) * 0x1p-44f);
     }
+    return true;
 }
 
 // From a row's values to its token.  top is this thread's largest value.
@@ -929,11 +940,21 @@ __device__ __forceinline__ void draw(const SampleArgs& a, const Filters& q, Shar
         sh.max[warp] = top;
         sh.low[warp] = kBound;
     }
-    meet(team);                                        // every CTA of the cluster has started
+    __syncthreads();
+    // (groups of several warps where fewer groups are enough: what is above their bound is less)
+    int together = 1;
+    while (together < kWarps && groups / (2 * together) >= q.k) together *= 2;
+    kBound = INFINITY;
+    float own = -INFINITY;
     for (int i = 0; i < kWarps; i++) {
         top = fmaxf(top, sh.max[i]);
-        kBound = fminf(kBound, sh.low[i]);
+        own = fmaxf(own, sh.low[i]);
+        if (together == 1 || (i + 1) % together == 0) {
+            kBound = fminf(kBound, own);
+            own = -INFINITY;
+        }
     }
+    if (team.size > 1) cluster_wait();                 // every CTA of the cluster has started
     {
         const u64 mine[kWords] = {__float_as_uint(top), __float_as_uint(kBound), 0, 0};
         const u64(*box)[kWords] = exchange(sh, team, mine);
@@ -967,102 +988,127 @@ __device__ __forceinline__ void draw(const SampleArgs& a, const Filters& q, Shar
     // (those below (1 - p) of the mean are outside it, all of them together), minP's is a weight.
     u64 exact = 0, total = 0;
     float bound = -INFINITY, pBound = -INFINITY;
-    if (q.k == 1) {
-        bound = kBound = top;
-    } else if (q.limited) {
-        bound = kBound;
-    } else if (q.nucleus) {
-        total = exact = exact_sum(sh, team, cols, w);
-        bound = pBound = value_at(w, (1.0f - fmaxf(q.p, 0.0f)) * 0.99f * ((float)exact * 0x1p-44f) / (float)a.vocab);
-    }
+    const bool share = q.nucleus && !q.limited;        // topP of all
+    if (q.k == 1) bound = kBound = top;
+    else if (q.limited) bound = kBound;
     if (!q.nucleus && q.least > 0.0f) bound = fmaxf(bound, value_at(w, fminf(q.least, 1.0f)));
-    if (!(bound <= top)) bound = bound > top ? top : -INFINITY;
+    const auto within = [&](float b) { return b <= top ? b : b > top ? top : -INFINITY; };
+    bound = within(bound);
 
-    // The sum of all weights where it is not exact yet, and what is above the bound.
-    const bool filtered = q.limited || q.nucleus || q.least > 0.0f;
-    u64 sum = 0, count = 0;
-    if (filtered) {
+    // The sum of all weights, roughly, and how many values are above the bound.
+    u64 few = 0, ahead = 0, mine = 0;                  // of the row, of the CTAs before, of this thread
+    const auto go_through = [&](bool sums, bool counts) {
+        u64 sum = 0, count = 0;
         cols.each([&](int, const uint4& v) {
             const float m = V::largest(v);
-            if (total && m < bound) return;
+            if (!sums && m < bound) return;
             float f[E];
             widen_vec<DT>(v, f);
-            if (!total) {
-                if (m == top) {      // the largest apart: what is beside them may be small
+            if (counts && m >= bound) {
 #pragma unroll
-                    for (int j = 0; j < E; j++) {
-                        sum += f[j] == top ? 1ull << kFix : 0ull;
-                        f[j] = f[j] == top ? -INFINITY : f[j];
-                    }
-                }
-                const float part = w.rough(f);
-                sum += __float2ull_rn(part * (float)(1ull << kFix));
+                for (int j = 0; j < E; j++) count += f[j] >= bound;
             }
-            if (m < bound) return;
-            widen_vec<DT>(v, f);
+            if (!sums) return;
+            if (m == top) {          // the largest apart: what is beside them may be small
 #pragma unroll
-            for (int j = 0; j < E; j++) count += f[j] >= bound;
+                for (int j = 0; j < E; j++) {
+                    sum += f[j] == top ? 1ull << kFix : 0ull;
+                    f[j] = f[j] == top ? -INFINITY : f[j];
+                }
+            }
+            sum += __float2ull_rn(w.rough(f) * (float)(1ull << kFix));
         });
-        u64 blockSum = sum, blockCount = count;
-        block_sums(sh, blockSum, blockCount);          // leaves every warp's sums in sh.warp
-        const u64 mine[kWords] = {blockSum, blockCount, 0, 0};
-        const u64(*box)[kWords] = exchange(sh, team, mine);
-        u64 all = 0, ahead = 0, few = 0;
+        mine = count;
+        block_sums(sh, sum, count);                    // leaves every warp's sums in sh.warp
+        const u64 words[kWords] = {sum, count, 0, 0};
+        const u64(*box)[kWords] = exchange(sh, team, words);
+        u64 all = 0;
+        few = ahead = 0;
         for (int c = 0; c < team.size; c++) {
             all += box[c][0];
             if (c < team.rank) ahead += box[c][1];
             few += box[c][1];
         }
-        if (!total) total = all;
+        if (sums) total = all;
+    };
+    // A weight of the rough sum is at most kRough of itself off: 45 units of the exponent rounded twice,
+    // and the exponential's 2^-22.
+    constexpr float kRough = 0x1p-17f;
+    if (q.limited || q.nucleus || q.least > 0.0f) {
+        if (a.logprob || share) go_through(true, !share);
+        else go_through(false, true);
+        if (share) {
+            pBound = bound = within(value_at(w, (1.0f - fmaxf(q.p, 0.0f)) * 0.98f * ((float)total * 0x1p-44f) / (float)a.vocab));
+            go_through(false, true);
+        }
         if (few <= (u64)kSampleList) {
             // to the first CTA's list, in order
-            int at = (int)ahead;
-            for (int i = 0; i < warp; i++) at += (int)sh.warp[1][i];
-            cols.each([&](int s, const uint4& v) {
-                const bool any = V::largest(v) >= bound;
-                if (!__any_sync(~0u, any)) return;
-                float f[E];
-                widen_vec<DT>(v, f);
-                int n = 0;
-                if (any) {
+            int to = (int)mine;
 #pragma unroll
-                    for (int j = 0; j < E; j++) n += f[j] >= bound;
-                }
-                int run = n;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int x = __shfl_up_sync(~0u, run, o);
-                    if (lane >= o) run += x;
-                }
-                int to = at + run - n;
-                if (any) {
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(~0u, to, o);
+                if (lane >= o) to += x;
+            }
+            to += (int)ahead - (int)mine;
+            for (int i = 0; i < warp; i++) to += (int)sh.warp[1][i];
+            if (mine) {
+                cols.each([&](int k, const uint4& v) {
+                    if (V::largest(v) < bound) return;
+                    float f[E];
+                    widen_vec<DT>(v, f);
 #pragma unroll
                     for (int j = 0; j < E; j++) {
                         if (!(f[j] >= bound)) continue;
-                        const int number = (cols.first + s * 32) * E + j;
+                        const int number = (cols.first + k) * E + j;
                         if (team.size == 1) {
                             listValues[to] = f[j];
                             listTokens[to] = number;
                         } else {
                             st_cluster(listValues + to, 0, __float_as_uint(f[j]));
-                            st_cluster(listTokens + to, 0, (uint32_t)number | (uint32_t)team.rank << 28);
+                            st_cluster(listTokens + to, 0, (uint32_t)number);
                         }
                         to++;
                     }
-                }
-                at += __shfl_sync(~0u, run, 31);
-            });
+                });
+            }
             meet(team);
-            if (team.rank != 0) return;
+            if (!share && team.rank != 0) return;
+            const auto token_at = [&](int i) { return token_of(listTokens[i]); };
             const uint32_t most = bound >= top ? 0u : key_of<DT>(top) - key_of<DT>(fmaxf(bound, -3.40282347e38f));
-            decide_list<DT>(a, q, sh, listValues, (int)few, w, most, exact, total, row, [&](int i) {
-                const int v = listTokens[i];
-                return token_of(v & 0x0FFFFFFF, v >> 28);
-            });
+            if (!share) {
+                decide_list<DT>(a, q, sh, listValues, (int)few, w, most, 0, 0, total, row, token_at);
+                return;
+            }
+            // topP of a sum that is exact for what is listed and rough for the rest, which is less than a
+            // (1 - p)-th of it: mostly that leaves nothing open.
+            bool settled = false;
+            if (team.rank == 0) {
+                u64 own = 0, rough = 0;
+                for (int i = threadIdx.x; i < (int)few; i += kSampleThreads) {
+                    const float x = listValues[i], pair[2] = {x == top ? -INFINITY : x, -INFINITY};
+                    own += w.fixed(x);
+                    rough += x == top ? 1ull << kFix : __float2ull_rn(w.rough(pair) * (float)(1ull << kFix));
+                }
+                block_sums(sh, own, rough);
+                const u64 rest = total > rough ? total - rough : 0;
+                // (and for the rounding of both rough sums, a unit of 2^-23 a vector or value)
+                const u64 off = (u64)((float)rest * kRough) + (u64)((float)total * 0x1p-21f) + (u64)a.vocab;
+                const u64 least = own + (rest > off ? rest - off : 0), exactMost = own + rest + off;
+                settled = decide_list<DT>(a, q, sh, listValues, (int)few, w, most, least, exactMost, total, row, token_at);
+                if ((int)threadIdx.x < team.size) {
+                    if (team.size == 1) sh.settled = settled;
+                    else st_cluster(&sh.settled, threadIdx.x, (uint32_t)settled);
+                }
+            }
+            meet(team);
+            if (sh.settled) return;
+            exact = total = exact_sum(sh, team, cols, w);
+            if (team.rank == 0) decide_list<DT>(a, q, sh, listValues, (int)few, w, most, exact, exact, total, row, token_at);
             return;
         }
+        if (share) exact = total = exact_sum(sh, team, cols, w);
     }
-    decide<DT>(a, q, sh, team, hist, cols, w, kBound, pBound, exact, total, row, [&](int i) { return token_of(i, team.rank); });
+    decide<DT>(a, q, sh, team, hist, cols, w, kBound, pBound, exact, total, row, token_of);
 }
 
 __device__ __forceinline__ Filters filters_of(const SampleArgs& a, int row) {
@@ -1084,14 +1130,17 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     constexpr int E = kVecElems<DT>;
     extern __shared__ __align__(16) unsigned char dynamic[];
     __shared__ Shared sh;
+    // either a list or a histogram
     uint32_t* const hist = reinterpret_cast<uint32_t*>(dynamic);
-    float* const listValues = reinterpret_cast<float*>(hist + 2 * kSampleBins);
+    float* const listValues = reinterpret_cast<float*>(dynamic);
+    static_assert(2 * kSampleBins * 4 <= kSampleList * 8, "the histogram has room where the list is");
     int* const listTokens = reinterpret_cast<int*>(listValues + kSampleList);
     const uint32_t values = (uint32_t)__cvta_generic_to_shared(listTokens + kSampleList);
     Team team;
     team.size = a.cluster;
     team.rank = a.cluster > 1 ? (int)cluster_rank() : 0;
     team.flip = team.flipFound = 0;
+    if (team.size > 1) cluster_arrive();               // waited for before another CTA's memory is touched
     const int row = (int)(blockIdx.x / (unsigned)team.size), warp = (int)threadIdx.x >> 5;
     if (threadIdx.x < 32) sh.powers[threadIdx.x] = kPowers[threadIdx.x];
     const Filters q = filters_of(a, row);
@@ -1099,20 +1148,20 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     // every warp of the cluster the same share of the blocks, so that none is without a value
     const int total = sh.blocks[a.nParts], warps = team.size * kWarps;
     const auto share = [&](int w) { return (int)((long long)total * w / warps); };
-    const int c0 = share(team.rank * kWarps), c1 = share((team.rank + 1) * kWarps);
-    load_blocks<DT>(sh, a.nParts, c0, c1, values);
-    const Columns<DT> cols(values, share(team.rank * kWarps + warp) - c0, share(team.rank * kWarps + warp + 1) - c0);
+    const int begin = share(team.rank * kWarps + warp), end = share(team.rank * kWarps + warp + 1);
+    load_blocks<DT>(sh, a.nParts, begin, end, a.each, values);
+    const Columns<DT> cols(values, begin, end, a.each);
     // a NaN counts as minus infinity, and is overwritten by it
     float top = -INFINITY;
-    cols.each([&](int s, uint4 v) {
+    cols.each([&](int k, uint4 v) {
         if (Vec<DT>::suspect(v)) {
             v = Vec<DT>::only(v, 0, E);
-            if (s * 32 < cols.left) cols.put(s, v);
+            cols.put(k, v);
         }
         top = fmaxf(top, Vec<DT>::largest(v));
     });
-    draw<DT>(a, q, sh, team, hist, listValues, listTokens, cols, top, row, [&](int number, int rank) {
-        const int block = number / E + share(rank * kWarps), r = part_of(sh, block, 0);
+    draw<DT>(a, q, sh, team, hist, listValues, listTokens, cols, top, row, [&](int number) {
+        const int block = number / E, r = part_of(sh, block, 0);
         return r * a.part + (block - sh.blocks[r]) * E - sh.shift[r] + number % E;
     });
 }
@@ -1126,7 +1175,7 @@ cudaError_t sample_launch(const SampleArgs& a, cudaStream_t s) {
     NormShape sh = {};
     sh.threads = kSampleThreads;
     sh.cluster = a.cluster;
-    const size_t smem = 2 * kSampleBins * 4 + kSampleList * 8 + (size_t)a.blocks * 16;
+    const size_t smem = kSampleList * 8 + (size_t)kSampleThreads * (a.each | 1) * 16;
     return norm_launch(kernel, (unsigned)a.rows * (unsigned)sh.cluster, sh, smem, s, a);
 }
 

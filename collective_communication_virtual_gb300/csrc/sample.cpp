@@ -60,17 +60,17 @@ vResult_t sample(const vSampleDesc_t* desc, const void* const* logits, const flo
     a.rows = (int)d.rows;
     a.vocab = (int)d.vocab;
     a.part = (int)d.part;
-    // Blocks of a row, at most: a part may begin and end inside one.  As many CTAs as leave a thread four
-    // of them while SMs are idle; of more rows than SMs, as leave two CTAs an SM.
+    // Blocks of a row, at most (a part may begin and end inside one), in equal shares for the warps of a
+    // cluster and their lanes.  As many CTAs as leave an SM room for two, and more while SMs are idle.
     const size_t blocks = d.vocab / e + 2 * (size_t)a.nParts;
-    const auto each = [&]() { return (blocks + a.cluster - 1) / a.cluster + 1; };
+    const auto each = [&]() { return (int)(((blocks + 16 * a.cluster - 1) / (16 * a.cluster) + 31) / 32); };
     a.cluster = 1;
     while (a.cluster < vc::kSampleCluster &&
-           (each() * 16 > vc::kSamplePair || (each() > vc::kSampleThreads && d.rows * a.cluster < (size_t)v.smCount))) a.cluster *= 2;
-    a.blocks = (int)each();
+           (each() > vc::kSamplePair || (each() > 1 && d.rows * a.cluster < (size_t)v.smCount))) a.cluster *= 2;
+    a.each = each();
     if (v.debug)
-        std::fprintf(stderr, "vcomm INFO Sample rows=%d vocab=%d dt=%d N=%d cluster=%d blocks=%d\n", a.rows, a.vocab,
-                     (int)d.datatype, v.nRanks, a.cluster, a.blocks);
+        std::fprintf(stderr, "vcomm INFO Sample rows=%d vocab=%d dt=%d N=%d cluster=%d each=%d\n", a.rows, a.vocab,
+                     (int)d.datatype, v.nRanks, a.cluster, a.each);
     return comm_launch(c, "sample", [&]() { return vc::launch_sample(a, d.datatype, stream); });
 }
 

@@ -9,7 +9,7 @@ constexpr int kSampleThreads = 512;
 constexpr int kSampleCluster = 8;
 constexpr int kSampleBins = 2048;
 constexpr int kSampleMaxSmem = 192 * 1024;
-constexpr int kSamplePair = 72 * 1024;   // bytes of a row that leave an SM room for two CTAs
+constexpr int kSamplePair = 9;       // blocks of a thread that leave an SM room for two CTAs
 constexpr int kSampleList = 2560;    // values above a row's bound that one CTA takes
 
 struct SampleArgs {
@@ -26,7 +26,7 @@ struct SampleArgs {
     int nParts;                              // ranks that hold columns below vocab
     int nOut;
     int cluster;                             // CTAs that share a row
-    int blocks;                              // 16-byte blocks of it that a CTA has at most
+    int each;                                // 16-byte blocks of it that a thread has, at most
 };
 cudaError_t launch_sample(const SampleArgs& a, vDataType_t dt, cudaStream_t s);
 
