@@ -984,8 +984,8 @@ __device__ __forceinline__ void draw(const SampleArgs& a, const Filters& q, Shar
         if (w.ch != c || !(fabsf(w.cl) <= 1e-6f * c)) w.cl = 0.0f;
     }
 
-    // All that may be kept is at least `bound`: topK's is known, topP's follows from the sum of all weights
-    // (those below (1 - p) of the mean are outside it, all of them together), minP's is a weight.
+    // All that may be kept is at least `bound`: topK's is known, topP's follows from the sum of all weights,
+    // minP's is a weight.  (pBound: weights below (1 - p) of the mean are outside topP, all of them together.)
     u64 exact = 0, total = 0;
     float bound = -INFINITY, pBound = -INFINITY;
     const bool share = q.nucleus && !q.limited;        // topP of all
@@ -997,51 +997,60 @@ __device__ __forceinline__ void draw(const SampleArgs& a, const Filters& q, Shar
 
     // The sum of all weights, roughly, and how many values are above the bound.
     u64 few = 0, ahead = 0, mine = 0;                  // of the row, of the CTAs before, of this thread
-    const auto go_through = [&](bool sums, bool counts) {
+    // The rough sum of a vector's values, whose largest is m; of those that are at least `from`.
+    const auto rough = [&](float (&f)[E], float m, float from) {
+        u64 sum = 0;
+        if (m == top || from > -INFINITY) {            // the largest apart: what is beside them may be small
+#pragma unroll
+            for (int j = 0; j < E; j++) {
+                sum += f[j] == top ? 1ull << kFix : 0ull;
+                f[j] = f[j] == top || f[j] < from ? -INFINITY : f[j];
+            }
+        }
+        return sum + __float2ull_rn(w.rough(f) * (float)(1ull << kFix));
+    };
+    // Goes through all values: the rough sum of all, or of those above the bound, and their number.
+    const auto go_through = [&](bool all, bool above, bool counts) {
         u64 sum = 0, count = 0;
         cols.each([&](int, const uint4& v) {
             const float m = V::largest(v);
-            if (!sums && m < bound) return;
+            if (!all && m < bound) return;
             float f[E];
             widen_vec<DT>(v, f);
             if (counts && m >= bound) {
 #pragma unroll
                 for (int j = 0; j < E; j++) count += f[j] >= bound;
             }
-            if (!sums) return;
-            if (m == top) {          // the largest apart: what is beside them may be small
-#pragma unroll
-                for (int j = 0; j < E; j++) {
-                    sum += f[j] == top ? 1ull << kFix : 0ull;
-                    f[j] = f[j] == top ? -INFINITY : f[j];
-                }
-            }
-            sum += __float2ull_rn(w.rough(f) * (float)(1ull << kFix));
+            if (all || above) sum += rough(f, m, all ? -INFINITY : bound);
         });
         mine = count;
         block_sums(sh, sum, count);                    // leaves every warp's sums in sh.warp
         const u64 words[kWords] = {sum, count, 0, 0};
         const u64(*box)[kWords] = exchange(sh, team, words);
-        u64 all = 0;
+        u64 sums = 0;
         few = ahead = 0;
         for (int c = 0; c < team.size; c++) {
-            all += box[c][0];
+            sums += box[c][0];
             if (c < team.rank) ahead += box[c][1];
             few += box[c][1];
         }
-        if (sums) total = all;
+        return sums;
     };
     // A weight of the rough sum is at most kRough of itself off: 45 units of the exponent rounded twice,
     // and the exponential's 2^-22.
     constexpr float kRough = 0x1p-17f;
     if (q.limited || q.nucleus || q.least > 0.0f) {
-        if (a.logprob || share) go_through(true, !share);
-        else go_through(false, true);
+        if (a.logprob || share) total = go_through(true, false, !share);
+        else go_through(false, false, true);
+        bool listed = true;
         if (share) {
-            pBound = bound = within(value_at(w, (1.0f - fmaxf(q.p, 0.0f)) * 0.98f * ((float)total * 0x1p-44f) / (float)a.vocab));
-            go_through(false, true);
+            // at most a list's worth of weights can be above a list's part of their sum; mostly they hold topP
+            bound = within(value_at(w, (float)total * 0x1p-44f / (kSampleList - 64)));
+            const u64 held = go_through(false, true, true);
+            listed = (float)held * (1.0f - 4.0f * kRough) > fmaxf(q.p, 0.0f) * (float)total;
         }
-        if (few <= (u64)kSampleList) {
+        if (few > (u64)kSampleList) listed = false;
+        if (listed) {
             // to the first CTA's list, in order
             int to = (int)mine;
 #pragma unroll
@@ -1079,8 +1088,8 @@ __device__ __forceinline__ void draw(const SampleArgs& a, const Filters& q, Shar
                 decide_list<DT>(a, q, sh, listValues, (int)few, w, most, 0, 0, total, row, token_at);
                 return;
             }
-            // topP of a sum that is exact for what is listed and rough for the rest, which is less than a
-            // (1 - p)-th of it: mostly that leaves nothing open.
+            // topP of a sum that is exact for what is listed and rough for the rest, a (1 - p)-th of it at most:
+            // mostly that leaves nothing open.
             bool settled = false;
             if (team.rank == 0) {
                 u64 own = 0, rough = 0;
@@ -1106,7 +1115,10 @@ __device__ __forceinline__ void draw(const SampleArgs& a, const Filters& q, Shar
             if (team.rank == 0) decide_list<DT>(a, q, sh, listValues, (int)few, w, most, exact, exact, total, row, token_at);
             return;
         }
-        if (share) exact = total = exact_sum(sh, team, cols, w);
+        if (share) {
+            exact = total = exact_sum(sh, team, cols, w);
+            pBound = value_at(w, (1.0f - fmaxf(q.p, 0.0f)) * 0.99f * ((float)exact * 0x1p-44f) / (float)a.vocab);
+        }
     }
     decide<DT>(a, q, sh, team, hist, cols, w, kBound, pBound, exact, total, row, token_of);
 }
