@@ -160,26 +160,50 @@ struct Weights {
         }
         return sum.x + sum.y;
     }
-    // 2^44 e, as an integer: the difference and its product with ch + cl with their rounding errors,
-    // 2^(k/32) from a table and 2^g, |g| <= 1/64, from its series.
-    __device__ __forceinline__ u64 fixed(float x) const {
-        if (x == top) return 1ull << kFix;
-        const float dh = __fsub_rn(x, top);
-        const float p = __fmul_rn(dh, ch);
-        if (!(p >= -(float)kFix - 1.0f)) return 0;
-        const float b = __fsub_rn(dh, x);
-        const float dl = __fadd_rn(__fsub_rn(x, __fsub_rn(dh, b)), __fsub_rn(-top, b));
-        const float pl = __fmaf_rn(dh, ch, -p) + __fmaf_rn(dh, cl, dl * ch);
+    // 2^44 e of two values, as integers: the difference and its product with ch + cl with their rounding
+    // errors, 2^(k/32) from a table and 2^g, |g| <= 1/64, from its series; without branches, two at a
+    // time, as every exact sum goes through here.
+    __device__ __forceinline__ void fixed2(float x, float y, u64& vx, u64& vy) const {
+        if (isinf(top)) {            // there is nothing beside infinities
+            vx = x == top ? 1ull << kFix : 0;
+            vy = y == top ? 1ull << kFix : 0;
+            return;
+        }
+        const auto both = [](float c) { return make_float2(c, c); };
+        const float2 f = make_float2(x, y), minus = both(-1.0f);
+        // f - top = d + low
+        const float2 d = add2(f, both(-top)), b = fma2(f, minus, d), t = fma2(b, minus, d);
+        const float2 low = add2(fma2(t, minus, f), fma2(b, minus, both(-top)));
+        const float2 np = mul2(d, both(-ch));          // -p, p = log2 e to 24 bits
+        float2 pl = fma2(d, both(ch), np);
+        pl = fma2(d, both(cl), pl);
+        pl = fma2(low, both(ch), pl);
         const float magic = 12582912.0f;               // 1.5 2^23: the sum's low bits are the integer
-        const float r = __fadd_rn(p * 32.0f, magic);
-        const int k = __float_as_int(r) - __float_as_int(magic);
-        const float g = __fmaf_rn(__fsub_rn(r, magic), -0.03125f, p) + pl;
-        const float q = g * fmaf(g, fmaf(g, fmaf(g, 0.009618129107628477f, 0.055504108664821576f), 0.2402265069591007f),
-                                 0.6931471805599453f);
-        const uint32_t t = powers[k & 31];
-        const uint32_t m = t + (uint32_t)(int)(((long long)t * __float2int_rn(q * 4294967296.0f)) >> 32);
-        const int down = -(k >> 5);
-        return ((u64)m << (kFix - 31)) >> max(0, down);
+        const float2 at = make_float2(fminf(np.x, kFix + 2.0f), fminf(np.y, kFix + 2.0f));     // beyond this nothing is left
+        const float2 r = fma2(at, both(-32.0f), both(magic));
+        const float2 k = add2(r, both(-magic));
+        const float2 g = fma2(fma2(k, both(0.03125f), np), minus, pl);
+        float2 q = fma2(g, both(0.009618129107628477f), both(0.055504108664821576f));
+        q = fma2(g, q, both(0.2402265069591007f));
+        q = fma2(g, q, both(0.6931471805599453f));
+        q = mul2(mul2(g, q), both(8589934592.0f));     // 2^33
+        vx = assemble(r.x, q.x);
+        vy = assemble(r.y, q.y);
+    }
+    __device__ __forceinline__ u64 assemble(float r, float q) const {
+        const int k = __float_as_int(r) - __float_as_int(12582912.0f);
+        const uint32_t t = powers[k & 31], m = t + (uint32_t)__mulhi((int)(t >> 1), __float2int_rn(q));
+        return ((u64)m << (kFix - 31)) >> max(0, -(k >> 5));
+    }
+    __device__ __forceinline__ u64 fixed(float x) const {
+        u64 a, b;
+        fixed2(x, x, a, b);
+        return a;
+    }
+    template <int E>
+    __device__ __forceinline__ void fixed(const float (&f)[E], u64 (&v)[E]) const {
+#pragma unroll
+        for (int j = 0; j < E; j += 2) fixed2(f[j], f[j + 1], v[j], v[j + 1]);
     }
 };
 
@@ -336,11 +360,15 @@ __device__ bool search(Shared& sh, Team& team, uint32_t* hist, const Cols& cols,
     int shift = max(0, 32 - __clz((int)most) - 11);
     for (;;) {
         const bool masses = BY_MASS && shift > 0;      // a bin of one value needs counts alone
+        const float lowest = value_of<DT>(keyTop - most);
         for (int i = threadIdx.x; i < kSampleBins * (masses ? 2 : 1); i += kSampleThreads) hist[i] = 0;
         __syncthreads();
         cols.each([&](int, const uint4& v) {
+            if (Cols::V::largest(v) < lowest) return;
             float f[E];
             widen_vec<Cols::kType>(v, f);
+            u64 weight[E];
+            if (masses) w.fixed(f, weight);
 #pragma unroll
             for (int j = 0; j < E; j++) {
                 const uint32_t d = keyTop - key_of<DT>(f[j]);
@@ -349,7 +377,7 @@ __device__ bool search(Shared& sh, Team& team, uint32_t* hist, const Cols& cols,
                 if (!masses) {
                     atomicAdd(&low[bin], 1u);
                 } else {
-                    const u64 e = w.fixed(f[j]);
+                    const u64 e = weight[j];
                     const uint32_t old = atomicAdd(&low[bin], (uint32_t)e);
                     const uint32_t carry = (uint32_t)(e >> 32) + (old + (uint32_t)e < old ? 1u : 0u);
                     if (carry) atomicAdd(&high[bin], carry);
@@ -452,9 +480,11 @@ __device__ u64 exact_sum(Shared& sh, Team& team, const Cols& cols, const Weights
     u64 s = 0, none = 0;
     cols.each([&](int, const uint4& v) {
         float f[Cols::E];
+        u64 e[Cols::E];
         widen_vec<Cols::kType>(v, f);
+        w.fixed(f, e);
 #pragma unroll
-        for (int j = 0; j < Cols::E; j++) s += w.fixed(f[j]);
+        for (int j = 0; j < Cols::E; j++) s += e[j];
     });
     block_sums(sh, s, none);
     const u64 mine[kWords] = {s, 0, 0, 0};
@@ -500,11 +530,14 @@ __device__ __forceinline__ void decide(const SampleArgs& a, const Filters& q, Sh
         if (cut) {                   // the sum of the topK
             u64 s = 0, none = 0;
             cols.each([&](int, const uint4& v) {
+                if (Cols::V::largest(v) < value_of<DT>(keyTop - edge)) return;
                 float f[E];
+                u64 weight[E];
                 widen_vec<Cols::kType>(v, f);
+                w.fixed(f, weight);
 #pragma unroll
                 for (int j = 0; j < E; j++)
-                    if (keyTop - key_of<DT>(f[j]) < edge) s += w.fixed(f[j]);
+                    if (keyTop - key_of<DT>(f[j]) < edge) s += weight[j];
             });
             block_sums(sh, s, none);
             const u64 mine[kWords] = {s, 0, 0, 0};
@@ -532,12 +565,10 @@ __device__ __forceinline__ void decide(const SampleArgs& a, const Filters& q, Sh
     // Weights kept by every warp, its ties at the edge aside.
     u64 atEdge = cut ? w.fixed(value_of<DT>(keyTop - edge)) : 0;
     if (atEdge < floorWeight) atEdge = 0;
-    const auto kept = [&](float x, bool* tie) {
+    const auto kept = [&](float x, u64 weight, bool* tie) {
         const uint32_t d = keyTop - key_of<DT>(x);
         *tie = cut && d == edge;
-        if ((cut && d >= edge) || x < floorValue) return 0ull;
-        const u64 v = w.fixed(x);
-        return v >= floorWeight ? v : 0ull;
+        return (cut && d >= edge) || weight < floorWeight ? 0ull : weight;
     };
     // What lies below this is not kept, and no tie.
     const float bottom = fmaxf(cut ? value_of<DT>(keyTop - edge) : -INFINITY, floorValue);
@@ -545,11 +576,13 @@ __device__ __forceinline__ void decide(const SampleArgs& a, const Filters& q, Sh
     cols.each([&](int, const uint4& v) {
         if (Cols::V::largest(v) < bottom) return;
         float f[E];
+        u64 weight[E];
         widen_vec<Cols::kType>(v, f);
+        w.fixed(f, weight);
 #pragma unroll
         for (int j = 0; j < E; j++) {
             bool tie;
-            sum += kept(f[j], &tie);
+            sum += kept(f[j], weight[j], &tie);
             count += tie;
         }
     });
@@ -601,7 +634,7 @@ __device__ __forceinline__ void decide(const SampleArgs& a, const Filters& q, Sh
         widen_vec<Cols::kType>(cols.raw(k), f);
         for (int j = 0; j < E; j++) {
             bool tie;
-            u64 e = kept(f[j], &tie);
+            u64 e = kept(f[j], w.fixed(f[j]), &tie);
             if (tie && left > 0) {
                 left--;
                 e = atEdge;
