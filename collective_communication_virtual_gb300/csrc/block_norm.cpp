@@ -23,14 +23,25 @@ vResult_t check_block(const vBlockNormDesc_t* desc, Checked* k) {
     return check_desc(&d, k);
 }
 
-vc::NormCall block_call(const Checked& k, const CommView& v, const Buffers& b, bool backward) {
+vc::NormCall block_call(const Checked& k, const CommView& v, const Buffers& b, bool backward, int segments) {
     vc::NormCall c = norm_call(k, v, b);
     c.weightSize += 4;               // beside the weight before the next block, post * gate in fp32
     c.extraRowBuffers = 1;
     c.backward = backward;
+    c.segments = segments;
+    // A row's two reductions, one behind the other, are waited for: with many inputs more threads a row
+    // hide that (8 x 4096 x 4096 bf16: 99 us with one vector a thread, 102 with two, 113 with four;
+    // 4 x 4096 x 4096: 65, 62 and 72), with few the instructions count (1 x 16384 x 4096: 150, 131 and
+    // 112; 1 x 9000 x 1001: 41, 35 and 24).  Backward, one vector keeps both sums in registers, which pays
+    // for long rows of several ranks (3 x 4000 x 4096: 69 us, 80 with two, 111 with four; but 8 x 8000 x
+    // 1024: 82, 67 and 96; 1 x 16384 x 4096: 200, 158 and 282).
+    const size_t vectors = k.d.hidden * k.esz / 16;
     if (backward) {
         c.extraSums = 1;
         c.regs = 128;
+        c.vecs = segments >= 6 && vectors > 256 && !c.general ? 1 : 2;
+    } else {
+        c.vecs = segments <= (c.general ? 4 : 2) ? 4 : segments >= 7 && !c.general ? 1 : 2;
     }
     return c;
 }
@@ -91,8 +102,7 @@ vResult_t block_forward(const vBlockNormDesc_t* desc, const void* const* send, c
     a.weightF32 = k.d.weightType == vFloat32;
     a.eps = k.d.eps;
     a.scale = desc->residualScale;
-    vc::NormCall call = block_call(k, v, b, false);
-    call.segments = v.nRanks + (residual ? 1 : 0);
+    const vc::NormCall call = block_call(k, v, b, false, v.nRanks + (residual ? 1 : 0));
     a.shape = vc::norm_shape(call);
     debug_block(v, "AllReduceBlockNorm", k, a.shape);
     return comm_launch(c, "allreduce block norm", [&]() { return vc::launch_block_norm(a, k.d.datatype, stream); });
@@ -163,8 +173,7 @@ vResult_t block_backward(const vBlockNormDesc_t* desc, const void* const* send, 
     a.outSame = b.outSame;
     a.weightF32 = k.d.weightType == vFloat32;
     a.scale = desc->residualScale;
-    vc::NormCall call = block_call(k, v, b, true);
-    call.segments = v.nRanks + 2 + (gradStream ? 1 : 0);
+    const vc::NormCall call = block_call(k, v, b, true, v.nRanks + 2 + (gradStream ? 1 : 0));
     a.shape = vc::norm_shape(call);
     a.parts = vc::norm_backward_parts(a.rows, a.shape, v.smCount);
     if (!workspace || !at(workspace, 16) || workspaceBytes < (size_t)a.parts * 2 * k.d.hidden * sizeof(float))
@@ -202,8 +211,7 @@ vResult_t vBlockNormBackwardWorkspace(const vBlockNormDesc_t* desc, vcomm_t comm
         Buffers b;
         b.aligned = (i & 1) != 0;
         if (b.aligned && k.d.hidden % (16 / k.esz) != 0) continue;
-        vc::NormCall call = block_call(k, v, b, true);
-        call.segments = v.nRanks + 2 + (i >> 1);
+        const vc::NormCall call = block_call(k, v, b, true, v.nRanks + 2 + (i >> 1));
         const int parts = vc::norm_backward_parts(k.d.rows, vc::norm_shape(call), v.smCount);
         *bytes = std::max(*bytes, (size_t)parts * 2 * k.d.hidden * sizeof(float));
     }

@@ -48,14 +48,14 @@ __device__ __forceinline__ int find_slots(const int* ids, int total, int e, int 
 }
 
 // A lane's elements of one step along a row: ALIGNED a 16-byte vector from j on, else j + 32 i.
-template <int DT, bool ALIGNED> constexpr int kElems = ALIGNED ? 16 / DTypeOf<DT>::size : 4;
+template <int DT, bool ALIGNED> constexpr int kElems = ALIGNED ? 16 / DTypeOf<DT>::size : 8;
 template <int DT, bool ALIGNED>
 __device__ __forceinline__ void load_part(const void* row, int j, int width, float (&f)[kElems<DT, ALIGNED>]) {
     if constexpr (ALIGNED) {
         widen_vec<DT>(*reinterpret_cast<const uint4*>((const char*)row + (size_t)j * DTypeOf<DT>::size), f);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int i = 0; i < 8; i++) {
             const int e = j + 32 * i;
             f[i] = 0.0f;
             if (e >= width) continue;
@@ -74,7 +74,7 @@ __device__ __forceinline__ void dots(const char* const (&w)[R], const void* cons
     for (int r = 0; r < R; r++)
 #pragma unroll
         for (int g = 0; g < G; g++) acc[r][g] = 0.0f;
-    for (int j = ALIGNED ? lane * E : lane; j < width; j += ALIGNED ? 32 * E : 128) {
+    for (int j = ALIGNED ? lane * E : lane; j < width; j += 32 * E) {
         float f[R][E];
 #pragma unroll
         for (int r = 0; r < R; r++) load_part<WT, ALIGNED>(w[r], j, width, f[r]);
@@ -116,9 +116,9 @@ __global__ void __launch_bounds__(kThreads) k_moe_up(const __grid_constant__ Exp
     const int e = (int)blockIdx.y, total = a.rows * a.topK;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x == 0 && e == 0)
-        for (int i = threadIdx.x; i < (a.hidden + kMoeTile - 1) / kMoeTile; i += kThreads) a.done[i] = 0;
+        for (int i = threadIdx.x; i < (a.hidden + a.tileDown - 1) / a.tileDown; i += kThreads) a.done[i] = 0;
     const char* base = (const char*)a.up[e / a.share] + (size_t)(e % a.share) * 2 * a.ffn * a.hidden * ESZ;
-    const int f0 = (int)blockIdx.x * kMoeTile, f1 = min(a.ffn, f0 + kMoeTile);
+    const int f0 = (int)blockIdx.x * a.tileUp, f1 = min(a.ffn, f0 + a.tileUp);
     for (int from = 0, n; from < total;) {
         from = find_slots(a.ids, total, e, from, list, &n);
         for (int g0 = 0; g0 < n; g0 += kGroup) {
@@ -142,23 +142,35 @@ __global__ void __launch_bounds__(kThreads) k_moe_up(const __grid_constant__ Exp
     }
 }
 
-// Columns [h0, h1) of every rank's output, from all slots' y.
+// Columns [h0, h1) of every rank's output, from all slots' y.  What up to eight slots need is loaded
+// together, whether it counts or not: the wait for memory is most of this.
 template <int DT>
 __device__ __forceinline__ void combine(const ExpertsArgs& a, int h0, int h1) {
-    constexpr int ESZ = DTypeOf<DT>::size;
+    constexpr int ESZ = DTypeOf<DT>::size, UN = 8;
     const int columns = h1 - h0;
     for (int i = threadIdx.x; i < a.rows * columns; i += kThreads) {
         const int t = i / columns, h = h0 + i % columns;
-        const int* ids = a.ids + (size_t)t * a.topK;
-        for (int r = 0; r < a.nRanks; r++) {
-            const int lo = r * a.share, hi = min(a.experts, lo + a.share);
+        for (int r0 = 0; r0 < a.nRanks; r0 = a.topK <= UN ? a.nRanks : r0 + 1) {
+            // all ranks from one set of loads, or (more slots) a rank at a time
             float s = 0.0f;
-            for (int k = 0; k < a.topK; k++) {
-                if (ids[k] < lo || ids[k] >= hi) continue;
-                const size_t slot = (size_t)t * a.topK + k;
-                s = fmaf(a.weights[slot], __ldcg(a.y + slot * a.hidden + h), s);
+            for (int k0 = 0; k0 < a.topK; k0 += UN) {
+                int rank[UN];
+                float w[UN], y[UN];
+#pragma unroll
+                for (int k = 0; k < UN; k++) {
+                    const size_t slot = (size_t)t * a.topK + min(k0 + k, a.topK - 1);
+                    const int e = a.ids[slot];
+                    w[k] = a.weights[slot];
+                    y[k] = __ldcg(a.y + slot * a.hidden + h);
+                    rank[k] = k0 + k < a.topK && e >= 0 && e < a.experts ? e / a.share : -1;
+                }
+                for (int r = r0; r < (a.topK <= UN ? a.nRanks : r0 + 1); r++) {
+                    if (k0 == 0) s = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < UN; k++) s = rank[k] == r ? fmaf(w[k], y[k], s) : s;
+                    if (k0 + UN >= a.topK) st_elem<ESZ>(a.recv[r], (size_t)t * a.recvStride + h, f32_to_elem<DT>(s));
+                }
             }
-            st_elem<ESZ>(a.recv[r], (size_t)t * a.recvStride + h, f32_to_elem<DT>(s));
         }
     }
 }
@@ -172,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_down(const __grid_constant__ E
     __shared__ int last;
     const int e = (int)blockIdx.y, total = a.rows * a.topK;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int h0 = (int)blockIdx.x * kMoeTile, h1 = min(a.hidden, h0 + kMoeTile);
+    const int h0 = (int)blockIdx.x * a.tileDown, h1 = min(a.hidden, h0 + a.tileDown);
     const char* base = (const char*)a.down[e / a.share] + (size_t)(e % a.share) * a.hidden * a.ffn * ESZ;
     int found = 0;
     for (int from = 0, n; from < total;) {
@@ -220,9 +232,9 @@ __global__ void __launch_bounds__(kThreads) k_moe_down(const __grid_constant__ E
 
 template <int DT, bool ALIGNED>
 cudaError_t experts_launch(const ExpertsArgs& a, cudaStream_t s) {
-    const auto run = [&](auto kernel, int columns) {
+    const auto run = [&](auto kernel, int columns, int tile) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)((columns + kMoeTile - 1) / kMoeTile), (unsigned)a.experts);
+        cfg.gridDim = dim3((unsigned)((columns + tile - 1) / tile), (unsigned)a.experts);
         cfg.blockDim = dim3(kThreads);
         cfg.stream = s;
         cudaLaunchAttribute attr[1];
@@ -232,8 +244,8 @@ cudaError_t experts_launch(const ExpertsArgs& a, cudaStream_t s) {
         cfg.numAttrs = pdl_enabled() ? 1 : 0;
         return cudaLaunchKernelEx(&cfg, kernel, a);
     };
-    const cudaError_t e = run(k_moe_up<DT, ALIGNED>, a.ffn);
-    return e != cudaSuccess ? e : run(k_moe_down<DT, ALIGNED>, a.hidden);
+    const cudaError_t e = run(k_moe_up<DT, ALIGNED>, a.ffn, a.tileUp);
+    return e != cudaSuccess ? e : run(k_moe_down<DT, ALIGNED>, a.hidden, a.tileDown);
 }
 
 }  // namespace

@@ -192,6 +192,13 @@ vResult_t experts(const vMoeDesc_t* desc, const void* x, const int* ids, const f
                          a.rows, a.hidden, a.ffn, a.experts, a.topK, a.nRanks, t.tokens, t.splitUp, t.splitDown, t.gridUp, t.gridDown);
         return vc::comm_launch_tracked(c, "moe experts", stream, [&]() { return vc::launch_moe_tiles(a, t, m.d.datatype, stream); });
     }
+    // A warp one row of the weights (two on the way down), and more where there are CTAs enough: each looks
+    // through the router's list first (13 tokens on 10 experts of 1001 x 333: 54 us with four a warp).
+    const size_t groups = std::min<size_t>(a.experts, m.slots), enough = 24 * (size_t)v.smCount;
+    a.tileUp = vc::kMoeTile;
+    while (a.tileUp < 32 && groups * a.ffn / a.tileUp > enough) a.tileUp *= 2;
+    a.tileDown = 2 * vc::kMoeTile;
+    while (a.tileDown < 32 && groups * a.hidden / a.tileDown > enough) a.tileDown *= 2;
     if (v.debug)
         std::fprintf(stderr, "vcomm INFO MoeExperts rows=%d hidden=%d ffn=%d experts=%d topK=%d N=%d aligned=%d\n", a.rows,
                      a.hidden, a.ffn, a.experts, a.topK, a.nRanks, a.aligned);

@@ -45,6 +45,7 @@ struct ExpertsArgs {
     int nRanks;
     int share;                       // experts of a rank
     int aligned;                     // every row of x and of the weights starts on 16 bytes and ends with a vector
+    int tileUp, tileDown;            // output columns of a CTA: 8 to 32, and 16 or 32
     int recvAligned;                 // every row of the outputs starts on 8 bytes
     int split;                       // tensor cores: CTAs of a cluster that share a tile's columns
     int stages;                      // the same: stages of a CTA
@@ -52,7 +53,7 @@ struct ExpertsArgs {
     Status* status;                  // device copy
     volatile Status* statusHost;     // pinned mirror
 };
-constexpr int kMoeTile = 32;         // output columns of a CTA in both launches
+constexpr int kMoeTile = 8;          // output columns of a CTA, at least
 cudaError_t launch_moe_experts(const ExpertsArgs& a, vDataType_t dt, cudaStream_t s);
 
 // The same on the tensor cores.

@@ -68,7 +68,8 @@ NormShape norm_shape(const NormCall& c) {
             // a cluster's CTAs are whole teams of several warps
             if (team > kStageMaxThreads || (s.cluster > 1 && team <= 32)) continue;
             const bool four = !few && (!c.backward || team == 32);
-            const double weight = vecs == 4 ? (four ? 1.0 : 0.8) : vecs == 2 ? 0.92 : 0.8;
+            const double weight = c.vecs ? (vecs == c.vecs ? 1.0 : vecs == 2 ? 0.9 : 0.8)
+                                  : vecs == 4 ? (four ? 1.0 : 0.8) : vecs == 2 ? 0.92 : 0.8;
             const double use = weight * part / ((double)team * vecs);
             if (use > best) {
                 best = use;

@@ -79,6 +79,7 @@ struct NormCall {
     bool groups;                     // 8-bit output with a scale per 128 elements
     int extraSums;                   // backward: sums down the columns besides the weight's gradient
     int extraRowBuffers;             // GENERAL: row buffers of a team besides those above
+    int vecs;                        // staged: vectors a thread that suit it best; 0: as the RMS norm's
     int regs;                        // registers of a thread where they are not the RMS norm's; 0: they are
 };
 NormShape norm_shape(const NormCall& c);
