@@ -14,7 +14,8 @@
 // sixteen and sixteen in turn, so that both sums of an element lie in one warp.  silu(g) u goes into the
 // workspace as two values of the weights' type, the second what the first leaves out, 2^-18 of the value
 // off (bf16), for which the way down makes two products of every tile: in 16 bits alone the result would
-// be as far off again as its own rounding.
+// be as far off again as its own rounding.  Beyond fp16's largest value the second is up to as large as the
+// first, 2^-12 of the value off, and beyond twice that infinite.
 // The way down: every slot's output goes into the workspace in fp32; for few tokens the last warp of a
 // tile of columns adds them up, for more a third launch.
 #include "moe.h"
@@ -32,6 +33,7 @@ constexpr int kProducers = 32 * kProducerWarps;
 constexpr int kM = 128;              // rows of a tile
 constexpr int kK = 128;              // columns of a stage: two swizzled halves of 64
 constexpr int kHalfA = kM * 128;     // bytes of a half of A
+template <int DT> constexpr float kLargest = DT == kF16 ? 65504.0f : 0x1.FEp127f;
 static_assert(kProducers == 16 * 16, "a producer: one 16-byte chunk of a stage's row, sixteen rows apart");
 
 struct Shared {
@@ -339,6 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
     } else if (warp == kIssuer) {
         // ---- the issuer
         if (lane == 0) {
+            // (no copy of B is under way before that: the limited waits below begin with it)
+            if (!UP) asm volatile("griddepcontrol.wait;" ::: "memory");
             int at = 0, unit = 0;
             uint32_t round = 0;
             bool ok = true;
@@ -410,11 +414,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
                         const int column = j0 + j + (lane >> 4);
                         if (column >= g.count || f >= a.ffn) continue;
                         const float x = gate / (1.0f + expf(-gate)) * linear;
-                        const uint16_t hi = narrow16<DT>(x);
-                        const float rest = x - widen16<DT>(hi);
+                        // (infinities and NaNs go into the second value)
+                        const uint16_t hi = narrow16<DT>(fminf(fmaxf(x, -kLargest<DT>), kLargest<DT>));
                         uint16_t* to = act + (size_t)l.slots[g.first + column] * 2 * a.ffn + f;
                         to[0] = hi;
-                        to[a.ffn] = narrow16<DT>(isfinite(x) ? rest : 0.0f);
+                        to[a.ffn] = narrow16<DT>(x - widen16<DT>(hi));
                     }
                 } else {
                     const int h = m * kM + row;

@@ -216,6 +216,34 @@ def test_tokens_that_are_not_finite_stay_alone(comms, hidden, ffn):
             assert torch.isnan(got[t].float()).all() if touched else torch.isfinite(got[t].float()).all()
 
 
+@pytest.mark.parametrize("ffn", [64, 63])
+@pytest.mark.parametrize("dtype,scale", [(F16, 300.0), (BF16, 1e18)])
+def test_inner_values_near_the_end_of_the_type(comms, ffn, dtype, scale):
+    # silu(g) u of 50,000 to 130,000 (fp16: largest value 65504, twice that at most), or to 1.4e36
+    gen = torch.Generator().manual_seed(91)
+    rows, hidden, experts = 5, 64, 2
+    x = torch.full((rows, hidden), 16.0).to(dtype)
+    one = scale * (0.75 + 0.43 * torch.rand(experts, 2 * ffn, 1, generator=gen)) / (16 * hidden)
+    up = one.expand(-1, -1, hidden).to(dtype)
+    down = (torch.randn(experts, hidden, ffn, generator=gen) * 2.0 ** -12 / scale).to(dtype)
+    ids, weights = torch.tensor([[0], [1], [0], [1], [1]], dtype=torch.int32), torch.ones(rows, 1)
+    desc = V.vMoeDesc(rows, hidden, ffn, experts, 1, dtype)
+    out = torch.empty(rows, hidden, dtype=dtype, device=DEV)
+    ws = torch.empty(V.vMoeExpertsWorkspace(desc, comms(1)), dtype=torch.uint8, device=DEV)
+    V.vMoeExperts(desc, place(x), place(ids), place(weights), [place(up)], [place(down)], [out], ws, comms(1))
+    want, slack = M.layer(x, ids.long(), weights, [up], [down])
+    # the second of two fp16 values is below 65504, so off by half a step of 2^-11 of that at most: 16, and
+    # the values are above 2^16
+    wide = (x.double()[:, None] @ up[ids[:, 0].long()].double().transpose(1, 2))[:, 0]
+    a = wide[:, :ffn] / (1 + (-wide[:, :ffn]).exp()) * wide[:, ffn:]
+    more = 2.0 ** -12 * (a[:, None] * down[ids[:, 0].long()].double().abs()).sum(2) if dtype == F16 else 0
+    R.assert_close(out, want[0], slack[0] + more, dtype, "output")
+    # beyond: with fp16 infinite (aligned rows), and what comes of it is not finite
+    if dtype == F16 and ffn == 64:
+        V.vMoeExperts(desc, place(x * 2), place(ids), place(weights), [place(up)], [place(down.abs())], [out], ws, comms(1))
+        assert not out.isfinite().any()
+
+
 def test_the_same_bits_again(comms):
     for hidden, ffn in ((1024, 256), (1001, 255)):
         x, ids, weights, up, down = make(4, 40, hidden, ffn, 12, 4, BF16, 15)
