@@ -11,14 +11,15 @@
 // Where that leaves open which of two scores is the larger, and one of the two is chosen, both logits
 // are computed anew with every product and sum as a value and its error, some 2^-45 of the magnitudes
 // off.  No fp64: its rate here is a 64th of fp32's (256 x 4096 of 128 experts with the choice in fp64:
-// 164 us, 32 as it is).
+// 164 us, 30 as it is).
 //
-// A cluster of CTAs takes a few tokens, each CTA a share of the experts.  Up to four tokens: a warp
-// takes an expert, its lanes stride along the row (1 x 4096 of 64: 6 us, most of it launch and latency).
-// More: eight tokens, a warp four of them by four experts, so that what it loads serves four times; tiles
-// staged in shared memory and read by threads that share rows took four times as long, as every 16-byte
-// load of a quarter warp is a pass through shared memory, shared or not.  The logits go to the CTA that
-// picks for their token.
+// A cluster of CTAs takes a few tokens, each CTA a share of the experts.  Few tokens: up to four a
+// cluster, a warp takes an expert, its lanes stride along the row (1 x 4096 of 64: 6 us, most of it launch and
+// latency).  More: eight tokens, a warp four of them by four experts, so that what it loads serves four
+// times (256 x 4096 of 128, fp32 router: 30 us, of which the loop over the columns takes 15, bound by its
+// instructions, near 390 a warp and 256 columns, and logits computed anew 7; tiles staged in shared
+// memory and read by threads that share rows 67, the same warp's tiles from stages copied ahead 37).  The
+// logits go to the CTA that picks for their token.
 #include "moe.h"
 #include "norm_stage.cuh"
 
@@ -286,7 +287,7 @@ __device__ __forceinline__ void pick(const RouteArgs& a, const Picks& all, Redo&
     }
 }
 
-// ---- up to four tokens: a warp an expert, lanes along its row -----------------------------------
+// ---- up to four tokens a cluster: a warp an expert, lanes along its row --------------------------
 
 template <int DT, int WT, int TOKENS, bool ALIGNED>
 __global__ void __launch_bounds__(kRouteThreads) k_moe_route_few(const __grid_constant__ RouteArgs a) {
@@ -299,6 +300,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route_few(const __grid_co
     const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
     if (a.cluster > 1) cluster_arrive();
     bool started = a.cluster == 1;
+    const int row0 = (int)(blockIdx.x / (unsigned)a.cluster) * TOKENS;
     const int last = min(a.experts, (rank + 1) * a.share);
     for (int e = rank * a.share + warp; e < last; e += warps) {
         const char* w = (const char*)a.router + (size_t)e * a.hidden * DTypeOf<WT>::size;
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route_few(const __grid_co
             }
 #pragma unroll
             for (int t = 0; t < TOKENS; t++) {
-                const int row = min(t, a.rows - 1);
+                const int row = min(row0 + t, a.rows - 1);
                 const char* x = (const char*)a.x + (size_t)row * a.rowStride * DTypeOf<DT>::size;
                 float v[STEPS][E];
 #pragma unroll
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route_few(const __grid_co
     } else {
         __syncthreads();
     }
-    pick<DT, WT, ALIGNED, kRouteThreads>(a, picks, redo, a.rows, [](int at) { return at; });
+    pick<DT, WT, ALIGNED, kRouteThreads>(a, picks, redo, min(TOKENS, a.rows - row0), [&](int at) { return row0 + at; });
 }
 
 // ---- more: tiles of eight tokens and thirty-two experts -----------------------------------------
@@ -381,29 +383,15 @@ __global__ void __launch_bounds__(kRouteTileThreads, 1) k_moe_route(const __grid
     const char* x[kSide];
 #pragma unroll
     for (int t = 0; t < kSide; t++) x[t] = (const char*)a.x + (size_t)min(row0 + t0 + t, a.rows - 1) * a.rowStride * DTypeOf<DT>::size;
-    // the tokens' norms, a warp one
-    if (warp < kRouteTile) {
-        const char* row = (const char*)a.x + (size_t)min(row0 + warp, a.rows - 1) * a.rowStride * DTypeOf<DT>::size;
-        float square = 0.0f;
-#pragma unroll 4
-        for (int j = lane * 8; j < a.hidden; j += 256) {
-            float f[8];
-            load_row<DT, 8, ALIGNED>(row, j, min(8, a.hidden - j), f);
-#pragma unroll
-            for (int i = 0; i < 8; i++) square = fmaf(f[i], f[i], square);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) square += __shfl_xor_sync(~0u, square, o);
-        if (lane == 0) tokenNorm[warp] = sqrtf(square);
-    }
-    __syncthreads();
     bool started = a.cluster == 1;
-    for (int e0 = rank * a.share + warp / (kRouteTile / kSide) * kSide; e0 < last; e0 += kPass) {
+    const int group = warp / (kRouteTile / kSide);
+    for (int pass = rank * a.share; pass < last; pass += kPass) {
+        const int e0 = pass + group * kSide;
         const char* w[kSide];
 #pragma unroll
         for (int e = 0; e < kSide; e++) w[e] = (const char*)a.router + (size_t)min(e0 + e, last - 1) * a.hidden * DTypeOf<WT>::size;
         float s[kSide][kSide] = {}, c[kSide][kSide] = {};
-        float2 p[kSide][kSide] = {}, square[kSide] = {};
+        float2 p[kSide][kSide] = {}, square[kSide] = {}, token = {};
         int folded = 0;
         for (int j = lane * 8; j < a.hidden; j += 256) {
             const int left = min(8, a.hidden - j);
@@ -411,7 +399,15 @@ __global__ void __launch_bounds__(kRouteTileThreads, 1) k_moe_route(const __grid
 #pragma unroll
             for (int e = 0; e < kSide; e++) load_row<WT, 8, ALIGNED>(w[e], j, left, f[e]);
 #pragma unroll
-            for (int t = 0; t < kSide; t++) load_row<DT, 8, ALIGNED>(x[t], j, left, v[t]);
+            for (int t = 0; t < kSide; t++) {
+                load_row<DT, 8, ALIGNED>(x[t], j, left, v[t]);
+                if (group != t) continue;              // the token's norm, by one warp
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const float2 two = make_float2(v[t][i], v[t][i + 1]);
+                    token = fma2(two, two, token);
+                }
+            }
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
 #pragma unroll
@@ -464,6 +460,11 @@ __global__ void __launch_bounds__(kRouteTileThreads, 1) k_moe_route(const __grid
             for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(~0u, q, o);
             if ((lane & 3) == e) norm = sqrtf(q);
         }
+        float q = token.x + token.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(~0u, q, o);
+        if (pass == rank * a.share && group < kSide && lane == 0) tokenNorm[t0 + group] = sqrtf(q);
+        __syncthreads();
         if (!started) {                                // every CTA of the cluster has
             cluster_wait();
             started = true;
@@ -501,13 +502,13 @@ cudaError_t route_start(K kernel, const RouteArgs& a, int threads, int groups, s
 }
 template <int DT, int WT, bool ALIGNED>
 cudaError_t route_launch(const RouteArgs& a, cudaStream_t s) {
-    if (a.rows > kRouteFew) {
+    if (!a.few) {
         return route_start(k_moe_route<DT, WT, ALIGNED>, a, kRouteTileThreads, (a.rows + kRouteTile - 1) / kRouteTile,
                            pick_bytes((kRouteTile + a.cluster - 1) / a.cluster, a.experts), s);
     }
     if (a.rows == 1) return route_start(k_moe_route_few<DT, WT, 1, ALIGNED>, a, kRouteThreads, 1, pick_bytes(1, a.experts), s);
     if (a.rows == 2) return route_start(k_moe_route_few<DT, WT, 2, ALIGNED>, a, kRouteThreads, 1, pick_bytes(2, a.experts), s);
-    return route_start(k_moe_route_few<DT, WT, 4, ALIGNED>, a, kRouteThreads, 1, pick_bytes(4, a.experts), s);
+    return route_start(k_moe_route_few<DT, WT, 4, ALIGNED>, a, kRouteThreads, (a.rows + 3) / 4, pick_bytes(4, a.experts), s);
 }
 template <int DT, int WT>
 cudaError_t route_launch_a(const RouteArgs& a, cudaStream_t s) {

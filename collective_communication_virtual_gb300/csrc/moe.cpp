@@ -111,11 +111,22 @@ vResult_t route(const vMoeDesc_t* desc, const void* x, const void* router, const
     a.hidden = (int)m.d.hidden;
     a.experts = m.d.experts;
     a.topK = m.d.topK;
-    // an expert for every warp, or a pass of experts for every CTA, as far as a cluster goes
-    const bool few = a.rows <= vc::kRouteFew;
-    const int each = few ? vc::kRouteThreads / 32 : vc::kRouteTileThreads / 16;
-    a.cluster = 1;
-    while (a.cluster < (few ? vc::kRouteCluster : vc::kRouteTileCluster) && a.cluster * each < a.experts) a.cluster *= 2;
+    // An expert for every warp, or a pass of experts for every CTA, as far as a cluster goes.  A warp an
+    // expert for up to four tokens, and for more while there is an SM for every CTA and no warp has more than two
+    // experts (bf16, us against tiles: 32 x 4096 of 128 experts 18 against 22.5, 64 x 2048 of 64 10 against 14, 5 x
+    // 4096 of 16 9 against 19; but 64 x 4096 of 256 54 against 28, 128 x 8192 fp32 of 128 89 against 55).  Tiles:
+    // larger clusters only where that leaves no SM twice as much to do (64 x 4096 of 256: 28 against 44).
+    const auto cluster = [&](int each, int most) {
+        int c = 1;
+        while (c < most && c * each < a.experts) c *= 2;
+        return c;
+    };
+    const int warps = vc::kRouteThreads / 32, fours = (a.rows + 3) / 4, tiles = (a.rows + vc::kRouteTile - 1) / vc::kRouteTile;
+    a.cluster = cluster(warps, vc::kRouteCluster);
+    a.few = a.rows <= vc::kRouteFew || (a.experts <= 2 * a.cluster * warps && fours * a.cluster <= v.smCount);
+    if (!a.few)
+        a.cluster = cluster(vc::kRouteTileThreads / 16,
+                            vc::kRouteCluster * tiles <= v.smCount / 2 ? vc::kRouteCluster : vc::kRouteTileCluster);
     a.share = (a.experts + a.cluster - 1) / a.cluster;
     a.routerF32 = m.d.routerType == vFloat32;
     a.normalize = m.d.normalize != 0;

@@ -6,10 +6,10 @@
 
 namespace vc {
 
-constexpr int kRouteFew = 4;         // tokens up to which a warp takes an expert's whole row
-constexpr int kRouteTile = 8;        // tokens of a cluster beyond that
-constexpr int kRouteCluster = 8;     // CTAs of a cluster, at most, for a few tokens,
-constexpr int kRouteTileCluster = 4; // and beyond them: larger ones do not fill the SMs at one CTA on each
+constexpr int kRouteFew = 4;         // tokens of a cluster where a warp takes an expert's whole row
+constexpr int kRouteTile = 8;        // where it takes a tile
+constexpr int kRouteCluster = 8;     // CTAs of a cluster, at most,
+constexpr int kRouteTileCluster = 4; // and for many tiles: larger ones do not fill the SMs at one CTA on each
 constexpr int kRouteThreads = 256;
 constexpr int kRouteTileThreads = 512;
 constexpr int kRouteMaxSmem = 180 * 1024;
@@ -22,6 +22,7 @@ struct RouteArgs {
     float* weights;
     size_t rowStride;
     int rows, hidden, experts, topK;
+    int few;                         // a warp takes an expert's whole row, for up to four tokens, else a tile
     int cluster;                     // CTAs that share the experts
     int share;                       // experts of a CTA
     int routerF32;

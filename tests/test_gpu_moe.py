@@ -79,6 +79,13 @@ def test_route(comms, rows, hidden, experts, k, dtype, wtype):
     run_route(comms(2), rows, hidden, experts, k, dtype, wtype, seed=hidden, normalize=False, bias=True)
 
 
+@pytest.mark.parametrize("dtype,wtype", [(BF16, BF16), (F32, F32)])
+@pytest.mark.parametrize("rows,hidden,experts,k", [(5, 264, 128, 8), (7, 130, 100, 3), (64, 96, 60, 4), (77, 96, 60, 4), (9, 512, 129, 4),
+                                                   (64, 256, 256, 8), (80, 250, 200, 5), (700, 96, 20, 3), (1024, 72, 33, 2)])
+def test_route_of_a_warp_an_expert_and_of_tiles(comms, rows, hidden, experts, k, dtype, wtype):
+    run_route(comms(1), rows, hidden, experts, k, dtype, wtype, seed=rows + hidden, bias=rows % 2 == 1)
+
+
 @pytest.mark.parametrize("kw", [dict(pad=3), dict(offset=1), dict(pad=8), dict(pad=5, offset=3)])
 @pytest.mark.parametrize("hidden", [64, 250])
 def test_route_strides_and_offsets(comms, hidden, kw):
