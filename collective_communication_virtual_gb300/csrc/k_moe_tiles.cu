@@ -46,14 +46,14 @@ struct Shared {
 };
 // In dynamic shared memory, as long as the call needs them.
 struct Lists {
-    int* count;                      // slots of an expert, then where the next one goes
+    int* first;                      // of an expert's slots
     uint16_t* slots;                 // by expert
     MoeGroup* groups;
 };
 
-// The slots sorted by expert, and the groups.  All threads.
+// The slots sorted by expert, and the groups.  All threads; `scratch` holds two bytes a warp and expert.
 template <int NT>
-__device__ __forceinline__ void make_lists(Shared& sh, const Lists& l, const ExpertsArgs& a) {
+__device__ __forceinline__ void make_lists(Shared& sh, const Lists& l, uint16_t* scratch, const ExpertsArgs& a) {
     const int total = a.rows * a.topK, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (total <= 32 && NT >= 16) {   // by one warp, experts in the order of their first slots
         if (warp == 0) {
@@ -78,23 +78,38 @@ __device__ __forceinline__ void make_lists(Shared& sh, const Lists& l, const Exp
         __syncthreads();
         return;
     }
-    for (int e = threadIdx.x; e < a.experts; e += kThreads) l.count[e] = 0;
+    // A stable sort by expert, every warp a run of the slots: how many of each expert it has, where they go,
+    // and there they go, so that all CTAs agree on which slots a group has.
+    constexpr int kWarps = kThreads / 32;
+    for (int i = threadIdx.x; i < (kWarps * a.experts + 1) / 2; i += kThreads) reinterpret_cast<uint32_t*>(scratch)[i] = 0u;
     __syncthreads();
-    for (int i = threadIdx.x; i < total; i += kThreads) {
-        const int e = a.ids[i];
-        if (e >= 0 && e < a.experts) atomicAdd(&l.count[e], 1);
+    uint16_t* const own = scratch + warp * a.experts;
+    const int each = (total + 32 * kWarps - 1) / (32 * kWarps) * 32, from = warp * each, to = min(total, from + each);
+    for (int i0 = from; i0 < to; i0 += 32) {
+        const int i = i0 + lane, e = i < to ? a.ids[i] : -1;
+        const bool counts = e >= 0 && e < a.experts;
+        const unsigned same = __match_any_sync(~0u, counts ? e : -1);
+        if (counts && lane == 31 - __clz((int)same)) own[e] += (uint16_t)__popc(same);
+        __syncwarp();
     }
     __syncthreads();
     // running sums of slots and of groups, three experts a thread
     constexpr int PER = (VCOMM_MAX_EXPERTS + kThreads - 1) / kThreads;
-    int slots = 0, groups = 0;
+    int n[PER], slots = 0, groups = 0;
+#pragma unroll
     for (int i = 0; i < PER; i++) {
         const int e = (int)threadIdx.x * PER + i;
+        n[i] = 0;
         if (e >= a.experts) break;
-        slots += l.count[e];
-        groups += (l.count[e] + NT - 1) / NT;
+        for (int w = 0; w < kWarps; w++) {             // what a warp has, then what the warps before have
+            const int m = scratch[w * a.experts + e];
+            scratch[w * a.experts + e] = (uint16_t)n[i];
+            n[i] += m;
+        }
+        slots += n[i];
+        groups += (n[i] + NT - 1) / NT;
     }
-    int run = slots | groups << 16;                    // both below 2^15
+    int run = slots | groups << 16;                    // neither above 2^15
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(~0u, run, o);
@@ -103,35 +118,33 @@ __device__ __forceinline__ void make_lists(Shared& sh, const Lists& l, const Exp
     if (lane == 31) sh.warpSum[warp] = run;
     __syncthreads();
     int ahead = run - (slots | groups << 16), all = 0;
-    for (int w = 0; w < kThreads / 32; w++) {
+    for (int w = 0; w < kWarps; w++) {
         if (w < warp) ahead += sh.warpSum[w];
         all += sh.warpSum[w];
     }
     int slot = ahead & 0xFFFF, group = ahead >> 16;
+#pragma unroll
     for (int i = 0; i < PER; i++) {
         const int e = (int)threadIdx.x * PER + i;
         if (e >= a.experts) break;
-        const int n = l.count[e];
-        for (int j = 0; j < n; j += NT) l.groups[group++] = MoeGroup{(uint16_t)e, (uint16_t)(slot + j), (uint16_t)min(NT, n - j)};
-        l.count[e] = slot;
-        slot += n;
+        for (int j = 0; j < n[i]; j += NT)
+            l.groups[group++] = MoeGroup{(uint16_t)e, (uint16_t)(slot + j), (uint16_t)min(NT, n[i] - j)};
+        l.first[e] = slot;
+        slot += n[i];
     }
     if (threadIdx.x == 0) sh.nGroups = all >> 16;
     __syncthreads();
-    // in order, so that all CTAs agree on which slots a group of an expert's has
-    if (warp == 0) {
-        for (int i0 = 0; i0 < total; i0 += 32) {
-            const int i = i0 + lane, e = i < total ? a.ids[i] : -1;
-            const bool counts = e >= 0 && e < a.experts;
-            const unsigned same = __match_any_sync(~0u, counts ? e : -1);
-            const int at = counts ? l.count[e] : 0;
-            __syncwarp();
-            if (counts) {
-                l.slots[at + __popc(same & ((1u << lane) - 1))] = (uint16_t)i;
-                if (lane == 31 - __clz((int)same)) l.count[e] = at + __popc(same);
-            }
-            __syncwarp();
+    for (int i0 = from; i0 < to; i0 += 32) {
+        const int i = i0 + lane, e = i < to ? a.ids[i] : -1;
+        const bool counts = e >= 0 && e < a.experts;
+        const unsigned same = __match_any_sync(~0u, counts ? e : -1);
+        const int at = counts ? own[e] : 0;
+        __syncwarp();
+        if (counts) {
+            l.slots[l.first[e] + at + __popc(same & ((1u << lane) - 1))] = (uint16_t)i;
+            if (lane == 31 - __clz((int)same)) own[e] = (uint16_t)(at + __popc(same));
         }
+        __syncwarp();
     }
     __syncthreads();
 }
@@ -215,8 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
     const int nStages = a.stages;
     float* const parts = reinterpret_cast<float*>(raw + (stages - smem_at(raw)) + nStages * kStage);   // [split - 1][NT][128]
     Lists l;
-    l.count = reinterpret_cast<int*>(parts + (split - 1) * NT * kM);
-    l.groups = reinterpret_cast<MoeGroup*>(l.count + a.experts);
+    l.first = reinterpret_cast<int*>(parts + (split - 1) * NT * kM);
+    l.groups = reinterpret_cast<MoeGroup*>(l.first + a.experts);
     l.slots = reinterpret_cast<uint16_t*>(l.groups + moe_groups(a.experts, a.rows * a.topK, NT));
     // The way up waits for what the calls before wrote, ids and tokens among it, before it lets the way
     // down start; so that one may read ids and weights at once, and what the way up writes after its wait.
@@ -243,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kIssuer) tmem_alloc(&sh.tmem, NT <= 16 ? 32 : 2 * NT);
-    make_lists<NT>(sh, l, a);
+    make_lists<NT>(sh, l, reinterpret_cast<uint16_t*>(raw + (stages - smem_at(raw))), a);    // (no stage is in use yet)
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();

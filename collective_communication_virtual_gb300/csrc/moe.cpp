@@ -196,7 +196,7 @@ vResult_t experts(const vMoeDesc_t* desc, const void* x, const int* ids, const f
     a.combineHere = 1;
     a.status = v.status;
     a.statusHost = v.statusHost;
-    if (a.aligned && m.esz == 2 && m.slots <= (size_t)vc::kMoeTileSlots) {
+    if (a.aligned && m.esz == 2) {
         const vc::MoeTiles t = moe_tiles(a, v.smCount);
         if (v.debug)
             std::fprintf(stderr, "vcomm INFO MoeExperts rows=%d hidden=%d ffn=%d experts=%d topK=%d N=%d tokens=%d split=%d,%d grid=%d,%d\n",

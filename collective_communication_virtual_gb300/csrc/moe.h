@@ -58,7 +58,6 @@ constexpr int kMoeTile = 8;          // output columns of a CTA, at least
 cudaError_t launch_moe_experts(const ExpertsArgs& a, vDataType_t dt, cudaStream_t s);
 
 // The same on the tensor cores.
-constexpr int kMoeTileSlots = 4096;  // rows * topK, at most
 constexpr int kMoeMaxStages = 8;
 constexpr int kMoeMaxSmem = 225 * 1024;
 struct MoeGroup {                    // tokens of one expert, as many as a tile takes

@@ -223,6 +223,12 @@ def test_tokens_that_are_not_finite_stay_alone(comms, hidden, ffn):
             assert torch.isnan(got[t].float()).all() if touched else torch.isfinite(got[t].float()).all()
 
 
+@pytest.mark.parametrize("ranks,rows,hidden,ffn,experts,k", [(2, 1024, 64, 64, 16, 8), (1, 1024, 72, 40, 64, 32), (3, 700, 64, 32, 1000, 20),
+                                                             (1, 1001, 40, 24, 32, 32), (2, 500, 64, 64, 1024, 1)])
+def test_many_slots(comms, ranks, rows, hidden, ffn, experts, k):
+    run_experts(comms(ranks), *make(ranks, rows, hidden, ffn, experts, k, BF16, seed=rows + k))
+
+
 @pytest.mark.parametrize("ffn", [64, 63])
 @pytest.mark.parametrize("dtype,scale", [(F16, 300.0), (BF16, 1e18)])
 def test_inner_values_near_the_end_of_the_type(comms, ffn, dtype, scale):
