@@ -1,5 +1,5 @@
-// k_moe_experts.cu -- the experts' layer of a mixture of experts for a few tokens, the experts split
-// over the ranks.
+// k_moe_experts.cu -- the experts' layer of a mixture of experts for a few tokens in fp32, the experts
+// split over the ranks.
 //
 //   g = Wgate_e x_t,  u = Wlinear_e x_t,  a = silu(g) u,  silu(g) = g / (1 + exp(-g))
 //   recv_r[t] = sum over the token's chosen experts e of rank r of weight_te Wdown_e a
@@ -48,27 +48,24 @@ __device__ __forceinline__ int find_slots(const int* ids, int total, int e, int 
 }
 
 // A lane's elements of one step along a row: ALIGNED a 16-byte vector from j on, else j + 32 i.
-template <int DT, bool ALIGNED> constexpr int kElems = ALIGNED ? 16 / DTypeOf<DT>::size : 8;
-template <int DT, bool ALIGNED>
-__device__ __forceinline__ void load_part(const void* row, int j, int width, float (&f)[kElems<DT, ALIGNED>]) {
+template <bool ALIGNED> constexpr int kElems = ALIGNED ? 4 : 8;
+template <bool ALIGNED>
+__device__ __forceinline__ void load_part(const float* row, int j, int width, float (&f)[kElems<ALIGNED>]) {
     if constexpr (ALIGNED) {
-        widen_vec<DT>(*reinterpret_cast<const uint4*>((const char*)row + (size_t)j * DTypeOf<DT>::size), f);
+        widen_vec<kF32>(*reinterpret_cast<const uint4*>(row + j), f);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             const int e = j + 32 * i;
-            f[i] = 0.0f;
-            if (e >= width) continue;
-            if (DT == kF32) f[i] = ((const float*)row)[e];
-            else f[i] = widen16<DT>(((const uint16_t*)row)[e]);
+            f[i] = e < width ? row[e] : 0.0f;
         }
     }
 }
 
 // Dot products of R rows of the weights with n <= G vectors; every lane ends with all of them.
-template <int WT, int XT, bool ALIGNED, int R, int G>
-__device__ __forceinline__ void dots(const char* const (&w)[R], const void* const (&x)[G], int n, int width, float (&acc)[R][G]) {
-    constexpr int E = kElems<WT, ALIGNED>;
+template <bool ALIGNED, int R, int G>
+__device__ __forceinline__ void dots(const float* const (&w)[R], const float* const (&x)[G], int n, int width, float (&acc)[R][G]) {
+    constexpr int E = kElems<ALIGNED>;
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int r = 0; r < R; r++)
@@ -77,23 +74,12 @@ __device__ __forceinline__ void dots(const char* const (&w)[R], const void* cons
     for (int j = ALIGNED ? lane * E : lane; j < width; j += 32 * E) {
         float f[R][E];
 #pragma unroll
-        for (int r = 0; r < R; r++) load_part<WT, ALIGNED>(w[r], j, width, f[r]);
+        for (int r = 0; r < R; r++) load_part<ALIGNED>(w[r], j, width, f[r]);
 #pragma unroll
         for (int g = 0; g < G; g++) {
             if (g >= n) break;
             float v[E];
-            if constexpr (ALIGNED && WT != kF32 && XT == kF32) {
-                float lo[4], hi[4];
-                load_part<kF32, true>(x[g], j, width, lo);
-                load_part<kF32, true>(x[g], j + 4, width, hi);
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    v[i] = lo[i];
-                    v[i + 4] = hi[i];
-                }
-            } else {
-                load_part<XT, ALIGNED>(x[g], j, width, v);
-            }
+            load_part<ALIGNED>(x[g], j, width, v);
 #pragma unroll
             for (int r = 0; r < R; r++)
 #pragma unroll
@@ -108,29 +94,28 @@ __device__ __forceinline__ void dots(const char* const (&w)[R], const void* cons
             for (int o = 16; o > 0; o >>= 1) acc[r][g] += __shfl_xor_sync(~0u, acc[r][g], o);
 }
 
-template <int DT, bool ALIGNED>
+template <bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_moe_up(const __grid_constant__ ExpertsArgs a) {
     pdl_begin();
-    constexpr int ESZ = DTypeOf<DT>::size;
     __shared__ int list[kList];
     const int e = (int)blockIdx.y, total = a.rows * a.topK;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x == 0 && e == 0)
         for (int i = threadIdx.x; i < (a.hidden + a.tileDown - 1) / a.tileDown; i += kThreads) a.done[i] = 0;
-    const char* base = (const char*)a.up[e / a.share] + (size_t)(e % a.share) * 2 * a.ffn * a.hidden * ESZ;
+    const float* base = (const float*)a.up[e / a.share] + (size_t)(e % a.share) * 2 * a.ffn * a.hidden;
     const int f0 = (int)blockIdx.x * a.tileUp, f1 = min(a.ffn, f0 + a.tileUp);
     for (int from = 0, n; from < total;) {
         from = find_slots(a.ids, total, e, from, list, &n);
         for (int g0 = 0; g0 < n; g0 += kGroup) {
             const int some = min(kGroup, n - g0);
-            const void* x[kGroup];
+            const float* x[kGroup];
 #pragma unroll
             for (int g = 0; g < kGroup; g++)
-                x[g] = (const char*)a.x + (size_t)(list[g0 + min(g, some - 1)] / a.topK) * a.rowStride * ESZ;
+                x[g] = (const float*)a.x + (size_t)(list[g0 + min(g, some - 1)] / a.topK) * a.rowStride;
             for (int f = f0 + warp; f < f1; f += kWarps) {
-                const char* const w[kRows] = {base + (size_t)f * a.hidden * ESZ, base + (size_t)(a.ffn + f) * a.hidden * ESZ};
+                const float* const w[kRows] = {base + (size_t)f * a.hidden, base + (size_t)(a.ffn + f) * a.hidden};
                 float acc[kRows][kGroup];
-                dots<DT, DT, ALIGNED>(w, x, some, a.hidden, acc);
+                dots<ALIGNED>(w, x, some, a.hidden, acc);
 #pragma unroll
                 for (int g = 0; g < kGroup; g++) {
                     if (lane != g || g >= some) continue;
@@ -144,9 +129,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_up(const __grid_constant__ Exp
 
 // Columns [h0, h1) of every rank's output, from all slots' y.  What up to eight slots need is loaded
 // together, whether it counts or not: the wait for memory is most of this.
-template <int DT>
 __device__ __forceinline__ void combine(const ExpertsArgs& a, int h0, int h1) {
-    constexpr int ESZ = DTypeOf<DT>::size, UN = 8;
+    constexpr int UN = 8;
     const int columns = h1 - h0;
     for (int i = threadIdx.x; i < a.rows * columns; i += kThreads) {
         const int t = i / columns, h = h0 + i % columns;
@@ -168,37 +152,36 @@ __device__ __forceinline__ void combine(const ExpertsArgs& a, int h0, int h1) {
                     if (k0 == 0) s = 0.0f;
 #pragma unroll
                     for (int k = 0; k < UN; k++) s = rank[k] == r ? fmaf(w[k], y[k], s) : s;
-                    if (k0 + UN >= a.topK) st_elem<ESZ>(a.recv[r], (size_t)t * a.recvStride + h, f32_to_elem<DT>(s));
+                    if (k0 + UN >= a.topK) ((float*)a.recv[r])[(size_t)t * a.recvStride + h] = s;
                 }
             }
         }
     }
 }
 
-template <int DT, bool ALIGNED>
+template <bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_moe_down(const __grid_constant__ ExpertsArgs a) {
     pdl_begin();
-    constexpr int ESZ = DTypeOf<DT>::size;
     __shared__ int list[kList];
     __shared__ unsigned seen[VCOMM_MAX_EXPERTS / 32];
     __shared__ int last;
     const int e = (int)blockIdx.y, total = a.rows * a.topK;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int h0 = (int)blockIdx.x * a.tileDown, h1 = min(a.hidden, h0 + a.tileDown);
-    const char* base = (const char*)a.down[e / a.share] + (size_t)(e % a.share) * a.hidden * a.ffn * ESZ;
+    const float* base = (const float*)a.down[e / a.share] + (size_t)(e % a.share) * a.hidden * a.ffn;
     int found = 0;
     for (int from = 0, n; from < total;) {
         from = find_slots(a.ids, total, e, from, list, &n);
         found += n;
         for (int g0 = 0; g0 < n; g0 += kGroup) {
             const int some = min(kGroup, n - g0);
-            const void* x[kGroup];
+            const float* x[kGroup];
 #pragma unroll
             for (int g = 0; g < kGroup; g++) x[g] = a.act + (size_t)list[g0 + min(g, some - 1)] * a.ffn;
             for (int h = h0 + kRows * warp; h < h1; h += kRows * kWarps) {
-                const char* const w[kRows] = {base + (size_t)h * a.ffn * ESZ, base + (size_t)min(h + 1, h1 - 1) * a.ffn * ESZ};
+                const float* const w[kRows] = {base + (size_t)h * a.ffn, base + (size_t)min(h + 1, h1 - 1) * a.ffn};
                 float acc[kRows][kGroup];
-                dots<DT, kF32, ALIGNED>(w, x, some, a.ffn, acc);
+                dots<ALIGNED>(w, x, some, a.ffn, acc);
 #pragma unroll
                 for (int g = 0; g < kGroup; g++) {
                     if (lane != g || g >= some) continue;
@@ -227,10 +210,10 @@ __global__ void __launch_bounds__(kThreads) k_moe_down(const __grid_constant__ E
     __syncthreads();
     if (!last) return;
     __threadfence();
-    combine<DT>(a, h0, h1);
+    combine(a, h0, h1);
 }
 
-template <int DT, bool ALIGNED>
+template <bool ALIGNED>
 cudaError_t experts_launch(const ExpertsArgs& a, cudaStream_t s) {
     const auto run = [&](auto kernel, int columns, int tile) {
         cudaLaunchConfig_t cfg = {};
@@ -244,19 +227,14 @@ cudaError_t experts_launch(const ExpertsArgs& a, cudaStream_t s) {
         cfg.numAttrs = pdl_enabled() ? 1 : 0;
         return cudaLaunchKernelEx(&cfg, kernel, a);
     };
-    const cudaError_t e = run(k_moe_up<DT, ALIGNED>, a.ffn, a.tileUp);
-    return e != cudaSuccess ? e : run(k_moe_down<DT, ALIGNED>, a.hidden, a.tileDown);
+    const cudaError_t e = run(k_moe_up<ALIGNED>, a.ffn, a.tileUp);
+    return e != cudaSuccess ? e : run(k_moe_down<ALIGNED>, a.hidden, a.tileDown);
 }
 
 }  // namespace
 
-cudaError_t launch_moe_experts(const ExpertsArgs& a, vDataType_t dt, cudaStream_t s) {
-    switch (dt) {
-    case vFloat32: return a.aligned ? experts_launch<kF32, true>(a, s) : experts_launch<kF32, false>(a, s);
-    case vFloat16: return a.aligned ? experts_launch<kF16, true>(a, s) : experts_launch<kF16, false>(a, s);
-    case vBFloat16: return a.aligned ? experts_launch<kBF16, true>(a, s) : experts_launch<kBF16, false>(a, s);
-    default: return cudaErrorInvalidValue;
-    }
+cudaError_t launch_moe_experts(const ExpertsArgs& a, cudaStream_t s) {
+    return a.aligned ? experts_launch<true>(a, s) : experts_launch<false>(a, s);
 }
 
 }  // namespace vc

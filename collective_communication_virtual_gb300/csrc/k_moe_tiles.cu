@@ -1,5 +1,4 @@
-// k_moe_tiles.cu -- the experts' layer for a few tokens on the tensor cores: 16-bit types, rows that
-// start on 16 bytes and end with a vector.
+// k_moe_tiles.cu -- the experts' layer for a few tokens on the tensor cores: 16-bit types.
 //
 // A tile of 128 rows of an expert's weights is the matrix A of the products, the tokens that chose the
 // expert (up to NT of them) are B, so the weights are read from memory once and a product has as few
@@ -8,7 +7,12 @@
 // where there are fewer tiles than SMs, walks over tiles of one (expert, tokens) group after another.
 // Eight warps copy the next stages asynchronously, 128 columns each, into the swizzled layout; one
 // thread issues the products; four warps take finished sums out of tensor memory, where two tiles' sums
-// have room.
+// have room.  Rows that start off 16 bytes come through registers, a stage ahead, as the aligned words that
+// hold them.
+//
+// Measured (bf16): 64 tokens on 8 of 128 experts of 4096 x 1536, 4.8 GB of weights, 785 us (6.1 TB/s; the way up
+// 499), with 4095 x 1535 1741 (2.7); 8 tokens there 341 us (5.7 TB/s), one token 69 (4.4); one token on 4 of
+// 64 experts of 2048 x 1024 25 us (2.0), a chain of latencies: ids, weights, sums, ids, weights, sums.
 //
 // The way up: the tile's rows are 64 of the gate and the 64 of the linear part that belong to them,
 // sixteen and sixteen in turn, so that both sums of an element lie in one warp.  silu(g) u goes into the
@@ -152,6 +156,28 @@ __device__ __forceinline__ void make_lists(Shared& sh, const Lists& l, uint16_t*
 __device__ __forceinline__ void copy_chunk(uint32_t to, const void* from, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
 }
+// Eight elements that start anywhere, `left` of them inside their row (the rest zeros): the aligned words that
+// hold some of them, and what they make.
+__device__ __forceinline__ void load_words(const uint16_t* from, int left, uint32_t (&r)[5]) {
+    const uintptr_t p = (uintptr_t)from;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(p & ~(uintptr_t)3);
+    const int ahead = (int)(p >> 1) & 1;               // elements of the first word before them
+#pragma unroll
+    for (int i = 0; i < 5; i++) {
+        r[i] = 0u;
+        if (2 * i - ahead < min(left, 8)) r[i] = w[i];
+    }
+}
+__device__ __forceinline__ uint4 from_words(const uint16_t* from, int left, const uint32_t (&r)[5]) {
+    const uint32_t shift = ((uint32_t)(uintptr_t)from & 2u) * 8u;
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        v[i] = __funnelshift_r(r[i], r[i + 1], shift);
+        if (2 * i + 1 >= left) v[i] = 2 * i >= left ? 0u : v[i] & 0xFFFFu;
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
 
 // Columns [h, h + 4) of every rank's output for token t, from its slots' y.  What up to eight slots need is
 // loaded together, whether it counts or not: the wait for memory is most of this.
@@ -161,19 +187,20 @@ __device__ __forceinline__ void combine(const ExpertsArgs& a, int t, int h) {
     static_assert(ESZ == 2, "the tensor cores' types");
     const auto put = [&](int r, const float (&s)[4]) {
         uint16_t* to = (uint16_t*)a.recv[r] + (size_t)t * a.recvStride + h;
-        if (a.recvAligned) {
+        if (a.recvAligned && h + 4 <= a.hidden) {
             *reinterpret_cast<uint2*>(to) = make_uint2(narrow16<DT>(s[0]) | (uint32_t)narrow16<DT>(s[1]) << 16,
                                                        narrow16<DT>(s[2]) | (uint32_t)narrow16<DT>(s[3]) << 16);
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; j++) to[j] = narrow16<DT>(s[j]);
+            for (int j = 0; j < 4; j++)
+                if (h + j < a.hidden) to[j] = narrow16<DT>(s[j]);
         }
     };
     const auto add = [&](int k0, int k, float4& y, float& w, int& r) {
         const size_t slot = (size_t)t * a.topK + min(k0 + k, a.topK - 1);
         const int e = a.ids[slot];
         w = a.weights[slot];
-        y = __ldcg(reinterpret_cast<const float4*>(a.y + slot * a.hidden + h));
+        y = __ldcg(reinterpret_cast<const float4*>(a.y + slot * moe_y_stride(a.hidden) + h));
         r = k0 + k < a.topK && e >= 0 && e < a.experts ? e / a.share : -1;
     };
     if (a.topK <= UN) {
@@ -215,7 +242,7 @@ __device__ __forceinline__ void combine(const ExpertsArgs& a, int t, int h) {
 
 // UP: the way up, K = hidden, tiles of 64 of the ffn elements; else the way down, K = ffn, tiles of 128
 // columns of the output.
-template <int DT, int NT, bool UP>
+template <int DT, int NT, bool UP, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant__ ExpertsArgs a) {
     constexpr int COPIES = UP ? 1 : 2;                 // of B: the tokens, or both values of silu(g) u
     constexpr int kHalfB = NT * 128;
@@ -242,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < nStages; i++) {
-            bar_init(&sh.full[i], kProducers);
+            bar_init(&sh.full[i], ALIGNED || UP ? kProducers : 2 * kProducers);
             bar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < 2; i++) {
@@ -276,57 +303,109 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
         const int t = (int)threadIdx.x - 32 * (kIssuer + 1), c = t & 15, r0 = t >> 4;
         const uint32_t column = (uint32_t)(c >> 3), swizzled = (uint32_t)(((c & 7) ^ (r0 & 7)) << 4);
         bool ok = true;
-        // One stage's A, or B.
+        const auto weights = [&](const MoeGroup& g) {
+            const size_t e = (size_t)(g.expert % a.share);
+            return UP ? (const uint16_t*)a.up[g.expert / a.share] + e * 2 * a.ffn * K
+                      : (const uint16_t*)a.down[g.expert / a.share] + e * a.hidden * K;
+        };
+        // Row 16 i + r0 of a tile; on the way up sixteen of the gate, sixteen of the linear part.
+        const auto row = [&](int m, int i) { return UP ? m * (kM / 2) + (i >> 1) * 16 + r0 : m * kM + 16 * i + r0; };
+        const auto first_of = [&](int n, int i) { return ((size_t)(UP && (i & 1) ? a.ffn : 0) + n) * K; };
+        const int rows = UP ? a.ffn : a.hidden;
+        const auto at_a = [&](int at) { return stages + (uint32_t)(at * kStage) + column * kHalfA + (uint32_t)r0 * 128 + swizzled; };
+        const auto at_b = [&](int at) {
+            return stages + (uint32_t)(at * kStage) + 2 * kHalfA + column * kHalfB + (uint32_t)r0 * 128 + swizzled;
+        };
+        const auto token = [&](const MoeGroup& g, int r) {
+            return (const uint16_t*)a.x + (size_t)(l.slots[g.first + r] / a.topK) * a.rowStride;
+        };
+        // One stage's A, or B, asynchronously.
         const auto copy_a = [&](int u, int chunk, int at) {
             const MoeGroup g = l.groups[u / tiles];
             const int m = u % tiles, k = chunk * kK + c * 8;
-            const size_t e = (size_t)(g.expert % a.share);
-            const uint32_t to = stages + (uint32_t)(at * kStage) + column * kHalfA + (uint32_t)r0 * 128 + swizzled;
-            if (UP) {
-                const uint16_t* w = (const uint16_t*)a.up[g.expert / a.share] + e * 2 * a.ffn * K + k;
+            const uint32_t to = at_a(at);
+            const uint16_t* w = weights(g) + k;
 #pragma unroll
-                for (int i = 0; i < 8; i++) {          // rows 16 i + r0: sixteen of the gate, sixteen of the linear part
-                    const int f = m * (kM / 2) + (i >> 1) * 16 + r0;
-                    const bool in = f < a.ffn && k < K;
-                    copy_chunk(to + i * 16 * 128, in ? w + ((size_t)(i & 1 ? a.ffn : 0) + f) * K : w - k, in);
-                }
-            } else {
-                const uint16_t* w = (const uint16_t*)a.down[g.expert / a.share] + e * a.hidden * K + k;
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const int h = m * kM + 16 * i + r0;
-                    const bool in = h < a.hidden && k < K;
-                    copy_chunk(to + i * 16 * 128, in ? w + (size_t)h * K : w - k, in);
-                }
+            for (int i = 0; i < 8; i++) {
+                const int n = row(m, i);
+                const bool in = n < rows && k < K;
+                copy_chunk(to + i * 16 * 128, in ? w + first_of(n, i) : w - k, in);
             }
         };
         const auto copy_b = [&](int u, int chunk, int at) {
             const MoeGroup g = l.groups[u / tiles];
-            const int k = chunk * kK + c * 8;
-            const uint32_t to = stages + (uint32_t)(at * kStage) + 2 * kHalfA + column * kHalfB + (uint32_t)r0 * 128 + swizzled;
+            const int k = chunk * kK + c * 8, width = UP ? K : moe_act_stride(K);
+            const uint32_t to = at_b(at);
             for (int r = r0; r < g.count; r += 16) {
-                const int slot = l.slots[g.first + r];
-                const bool in = k < K;
+                const bool in = k < width;
                 if (UP) {
-                    const uint16_t* x = (const uint16_t*)a.x + (size_t)(slot / a.topK) * a.rowStride;
+                    const uint16_t* x = token(g, r);
                     copy_chunk(to + (r - r0) * 128, in ? x + k : x, in);
                 } else {
-                    const uint16_t* x = (const uint16_t*)a.act + (size_t)slot * 2 * K;
+                    const uint16_t* x = (const uint16_t*)a.act + (size_t)l.slots[g.first + r] * 2 * width;
                     copy_chunk(to + (r - r0) * 128, in ? x + k : x, in);
-                    copy_chunk(to + (r - r0) * 128 + 2 * kHalfB, in ? x + K + k : x, in);
+                    copy_chunk(to + (r - r0) * 128 + 2 * kHalfB, in ? x + width + k : x, in);
                 }
             }
         };
-        // The way down: the weights of the first stages need not wait for the way up.
-        int early = 0;
-        if (!UP) {
-            for (int u = first, chunk = chunk0; u < units && early < nStages; early++) {
-                copy_a(u, chunk, early);
-                if (++chunk == chunk1) {
-                    chunk = chunk0;
-                    u += step;
+        // The same of rows that start anywhere: through registers, which hold one stage's ahead.
+        uint32_t wordsA[ALIGNED ? 1 : 8][5], wordsB[ALIGNED || !UP ? 1 : NT / 16][5];
+        const auto load_a = [&](int u, int chunk) {
+            if (ALIGNED || u >= units) return;
+            const MoeGroup g = l.groups[u / tiles];
+            const int m = u % tiles, k = chunk * kK + c * 8;
+            const uint16_t* w = weights(g);
+#pragma unroll
+            for (int i = 0; i < (ALIGNED ? 1 : 8); i++) {
+                const int n = row(m, i);
+                const bool in = n < rows && k < K;
+                load_words(in ? w + first_of(n, i) + k : w, in ? K - k : 0, wordsA[i]);
+            }
+            if constexpr (UP && !ALIGNED) {
+#pragma unroll
+                for (int i = 0; i < NT / 16; i++) {
+                    const int r = r0 + 16 * i;
+                    const bool in = r < g.count && k < K;
+                    load_words(in ? token(g, r) + k : w, in ? K - k : 0, wordsB[i]);
                 }
             }
+        };
+        const auto store_a = [&](int u, int chunk, int at) {
+            const MoeGroup g = l.groups[u / tiles];
+            const int m = u % tiles, k = chunk * kK + c * 8;
+            const uint16_t* w = weights(g);
+#pragma unroll
+            for (int i = 0; i < (ALIGNED ? 1 : 8); i++)
+                st_smem(at_a(at) + i * 16 * 128, from_words(w + first_of(row(m, i), i) + k, K - k, wordsA[i]));
+            if constexpr (UP && !ALIGNED) {
+#pragma unroll
+                for (int i = 0; i < NT / 16; i++) {
+                    const int r = r0 + 16 * i;
+                    if (r < g.count) st_smem(at_b(at) + i * 16 * 128, from_words(token(g, r) + k, K - k, wordsB[i]));
+                }
+            }
+        };
+        const auto next = [&](int& u, int& chunk) {
+            if (++chunk == chunk1) {
+                chunk = chunk0;
+                u += step;
+            }
+        };
+        // The way down: the weights of the first stages need not wait for the way up.
+        int early = 0, aheadU = first, aheadChunk = chunk0;            // of A: what is loaded next
+        if (!UP) {
+            for (; aheadU < units && early < nStages; early++) {
+                if (ALIGNED) {
+                    copy_a(aheadU, aheadChunk, early);
+                } else {
+                    load_a(aheadU, aheadChunk);
+                    store_a(aheadU, aheadChunk, early);
+                }
+                next(aheadU, aheadChunk);
+            }
+        }
+        load_a(aheadU, aheadChunk);
+        if (!UP) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
             asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         }
@@ -338,12 +417,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
                     ok = __all_sync(~0u, bar_wait(&sh.empty[at], (round - 1) & 1u, &sh.failed));
                     if (!ok) break;
                 }
+                const bool stored = !ALIGNED && early == 0;
                 if (early > 0) early--;
-                else copy_a(u, chunk, at);
-                copy_b(u, chunk, at);
-                // arrives when this thread's copies are there; the issuer makes them visible to its products (a
-                // fence here would wait for the stages under way: 816 us for the way up of 64 x 4096 x 1536, 499)
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_at(&sh.full[at])) : "memory");
+                else if (ALIGNED) copy_a(u, chunk, at);
+                else store_a(u, chunk, at);
+                if (!ALIGNED) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    bar_arrive(&sh.full[at]);
+                }
+                if (ALIGNED || !UP) {
+                    copy_b(u, chunk, at);
+                    // arrives when this thread's copies are there; the issuer makes them visible to its products (a
+                    // fence here would wait for the stages under way: 816 us for the way up of 64 x 4096 x 1536, 499)
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_at(&sh.full[at])) : "memory");
+                }
+                if (stored) {
+                    next(aheadU, aheadChunk);
+                    load_a(aheadU, aheadChunk);
+                }
                 if (++at == nStages) {
                     at = 0;
                     round++;
@@ -420,24 +511,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
                     // even columns, the others the odd ones
                     const int f = m * (kM / 2) + warp * 16 + (lane & 15);
                     uint16_t* const act = (uint16_t*)a.act;
+                    const int width = moe_act_stride(a.ffn);           // zeros from ffn on
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
                         const float other = __shfl_xor_sync(~0u, lane < 16 ? v[j + 1] : v[j], 16);
                         const float gate = lane < 16 ? v[j] : other, linear = lane < 16 ? other : v[j + 1];
                         const int column = j0 + j + (lane >> 4);
-                        if (column >= g.count || f >= a.ffn) continue;
-                        const float x = gate / (1.0f + expf(-gate)) * linear;
+                        if (column >= g.count || f >= width) continue;
+                        const float x = f < a.ffn ? gate / (1.0f + expf(-gate)) * linear : 0.0f;
                         // (infinities and NaNs go into the second value)
                         const uint16_t hi = narrow16<DT>(fminf(fmaxf(x, -kLargest<DT>), kLargest<DT>));
-                        uint16_t* to = act + (size_t)l.slots[g.first + column] * 2 * a.ffn + f;
+                        uint16_t* to = act + (size_t)l.slots[g.first + column] * 2 * width + f;
                         to[0] = hi;
-                        to[a.ffn] = narrow16<DT>(x - widen16<DT>(hi));
+                        to[width] = narrow16<DT>(x - widen16<DT>(hi));
                     }
                 } else {
                     const int h = m * kM + row;
 #pragma unroll
                     for (int j = 0; j < 16; j++)
-                        if (j0 + j < g.count && h < a.hidden) a.y[(size_t)l.slots[g.first + j0 + j] * a.hidden + h] = v[j];
+                        if (j0 + j < g.count && h < a.hidden) a.y[(size_t)l.slots[g.first + j0 + j] * moe_y_stride(a.hidden) + h] = v[j];
                 }
             }
             tmem_fence_before();
@@ -486,7 +578,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_moe_combine(const __grid_co
 
 template <int DT, int NT, bool UP>
 cudaError_t tiles_launch(const ExpertsArgs& a, const MoeTiles& t, cudaStream_t s) {
-    const auto kernel = k_moe_tiles<DT, NT, UP>;
+    const auto kernel = a.aligned ? k_moe_tiles<DT, NT, UP, true> : k_moe_tiles<DT, NT, UP, false>;
     // one value for every launch, as host threads share the kernel's limit
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoeMaxSmem);
     if (e != cudaSuccess) return e;

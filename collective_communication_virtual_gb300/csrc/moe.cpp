@@ -37,8 +37,8 @@ vResult_t check_moe(const vMoeDesc_t* desc, int nRanks, Moe* m) {
 struct Layout {
     size_t act, y, done;
     explicit Layout(const Moe& m)
-        : act((m.slots * m.d.ffn * 4 + 255) / 256 * 256),
-          y((m.slots * m.d.hidden * 4 + 255) / 256 * 256),
+        : act((m.slots * vc::moe_act_stride((int)m.d.ffn) * 4 + 255) / 256 * 256),
+          y((m.slots * vc::moe_y_stride((int)m.d.hidden) * 4 + 255) / 256 * 256),
           done((m.d.hidden + vc::kMoeTile - 1) / vc::kMoeTile * 4) {}
     size_t total() const { return act + y + done + 16; }
 };
@@ -196,15 +196,16 @@ vResult_t experts(const vMoeDesc_t* desc, const void* x, const int* ids, const f
     a.combineHere = 1;
     a.status = v.status;
     a.statusHost = v.statusHost;
-    if (a.aligned && m.esz == 2) {
+    if (m.esz == 2) {
         const vc::MoeTiles t = moe_tiles(a, v.smCount);
         if (v.debug)
-            std::fprintf(stderr, "vcomm INFO MoeExperts rows=%d hidden=%d ffn=%d experts=%d topK=%d N=%d tokens=%d split=%d,%d grid=%d,%d\n",
-                         a.rows, a.hidden, a.ffn, a.experts, a.topK, a.nRanks, t.tokens, t.splitUp, t.splitDown, t.gridUp, t.gridDown);
+            std::fprintf(stderr, "vcomm INFO MoeExperts rows=%d hidden=%d ffn=%d experts=%d topK=%d N=%d aligned=%d tokens=%d split=%d,%d grid=%d,%d\n",
+                         a.rows, a.hidden, a.ffn, a.experts, a.topK, a.nRanks, a.aligned, t.tokens, t.splitUp, t.splitDown, t.gridUp, t.gridDown);
         return vc::comm_launch_tracked(c, "moe experts", stream, [&]() { return vc::launch_moe_tiles(a, t, m.d.datatype, stream); });
     }
     // A warp one row of the weights (two on the way down), and more where there are CTAs enough: each looks
-    // through the router's list first (13 tokens on 10 experts of 1001 x 333: 54 us with four a warp).
+    // through the router's list first (13 tokens on 10 experts of 1001 x 333, when fp16 came here: 54 us with four
+    // a warp, 28 so).
     const size_t groups = std::min<size_t>(a.experts, m.slots), enough = 24 * (size_t)v.smCount;
     a.tileUp = vc::kMoeTile;
     while (a.tileUp < 32 && groups * a.ffn / a.tileUp > enough) a.tileUp *= 2;
@@ -213,7 +214,7 @@ vResult_t experts(const vMoeDesc_t* desc, const void* x, const int* ids, const f
     if (v.debug)
         std::fprintf(stderr, "vcomm INFO MoeExperts rows=%d hidden=%d ffn=%d experts=%d topK=%d N=%d aligned=%d\n", a.rows,
                      a.hidden, a.ffn, a.experts, a.topK, a.nRanks, a.aligned);
-    return comm_launch(c, "moe experts", [&]() { return vc::launch_moe_experts(a, m.d.datatype, stream); });
+    return comm_launch(c, "moe experts", [&]() { return vc::launch_moe_experts(a, stream); });
 }
 
 }  // namespace

@@ -38,15 +38,16 @@ struct ExpertsArgs {
     const void* x;
     const int* ids;                  // [rows][topK]
     const float* weights;
-    float* act;                      // workspace: [rows * topK][ffn], what goes into the way down
-    float* y;                        // workspace: [rows * topK][hidden], every slot's output
+    float* act;                      // workspace: what goes into the way down, [rows * topK][ffn], or, of 16-bit types,
+                                     // [rows * topK][2][moe_act_stride(ffn)] of them
+    float* y;                        // workspace: every slot's output, [rows * topK][hidden], or [..][moe_y_stride(hidden)]
     unsigned int* done;              // workspace: experts that have finished a tile of columns
     size_t rowStride, recvStride;
     int rows, hidden, ffn, experts, topK;
     int nRanks;
     int share;                       // experts of a rank
     int aligned;                     // every row of x and of the weights starts on 16 bytes and ends with a vector
-    int tileUp, tileDown;            // output columns of a CTA: 8 to 32, and 16 or 32
+    int tileUp, tileDown;            // fp32: output columns of a CTA, 8 to 32, and 16 or 32
     int recvAligned;                 // every row of the outputs starts on 8 bytes
     int split;                       // tensor cores: CTAs of a cluster that share a tile's columns
     int stages;                      // the same: stages of a CTA
@@ -55,14 +56,22 @@ struct ExpertsArgs {
     volatile Status* statusHost;     // pinned mirror
 };
 constexpr int kMoeTile = 8;          // output columns of a CTA, at least
-cudaError_t launch_moe_experts(const ExpertsArgs& a, vDataType_t dt, cudaStream_t s);
+cudaError_t launch_moe_experts(const ExpertsArgs& a, cudaStream_t s);
 
-// The same on the tensor cores.
+// The same on the tensor cores, of 16-bit types.
 constexpr int kMoeMaxStages = 8;
 constexpr int kMoeMaxSmem = 225 * 1024;
 struct MoeGroup {                    // tokens of one expert, as many as a tile takes
     uint16_t expert, first, count;   // first: of its slots in the list
 };
+#if defined(__CUDACC__)
+__host__ __device__
+#endif
+constexpr int moe_act_stride(int ffn) { return (ffn + 7) / 8 * 8; }
+#if defined(__CUDACC__)
+__host__ __device__
+#endif
+constexpr int moe_y_stride(int hidden) { return (hidden + 3) / 4 * 4; }
 #if defined(__CUDACC__)
 __host__ __device__
 #endif

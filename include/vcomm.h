@@ -467,8 +467,8 @@ vResult_t vMoeRoute(const vMoeDesc_t* desc, const void* x, const void* routerWei
  *   recvbuffs[r][t] = sum over k with expertIds[t][k] = e held by rank r of
  *                     expertWeights[t][k] * (down_e * a)
  * in the order of k and in fp32, rounded once: the ranks' partial sums, which vAllReduceRmsNorm or
- * vAllReduceBlockNorm adds up.  (a is held in fp32, or in two values of the data type: with fp16 an a
- * beyond 65504 is right to 2^-12 of itself, and one beyond 131008 becomes infinite.)  A token that goes to no expert of a rank gets zeros there.  An id
+ * vAllReduceBlockNorm adds up.  (a is held in fp32, with 16-bit types as the sum of two of their values:
+ * with fp16 an a beyond 65504 is right to 2^-12 of itself, and one beyond 131008 becomes infinite.)  A token that goes to no expert of a rank gets zeros there.  An id
  * outside [0, experts) is no expert (padding); an expert named twice counts twice.  A rank that
  * holds no expert may pass NULL weights; every recvbuffs entry is written.  Outputs overlap no
  * input.  The workspace is at least what vMoeExpertsWorkspace gives for the descriptor, 16-byte

@@ -57,7 +57,7 @@ cudaError_t launch_block_norm_backward(const BlockNormBackwardArgs& a, vDataType
     return g_launches++, g_back = a, cudaSuccess;
 }
 cudaError_t launch_moe_route(const RouteArgs& a, vDataType_t, cudaStream_t) { return g_launches++, g_route = a, cudaSuccess; }
-cudaError_t launch_moe_experts(const ExpertsArgs& a, vDataType_t, cudaStream_t) {
+cudaError_t launch_moe_experts(const ExpertsArgs& a, cudaStream_t) {
     g_tiles = {};
     return g_launches++, g_experts = a, cudaSuccess;
 }
