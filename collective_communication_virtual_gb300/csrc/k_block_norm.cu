@@ -10,7 +10,10 @@
 // A row needs two reductions, one behind the other: r2 could be had from the sums of b^2, b h and
 // residual^2 alone, but those cancel where the residual and the block's output nearly do.  A thread
 // keeps its part of b, then of h, in registers, so every input byte is read once and every output
-// byte written once.
+// byte written once: 18 of them a column and row of 8 ranks in bf16.  Memory bounds the long calls:
+// 8 x 4096 x 4096 bf16 99 us, 6.4 TB/s of 6.8, where two warps of three wait for a load, a barrier of the row's
+// reductions or shared memory; that is why many inputs get one vector a thread and two CTAs an SM, few
+// inputs, where instructions count, four.  One row of 8192 takes 6 us, all launch and latency.
 #include "block_norm.cuh"
 
 namespace vc {

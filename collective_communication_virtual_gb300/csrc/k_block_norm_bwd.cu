@@ -13,6 +13,10 @@
 // both.  A CTA (or cluster) strides over the rows and keeps its two sums in fp32; each writes them as
 // one row of the workspace, and a second launch adds them up and multiplies.  The order of the
 // additions follows from the launch shape alone.
+//
+// Memory bounds aligned rows: 8 x 4096 x 4096 bf16 114 us (5.9 TB/s of 6.8; 105 the first launch alone).
+// Rows off 16 bytes are bound by instructions: 3 x 1537 x 2731 fp16 46 us (1.8 TB/s), at 125 registers with both
+// sums in shared memory, where every vector is shifted in and out and read and written back to the sums.
 #include "block_norm.cuh"
 
 namespace vc {

@@ -24,6 +24,13 @@
 //
 // A row's part on a rank is read by whole 16-byte blocks, wherever it starts; what a block holds besides
 // counts as minus infinity.
+//
+// Instructions and the latencies between a row's reductions bound it, not memory (256 rows of 131072 bf16
+// are read in 10 us): those take 67 us where the largest is taken, 87 with topK 50 and topP, 113 with topK
+// 200, 133 without filters (a weight of every logit), 150 with topP 0.9 at temperature 0.6, where the
+// nucleus fits the list, and 356 at 1.2, where it holds most of the row and the histograms decide.  One row
+// takes 12 to 24 us on eight CTAs, and 50 with such a nucleus.  A CTA that streams its row from memory several times,
+// a row a CTA, was slower (403 us against 176 for rows of all kinds).
 #include "norm_stage.cuh"
 #include "sample.h"
 
