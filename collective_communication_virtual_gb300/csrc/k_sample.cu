@@ -26,11 +26,11 @@
 // counts as minus infinity.
 //
 // Instructions and the latencies between a row's reductions bound it, not memory (256 rows of 131072 bf16
-// are read in 10 us): those take 67 us where the largest is taken, 87 with topK 50 and topP, 113 with topK
-// 200, 133 without filters (a weight of every logit), 150 with topP 0.9 at temperature 0.6, where the
-// nucleus fits the list, and 356 at 1.2, where it holds most of the row and the histograms decide.  One row
+// are read in 10 us): those take 68 us where the largest is taken, 88 with topK 50 and topP, 112 with topK
+// 200, 126 without filters (a weight of every logit), 146 with topP 0.9 at temperature 0.6, where the
+// nucleus fits the list, and 354 at 1.2, where it holds most of the row and the histograms decide.  One row
 // takes 12 to 24 us on eight CTAs, and 50 with such a nucleus.  A CTA that streams its row from memory several times,
-// a row a CTA, was slower (403 us against 176 for rows of all kinds).
+// a row a CTA, was slower (403 us against 169 for rows of all kinds).
 #include "norm_stage.cuh"
 #include "sample.h"
 
@@ -635,27 +635,37 @@ __device__ __forceinline__ void decide(const SampleArgs& a, const Filters& q, Sh
     }
     ahead += run - sum;
     if (goal < ahead || goal >= ahead + sum) return;
-    // The thread whose values hold the token goes through them in order.
+    // The thread whose values hold the token goes through them in order, a vector's weights at a time (256 rows
+    // of 131072 without filters 126 us; one weight behind the other 133).
     for (int k = 0; k < cols.count; k++) {
-        float f[E];
-        widen_vec<Cols::kType>(cols.raw(k), f);
+        const uint4 vec = cols.raw(k);
+        if (Cols::V::largest(vec) < bottom) continue;
+        float f[E], x = 0.0f;
+        u64 weight[E];
+        widen_vec<Cols::kType>(vec, f);
+        w.fixed(f, weight);
+        int at = -1;
+#pragma unroll
         for (int j = 0; j < E; j++) {
             bool tie;
-            u64 e = kept(f[j], w.fixed(f[j]), &tie);
+            u64 e = kept(f[j], weight[j], &tie);
             if (tie && left > 0) {
                 left--;
                 e = atEdge;
             }
             ahead += e;
-            if (goal >= ahead) continue;
-            const int token = token_of((cols.first + k) * E + j);
-            for (int o = 0; o < a.nOut; o++) a.tokens[o][row] = token;
-            if (a.logprob) {
-                const float x = f[j], z = x == top ? 0.0f : q.greedy ? x - top : (x - top) / q.heat;
-                a.logprob[row] = z - log1pf((float)((total ? total : all) - (1ull << kFix)) * 0x1p-44f);
-            }
-            return;
+            if (at >= 0 || goal >= ahead) continue;
+            at = j;
+            x = f[j];
         }
+        if (at < 0) continue;
+        const int token = token_of((cols.first + k) * E + at);
+        for (int o = 0; o < a.nOut; o++) a.tokens[o][row] = token;
+        if (a.logprob) {
+            const float z = x == top ? 0.0f : q.greedy ? x - top : (x - top) / q.heat;
+            a.logprob[row] = z - log1pf((float)((total ? total : all) - (1ull << kFix)) * 0x1p-44f);
+        }
+        return;
     }
 }
 
