@@ -10,8 +10,8 @@
 // have room.  Rows that start off 16 bytes come through registers, a stage ahead, as the aligned words that
 // hold them.
 //
-// Measured (bf16): 64 tokens on 8 of 128 experts of 4096 x 1536, 4.8 GB of weights, 785 us (6.1 TB/s; the way up
-// 499), with 4095 x 1535 1741 (2.7); 8 tokens there 341 us (5.7 TB/s), one token 69 (4.4); one token on 4 of
+// Measured (bf16): 64 tokens on 8 of 128 experts of 4096 x 1536, 4.8 GB of weights, 780 us (6.1 TB/s; the way up
+// 499), with 4095 x 1535 1741 (2.7); 8 tokens there 339 us (5.7 TB/s), one token 69 (4.4); one token on 4 of
 // 64 experts of 2048 x 1024 25 us (2.0), a chain of latencies: ids, weights, sums, ids, weights, sums.
 //
 // The way up: the tile's rows are 64 of the gate and the 64 of the linear part that belong to them,
@@ -302,7 +302,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
         // ---- producers: chunk `c` of rows r0, r0 + 16, ... of a stage
         const int t = (int)threadIdx.x - 32 * (kIssuer + 1), c = t & 15, r0 = t >> 4;
         const uint32_t column = (uint32_t)(c >> 3), swizzled = (uint32_t)(((c & 7) ^ (r0 & 7)) << 4);
-        bool ok = true;
         const auto weights = [&](const MoeGroup& g) {
             const size_t e = (size_t)(g.expert % a.share);
             return UP ? (const uint16_t*)a.up[g.expert / a.share] + e * 2 * a.ffn * K
@@ -348,9 +347,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
                 }
             }
         };
-        // The same of rows that start anywhere: through registers, which hold one stage's ahead.
-        uint32_t wordsA[ALIGNED ? 1 : 8][5], wordsB[ALIGNED || !UP ? 1 : NT / 16][5];
-        const auto load_a = [&](int u, int chunk) {
+        // The same of rows that start anywhere: through registers, which hold one stage's ahead (two
+        // stages': 1904 us against 1741 for 64 tokens on 8 of 128 experts of 4095 x 1535).
+        struct Words {
+            uint32_t a[ALIGNED ? 1 : 8][5], b[ALIGNED || !UP ? 1 : NT / 16][5];
+        };
+        const auto load_a = [&](int u, int chunk, Words& words) {
             if (ALIGNED || u >= units) return;
             const MoeGroup g = l.groups[u / tiles];
             const int m = u % tiles, k = chunk * kK + c * 8;
@@ -359,29 +361,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
             for (int i = 0; i < (ALIGNED ? 1 : 8); i++) {
                 const int n = row(m, i);
                 const bool in = n < rows && k < K;
-                load_words(in ? w + first_of(n, i) + k : w, in ? K - k : 0, wordsA[i]);
+                load_words(in ? w + first_of(n, i) + k : w, in ? K - k : 0, words.a[i]);
             }
             if constexpr (UP && !ALIGNED) {
 #pragma unroll
                 for (int i = 0; i < NT / 16; i++) {
                     const int r = r0 + 16 * i;
                     const bool in = r < g.count && k < K;
-                    load_words(in ? token(g, r) + k : w, in ? K - k : 0, wordsB[i]);
+                    load_words(in ? token(g, r) + k : w, in ? K - k : 0, words.b[i]);
                 }
             }
         };
-        const auto store_a = [&](int u, int chunk, int at) {
+        const auto store_a = [&](int u, int chunk, int at, const Words& words) {
             const MoeGroup g = l.groups[u / tiles];
             const int m = u % tiles, k = chunk * kK + c * 8;
             const uint16_t* w = weights(g);
 #pragma unroll
             for (int i = 0; i < (ALIGNED ? 1 : 8); i++)
-                st_smem(at_a(at) + i * 16 * 128, from_words(w + first_of(row(m, i), i) + k, K - k, wordsA[i]));
+                st_smem(at_a(at) + i * 16 * 128, from_words(w + first_of(row(m, i), i) + k, K - k, words.a[i]));
             if constexpr (UP && !ALIGNED) {
 #pragma unroll
                 for (int i = 0; i < NT / 16; i++) {
                     const int r = r0 + 16 * i;
-                    if (r < g.count) st_smem(at_b(at) + i * 16 * 128, from_words(token(g, r) + k, K - k, wordsB[i]));
+                    if (r < g.count) st_smem(at_b(at) + i * 16 * 128, from_words(token(g, r) + k, K - k, words.b[i]));
                 }
             }
         };
@@ -392,55 +394,55 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
             }
         };
         // The way down: the weights of the first stages need not wait for the way up.
+        Words words;
         int early = 0, aheadU = first, aheadChunk = chunk0;            // of A: what is loaded next
         if (!UP) {
             for (; aheadU < units && early < nStages; early++) {
                 if (ALIGNED) {
                     copy_a(aheadU, aheadChunk, early);
                 } else {
-                    load_a(aheadU, aheadChunk);
-                    store_a(aheadU, aheadChunk, early);
+                    load_a(aheadU, aheadChunk, words);
+                    store_a(aheadU, aheadChunk, early, words);
                 }
                 next(aheadU, aheadChunk);
             }
         }
-        load_a(aheadU, aheadChunk);
+        load_a(aheadU, aheadChunk, words);
         if (!UP) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
             asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         }
-        int at = 0;
+        int at = 0, u = first, chunk = chunk0;
         uint32_t round = 0;                            // times that all stages have been filled
-        for (int u = first; u < units && ok; u += step) {
-            for (int chunk = chunk0; chunk < chunk1; chunk++) {
-                if (round > 0) {
-                    ok = __all_sync(~0u, bar_wait(&sh.empty[at], (round - 1) & 1u, &sh.failed));
-                    if (!ok) break;
-                }
-                const bool stored = !ALIGNED && early == 0;
-                if (early > 0) early--;
-                else if (ALIGNED) copy_a(u, chunk, at);
-                else store_a(u, chunk, at);
-                if (!ALIGNED) {
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    bar_arrive(&sh.full[at]);
-                }
-                if (ALIGNED || !UP) {
-                    copy_b(u, chunk, at);
-                    // arrives when this thread's copies are there; the issuer makes them visible to its products (a
-                    // fence here would wait for the stages under way: 816 us for the way up of 64 x 4096 x 1536, 499)
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_at(&sh.full[at])) : "memory");
-                }
-                if (stored) {
-                    next(aheadU, aheadChunk);
-                    load_a(aheadU, aheadChunk);
-                }
-                if (++at == nStages) {
-                    at = 0;
-                    round++;
-                }
+        // The next stage; false at the end.
+        const auto fill = [&](bool early) {
+            if (round > 0 && !__all_sync(~0u, bar_wait(&sh.empty[at], (round - 1) & 1u, &sh.failed))) return false;
+            if (ALIGNED && !early) copy_a(u, chunk, at);
+            if (!ALIGNED) {
+                if (!early) store_a(u, chunk, at, words);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                bar_arrive(&sh.full[at]);
             }
-        }
+            if (ALIGNED || !UP) {
+                copy_b(u, chunk, at);
+                // arrives when this thread's copies are there; the issuer makes them visible to its products (a
+                // fence here would wait for the stages under way: 816 us for the way up of 64 x 4096 x 1536, 499)
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_at(&sh.full[at])) : "memory");
+            }
+            if (!ALIGNED && !early) {
+                next(aheadU, aheadChunk);
+                load_a(aheadU, aheadChunk, words);
+            }
+            if (++at == nStages) {
+                at = 0;
+                round++;
+            }
+            next(u, chunk);
+            return u < units;
+        };
+        bool more = u < units;
+        for (; more && early > 0; early--) more = fill(true);
+        while (more) more = fill(false);
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == kIssuer) {
         // ---- the issuer
