@@ -16,10 +16,12 @@
 //
 // The way up: the tile's rows are 64 of the gate and the 64 of the linear part that belong to them,
 // sixteen and sixteen in turn, so that both sums of an element lie in one warp.  silu(g) u goes into the
-// workspace as two values of the weights' type, the second what the first leaves out, 2^-18 of the value
-// off (bf16), for which the way down makes two products of every tile: in 16 bits alone the result would
-// be as far off again as its own rounding.  Beyond fp16's largest value the second is up to as large as the
-// first, 2^-12 of the value off, and beyond twice that infinite.
+// workspace as two values of the weights' type, the second what the first leaves out, for which the way
+// down makes two products of every tile: in 16 bits alone the result would be as far off again as its own
+// rounding.  In bf16 the two add up to the value, 2^-18 of it off.  fp16 has steps of 2^-24 at the least, so
+// there the first is in units of 2 and the second in units of 2^-10, and each has sums of its own, which
+// meet in fp32: 2^-22 of the value off, or 2^-35 where it is small; beyond 2 x 65504 it is infinite.  (Both in
+// units of 1, one sum: 2^-25 off, more than the result's own rounding for values below 10^-4.)
 // The way down: every slot's output goes into the workspace in fp32; for few tokens the last warp of a
 // tile of columns adds them up, for more a third launch.
 #include "moe.h"
@@ -37,7 +39,12 @@ constexpr int kProducers = 32 * kProducerWarps;
 constexpr int kM = 128;              // rows of a tile
 constexpr int kK = 128;              // columns of a stage: two swizzled halves of 64
 constexpr int kHalfA = kM * 128;     // bytes of a half of A
-template <int DT> constexpr float kLargest = DT == kF16 ? 65504.0f : 0x1.FEp127f;
+constexpr float kLargest = 0x1.FEp127f;                // of bf16
+// fp16: what the two values of silu(g) u are in units of
+constexpr float kFirstUnit = 2.0f, kSecondUnit = 0x1p-10f;
+// Sums of a tile that the way down keeps apart, and columns of tensor memory, two tiles' (32 at least).
+template <int DT, bool UP> constexpr int kSums = DT == kF16 && !UP ? 2 : 1;
+template <int DT, int NT, bool UP> constexpr int kColumns = 2 * NT * kSums<DT, UP>;
 static_assert(kProducers == 16 * 16, "a producer: one 16-byte chunk of a stage's row, sixteen rows apart");
 
 struct Shared {
@@ -246,6 +253,8 @@ template <int DT, int NT, bool UP, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant__ ExpertsArgs a) {
     constexpr int COPIES = UP ? 1 : 2;                 // of B: the tokens, or both values of silu(g) u
     constexpr int kHalfB = NT * 128;
+    constexpr int SUMS = kSums<DT, UP>, COLUMNS = kColumns<DT, NT, UP>;
+    static_assert(COLUMNS >= 32 && (COLUMNS & (COLUMNS - 1)) == 0 && COLUMNS <= 256, "tensor memory comes in powers of two from 32 on");
     constexpr int kStage = 2 * kHalfA + 2 * COPIES * kHalfB;
     extern __shared__ unsigned char raw[];
     __shared__ Shared sh;
@@ -282,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
         sh.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kIssuer) tmem_alloc(&sh.tmem, NT <= 16 ? 32 : 2 * NT);
+    if (warp == kIssuer) tmem_alloc(&sh.tmem, COLUMNS);
     make_lists<NT>(sh, l, reinterpret_cast<uint16_t*>(raw + (stages - smem_at(raw))), a);    // (no stage is in use yet)
     tmem_fence_before();
     __syncthreads();
@@ -454,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
             bool ok = true;
             for (int u = first; u < units && ok; u += step, unit++) {
                 const int n = (l.groups[u / tiles].count + 15) & ~15, buffer = unit & 1;
-                const uint32_t shape = product_shape<DT>(n), d = tmem + (uint32_t)(buffer * NT);
+                const uint32_t shape = product_shape<DT>(n), d = tmem + (uint32_t)(buffer * NT * SUMS);
                 if (unit >= 2 && !(ok = bar_wait(&sh.sumsEmpty[buffer], (uint32_t)(unit / 2 - 1) & 1u, &sh.failed))) break;
                 tmem_fence_after();
                 for (int chunk = chunk0; chunk < chunk1; chunk++) {
@@ -467,8 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
                         const uint64_t opA = operand(sa + (i >> 2) * kHalfA + (i & 3) * 32);
 #pragma unroll
                         for (int v = 0; v < COPIES; v++)
-                            multiply(d, opA, operand(sb + v * 2 * kHalfB + (i >> 2) * kHalfB + (i & 3) * 32), shape,
-                                     chunk > chunk0 || i > 0 || v > 0);
+                            multiply(d + (SUMS > 1 ? v * NT : 0), opA, operand(sb + v * 2 * kHalfB + (i >> 2) * kHalfB + (i & 3) * 32),
+                                     shape, chunk > chunk0 || i > 0 || (SUMS == 1 && v > 0));
                     }
                     products_done(&sh.empty[at]);
                     if (++at == nStages) {
@@ -498,7 +507,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
             tmem_fence_after();
             for (int j0 = 0; j0 < g.count; j0 += 16) {
                 float v[16];
-                tmem_load(tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)(buffer * NT + j0), v);
+                const uint32_t sums = tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)(buffer * NT * SUMS + j0);
+                tmem_load(sums, v);
+                if constexpr (SUMS > 1) {
+                    float second[16];
+                    tmem_load(sums + NT, second);
+#pragma unroll
+                    for (int j = 0; j < 16; j++) v[j] = fmaf(second[j], kSecondUnit, v[j] * kFirstUnit);
+                }
                 if (rank > 0) {      // to the first CTA of the cluster
 #pragma unroll
                     for (int j = 0; j < 16; j++)
@@ -521,11 +537,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
                         const int column = j0 + j + (lane >> 4);
                         if (column >= g.count || f >= width) continue;
                         const float x = f < a.ffn ? gate / (1.0f + expf(-gate)) * linear : 0.0f;
-                        // (infinities and NaNs go into the second value)
-                        const uint16_t hi = narrow16<DT>(fminf(fmaxf(x, -kLargest<DT>), kLargest<DT>));
                         uint16_t* to = act + (size_t)l.slots[g.first + column] * 2 * width + f;
-                        to[0] = hi;
-                        to[width] = narrow16<DT>(x - widen16<DT>(hi));
+                        if constexpr (DT == kF16) {    // (infinities and NaNs go into the first value)
+                            const uint16_t first = narrow16<DT>(x * (1.0f / kFirstUnit));
+                            const float near = widen16<DT>(first) * kFirstUnit;
+                            to[0] = first;
+                            to[width] = isfinite(near) ? narrow16<DT>((x - near) * (1.0f / kSecondUnit)) : (uint16_t)0;
+                        } else {                       // (into the second)
+                            const uint16_t first = narrow16<DT>(fminf(fmaxf(x, -kLargest), kLargest));
+                            to[0] = first;
+                            to[width] = narrow16<DT>(x - widen16<DT>(first));
+                        }
                     }
                 } else {
                     const int h = m * kM + row;
@@ -561,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    if (warp == kIssuer) tmem_free(tmem, NT <= 16 ? 32 : 2 * NT);
+    if (warp == kIssuer) tmem_free(tmem, COLUMNS);
     if (threadIdx.x == 0 && sh.failed) report_error(a.status, a.statusHost, vTimeout, blockIdx.x, 0, UP ? 0 : 1);
     if (split > 1) {                                   // another CTA may still arrive here
         cluster_arrive();

@@ -467,12 +467,14 @@ vResult_t vMoeRoute(const vMoeDesc_t* desc, const void* x, const void* routerWei
  *   recvbuffs[r][t] = sum over k with expertIds[t][k] = e held by rank r of
  *                     expertWeights[t][k] * (down_e * a)
  * in the order of k and in fp32, rounded once: the ranks' partial sums, which vAllReduceRmsNorm or
- * vAllReduceBlockNorm adds up.  (a is held in fp32, with 16-bit types as the sum of two of their values:
- * with fp16 an a beyond 65504 is right to 2^-12 of itself, and one beyond 131008 becomes infinite.)  A token that goes to no expert of a rank gets zeros there.  An id
- * outside [0, experts) is no expert (padding); an expert named twice counts twice.  A rank that
- * holds no expert may pass NULL weights; every recvbuffs entry is written.  Outputs overlap no
- * input.  The workspace is at least what vMoeExpertsWorkspace gives for the descriptor, 16-byte
- * aligned, and used by nothing else until the call's work is done. */
+ * vAllReduceBlockNorm adds up.  With 16-bit types the products are the tensor cores', whose fp32 sums may
+ * cut off where others round, and a is held as two values of the type: right to 2^-18 of itself with bf16,
+ * with fp16 to 2^-22 of itself or 2^-35, whichever is more, and infinite beyond 131008.  With fp32 all of it
+ * is in fp32.  A token that goes to no expert of a rank gets zeros there.  An id outside [0, experts) is
+ * no expert (padding); an expert named twice counts twice.  A rank that holds no expert may pass NULL
+ * weights; every recvbuffs entry is written.  Outputs overlap no input.  The workspace is at least what
+ * vMoeExpertsWorkspace gives for the descriptor, 16-byte aligned, and used by nothing else until the
+ * call's work is done. */
 vResult_t vMoeExpertsWorkspace(const vMoeDesc_t* desc, vcomm_t comm, size_t* bytes);
 vResult_t vMoeExperts(const vMoeDesc_t* desc, const void* x, const int32_t* expertIds, const float* expertWeights,
                       const void* const* upbuffs, const void* const* downbuffs, void* const* recvbuffs,

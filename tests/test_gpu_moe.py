@@ -373,3 +373,15 @@ def test_refusals(comms):
     V.vcommGroupStart(comm)
     V.vMoeExperts(d, None, ids, weights, [w, w], [w, w], buf[1:], ws, comm)
     refused(V.vcommGroupEnd, comm)
+
+
+@pytest.mark.parametrize("inner", [1e-3, 1e-5, 1e-6, 1e-8])
+@pytest.mark.parametrize("rows,ffn", [(5, 1024), (5, 1023), (40, 600), (200, 1024), (200, 333)])
+def test_small_inner_values_of_fp16(comms, monkeypatch, rows, ffn, inner):
+    # silu(g) u far below what steps of 2^-24 resolve, under down weights around 1: held to 2^-22 of itself, or to
+    # 2^-35 (the second of the two values in units of 2^-10, its smallest step 2^-24, half of it lost)
+    monkeypatch.setitem(M.SPLIT, F16, (2.0 ** -22, 2.0 ** -35))
+    x, ids, weights, up, _ = make(2, rows, 64, ffn, 2, 1, F16, 101)
+    gen = torch.Generator().manual_seed(102)
+    down = [torch.randn(1, 64, ffn, generator=gen).to(F16) for _ in range(2)]
+    run_experts(comms(2), (x * (2 * inner) ** 0.5).to(F16), ids, weights, up, down)
