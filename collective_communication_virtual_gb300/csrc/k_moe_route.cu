@@ -366,12 +366,22 @@ constexpr int kSide = 4;             // a warp's tile: four tokens by four exper
 constexpr int kPass = kRouteTileThreads / 32 / (kRouteTile / kSide) * kSide;   // experts of a CTA at a time
 constexpr int kFold = 4;             // vectors of eight products that a lane adds before the error-free sum
 
+// How far off a logit of a tile is at most, from the squared norms of its token and expert: seventeen
+// roundings a product, and the magnitudes' sum is at most the product of the norms.  Squares below 2^-149 are
+// lost: with room for them no norm is too small, and none is zero beside an infinite one.  Scores closer
+// than 10^-24 are not told apart, which leaves tokens and experts of zeros at that.
+__device__ __noinline__ float bound_of(float token, float expert, int hidden) {
+    const float lost = (float)hidden * 0x1p-149f;
+    const float off = 20.0f * kUnit * sqrtf(token + lost) * sqrtf(expert + lost);
+    return off < 0x1p-81f ? 0.0f : off;
+}
+
 template <int DT, int WT, bool ALIGNED>
 __global__ void __launch_bounds__(kRouteTileThreads, 1) k_moe_route(const __grid_constant__ RouteArgs a) {
     pdl_begin();
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ Redo redo;
-    __shared__ float tokenNorm[kRouteTile];
+    __shared__ float tokenNorm[kRouteTile];             // squared
     const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
     const int mine = (kRouteTile + a.cluster - 1) / a.cluster;   // tokens that a CTA picks for
     const Picks picks = picks_at(smem, mine, a.experts);
@@ -452,18 +462,18 @@ __global__ void __launch_bounds__(kRouteTileThreads, 1) k_moe_route(const __grid
         const float s2 = __shfl_xor_sync(~0u, sum[0], 16), c2 = __shfl_xor_sync(~0u, rest[0], 16);
         add_exactly(sum[0], rest[0], s2);
         rest[0] = __fadd_rn(rest[0], c2);
-        float norm = 0.0f;           // of expert e0 + lane % 4
+        float norm = 0.0f;           // of expert e0 + lane % 4, squared
 #pragma unroll
         for (int e = 0; e < kSide; e++) {
             float q = square[e].x + square[e].y;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(~0u, q, o);
-            if ((lane & 3) == e) norm = sqrtf(q);
+            if ((lane & 3) == e) norm = q;
         }
         float q = token.x + token.y;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(~0u, q, o);
-        if (pass == rank * a.share && group < kSide && lane == 0) tokenNorm[t0 + group] = sqrtf(q);
+        if (pass == rank * a.share && group < kSide && lane == 0) tokenNorm[t0 + group] = q;
         __syncthreads();
         if (!started) {                                // every CTA of the cluster has
             cluster_wait();
@@ -472,9 +482,8 @@ __global__ void __launch_bounds__(kRouteTileThreads, 1) k_moe_route(const __grid
         // bits 3 and 2 of the lane chose the token, bits 1 and 0 the expert
         const int t = t0 + (lane >> 2 & 3), e = e0 + (lane & 3);
         if (lane < 16 && row0 + t < a.rows && e < last) {
-            // seventeen roundings a product; the magnitudes' sum is at most the product of the norms
             send(picks, (size_t)(t / a.cluster) * a.experts + e, t % a.cluster, a.cluster, settle(sum[0], rest[0]),
-                 20.0f * kUnit * tokenNorm[t] * norm);
+                 bound_of(tokenNorm[t], norm, a.hidden));
         }
     }
     if (a.cluster > 1) {

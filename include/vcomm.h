@@ -457,7 +457,8 @@ typedef struct {
  * index and a NaN last; expertWeights[t][k] (fp32) = exp(logit of it) / sum of exp(logits), over
  * the chosen experts or all (normalize).  Where fp32 sums leave open which of two scores is the
  * larger, their logits are computed anew with twice the digits, so the choice is that of exact
- * sums but for scores closer than about 2^-45 of their products' magnitudes, or than 10^-24. */
+ * sums but for scores closer than about 2^-45 of their products' magnitudes, or than 10^-24.  The
+ * weights' logits are fp32 sums, off by at most 17 units of 2^-24 of their products' magnitudes. */
 vResult_t vMoeRoute(const vMoeDesc_t* desc, const void* x, const void* routerWeight, const float* bias,
                     int32_t* expertIds, float* expertWeights, vcomm_t comm, cudaStream_t stream);
 

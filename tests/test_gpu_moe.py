@@ -385,3 +385,35 @@ def test_small_inner_values_of_fp16(comms, monkeypatch, rows, ffn, inner):
     gen = torch.Generator().manual_seed(102)
     down = [torch.randn(1, 64, ffn, generator=gen).to(F16) for _ in range(2)]
     run_experts(comms(2), (x * (2 * inner) ** 0.5).to(F16), ids, weights, up, down)
+
+
+def neighbours(rows, hidden, experts, seed):
+    """Experts in pairs whose logits differ by some 10^-7 of themselves, less than an fp32 sum's error."""
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, hidden, generator=gen).to(BF16)
+    w = torch.randn(experts, hidden, generator=gen) * hidden ** -0.5
+    w[1::2] = w[::2]
+    w[1::2, 7] += 2.0 ** -20 * torch.randn(experts // 2, generator=gen)
+    return x, w
+
+
+@pytest.mark.parametrize("tokens_by,weights_by", [(1.0, 1.0), (2.0 ** -80, 2.0 ** 54), (2.0 ** 60, 2.0 ** -80), (2.0 ** 70, 2.0 ** -70)])
+@pytest.mark.parametrize("rows,hidden,experts", [(16, 512, 64), (200, 1024, 64), (200, 600, 130)])
+def test_route_tells_neighbouring_scores_apart_at_any_scale(comms, rows, hidden, experts, tokens_by, weights_by):
+    # squares of the tokens or of the weights below fp32's smallest value, or above its largest
+    x, w = neighbours(rows, hidden, experts, hidden)
+    run_route(comms(1), rows, hidden, experts, 8, BF16, F32, 0, x=x * tokens_by, w=w * weights_by)
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_route_of_large_tokens_by_experts_of_zeros(comms, rows):
+    # one expert whose logit is some 2^-25 of its products' magnitudes, all others zero: its sign decides
+    hidden, experts = 512, 40
+    for seed in range(12):
+        gen = torch.Generator().manual_seed(seed)
+        x0 = torch.randn(hidden, generator=gen).to(BF16)
+        w = torch.zeros(experts, hidden)
+        w[17] = torch.randn(hidden, generator=gen)
+        for j in range(3):                            # down to the last bit of one weight after another
+            w[17, j] -= float(w[17].double() @ x0.double() / x0[j].double())
+        run_route(comms(1), rows, hidden, experts, 1, BF16, F32, 0, x=(x0 * 2.0 ** 70).expand(rows, -1), w=w)
