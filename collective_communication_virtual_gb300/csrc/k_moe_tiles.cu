@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
         uint32_t round = 0;                            // times that all stages have been filled
         // The next stage; false at the end.
         const auto fill = [&](bool early) {
-            if (round > 0 && !__all_sync(~0u, bar_wait(&sh.empty[at], (round - 1) & 1u, &sh.failed))) return false;
+            if (round > 0 && !__all_sync(~0u, bar_wait(&sh.empty[at], (round - 1) & 1u, &sh.failed, a.timeoutNs))) return false;
             if (ALIGNED && !early) copy_a(u, chunk, at);
             if (!ALIGNED) {
                 if (!early) store_a(u, chunk, at, words);
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
             next(u, chunk);
             return u < units;
         };
-        bool more = u < units;
+        bool more = u < units && (int)blockIdx.x != a.stallCta;
         for (; more && early > 0; early--) more = fill(true);
         while (more) more = fill(false);
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -464,10 +464,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
             for (int u = first; u < units && ok; u += step, unit++) {
                 const int n = (l.groups[u / tiles].count + 15) & ~15, buffer = unit & 1;
                 const uint32_t shape = product_shape<DT>(n), d = tmem + (uint32_t)(buffer * NT * SUMS);
-                if (unit >= 2 && !(ok = bar_wait(&sh.sumsEmpty[buffer], (uint32_t)(unit / 2 - 1) & 1u, &sh.failed))) break;
+                if (unit >= 2 && !(ok = bar_wait(&sh.sumsEmpty[buffer], (uint32_t)(unit / 2 - 1) & 1u, &sh.failed, a.timeoutNs))) break;
                 tmem_fence_after();
                 for (int chunk = chunk0; chunk < chunk1; chunk++) {
-                    if (!(ok = bar_wait(&sh.full[at], round & 1u, &sh.failed))) break;
+                    if (!(ok = bar_wait(&sh.full[at], round & 1u, &sh.failed, a.timeoutNs))) break;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     tmem_fence_after();
                     const uint32_t sa = stages + (uint32_t)(at * kStage), sb = sa + 2 * kHalfA;
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
             }
             // nothing of this CTA's is under way when its tensor memory is given back
             products_done(&sh.drained);
-            bar_drain(&sh.drained, 0, &sh.failed);
+            bar_drain(&sh.drained, 0, &sh.failed, a.timeoutNs);
         }
         __syncwarp();
     } else {
@@ -500,9 +500,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_tiles(const __grid_constant
         for (int u = first; u < units; u += step, unit++) {
             const MoeGroup g = l.groups[u / tiles];
             const int m = u % tiles, buffer = unit & 1;
-            bool ok = bar_wait(&sh.sumsFull[buffer], (uint32_t)(unit / 2) & 1u, &sh.failed);
-            if (rank > 0 && unit > 0) ok = ok && bar_wait(&sh.partEmpty, (uint32_t)(unit - 1) & 1u, &sh.failed);
-            if (split > 1 && rank == 0) ok = ok && bar_wait(&sh.partFull, (uint32_t)unit & 1u, &sh.failed);
+            bool ok = bar_wait(&sh.sumsFull[buffer], (uint32_t)(unit / 2) & 1u, &sh.failed, a.timeoutNs);
+            if (rank > 0 && unit > 0) ok = ok && bar_wait(&sh.partEmpty, (uint32_t)(unit - 1) & 1u, &sh.failed, a.timeoutNs);
+            if (split > 1 && rank == 0) ok = ok && bar_wait(&sh.partFull, (uint32_t)unit & 1u, &sh.failed, a.timeoutNs);
             if (!__all_sync(~0u, ok)) break;
             tmem_fence_after();
             for (int j0 = 0; j0 < g.count; j0 += 16) {

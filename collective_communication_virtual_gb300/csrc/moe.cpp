@@ -196,6 +196,8 @@ vResult_t experts(const vMoeDesc_t* desc, const void* x, const int* ids, const f
     a.combineHere = 1;
     a.status = v.status;
     a.statusHost = v.statusHost;
+    a.timeoutNs = v.timeoutNs;
+    a.stallCta = v.testStallRank;
     if (m.esz == 2) {
         const vc::MoeTiles t = moe_tiles(a, v.smCount);
         if (v.debug)

@@ -54,6 +54,8 @@ struct ExpertsArgs {
     int combineHere;                 // the same: the way down adds up the slots
     Status* status;                  // device copy
     volatile Status* statusHost;     // pinned mirror
+    unsigned long long timeoutNs;    // limit of every wait
+    int stallCta;                    // test hook: this CTA of both launches copies no stage (-1 = off)
 };
 constexpr int kMoeTile = 8;          // output columns of a CTA, at least
 cudaError_t launch_moe_experts(const ExpertsArgs& a, cudaStream_t s);

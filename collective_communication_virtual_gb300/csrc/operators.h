@@ -19,6 +19,8 @@ struct CommView {
     bool grouping;                   // between vcommGroupStart and vcommGroupEnd
     Status* status;                  // where a kernel whose bounded wait runs out says so: the device's
     Status* statusHost;              // copy and the pinned mirror, both by device address
+    unsigned long long timeoutNs;    // limit of such a wait
+    int testStallRank;               // test hook (-1 = off)
 };
 // vInvalidArgument for a bad handle, the sticky error if there is one, else vSuccess.
 vResult_t comm_view(vcomm_t c, CommView* v);

@@ -32,14 +32,14 @@ __device__ __forceinline__ bool bar_test(uint64_t* bar, uint32_t parity) {
                  : "=r"(done) : "r"(smem_at(bar)), "r"(parity) : "memory");
     return done != 0;
 }
-// Wait for the phase of this parity, at most two seconds; a wait that gives up sets *failed, which ends
-// the CTA's other waits too.
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
+// Wait for the phase of this parity, at most `limit` nanoseconds; a wait that gives up sets *failed, which
+// ends the CTA's other waits too.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* failed, unsigned long long limit) {
     if (bar_test(bar, parity)) return true;
     const unsigned long long t0 = global_timer_ns();
     while (!bar_test(bar, parity)) {
         if (*failed) return false;
-        if (global_timer_ns() - t0 > 2000ull * 1000 * 1000) {
+        if (global_timer_ns() - t0 > limit) {
             *failed = 1;
             return false;
         }
@@ -48,10 +48,10 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
 }
 
 // The same for what has to be over before the CTA gives its memory back, whatever failed.
-__device__ __forceinline__ void bar_drain(uint64_t* bar, uint32_t parity, volatile int* failed) {
+__device__ __forceinline__ void bar_drain(uint64_t* bar, uint32_t parity, volatile int* failed, unsigned long long limit) {
     const unsigned long long t0 = global_timer_ns();
     while (!bar_test(bar, parity)) {
-        if (global_timer_ns() - t0 > 2000ull * 1000 * 1000) {
+        if (global_timer_ns() - t0 > limit) {
             *failed = 1;
             return;
         }

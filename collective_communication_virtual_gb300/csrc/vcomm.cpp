@@ -548,6 +548,8 @@ vResult_t comm_view(vcomm_t c, CommView* v) {
     v->grouping = c->groupDepth > 0;
     v->status = c->statusDev;
     v->statusHost = c->statusHostDev;
+    v->timeoutNs = (unsigned long long)c->cfg.timeoutMs * 1000000ull;
+    v->testStallRank = c->testStallRank;
     return vSuccess;
 }
 

@@ -141,7 +141,7 @@ typedef enum {
 vResult_t vcommInit(vcomm_t* comm, int nRanks, int nChannels, vProto_t protocol);
 
 /* Wait for the last enqueued work that uses the communicator's device memory (staged
- * ring transfers, variable all-to-all, bulk-copy fan-out), then free everything it owns.
+ * ring transfers, variable all-to-all, bulk-copy fan-out, vMoeExperts of 16-bit types), then free everything it owns.
  * The other collectives touch only the caller's buffers and need not have finished.
  * A NULL or already destroyed communicator gives vInvalidArgument. */
 vResult_t vcommDestroy(vcomm_t comm);
@@ -190,7 +190,7 @@ vResult_t vcommGroupEnd(vcomm_t comm);
  * 128-byte lines of 120 data bytes (LL128).  It must be a power of two in [4 KiB,
  * 64 MiB], or 0 for the planner's default: the largest power of two <= 1 MiB that keeps
  * all of the communicator's FIFOs (8 slots per channel and rank) within 1 GiB.
- * timeoutMs bounds every device-side wait (>= 1). */
+ * timeoutMs bounds every device-side wait (>= 1; default 2000). */
 vResult_t vcommSetAlgo(vcomm_t comm, vAlgo_t algo);
 vResult_t vcommSetProtocol(vcomm_t comm, vProto_t protocol);
 vResult_t vcommSetChunkBytes(vcomm_t comm, size_t chunkBytes);
@@ -640,7 +640,8 @@ vResult_t vPlanChannelRange(const vPlanInfo_t* plan, size_t count, int channel, 
 
 /* Test hook for failure detection: rank `rank` of every later ring transfer never
  * starts (its CTAs return at once), so its neighbours' bounded waits run out and the
- * transfer ends with the sticky error vTimeout.  -1 turns the hook off. */
+ * transfer ends with the sticky error vTimeout.  In vMoeExperts of 16-bit types it is CTA `rank`
+ * of both launches that copies nothing to its tensor core.  -1 turns the hook off. */
 vResult_t vcommTestSetStallRank(vcomm_t comm, int rank);
 
 /* Test hook for the LL128 line check: in every later LL128 ring transfer rank `rank`

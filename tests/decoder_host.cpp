@@ -33,6 +33,8 @@ vResult_t comm_view(vcomm_t c, CommView* v) {
     v->nRanks = g_ranks;
     v->smCount = 152;
     v->grouping = g_grouping != 0;
+    v->timeoutNs = 7654321;
+    v->testStallRank = 5;
     return vSuccess;
 }
 vResult_t comm_record(vcomm_t, std::function<vResult_t()> call) {
@@ -117,6 +119,8 @@ void host_experts(int* out) {
                           g_experts.aligned, g_experts.tileUp, g_experts.tileDown, g_experts.share};
     std::memcpy(out, fields, sizeof(fields));
 }
+long long host_experts_limit() { return (long long)g_experts.timeoutNs; }
+int host_experts_stall() { return g_experts.stallCta; }
 void host_sample(int* out) {
     const int fields[] = {g_sample.cluster, g_sample.each, g_sample.nParts, g_sample.nOut, g_sample.part};
     std::memcpy(out, fields, sizeof(fields));

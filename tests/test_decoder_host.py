@@ -233,6 +233,13 @@ def test_expert_shapes(host, dtype):
             assert need.value >= rows * k * 4 * (ffn + hidden) + -(-hidden // s["tile_down"]) * 4, where
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_the_communicators_limit_and_hook_reach_the_experts(host, dtype):
+    host.host_experts_limit.restype = ctypes.c_longlong
+    assert calls(host)["experts"](desc=V.vMoeDesc(4, 64, 32, 6, 2, dtype)) == OK
+    assert host.host_experts_limit() == 7654321 and host.host_experts_stall() == 5
+
+
 def test_sample_shapes(host):
     out = (ctypes.c_int * 5)()
     for ranks, rows, vocab, dtype, offset in itertools.product((1, 3, 8, 64), (1, 10, 40, 300, 1 << 20), (1, 2, 7, 63, 64, 1000, 4097, 50001, 131072, 262144),

@@ -1,6 +1,8 @@
 """The experts' router and their layer for a few tokens, against the formulas in 64 bits."""
 from __future__ import annotations
 
+import time
+
 import pytest
 import torch
 
@@ -417,3 +419,34 @@ def test_route_of_large_tokens_by_experts_of_zeros(comms, rows):
         for j in range(3):                            # down to the last bit of one weight after another
             w[17, j] -= float(w[17].double() @ x0.double() / x0[j].double())
         run_route(comms(1), rows, hidden, experts, 1, BF16, F32, 0, x=(x0 * 2.0 ** 70).expand(rows, -1), w=w)
+
+
+@pytest.mark.parametrize("rows,hidden,ffn,experts,k,stall", [(1, 2048, 1024, 16, 4, 0), (1, 2048, 1024, 16, 4, 1), (1, 2048, 1024, 16, 4, 3),
+                                                             (4, 33, 17, 5, 2, 0), (64, 512, 256, 8, 4, 2), (300, 500, 250, 4, 2, 1)])
+def test_a_wait_that_runs_out_ends_the_call_with_an_error(comms, rows, hidden, ffn, experts, k, stall):
+    # one CTA of both launches gets nothing to multiply: its waits, and those of the others that wait for it,
+    # give up after the communicator's limit, and the call is over
+    args = make(4, rows, hidden, ffn, experts, k, BF16, 21)
+    x, ids, weights = (place(t) for t in args[:3])
+    up, down = ([place(t) for t in ts] for ts in args[3:])
+    desc = V.vMoeDesc(rows, hidden, ffn, experts, k, BF16)
+    outs = [torch.empty(rows, hidden, dtype=BF16, device=DEV) for _ in range(4)]
+    comm = V.vcommInit(4)
+    try:
+        V.vcommSetTimeoutMs(comm, 100)
+        V.vcommTestSetStallRank(comm, stall)
+        ws = torch.empty(V.vMoeExpertsWorkspace(desc, comm), dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        V.vMoeExperts(desc, x, ids, weights, up, down, outs, ws, comm)
+        torch.cuda.synchronize()
+        # in each launch the stalled CTA's, then that of a CTA that waits for its sums
+        assert 0.1 <= time.perf_counter() - t0 < 1.0
+        assert V.vcommGetAsyncError(comm) == V.vTimeout
+        with pytest.raises(V.VcommError) as e:
+            V.vMoeExperts(desc, x, ids, weights, up, down, outs, ws, comm)
+        assert e.value.code == V.vTimeout
+    finally:
+        V.vcommDestroy(comm)
+    # the context and the tensor cores are as usable as before
+    run_experts(comms(4), *args)
