@@ -67,17 +67,17 @@ vc::MoeTiles moe_tiles(const vc::ExpertsArgs& a, int smCount) {
     };
     shape((a.ffn + 63) / 64, a.hidden, &t.splitUp, &t.gridUp);
     shape((a.hidden + 127) / 128, a.ffn, &t.splitDown, &t.gridDown);
-    const auto stages = [&](bool up, int bytes) {
+    // All stages that an SM has room for: its registers hold one CTA of either launch.  (72 registers a thread
+    // and 124 and 100 KiB hold one of each, the second's first weights on their way while the first runs, but
+    // spill: one token on 4 of 64 experts of 2048 x 1024 26.7 us, 26.2 so; on 8 of 128 of 4096 x 1536 71.4 and
+    // 69.0; on 2 of 8 of 6144 x 4096 74.7 and 83.7.)
+    const auto stages = [&](bool up, int split) {
         int n = 2;
-        while (n < vc::kMoeMaxStages &&
-               vc::moe_tiles_smem(a.experts, slots, t.tokens, up, up ? t.splitUp : t.splitDown, n + 1) <= bytes) n++;
+        while (n < vc::kMoeMaxStages && vc::moe_tiles_smem(a.experts, slots, t.tokens, up, split, n + 1) <= vc::kMoeMaxSmem) n++;
         return n;
     };
-    // A tile or two a CTA: both launches' CTAs on an SM, so that the second's first weights are on their
-    // way while the first still runs.
-    const bool few = groups * ((a.ffn + 63) / 64) * t.splitUp <= 2 * t.gridUp && t.tokens == 16;
-    t.stagesUp = stages(true, few ? 124 * 1024 : vc::kMoeMaxSmem);
-    t.stagesDown = stages(false, few ? 100 * 1024 : vc::kMoeMaxSmem);
+    t.stagesUp = stages(true, t.splitUp);
+    t.stagesDown = stages(false, t.splitDown);
     t.combineHere = a.rows <= 4;
     return t;
 }

@@ -233,6 +233,17 @@ def test_expert_shapes(host, dtype):
             assert need.value >= rows * k * 4 * (ffn + hidden) + -(-hidden // s["tile_down"]) * 4, where
 
 
+def test_few_tokens_get_all_stages_that_fit(host):
+    # a stage holds 128 columns of 128 rows of the weights, 32 KiB, and of 16 tokens one or two values, 4 KiB each
+    out = (ctypes.c_int * len(EXPERTS))()
+    for rows, hidden, ffn, experts, k in ((1, 2048, 1024, 64, 4), (1, 4096, 1536, 128, 8), (13, 1001, 333, 10, 3), (4, 64, 32, 6, 2)):
+        assert calls(host)["experts"](desc=V.vMoeDesc(rows, hidden, ffn, experts, k, BF16)) == OK
+        host.host_experts(out)
+        s = dict(zip(EXPERTS, out))
+        for way, stage in (("up", 36 * 1024), ("down", 40 * 1024)):
+            assert s["tokens"] == 16 and (s["stages_" + way] == 8 or s["smem_" + way] + stage > 225 * 1024), (rows, s)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_the_communicators_limit_and_hook_reach_the_experts(host, dtype):
     host.host_experts_limit.restype = ctypes.c_longlong
