@@ -16,7 +16,9 @@
 // place and what is kept before it by comparing it with all others.
 //
 // The draw is a comparison of sums, so these are exact: a weight is a 64-bit integer, 2^44 e, right to
-// 2^-30 of itself, and the order of additions does not matter.
+// 2^-28.8 of itself (sample_weight.cuh), and the order of additions does not matter.  Where a filter is given,
+// logprob's sum is one of fp32 exponentials, 2^-17 of itself off at most: a draw without filters, which sums
+// exact weights, takes 126 us for 256 rows of 131072, one of topK 50 87.
 //
 // A row is read once, into the shared memory of a cluster's CTAs, which exchange maxima and sums there.
 // What is above the bounds, where it is few, goes to the first of them, which decides alone, without the
@@ -33,22 +35,14 @@
 // a row a CTA, was slower (403 us against 169 for rows of all kinds).
 #include "norm_stage.cuh"
 #include "sample.h"
+#include "sample_weight.cuh"
 
 namespace vc {
 
 namespace {
 
 constexpr int kWarps = kSampleThreads / 32;
-constexpr int kFix = 44;             // weights in units of 2^-44
-typedef unsigned long long u64;
 constexpr int kWords = 4;            // that the CTAs of a cluster exchange at a time
-
-// 2^31 2^(k / 32), rounded
-__constant__ uint32_t kPowers[32] = {
-    2147483648u, 2194507417u, 2242560872u, 2291666561u, 2341847524u, 2393127307u, 2445529972u, 2499080105u,
-    2553802834u, 2609723834u, 2666869345u, 2725266179u, 2784941738u, 2845924021u, 2908241642u, 2971923842u,
-    3037000500u, 3103502151u, 3171459999u, 3240905930u, 3311872529u, 3384393094u, 3458501653u, 3534232978u,
-    3611622603u, 3690706840u, 3771522796u, 3854108391u, 3938502376u, 4024744348u, 4112874773u, 4202935003u};
 
 constexpr int kSampleFew = 256;      // values that are compared with one another
 struct alignas(16) FewValue {
@@ -149,10 +143,8 @@ __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~(o | ((1u << kKeyShift<DT>) - 1)));
 }
 
-// e of a value: x == top gives 1, also where both are infinite.
-struct Weights {
-    float top, ch, cl;               // ch + cl = log2(e) / temperature
-    const uint32_t* powers;
+// e of a value: as an integer, and roughly.
+struct Weights : FixedWeights {
     // The sum of E values' e, none of them the top's: 2^-20 off or so, and 0 below 2^-126.
     template <int E>
     __device__ __forceinline__ float rough(const float (&f)[E]) const {
@@ -166,41 +158,6 @@ struct Weights {
             sum = add2(sum, e);
         }
         return sum.x + sum.y;
-    }
-    // 2^44 e of two values, as integers: the difference and its product with ch + cl with their rounding
-    // errors, 2^(k/32) from a table and 2^g, |g| <= 1/64, from its series; without branches, two at a
-    // time, as every exact sum goes through here.
-    __device__ __forceinline__ void fixed2(float x, float y, u64& vx, u64& vy) const {
-        if (isinf(top)) {            // there is nothing beside infinities
-            vx = x == top ? 1ull << kFix : 0;
-            vy = y == top ? 1ull << kFix : 0;
-            return;
-        }
-        const auto both = [](float c) { return make_float2(c, c); };
-        const float2 f = make_float2(x, y), minus = both(-1.0f);
-        // f - top = d + low
-        const float2 d = add2(f, both(-top)), b = fma2(f, minus, d), t = fma2(b, minus, d);
-        const float2 low = add2(fma2(t, minus, f), fma2(b, minus, both(-top)));
-        const float2 np = mul2(d, both(-ch));          // -p, p = log2 e to 24 bits
-        float2 pl = fma2(d, both(ch), np);
-        pl = fma2(d, both(cl), pl);
-        pl = fma2(low, both(ch), pl);
-        const float magic = 12582912.0f;               // 1.5 2^23: the sum's low bits are the integer
-        const float2 at = make_float2(fminf(np.x, kFix + 2.0f), fminf(np.y, kFix + 2.0f));     // beyond this nothing is left
-        const float2 r = fma2(at, both(-32.0f), both(magic));
-        const float2 k = add2(r, both(-magic));
-        const float2 g = fma2(fma2(k, both(0.03125f), np), minus, pl);
-        float2 q = fma2(g, both(0.009618129107628477f), both(0.055504108664821576f));
-        q = fma2(g, q, both(0.2402265069591007f));
-        q = fma2(g, q, both(0.6931471805599453f));
-        q = mul2(mul2(g, q), both(8589934592.0f));     // 2^33
-        vx = assemble(r.x, q.x);
-        vy = assemble(r.y, q.y);
-    }
-    __device__ __forceinline__ u64 assemble(float r, float q) const {
-        const int k = __float_as_int(r) - __float_as_int(12582912.0f);
-        const uint32_t t = powers[k & 31], m = t + (uint32_t)__mulhi((int)(t >> 1), __float2int_rn(q));
-        return ((u64)m << (kFix - 31)) >> max(0, -(k >> 5));
     }
     __device__ __forceinline__ u64 fixed(float x) const {
         u64 a, b;
@@ -1023,16 +980,8 @@ __device__ __forceinline__ void draw(const SampleArgs& a, const Filters& q, Shar
     }
 
     Weights w;
-    w.top = top;
     w.powers = sh.powers;
-    {
-        // log2(e) / temperature and what its rounding lost, kept off zero and infinity
-        const float t = q.greedy ? 1.0f : q.heat, l2e = 1.44269504088896341f, l2eLow = 1.9259629911266175e-8f;
-        const float r = __frcp_rn(t), c = __fmul_rn(l2e, r);
-        w.ch = fminf(fmaxf(c, 1.17549435e-38f), 3.40282347e38f);
-        w.cl = (__fmaf_rn(-c, t, l2e) + l2eLow) * r;
-        if (w.ch != c || !(fabsf(w.cl) <= 1e-6f * c)) w.cl = 0.0f;
-    }
+    w.set(top, q.greedy ? 1.0f : q.heat);
 
     // All that may be kept is at least `bound`: topK's is known, topP's follows from the sum of all weights,
     // minP's is a weight.  (pBound: weights below (1 - p) of the mean are outside topP, all of them together.)

@@ -492,10 +492,12 @@ vResult_t vMoeExperts(const vMoeDesc_t* desc, const void* x, const int32_t* expe
  *           (sum of kept e up to i) > uniform * (sum of kept e)
  * A temperature that is not above zero takes the largest logit, the first of equals, without a
  * draw.  uniform lies in [0, 1); other values act as the nearest one, a NaN as 0.  Sums are
- * taken in units of 2^-44, of e right to 2^-30 of itself, and the same call gives the same tokens.
+ * taken in units of 2^-44, of e right to 2^-28.8 of itself (at temperatures from 10^-37 to 10^37), and the
+ * same call gives the same tokens.
  * tokenbuffs[r] (int32, one a row) may be NULL for ranks that want none, but not all; logprob (fp32,
  * one a row, may be NULL) = log of the token's share of all e before the filters (temperature 1 where
- * the largest is taken).
+ * the largest is taken); that sum is right to 2^-17 of itself where a filter is given, else as those
+ * above.
  * Logits of minus infinity and NaN are never drawn; infinite ones share the draw alone.  A row in
  * which nothing is left gives the token -1 and a NaN. */
 #define VCOMM_MAX_VOCAB 262144

@@ -1,7 +1,8 @@
 """Sampling in 64 bits.
 
-Weights are carried to 2^-30 of themselves, so a drawn number within 2^-28 of a token's border (in
-shares of the kept sum), and a filter whose border is that close to a running sum, may go either way:
+Weights are carried to d = 2^-28.8 of themselves, so a share s of a sum of them is off by at most
+2 d s (1 - s) < 2^-29, and a weight next to the largest by d.  A drawn number within 2^-28 of a token's border
+(in shares of the kept sum), and a filter whose border is that close to a running sum, may go either way:
 `matches` accepts those, and nothing else.
 """
 from __future__ import annotations
