@@ -203,19 +203,19 @@ __device__ __forceinline__ void combine(const ExpertsArgs& a, int t, int h) {
                 if (h + j < a.hidden) to[j] = narrow16<DT>(s[j]);
         }
     };
-    const auto add = [&](int k0, int k, float4& y, float& w, int& r) {
-        const size_t slot = (size_t)t * a.topK + min(k0 + k, a.topK - 1);
+    const auto add = [&](int k, float4& y, float& w, int& r) {
+        const size_t slot = (size_t)t * a.topK + min(k, a.topK - 1);
         const int e = a.ids[slot];
         w = a.weights[slot];
         y = __ldcg(reinterpret_cast<const float4*>(a.y + slot * moe_y_stride(a.hidden) + h));
-        r = k0 + k < a.topK && e >= 0 && e < a.experts ? e / a.share : -1;
+        r = k < a.topK && e >= 0 && e < a.experts ? e / a.share : -1;
     };
     if (a.topK <= UN) {
         float4 y[UN];
         float w[UN];
         int rank[UN];
 #pragma unroll
-        for (int k = 0; k < UN; k++) add(0, k, y[k], w[k], rank[k]);
+        for (int k = 0; k < UN; k++) add(k, y[k], w[k], rank[k]);
         for (int r = 0; r < a.nRanks; r++) {
             float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -236,7 +236,7 @@ __device__ __forceinline__ void combine(const ExpertsArgs& a, int t, int h) {
             float4 y;
             float w;
             int rank;
-            add(0, k, y, w, rank);
+            add(k, y, w, rank);
             if (rank != r) continue;
             s[0] = fmaf(w, y.x, s[0]);
             s[1] = fmaf(w, y.y, s[1]);

@@ -65,8 +65,8 @@ struct Shared {
     u64 found[2][3];                 // bin, what lies before it, what lies in it
     int count[2][kWarps];
     unsigned mass[2][3][kWarps];
-    u64 target, left, total;
-    int owner, settled;
+    u64 total;
+    int settled;
 };
 
 // What the exchanges between the CTAs of a cluster need.
