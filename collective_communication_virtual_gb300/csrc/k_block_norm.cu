@@ -13,7 +13,8 @@
 // byte written once: 18 of them a column and row of 8 ranks in bf16.  Memory bounds the long calls:
 // 8 x 4096 x 4096 bf16 99 us, 6.4 TB/s of 6.8, where two warps of three wait for a load, a barrier of the row's
 // reductions or shared memory; that is why many inputs get one vector a thread and two CTAs an SM, few
-// inputs, where instructions count, four.  One row of 8192 takes 6 us, all launch and latency.
+// inputs, where instructions count, four.  One row of 8192 takes 6 us, all launch and latency.  Rows too long to
+// stage have four vectors a thread and 96 registers, of which up to 864 bytes are spilled.
 #include "block_norm.cuh"
 
 namespace vc {

@@ -16,7 +16,8 @@
 //
 // Memory bounds aligned rows: 8 x 4096 x 4096 bf16 114 us (5.9 TB/s of 6.8; 105 the first launch alone).
 // Rows off 16 bytes are bound by instructions: 3 x 1537 x 2731 fp16 46 us (1.8 TB/s), at 125 registers with both
-// sums in shared memory, where every vector is shifted in and out and read and written back to the sums.
+// sums in shared memory, where every vector is shifted in and out and read and written back to the sums.  Rows too
+// long to stage spill up to 652 bytes a thread with four vectors.
 #include "block_norm.cuh"
 
 namespace vc {

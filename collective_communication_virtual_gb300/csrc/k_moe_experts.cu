@@ -11,7 +11,8 @@
 // one 16-byte vector a lane, against up to eight slots at a time.
 //
 // No tensor cores: theirs would round the factors to 11 bits.  16 tokens on 2 of 16 experts of 2048 x 1024
-// take 132 us (355 MB, 2.7 TB/s: the products' instructions count as much as the loads), one token 31 us.
+// take 128 us (355 MB, 2.8 TB/s: ten 16-byte loads a lane for 64 multiply-adds, which keep the load pipe busy),
+// one token 31 us.
 #include "moe.h"
 #include "norm.cuh"
 

@@ -18,7 +18,8 @@
 // latency).  More: eight tokens, a warp four of them by four experts, so that what it loads serves four
 // times (256 x 4096 of 128, fp32 router: 30 us, of which the loop over the columns takes 15, bound by its
 // instructions, near 390 a warp and 256 columns, and logits computed anew 7; tiles staged in shared
-// memory and read by threads that share rows 67, the same warp's tiles from stages copied ahead 37).  The
+// memory and read by threads that share rows 67, the same warp's tiles from stages copied ahead 37).  All 128
+// registers are taken: 28 to 64 bytes a thread are spilled around that loop, 236 to 284 of unaligned rows.  The
 // logits go to the CTA that picks for their token.
 #include "moe.h"
 #include "norm_stage.cuh"

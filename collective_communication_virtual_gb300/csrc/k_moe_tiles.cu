@@ -10,9 +10,10 @@
 // have room.  Rows that start off 16 bytes come through registers, a stage ahead, as the aligned words that
 // hold them.
 //
-// Measured (bf16): 64 tokens on 8 of 128 experts of 4096 x 1536, 4.8 GB of weights, 780 us (6.1 TB/s; the way up
-// 499), with 4095 x 1535 1741 (2.7); 8 tokens there 339 us (5.7 TB/s), one token 69 (4.4); one token on 4 of
-// 64 experts of 2048 x 1024 25 us (2.0), a chain of latencies: ids, weights, sums, ids, weights, sums.
+// Measured (bf16): 64 tokens on 8 of 128 experts of 4096 x 1536, 4.8 GB of weights, 757 to 773 us (6.2 TB/s; the
+// way up 499), with 4095 x 1535 1735 (2.7); 8 tokens there 338 us (5.7 TB/s), one token 69 (4.4); one token on 4
+// of 64 experts of 2048 x 1024 26 us (1.9), a chain of latencies: ids, weights, sums, ids, weights, sums.  The
+// second launch gets onto an SM when the first has left it: registers (69 and 115 a thread) hold one CTA.
 //
 // The way up: the tile's rows are 64 of the gate and the 64 of the linear part that belong to them,
 // sixteen and sixteen in turn, so that both sums of an element lie in one warp.  silu(g) u goes into the
@@ -21,7 +22,8 @@
 // rounding.  In bf16 the two add up to the value, 2^-18 of it off.  fp16 has steps of 2^-24 at the least, so
 // there the first is in units of 2 and the second in units of 2^-10, and each has sums of its own, which
 // meet in fp32: 2^-22 of the value off, or 2^-35 where it is small; beyond 2 x 65504 it is infinite.  (Both in
-// units of 1, one sum: 2^-25 off, more than the result's own rounding for values below 10^-4.)
+// units of 1, one sum: 2^-25 off, more than the result's own rounding for values below 10^-4; the second sums
+// cost 1 to 2 %, 96 tokens on 2 of 8 of 2048 x 1024 41.7 us in place of 40.9.)
 // The way down: every slot's output goes into the workspace in fp32; for few tokens the last warp of a
 // tile of columns adds them up, for more a third launch.
 #include "moe.h"

@@ -30,9 +30,10 @@
 // Instructions and the latencies between a row's reductions bound it, not memory (256 rows of 131072 bf16
 // are read in 10 us): those take 68 us where the largest is taken, 88 with topK 50 and topP, 112 with topK
 // 200, 126 without filters (a weight of every logit), 146 with topP 0.9 at temperature 0.6, where the
-// nucleus fits the list, and 354 at 1.2, where it holds most of the row and the histograms decide.  One row
-// takes 12 to 24 us on eight CTAs, and 50 with such a nucleus.  A CTA that streams its row from memory several times,
-// a row a CTA, was slower (403 us against 169 for rows of all kinds).
+// nucleus fits the list, and 354 at 1.2, where it holds most of the row and the histograms decide; rows of all
+// kinds 173.  One row takes 12 to 24 us on eight CTAs, 41 with topK 2000 and topP, and 50 with such a nucleus.  A
+// CTA that streams its row from memory several times, a row a CTA, was slower (403 us for rows of all kinds).  Two
+// CTAs an SM leave 64 registers a thread: 112 bytes of 16-bit types are spilled, 4 of fp32.
 #include "norm_stage.cuh"
 #include "sample.h"
 #include "sample_weight.cuh"
