@@ -612,6 +612,9 @@ cudaError_t tiles_launch(const ExpertsArgs& a, const MoeTiles& t, cudaStream_t s
     b.split = UP ? t.splitUp : t.splitDown;
     b.stages = UP ? t.stagesUp : t.stagesDown;
     b.combineHere = t.combineHere;
+    // A wait for a tile's sums lasts as long as its stages take, under a microsecond each where the memory is not
+    // shared with other work: 20 for each are no lack of progress.
+    b.timeoutNs += 20000ull * (unsigned)(((UP ? a.hidden : a.ffn) + kK - 1) / kK);
     NormShape sh = {};
     sh.threads = kThreads;
     sh.cluster = b.split;

@@ -190,7 +190,7 @@ vResult_t vcommGroupEnd(vcomm_t comm);
  * 128-byte lines of 120 data bytes (LL128).  It must be a power of two in [4 KiB,
  * 64 MiB], or 0 for the planner's default: the largest power of two <= 1 MiB that keeps
  * all of the communicator's FIFOs (8 slots per channel and rank) within 1 GiB.
- * timeoutMs bounds every device-side wait (>= 1; default 2000). */
+ * timeoutMs bounds every device-side wait that sees no progress (>= 1; default 2000). */
 vResult_t vcommSetAlgo(vcomm_t comm, vAlgo_t algo);
 vResult_t vcommSetProtocol(vcomm_t comm, vProto_t protocol);
 vResult_t vcommSetChunkBytes(vcomm_t comm, size_t chunkBytes);

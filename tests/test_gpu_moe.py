@@ -450,3 +450,17 @@ def test_a_wait_that_runs_out_ends_the_call_with_an_error(comms, rows, hidden, f
         V.vcommDestroy(comm)
     # the context and the tensor cores are as usable as before
     run_experts(comms(4), *args)
+
+
+@pytest.mark.parametrize("hidden,ffn", [(65536, 64), (65535, 63), (72, 65536), (71, 65535)])
+def test_the_shortest_limit_is_long_enough_for_the_longest_rows(hidden, ffn):
+    # a tile's 512 stages take up to a millisecond, in which there is progress
+    comm = V.vcommInit(1)
+    try:
+        V.vcommSetTimeoutMs(comm, 1)
+        args = make(1, 70, hidden, ffn, 2, 1, BF16, 31)
+        for _ in range(3):
+            run_experts(comm, *args)
+        assert V.vcommGetAsyncError(comm) == V.vSuccess
+    finally:
+        V.vcommDestroy(comm)
